@@ -7,7 +7,9 @@ and streams.  There is no fallback: if the library is missing or the device is
 not sm_103, the calls raise.
 
 Entry points (same names as the C ABI): ``tl_ag_gemm``, ``tl_gemm_rs``,
-``tl_mlp2``, ``tl_moe_combine`` and their ``*_workspace_bytes`` sizes, plus
+``tl_mlp2``, ``tl_moe_combine``, the serving operators ``tl_kv_append``,
+``tl_paged_attention``, ``tl_window_attention`` and ``tl_moe_tokens``, their
+``*_workspace_bytes`` sizes, plus
 ``Context`` (tl_ctx_create / tl_ctx_check / tl_ctx_destroy / tl_ctx_set_trace),
 the host-side tile maps ``tl_ag_tile_order`` / ``tl_rs_tile_order`` and
 ``tl_trace_bytes`` (the trace buffer is read by ``.trace``).
@@ -21,13 +23,14 @@ from . import _build
 
 __all__ = [
     "TL_OK", "TL_ERR_INVALID", "TL_ERR_UNSUPPORTED", "TL_ERR_CUDA", "TL_ERR_TIMEOUT", "TL_ERR_WORKSPACE",
-    "TLError", "Config", "Context", "lib", "library_path", "build",
+    "TL_ERR_INDEX", "TL_BF16", "TL_FP16", "TL_E4M3", "TLError", "PagedCache", "Config", "Context", "lib", "library_path", "build",
     "tl_ag_gemm", "tl_ag_gemm_ll_capable", "tl_allgather", "tl_gemm_rs", "tl_reduce_scatter", "tl_mlp2",
     "tl_moe_combine",
     "tl_ag_gemm_workspace_bytes", "tl_gemm_rs_workspace_bytes", "tl_gemm_rs_ring_workspace_bytes",
     "tl_mlp2_workspace_bytes", "tl_rs_ring_tile_order", "tl_moe_tile_order", "tl_moe_combine_order",
     "tl_moe_workspace_bytes", "tl_ag_tile_order", "tl_rs_tile_order", "tl_trace_bytes", "tl_ag_attention",
-    "tl_ag_attention_workspace_bytes", "EXPORTED_SYMBOLS",
+    "tl_ag_attention_workspace_bytes", "tl_kv_append", "tl_paged_attention", "tl_paged_attention_workspace_bytes",
+    "tl_window_attention", "tl_moe_tokens", "tl_moe_tokens_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 TL_OK = 0
@@ -36,6 +39,11 @@ TL_ERR_UNSUPPORTED = -2
 TL_ERR_CUDA = -3
 TL_ERR_TIMEOUT = -4
 TL_ERR_WORKSPACE = -5
+TL_ERR_INDEX = -6
+
+TL_BF16 = 0
+TL_FP16 = 1
+TL_E4M3 = 2
 
 library_path = _build.LIB
 build = _build.build
@@ -64,6 +72,27 @@ class Config(ctypes.Structure):
         ("mover_tma", _i),
     ]
 
+
+class PagedCache(ctypes.Structure):
+    """Mirror of ``tl_paged_cache`` (include/tl.h)."""
+    _fields_ = [
+        ("k", _vp),
+        ("v", _vp),
+        ("k_scale", _vp),
+        ("v_scale", _vp),
+        ("page_stride", ctypes.c_longlong),
+        ("row_stride", ctypes.c_longlong),
+        ("head_stride", ctypes.c_longlong),
+        ("dtype", _i),
+        ("num_pages", _i),
+        ("page_size", _i),
+        ("kv_heads", _i),
+        ("d", _i),
+    ]
+
+
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 
 # name -> (restype, argtypes); the full exported C ABI.
 _SIGS = {
@@ -94,6 +123,14 @@ _SIGS = {
     "tl_ag_attention_workspace_bytes": (_c_size, [_i, _i, _i, _i]),
     "tl_ag_attention": (_i, [_vp, _i, _i, _vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _c_size, _i, _i,
                              _i, _vp]),
+    "tl_kv_append": (_i, [_vp, _vp, _i, _vp, _vp, _ll, _ll, _ll, _ll, _vp, _i, _vp]),
+    "tl_paged_attention_workspace_bytes": (_c_size, [_i, _i, _i, _i]),
+    "tl_paged_attention": (_i, [_vp, _vp, _i, _vp, _ll, _ll, _vp, _i, _vp, _vp, _ll, _ll, _vp, _i, _i, _f, _i, _i, _vp,
+                                _c_size, _vp]),
+    "tl_window_attention": (_i, [_vp, _i, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _ll, _vp,
+                                 _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp]),
+    "tl_moe_tokens_workspace_bytes": (_c_size, [_i, _i, _i, _i, _i]),
+    "tl_moe_tokens": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _i, _i, _i, _i, _vp]),
     "tl_ag_tile_order": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _i]),
     "tl_rs_tile_order": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _i]),
     "tl_rs_ring_tile_order": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i]),
@@ -158,9 +195,14 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream)
 
 
+_dtypes: dict = {}
+
+
 def _need(t, dtype_name: str, what: str):
-    import torch
-    dt = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8}[dtype_name]
+    if not _dtypes:
+        import torch
+        _dtypes.update({"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8})
+    dt = _dtypes[dtype_name]
     if t is None:
         raise ValueError(f"{what} is required")
     if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
@@ -364,6 +406,144 @@ def tl_moe_combine(ctx: Context, x, logits, topk: int, w_gate, w_up, w_down, out
                               _ptr(out), _ptr(perm_out), _ptr(counts_out), _ptr(workspace), workspace.numel(),
                               T, H, E, F, _stream(stream))
     _check(rc, "tl_moe_combine")
+
+
+# ---------------------------------------------------------------- serving: cache, decoding, prompts
+_codes: dict = {}
+
+
+def _code(t, what: str) -> int:
+    """TL_BF16, TL_FP16 or TL_E4M3 of a CUDA tensor."""
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: TL_BF16, torch.float16: TL_FP16, torch.float8_e4m3fn: TL_E4M3})
+    c = _codes.get(t.dtype)
+    if c is None or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA bf16, fp16 or (a cache) e4m3 tensor (got {t.dtype}, {t.device})")
+    return c
+
+
+def _rows(t, what: str):
+    """The strides (elements) of a 3-D view with a contiguous innermost dimension: that of the first
+    dimension and that of the second; the stride of a dimension of one entry, which nothing uses, as 0."""
+    a, b, c = t.stride()
+    n, m, d = t.shape
+    if c != 1 and d > 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    return (a if n > 1 else 0), (b if m > 1 else 0)
+
+
+def _vec(t, n: int, dtype_name: str, what: str) -> int:
+    """The pointer of an optional contiguous CUDA tensor of n entries."""
+    if t is None:
+        return 0
+    _need(t, dtype_name, what)
+    if t.numel() != n:
+        raise ValueError(f"{what} must have {n} entries (got {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale) -> PagedCache:
+    code = _code(k_cache, "k_cache")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or not v_cache.is_cuda:
+        raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
+    pages, page, heads, d = k_cache.shape
+    a, b, c, one = k_cache.stride()
+    if v_cache.stride() != (a, b, c, one) or one != 1:
+        raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _vec(k_scale, heads, "f32", "k_scale"),
+                      _vec(v_scale, heads, "f32", "v_scale"), a if pages > 1 else 0, b if page > 1 else 0,
+                      c if heads > 1 else 0, code, pages, page, heads, d)
+
+
+def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None) -> None:
+    """Write the rows k, v (bf16 or fp16 [tokens, kv_heads, d]) into a paged cache ([pages, page_size,
+    kv_heads, d] views of any page, row and head strides; the type of k, or float8_e4m3fn holding
+    k / k_scale[h]) at slots (int32 [tokens]: page * page_size + row; negative: skipped)."""
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    code = _code(k, "k")
+    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or not v.is_cuda or \
+            k.shape[1:] != (cache.kv_heads, cache.d):
+        raise ValueError("inconsistent shapes")
+    n = k.shape[0]
+    sp = _vec(slots, n, "i32", "slots")
+    rc = lib().tl_kv_append(ctx.handle, ctypes.byref(cache), code, k.data_ptr(), v.data_ptr(), *_rows(k, "k"),
+                            *_rows(v, "v"), sp, n, _stream(stream))
+    _check(rc, "tl_kv_append")
+
+
+def tl_paged_attention_workspace_bytes(batch, heads, kv_heads, d) -> int:
+    return lib().tl_paged_attention_workspace_bytes(batch, heads, kv_heads, d)
+
+
+def tl_paged_attention(ctx: Context, q, k_cache, v_cache, page_table, lengths, out, workspace, lse=None, scale=None,
+                       window: int = 0, sinks: int = 0, k_scale=None, v_scale=None, stream=None) -> None:
+    """out[b, h] = softmax(scale q[b, h] K^T) V over the visible rows of sequence b in a paged cache: the
+    first lengths[b] rows, with a window only the last `window` and the first `sinks` of them.
+    q, out: bf16 or fp16 [batch, heads, d]; caches as tl_kv_append; page_table int32 [batch, max_pages];
+    lengths int32 [batch] (the new token's row counted); lse fp32 [batch, heads]; scale: 1/sqrt(d)."""
+    cache = _cache(k_cache, v_cache, k_scale, v_scale)
+    code = _code(q, "q")
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or q.shape[2] != cache.d or \
+            page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+        raise ValueError("inconsistent shapes")
+    batch, heads, d = q.shape
+    pages = page_table.shape[1]
+    _need(workspace, "u8", "workspace")
+    tp = _vec(page_table, batch * pages, "i32", "page_table")
+    lp = _vec(lengths, batch, "i32", "lengths")
+    rc = lib().tl_paged_attention(ctx.handle, ctypes.byref(cache), code, q.data_ptr(), *_rows(q, "q"), tp, pages, lp,
+                                  out.data_ptr(), *_rows(out, "out"), _vec(lse, batch * heads, "f32", "lse"), batch,
+                                  heads, d ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
+                                  workspace.numel(), _stream(stream))
+    _check(rc, "tl_paged_attention")
+
+
+def tl_window_attention(ctx: Context, q, k, v, cu_q, cu_k, out, lse=None, scale=None, window: int = 0, sinks: int = 0,
+                        stream=None) -> None:
+    """Causal attention of packed sequences: sequence b has the query rows cu_q[b]..cu_q[b+1] and the key
+    rows cu_k[b]..cu_k[b+1], its last query at its last key; with a window a query sees the last
+    `window` keys up to its own and the first `sinks` ones.  q, out: bf16 or fp16 [total_q, heads, d];
+    k, v: [total_k, kv_heads, d]; cu_q, cu_k: int32 [batch + 1]; lse: fp32 [total_q, heads]."""
+    code = _code(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or v.shape != k.shape or k.shape[2] != q.shape[2] or \
+            cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.numel() < 1:
+        raise ValueError("inconsistent shapes")
+    for t, what in ((k, "k"), (v, "v"), (out, "out")):
+        if t.dtype != q.dtype or not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor of q's type (got {t.dtype}, {t.device})")
+    total_q, heads, d = q.shape
+    batch = cu_q.numel() - 1
+    rc = lib().tl_window_attention(ctx.handle, code, q.data_ptr(), *_rows(q, "q"), k.data_ptr(), *_rows(k, "k"),
+                                   v.data_ptr(), *_rows(v, "v"), _vec(cu_q, batch + 1, "i32", "cu_q"),
+                                   _vec(cu_k, batch + 1, "i32", "cu_k"), out.data_ptr(), *_rows(out, "out"),
+                                   _vec(lse, total_q * heads, "f32", "lse"), batch, total_q, k.shape[0], heads,
+                                   k.shape[1], d, d ** -0.5 if scale is None else scale, window, sinks,
+                                   _stream(stream))
+    _check(rc, "tl_window_attention")
+
+
+def tl_moe_tokens_workspace_bytes(T, H, E, F, topk) -> int:
+    return lib().tl_moe_tokens_workspace_bytes(T, H, E, F, topk)
+
+
+def tl_moe_tokens(ctx: Context, x, logits, topk: int, w_gate, w_up, w_down, out, workspace, experts_out=None,
+                  gates_out=None, stream=None) -> None:
+    """tl_moe_combine's layer for the few tokens (at most 128) of a decoding step: out fp32 [T, H];
+    experts_out int32 and gates_out fp32 [T, topk] are optional."""
+    _need(x, "bf16", "x"); _need(logits, "f32", "logits"); _need(w_gate, "bf16", "w_gate")
+    _need(w_up, "bf16", "w_up"); _need(w_down, "bf16", "w_down"); _need(out, "f32", "out")
+    _need(workspace, "u8", "workspace")
+    T, H = x.shape
+    E, _, F = w_gate.shape
+    if logits.shape != (T, E) or w_gate.shape != (E, H, F) or w_up.shape != (E, H, F) or \
+            w_down.shape != (E, F, H) or out.shape != (T, H):
+        raise ValueError("inconsistent shapes")
+    rc = lib().tl_moe_tokens(ctx.handle, x.data_ptr(), logits.data_ptr(), topk, w_gate.data_ptr(), w_up.data_ptr(),
+                             w_down.data_ptr(), out.data_ptr(), _vec(experts_out, T * topk, "i32", "experts_out"),
+                             _vec(gates_out, T * topk, "f32", "gates_out"), workspace.data_ptr(), workspace.numel(),
+                             T, H, E, F, _stream(stream))
+    _check(rc, "tl_moe_tokens")
 
 
 # ---------------------------------------------------------------- host-side tile maps

@@ -170,7 +170,7 @@ int tl_ctx_check(tl_ctx* ctx) {
     (void)cudaGetLastError();
     rc = TL_ERR_CUDA;
   } else if (st.code != 0) {
-    rc = st.code == tl::kStatusTimeout ? TL_ERR_TIMEOUT : TL_ERR_CUDA;
+    rc = st.code == tl::kStatusTimeout ? TL_ERR_TIMEOUT : st.code == tl::kStatusIndex ? TL_ERR_INDEX : TL_ERR_CUDA;
     cudaMemset(ctx->status, 0, sizeof(tl::DevStatus));
     cudaDeviceSynchronize();
   }
@@ -214,6 +214,7 @@ const char* tl_strerror(int code) {
     case TL_ERR_CUDA: return "CUDA runtime/driver error";
     case TL_ERR_TIMEOUT: return "a bounded device wait on a signal ran out";
     case TL_ERR_WORKSPACE: return "workspace smaller than required";
+    case TL_ERR_INDEX: return "a slot, page or length read on the device was out of range";
     default: return "unknown status";
   }
 }

@@ -61,6 +61,7 @@ constexpr int kMaxMoverWarps = 4;
 
 // Status codes written to the device status word (host maps them to TL_ERR_*).
 constexpr unsigned kStatusTimeout = 4;
+constexpr unsigned kStatusIndex = 6;  // an index read on the device was out of range
 // Places a wait can run out (recorded in DevStatus::where).
 enum WaitSite : unsigned {
   kSiteSignal = 1, kSiteEmpty = 2, kSiteFull = 3, kSiteTmemEmpty = 4, kSiteTmemFull = 5,

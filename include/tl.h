@@ -65,6 +65,7 @@ typedef struct CUstream_st* tl_stream_t;
 #define TL_ERR_CUDA (-3)        /* a CUDA runtime or driver call failed                          */
 #define TL_ERR_TIMEOUT (-4)     /* (tl_ctx_check) a bounded device wait on a signal ran out        */
 #define TL_ERR_WORKSPACE (-5)   /* workspace smaller than *_workspace_bytes                     */
+#define TL_ERR_INDEX (-6)       /* (tl_ctx_check) a slot, page or length read on the device was out of range */
 
 /* ---------------------------------------------------------------- configuration
  * The BlockChannel-like launch context of [TL] §6: rank/world come per call; this struct
@@ -131,7 +132,8 @@ void tl_ctx_destroy(tl_ctx* ctx);
 
 /* Read and clear the device status word.  Call after synchronising the streams used with ctx.
  * Returns TL_OK, or TL_ERR_TIMEOUT if a bounded wait ran out (the results of that call are
- * undefined and its workspace must be zero-filled again), or TL_ERR_CUDA. */
+ * undefined and its workspace must be zero-filled again), or TL_ERR_INDEX if a serving operator
+ * met an index out of range (it left that entry out; its workspace stays valid), or TL_ERR_CUDA. */
 int tl_ctx_check(tl_ctx* ctx);
 
 /* Human-readable text for a status code (static storage). */
@@ -397,6 +399,126 @@ int tl_ag_attention(tl_ctx* ctx, int W, int rank, const void* q, const void* con
 #define TL_AG_GEMM_STATIC_SCRATCH_BYTES (16u << 20)
 int tl_ag_gemm_static_scratch(tl_ctx* ctx, int W, int rank, const void* const* a_shards, const void* b, void* c,
                               int m_per_rank, int n, int k, tl_stream_t stream);
+
+/* ---------------------------------------------------------------- serving: types and the paged cache
+ * The operators of a decoder's serving step: the cache append, the attention of one new token
+ * over the cache, the causal attention of prompts, and the MoE layer for a few tokens.  The
+ * pages have no counterpart of these four entry points.  They are the single-GPU steps that
+ * run between the overlapped operators when a model answers, on the same buffers and streams.
+ *
+ * Types: bf16 or fp16 activations; a cache holds the activations' type, or e4m3 (8-bit float, 4
+ * exponent and 3 mantissa bits, no infinity) with one fp32 scale per kv head: the value that a
+ * stored byte b stands for is scale * b.
+ * Rows: the innermost dimension (d) is contiguous; every other stride is the caller's, in
+ * elements, a multiple of 16 bytes.  So a view of a fused projection's output, or a cache that is
+ * token-major [pages][page_size][kv_heads][d] or head-major [pages][kv_heads][page_size][d], is
+ * passed as it is.
+ * Indices read on the device (slots, page numbers, lengths) are checked there: an entry out of
+ * range is left out, nothing outside the buffers is read or written, and tl_ctx_check returns
+ * TL_ERR_INDEX.  These four entry points wait on nothing and can be captured into a graph.
+ */
+#define TL_BF16 0
+#define TL_FP16 1
+#define TL_E4M3 2
+
+typedef struct tl_paged_cache {
+  void* k;                /* the K rows of all pages                                            */
+  void* v;                /* the V rows; the same strides as k                                  */
+  const float* k_scale;   /* e4m3: fp32 [kv_heads] (NULL: all 1); otherwise NULL                 */
+  const float* v_scale;
+  long long page_stride;  /* elements from a page to the next                                   */
+  long long row_stride;   /* elements from a row (token) of a page to the next                  */
+  long long head_stride;  /* elements from a kv head to the next                                */
+  int dtype;              /* TL_BF16, TL_FP16 or TL_E4M3                                         */
+  int num_pages;
+  int page_size;          /* rows in a page, any number >= 1                                    */
+  int kv_heads;
+  int d;                  /* head dim: 64 or 128                                                */
+} tl_paged_cache;
+
+/* ---------------------------------------------------------------- append to a paged cache
+ *   K[slot / page_size][slot % page_size][h] = k[t][h], V likewise, for slot = slots[t]
+ *
+ * k, v: dtype (TL_BF16 or TL_FP16) [tokens x kv_heads x d] with the strides given.  slots: int32
+ * [tokens]; a negative slot skips its token (padding); one >= num_pages * page_size is left out
+ * and reported.  Two tokens with the same slot: either may end up there, row by row.
+ * A cache of the activations' type takes the rows as they are.  An e4m3 cache takes
+ * k / k_scale[h], computed in fp32, rounded to nearest even and saturated at +-448 (infinities
+ * too; NaN stays NaN).
+ * Shapes: d 64 or 128; num_pages * page_size < 2^31.  tokens == 0 or kv_heads == 0 is a no-op.
+ */
+int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* k, const void* v,
+                 long long k_token_stride, long long k_head_stride, long long v_token_stride,
+                 long long v_head_stride, const int* slots, int tokens, tl_stream_t stream);
+
+/* ---------------------------------------------------------------- attention of one new token
+ * One query row per sequence over that sequence's rows of a paged cache.  n = lengths[b] counts
+ * the rows in the cache, the new token's own among them (append it first).  Row j is visible if
+ *   j < n  and  (window == 0  or  j >= n - window  or  j < sinks):
+ * a sliding window of the last `window` tokens beside the first `sinks` ones.  Row j of sequence
+ * b is row j % page_size of page page_table[b][j / page_size].
+ *   out[b][h] = sum_j p_j V_j[h / G],  p = softmax_j(scale * q[b][h] . K_j[h / G]),  G = heads / kv_heads
+ *   lse[b][h] = log sum_j exp(scale * q . K_j)         (fp32, natural log; lse may be NULL)
+ * A sequence with nothing visible (n == 0), or only scores of -inf, has out = 0 and lse = -inf.  Rows that are not visible
+ * are not read: whatever they hold has no effect.
+ * q, out: dtype (TL_BF16 or TL_FP16) [batch x heads x d] with the strides given (out must not
+ * overlap q).  cache: dtype or TL_E4M3.  page_table: int32 [batch x max_pages], dense; only the entries
+ * of visible rows are read.  lengths: int32 [batch]; a length over max_pages * page_size is cut to
+ * that and reported, a page out of range is left out (its rows are not visible) and reported.
+ * workspace: tl_paged_attention_workspace_bytes(): partial results of sequences split over several
+ * CTAs, and one counter per sequence, kv head and group of 16 query heads.
+ * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
+ * page_size < 2^31; scale finite and > 0.  batch == 0 or heads == 0 is a no-op.
+ * The result does not depend on what else runs, and is bit-identical run to run on one device.
+ */
+size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d);
+int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* q, long long q_seq_stride,
+                       long long q_head_stride, const int* page_table, int max_pages, const int* lengths, void* out,
+                       long long out_seq_stride, long long out_head_stride, float* lse, int batch, int heads,
+                       float scale, int window, int sinks, void* workspace, size_t workspace_bytes,
+                       tl_stream_t stream);
+
+/* ---------------------------------------------------------------- causal attention of prompts
+ * A batch of sequences packed one after the other: sequence b has the query rows
+ * [cu_q[b], cu_q[b+1]) and the key/value rows [cu_k[b], cu_k[b+1]).  Its last query stands at its
+ * last key: query i of n_q stands at p = n_k - n_q + i (n_k > n_q continues a sequence whose first
+ * keys were there already).  Key j is visible to it if
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
+ *   out[i][h] = softmax_j(scale * q[i][h] . k[j][h / G]) . v[j][h / G],  lse as tl_paged_attention.
+ * A query with nothing visible (p < 0), or only scores of -inf, has out = 0 and lse = -inf.  A key that is not visible to a
+ * query has no effect on it, whatever it holds (infinities and NaN too).
+ * q, out: dtype [total_q x heads x d]; k, v: dtype [total_k x kv_heads x d], strides as given (out
+ * must not overlap the inputs).  lse: fp32 [total_q x heads] or NULL.  cu_q, cu_k: int32 [batch + 1], not
+ * decreasing, cu_q[0] >= 0, cu_q[batch] <= total_q, cu_k likewise (rows outside every sequence are
+ * left alone); a bound out of order or range leaves that sequence out and is reported.
+ * Shapes: batch <= 1024; heads % kv_heads == 0, heads / kv_heads <= 128; d 64 or 128; window, sinks >= 0;
+ * scale finite and > 0; total_q * heads < 2^31.
+ * total_q == 0, heads == 0 or batch == 0 is a no-op.  No workspace.
+ */
+int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride,
+                        const void* k, long long k_token_stride, long long k_head_stride, const void* v,
+                        long long v_token_stride, long long v_head_stride, const int* cu_q, const int* cu_k,
+                        void* out, long long out_token_stride, long long out_head_stride, float* lse, int batch,
+                        int total_q, int total_k, int heads, int kv_heads, int d, float scale, int window, int sinks,
+                        tl_stream_t stream);
+
+/* ---------------------------------------------------------------- MoE layer for a few tokens
+ * The layer of tl_moe_combine (the same routing, weights and gates; cfg.moe_renorm applies) for the
+ * few tokens of a decoding step, where reading the chosen experts' weights is all that takes time:
+ *   y_(t,j) = (SiLU(x_t . Wg_e) * (x_t . Wu_e)) . Wd_e,   out_t = sum_j gate_(t,j) * y_(t,j)
+ * Unlike there, h keeps fp32 precision between the two products, the sums over j are taken in fp32
+ * in the order j = 0, 1, ... and each distinct expert's weights are read once; results are
+ * bit-identical run to run.
+ * x: bf16 [T x H]; logits: fp32 [T x E]; w_gate, w_up: bf16 [E x H x F]; w_down: bf16 [E x F x H];
+ * out: fp32 [T x H].  experts_out (int32 [T x topk]) and gates_out (fp32 [T x topk]) are optional: the
+ * chosen experts, best first, and their gates.  NaN logits count as the lowest (the gates are NaN).
+ * workspace: tl_moe_tokens_workspace_bytes().
+ * Shapes: 1 <= T <= 128; 1 <= topk <= 8; topk <= E <= 256; H % 8 == 0; F % 8 == 0.
+ */
+size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int topk);
+int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, const void* w_gate, const void* w_up,
+                  const void* w_down, float* out, int* experts_out, float* gates_out, void* workspace,
+                  size_t workspace_bytes, int T, int H, int E, int F, tl_stream_t stream);
 
 /* ---------------------------------------------------------------- host-side tile maps (no GPU)
  * The static tile-centric mappings the kernels use ([TL] §4.1), evaluated on the host by the
