@@ -1,4 +1,6 @@
 // The paged key/value cache: appending new rows, and the attention of one new token over it.
+#include <type_traits>
+
 #include "tl_serve.cuh"
 
 namespace tl {
@@ -67,6 +69,47 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 }
 
 // ---------------------------------------------------------------------------- attention of one token
+// For each sequence and kv head, G = heads / kv_heads query rows meet the same K and V rows:
+//   s = sc q K^T,  p = 2^(s - m),  O = p V,  l = sum p,  out = O / l
+// with the running maximum m (base 2: sc folds in log2 e) and O rescaled when m moves.  Every K and
+// V byte is read once and each meets 2 G flops, far below the ridge of the tensor cores, so HBM
+// bounds it; the products run on mma.sync m16n8k16 (16 query rows, the group padded with zero
+// rows), because 64 keys x 16 rows is far too small a tile for a tcgen05 instruction (M = 128) and
+// CUDA cores alone would need G fused multiply-adds per element: 27 T/s at G = 8 and full HBM rate,
+// of the 39 T/s that the SMs have.
+//
+// Work: an item is (sequence, kv head, 16 query heads), a tile 64 of its visible keys.  All tiles of
+// all items form one line, cut into equal ranges, one per CTA, so ragged batches are even and few
+// long sequences are spread over all SMs.  Each CTA derives the plan from the lengths by a prefix
+// sum.  A CTA's part of an item is a segment; warp w takes keys [16 w, 16 w + 16) of each of its
+// tiles, with its own m, l, O and its own ring of cp.async stages: inside a segment no warp waits for another, and
+// loads of the next segment are in flight while one ends.  At a segment's end the four warps merge
+// in shared memory.  A whole item is written at once; a part goes to the workspace (at most two per
+// CTA), and the CTA that finishes an item's last part (a counter, left at zero again) joins all
+// parts in the order of the line.  Nothing waits, and the order of the sums is fixed by the lengths.
+//
+// e4m3 rows are widened to fp16 (exact) in registers; q is brought to fp16 by a power of two per row
+// that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products run in
+// fp16.  Weights are rounded to the products' 16-bit type (2^-9 / 2^-12 relative, half a step; they meet V there), l sums
+// them unrounded in fp32.
+namespace paged {
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kRows = 16;
+constexpr int kRing = 65536;  // bytes of cp.async stages per CTA; two CTAs per SM
+template <bool Fp8, int D>
+struct Shape {
+  static constexpr int kRowBytes = D * (Fp8 ? 1 : 2);
+  static constexpr int kHalf = kKeys * kRowBytes;        // one warp's K (or V) rows of a stage
+  static constexpr int kFit = kRing / (kWarps * 2 * kHalf);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;    // 2 (16-bit, d 128) to 6
+  static constexpr int kPitch = D + 4;                   // floats of a merged row
+  static constexpr int kMergeOff = kStages * kWarps * 2 * kHalf;
+  static constexpr int kMlOff = kMergeOff + kWarps * kRows * kPitch * 4;
+  static constexpr int kSmem = kMlOff + kWarps * kRows * 2 * 4;
+};
+}  // namespace paged
+
+constexpr int kPagedMaxCtas = 512;
+
 struct PagedParams {
   CacheArgs c;
   DevStatus* status;
@@ -76,8 +119,11 @@ struct PagedParams {
   long long q_seq, q_head, out_seq, out_head;  // bytes
   const int* table;
   const int* lengths;
-  int max_pages, batch, heads;
-  float scale;
+  float* part;        // [CTA][2][16 rows][D + 2]: O, m, l of a segment
+  unsigned* counter;  // [item]: segments done
+  int max_pages, batch, heads, group, blocks;  // blocks: groups of 16 query heads per kv head
+  uint32_t div_mul, div_shift;  // row / page_size
+  float sl2;          // scale * log2(e)
   int window, sinks;
 };
 
@@ -100,82 +146,503 @@ __device__ __forceinline__ Visible visible_rows(int n, int window, int sinks) {
   return v;
 }
 
-// One CTA per (sequence, query head), a warp per key in turn with its own running maximum and
-// sum, joined at the end: the plain form of the operator.
-template <class T, bool Fp8, int D>
-__global__ void __launch_bounds__(256) paged_kernel(const PagedParams p) {
-  constexpr int kPer = D / 32, kWarps = 8;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int b = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = h / (p.heads / p.c.kv_heads);
-  int n = p.lengths[b];
+// The length of sequence b, cut to what its table holds (reported once, by CTA 0).
+__device__ __forceinline__ int paged_length(const PagedParams& p, int b, bool report) {
+  const int n = __ldg(p.lengths + b);
   const long long cap = static_cast<long long>(p.max_pages) * p.c.page_size;
   if (n < 0 || n > cap) {
-    if (threadIdx.x == 0) report_index(p.status, static_cast<unsigned long long>(b));
-    n = n < 0 ? 0 : static_cast<int>(cap);
+    if (report) report_index(p.status, static_cast<unsigned long long>(b));
+    return n < 0 ? 0 : static_cast<int>(cap);
   }
-  const Visible vis = visible_rows(n, p.window, p.sinks);
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-  const T* qp = reinterpret_cast<const T*>(p.q + b * p.q_seq + h * p.q_head);
-  const float sc = p.scale * kLog2E * (Fp8 && p.c.k_scale ? p.c.k_scale[hk] : 1.f);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = static_cast<float>(qp[lane * kPer + i]);
-    o[i] = 0.f;
-  }
-  for (int i = warp; i < vis.count; i += kWarps) {
-    const int row = i < vis.head ? i : i + vis.skip;
-    const int pg = row / p.c.page_size;
-    const int page = p.table[static_cast<long long>(b) * p.max_pages + pg];
-    if (page < 0 || page >= p.c.num_pages) {
-      if (lane == 0) report_index(p.status, static_cast<unsigned long long>(b));
-      continue;
-    }
-    const long long at = page * p.c.page_stride + (row - pg * p.c.page_size) * p.c.row_stride + hk * p.c.head_stride;
-    float k[kPer], v[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if constexpr (Fp8) {
-        k[j] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(p.c.k + at)[lane * kPer + j]);
-        v[j] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(p.c.v + at)[lane * kPer + j]);
-      } else {
-        k[j] = static_cast<float>(reinterpret_cast<const T*>(p.c.k + at)[lane * kPer + j]);
-        v[j] = static_cast<float>(reinterpret_cast<const T*>(p.c.v + at)[lane * kPer + j]);
+  return n;
+}
+__device__ __forceinline__ int paged_tiles(int count) { return (count + paged::kTile - 1) / paged::kTile; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// d += a b: 16 x 8 x 16, fp32 sums.
+template <class T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 values (the low 16 bits) as fp16, exactly.
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t v) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// Where a CTA stands on the line of tiles.
+struct PagedAt {
+  int b;        // sequence
+  int sub;      // kv head * blocks + block
+  int tile;     // of this item
+  int tiles;    // of this item
+  Visible vis;  // of this sequence
+};
+
+template <class T, bool Fp8, int D>
+__global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedParams p) {
+  using namespace paged;
+  using S = Shape<Fp8, D>;
+  using M = typename std::conditional<Fp8, __half, T>::type;  // the products' type
+  constexpr int kSteps = D / 16, kStages = S::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_sum[kThreads + 1];
+  __shared__ unsigned s_last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int subs = p.c.kv_heads * p.blocks;
+
+  // ---------------------------------------------------------------- plan
+  // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk).
+  const int chunk = (p.batch + kThreads - 1) / kThreads;
+  {
+    long long mine = 0;
+    for (int i = 0; i < chunk; ++i) {
+      const int b = static_cast<int>(threadIdx.x) * chunk + i;
+      if (b >= p.batch) break;
+      const int count = visible_rows(paged_length(p, b, blockIdx.x == 0), p.window, p.sinks).count;
+      mine += paged_tiles(count);
+      if (count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
+        for (int h = 0; h < p.heads; ++h) {
+          uint4* o = reinterpret_cast<uint4*>(p.out + b * p.out_seq + h * p.out_head);
+          for (int v = 0; v < D / 8; ++v) o[v] = make_uint4(0, 0, 0, 0);
+          if (p.lse) p.lse[static_cast<long long>(b) * p.heads + h] = -INFINITY;
+        }
       }
     }
-    float s = 0.f;
+    long long sum = mine;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) s += q[j] * k[j];
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= sc;
-    const float mn = fmaxf(m, s);
-    const float keep = m == -INFINITY ? 0.f : exp2f(m - mn), w = s == -INFINITY ? 0.f : exp2f(s - mn);
-    m = mn;
-    l = l * keep + w;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] = o[j] * keep + w * v[j];
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, sum, x);
+      if (lane >= x) sum += o;
+    }
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    __syncthreads();
+    s_sum[threadIdx.x + 1] = before + sum;
+    if (threadIdx.x == 0) s_sum[0] = 0;
+    __syncthreads();
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  const long long total = s_sum[kThreads] * subs;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long first = per * blockIdx.x;
+  const long long last = first + per < total ? first + per : total;
+  if (first >= last) return;
+  const int nsteps = static_cast<int>(last - first);
+
+  PagedAt at;
+  long long item_begin;  // position on the line of the current item's first tile
+  {
+    int lo = 0, hi = kThreads;  // the thread whose sequences hold `first`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s_sum[mid] * subs <= first) lo = mid; else hi = mid;
+    }
+    long long pos = s_sum[lo] * subs;
+    at.b = lo * chunk;
+    for (;;) {
+      at.vis = visible_rows(paged_length(p, at.b, false), p.window, p.sinks);
+      at.tiles = paged_tiles(at.vis.count);
+      const long long here = static_cast<long long>(at.tiles) * subs;
+      if (first < pos + here) break;
+      pos += here;
+      ++at.b;
+    }
+    at.sub = static_cast<int>((first - pos) / at.tiles);
+    at.tile = static_cast<int>((first - pos) - static_cast<long long>(at.sub) * at.tiles);
+    item_begin = first - at.tile;
   }
+  // One tile on; past the last one of the CTA's range the position is not used.
+  auto advance = [&](PagedAt& a) {
+    if (++a.tile < a.tiles) return;
+    a.tile = 0;
+    if (++a.sub < subs) return;
+    a.sub = 0;
+    while (++a.b < p.batch) {
+      a.vis = visible_rows(paged_length(p, a.b, false), p.window, p.sinks);
+      a.tiles = paged_tiles(a.vis.count);
+      if (a.tiles > 0) return;
+    }
+  };
+
+  // ---------------------------------------------------------------- loads
+  // The rows of a step are looked up (page table) one step before they are loaded; lane l < 16 (and
+  // l + 16) holds key l's.  `mask` has a bit for each key that is there.
+  PagedAt load_at = at;
+  int step_loaded = 0;  // steps issued
+  long long row_off = 0;
+  bool row_ok = false;
+  auto look_up = [&]() {
+    row_ok = false;
+    if (step_loaded >= nsteps) return;
+    const int i = load_at.tile * kTile + warp * kKeys + (lane & 15);
+    if (i < load_at.vis.count) {
+      const int row = i < load_at.vis.head ? i : i + load_at.vis.skip;
+      const uint32_t pg = (__umulhi(static_cast<uint32_t>(row), p.div_mul) + row) >> p.div_shift;
+      const int page = __ldg(p.table + static_cast<long long>(load_at.b) * p.max_pages + pg);
+      row_ok = page >= 0 && page < p.c.num_pages;
+      if (!row_ok) report_index(p.status, static_cast<unsigned long long>(load_at.b));
+      row_off = page * p.c.page_stride + (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
+                (load_at.sub / p.blocks) * p.c.head_stride;
+    }
+    if (!row_ok) row_off = 0;
+  };
+  const uint32_t ring = smem_u32(smem) + warp * (2 * S::kHalf);
+  auto stage_addr = [&](int s) { return ring + s * (kWarps * 2 * S::kHalf); };
+  uint32_t masks[kStages];  // one per stage, the same in all lanes
+  auto issue = [&](int s, uint32_t& mask) {
+    mask = __ballot_sync(0xffffffffu, row_ok) & 0xffffu;
+    if (step_loaded < nsteps) {
+      constexpr int kChunks = S::kRowBytes / 16, kPer = 32 / kChunks;  // rows a warp-wide copy covers
+      const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
+      const int c = lane % kChunks;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) s_o[warp][lane * kPer + j] = o[j];
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float mm = -INFINITY, ll = 0.f, acc = 0.f;
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - mm);
-    ll += f * s_l[w];
-    acc += f * s_o[w][threadIdx.x];
+      for (int j = 0; j < kKeys / kPer; ++j) {
+        const int key = j * kPer + lane / kChunks;
+        const long long off = __shfl_sync(0xffffffffu, row_off, key) + c * 16;
+        const uint32_t bytes = (mask >> key) & 1u ? 16u : 0u;  // 0: filled with zeros, nothing is read
+        uint32_t ck, cv;
+        if constexpr (!Fp8) {
+          ck = cv = key * S::kRowBytes + ((c ^ (key & 7)) << 4);
+        } else if constexpr (D == 128) {
+          ck = key * 128 + ((c ^ ((key & 1) << 2)) << 4);
+          cv = key * 128 + ((c ^ (((key >> 1) & 3) << 1)) << 4);
+        } else {
+          ck = key * 64 + (c << 4);
+          cv = key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+        }
+        cp_async16(sk + ck, p.c.k + off, bytes);
+        cp_async16(sv + cv, p.c.v + off, bytes);
+      }
+      advance(load_at);
+      ++step_loaded;
+    }
+    cp_async_commit();
+    look_up();
+  };
+
+  // ---------------------------------------------------------------- the running state of a segment
+  float o[D / 8][4], m[2], l[2], sc[2];
+  uint32_t qf[kSteps][4];
+  look_up();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s, masks[s]);
+
+  int step = 0;
+  while (step < nsteps) {
+    // a segment: this CTA's tiles of one item
+    const int seg_tile = at.tile;
+    const int seg = nsteps - step < at.tiles - at.tile ? nsteps - step : at.tiles - at.tile;
+    const int hk = at.sub / p.blocks, h0 = hk * p.group + (at.sub - hk * p.blocks) * kRows;
+    const int rows = p.group - (at.sub - hk * p.blocks) * kRows < kRows ? p.group - (at.sub - hk * p.blocks) * kRows : kRows;
+    // Q fragments of rows g and g + 8 (zero past the group)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool there = g + 8 * r < rows;
+      const uint8_t* qp = p.q + at.b * p.q_seq + (h0 + g + 8 * r) * p.q_head;
+      sc[r] = p.sl2;
+      if constexpr (Fp8) {
+        if (p.c.k_scale) sc[r] *= __ldg(p.c.k_scale + hk);
+        float top = 0.f;
+        float2 x[kSteps * 2];
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(qp + (64 * h + 16 * t) * 2) + w) : make_uint4(0, 0, 0, 0);
+            x[h * 8 + w * 4] = to_f32x2<T>(v.x);
+            x[h * 8 + w * 4 + 1] = to_f32x2<T>(v.y);
+            x[h * 8 + w * 4 + 2] = to_f32x2<T>(v.z);
+            x[h * 8 + w * 4 + 3] = to_f32x2<T>(v.w);
+          }
+#pragma unroll
+        for (int i = 0; i < kSteps * 2; ++i) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e and 2^e for top in [2^e, 2^(e+1)), e kept to where both are normal
+        int e = static_cast<int>(__float_as_uint(top) >> 23);
+        e = e < 2 ? 2 : e > 252 ? 252 : e;
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        sc[r] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          qf[i][r] = from_f32x2<__half>(x[2 * i].x * down, x[2 * i].y * down);
+          qf[i][2 + r] = from_f32x2<__half>(x[2 * i + 1].x * down, x[2 * i + 1].y * down);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          qf[i][r] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 2 * t) * 2)) : 0u;
+          qf[i][2 + r] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 8 + 2 * t) * 2)) : 0u;
+        }
+      }
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+    for (int i = 0; i < seg; ++i, ++step) {
+      // the stage of step - 1 is free (every lane has read it): fill it with step + kStages - 1
+      __syncwarp();
+      const int s = step % kStages, sn = (step + kStages - 1) % kStages;
+      uint32_t mask = 0, fresh;
+      issue(sn, fresh);
+#pragma unroll
+      for (int x = 0; x < kStages; ++x) {
+        if (x == sn) masks[x] = fresh;
+        if (x == s) mask = masks[x];
+      }
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
+      float x[2][4];  // scores of keys 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1; rows g (0, 1) and g + 8 (2, 3)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
+      if constexpr (!Fp8) {
+        const int key = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t b[4];
+          ldsm4(b, sk + key * S::kRowBytes + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+          mma16816<M>(x[0], qf[k], b[0], b[1]);
+          mma16816<M>(x[1], qf[k], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int key = 8 * n + g, c = 4 * h + t;
+            const uint4 w = lds128(sk + key * S::kRowBytes + ((D == 128 ? c ^ ((key & 1) << 2) : c) << 4));
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma16816<M>(x[n], qf[4 * h + k], widen_e4m3(v[k]), widen_e4m3(v[k] >> 16));
+          }
+      }
+      // scale, mask, running maximum
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool there = (mask >> (8 * n + 2 * t + (j & 1))) & 1u;
+          x[n][j] = there ? x[n][j] * sc[j >> 1] : -INFINITY;
+          top[j >> 1] = fmaxf(top[j >> 1], x[n][j]);
+        }
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+        moved |= top[r] > m[r];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], top[r]);
+          const float keep = mn == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
+          m[r] = mn;
+          l[r] *= keep;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][2 * r] *= keep;
+            o[d][2 * r + 1] *= keep;
+          }
+        }
+      }
+      uint32_t pf[4];  // the weights as the next product's A: rows g, g + 8 of keys 2t.., then of 8 + 2t..
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float w0 = ex2_approx(x[n][2 * r] - base), w1 = ex2_approx(x[n][2 * r + 1] - base);
+          l[r] += w0 + w1;
+          pf[2 * n + r] = from_f32x2<M>(w0, w1);
+        }
+      }
+      if constexpr (!Fp8) {
+        const int key = lane & 15;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t b[4];
+          ldsm4t(b, sv + key * S::kRowBytes + (((2 * d + (lane >> 4)) ^ (key & 7)) << 4));
+          mma16816<M>(o[2 * d], pf, b[0], b[1]);
+          mma16816<M>(o[2 * d + 1], pf, b[2], b[3]);
+        }
+      } else {
+        // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8): transposed bytewise, so
+        // that column g of product n is head dim g D/8 + n
+        constexpr int kW = D / 32;  // words
+        uint32_t w[4][kW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+          if constexpr (D == 128) {
+            const uint4 v = lds128(sv + key * 128 + ((g ^ (((key >> 1) & 3) << 1)) << 4));
+            w[k][0] = v.x;
+            w[k][1] = v.y;
+            w[k][2] = v.z;
+            w[k][3] = v.w;
+          } else {
+            const uint2 v = lds64(sv + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
+            w[k][0] = v.x;
+            w[k][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t lo = __byte_perm(w[0][i], w[1][i], z ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(w[2][i], w[3][i], z ? 0x7362 : 0x5140);
+            mma16816<M>(o[4 * i + 2 * z], pf, widen_e4m3(lo), widen_e4m3(hi));
+            mma16816<M>(o[4 * i + 2 * z + 1], pf, widen_e4m3(lo >> 16), widen_e4m3(hi >> 16));
+          }
+        }
+      }
+    }
+
+    // ---------------------------------------------------------------- the segment's end
+    float* merge = reinterpret_cast<float*>(smem + S::kMergeOff);
+    float2* ml = reinterpret_cast<float2*>(smem + S::kMlOff);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = g + 8 * r;
+      if (row < rows) {
+        float* dst = merge + (warp * kRows + row) * S::kPitch;
+        if (t == 0) ml[warp * kRows + row] = make_float2(m[r], l[r]);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          if constexpr (!Fp8) {
+            *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          } else {
+            dst[2 * t * (D / 8) + n] = o[n][2 * r];
+            dst[(2 * t + 1) * (D / 8) + n] = o[n][2 * r + 1];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = seg == at.tiles;
+    const int vecs = rows * (D / 4);  // float4s of the merged rows
+    float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_tile ? 0 : 1)) * (kRows * (D + 2));
+    const float vs = Fp8 && p.c.v_scale ? __ldg(p.c.v_scale + hk) : 1.f;
+    auto write_out = [&](int row, int d, float4 v, float mm, float ll) {
+      const float inv = ll == 0.f ? 0.f : vs / ll;
+      const int h = h0 + row;
+      *reinterpret_cast<uint2*>(p.out + at.b * p.out_seq + h * p.out_head + d * 2) =
+          make_uint2(from_f32x2<T>(v.x * inv, v.y * inv), from_f32x2<T>(v.z * inv, v.w * inv));
+      if (p.lse && d == 0)
+        p.lse[static_cast<long long>(at.b) * p.heads + h] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+    };
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+      const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+      float mm = -INFINITY, ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + row].x);
+      const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 z = ml[w * kRows + row];
+        const float f = ex2_approx(z.x - base);
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * S::kPitch + d);
+        ll += f * z.y;
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      if (whole) {
+        write_out(row, d, acc, mm, ll);
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * row) = make_float2(mm, ll);
+      }
+    }
+    if (!whole) {
+      // the item's parts lie in CTAs [c0, c1]: the first in slot 1 (it starts the item), the others in slot 0
+      const int c0 = static_cast<int>(item_begin / per), c1 = static_cast<int>((item_begin + at.tiles - 1) / per);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        unsigned* ctr = p.counter + static_cast<size_t>(at.b) * subs + at.sub;
+        const unsigned done = atomicAdd(ctr, 1u) + 1u;
+        s_last = done == static_cast<unsigned>(c1 - c0 + 1);
+        if (s_last) *ctr = 0u;
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        auto slot = [&](int c) { return p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * (kRows * (D + 2)); };
+        for (int i = threadIdx.x; i < vecs; i += kThreads) {
+          const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+          float mm = -INFINITY, ll = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(slot(c) + kRows * D + 2 * row));
+          const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 8
+          for (int c = c0; c <= c1; ++c) {
+            const float2 z = __ldcg(reinterpret_cast<const float2*>(slot(c) + kRows * D + 2 * row));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c) + row * D + d));
+            const float f = ex2_approx(z.x - base);
+            ll += f * z.y;
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
+          write_out(row, d, acc, mm, ll);
+        }
+      }
+    }
+    __syncthreads();  // merge, ml and s_last are read: the next segment may write them
+    at.tile += seg - 1;
+    item_begin += at.tiles;
+    advance(at);
   }
-  const bool none = ll == 0.f;
-  const float vs = Fp8 && p.c.v_scale ? p.c.v_scale[hk] : 1.f;
-  reinterpret_cast<T*>(p.out + b * p.out_seq + h * p.out_head)[threadIdx.x] = static_cast<T>(none ? 0.f : acc / ll * vs);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[static_cast<long long>(b) * p.heads + h] = none ? -INFINITY : mm * kLn2 + logf(ll);
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- host side
@@ -256,9 +723,13 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
   });
 }
 
+// Workspace: the parts of split items (two per CTA of the largest grid), then one counter per item.
+static int paged_blocks(int heads, int kv_heads) { return (heads / kv_heads + paged::kRows - 1) / paged::kRows; }
+static size_t paged_part_bytes(int d) { return align256(static_cast<size_t>(kPagedMaxCtas) * 2 * paged::kRows * (d + 2) * 4); }
+
 extern "C" size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d) {
   if (batch < 0 || batch > 4096 || !heads_ok(heads, kv_heads, d)) return 0;
-  return 256;
+  return paged_part_bytes(d) + align256(static_cast<size_t>(batch) * kv_heads * paged_blocks(heads, kv_heads) * 4 + 4);
 }
 
 extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* q,
@@ -295,12 +766,31 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   p.max_pages = max_pages;
   p.batch = batch;
   p.heads = heads;
-  p.scale = scale;
+  p.group = heads / cache->kv_heads;
+  p.blocks = paged_blocks(heads, cache->kv_heads);
+  p.part = static_cast<float*>(workspace);
+  p.counter = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + paged_part_bytes(cache->d));
+  p.sl2 = scale * kLog2E;
   p.window = window;
   p.sinks = sinks;
+  // row / page_size as (umulhi(row, mul) + row) >> shift, exact for row < 2^31
+  p.div_shift = 0;
+  while ((1ull << p.div_shift) < static_cast<unsigned long long>(cache->page_size)) ++p.div_shift;
+  p.div_mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << p.div_shift) - cache->page_size)) / cache->page_size + 1);
+  // no more CTAs than tiles there can be
+  long long cap = static_cast<long long>(max_pages) * cache->page_size;
+  if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
+  const long long most = batch * static_cast<long long>(cache->kv_heads) * p.blocks * (cap / paged::kTile + 1);
+  long long grid = 2LL * ctx->ctas < kPagedMaxCtas ? 2LL * ctx->ctas : kPagedMaxCtas;
+  if (grid > most) grid = most;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
-    paged_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>
-        <<<dim3(batch, heads), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    using S = paged::Shape<decltype(fp8)::value, decltype(d)::value>;
+    auto kern = paged_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return static_cast<int>(TL_ERR_CUDA);
+    }
+    kern<<<static_cast<unsigned>(grid), paged::kThreads, S::kSmem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return launched();
   });
 }
