@@ -1,4 +1,5 @@
 // The paged key/value cache: appending new rows, and the attention of one new token over it.
+#include <atomic>
 #include <type_traits>
 
 #include "tl_serve.cuh"
@@ -70,45 +71,51 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 
 // ---------------------------------------------------------------------------- attention of one token
 // For each sequence and kv head, G = heads / kv_heads query rows meet the same K and V rows:
-//   s = sc q K^T,  p = 2^(s - m),  O = p V,  l = sum p,  out = O / l
-// with the running maximum m (base 2: sc folds in log2 e) and O rescaled when m moves.  Every K and
-// V byte is read once and each meets 2 G flops, far below the ridge of the tensor cores, so HBM
-// bounds it; the products run on mma.sync m16n8k16 (16 query rows, the group padded with zero
-// rows), because 64 keys x 16 rows is far too small a tile for a tcgen05 instruction (M = 128) and
-// CUDA cores alone would need G fused multiply-adds per element: 27 T/s at G = 8 and full HBM rate,
-// of the 39 T/s that the SMs have.
+//   s = sc K q^T,  p = 2^(s - m),  O^T = V^T p,  l = sum p,  out = O / l
+// with the running maximum m (base 2: sc folds in log2 e).  m moves, and O and l are rescaled, only when a
+// score exceeds it by more than 8, so weights stay below 2^8 and most tiles need no reduction over keys.
+// Every K and V byte is read once and each meets 2 G flops, far below the ridge of the tensor
+// cores, so HBM bounds it.  The products run on mma.sync m16n8k16 with keys (then head dims) as the 16
+// rows and 8 query heads as the columns (twice 8 for G > 8): 64 keys x 8 queries is far too small a tile for
+// a tcgen05 instruction, and CUDA cores alone would need G fused multiply-adds per element, 27 T/s
+// at G = 8 and full HBM rate of the 39 T/s that the SMs have.
 //
-// Work: an item is (sequence, kv head, 16 query heads), a tile 64 of its visible keys.  All tiles of
+// Work: an item is (sequence, kv head, block of 8 or 16 query heads), a tile 64 of its visible keys.  All tiles of
 // all items form one line, cut into equal ranges, one per CTA, so ragged batches are even and few
 // long sequences are spread over all SMs.  Each CTA derives the plan from the lengths by a prefix
 // sum.  A CTA's part of an item is a segment; warp w takes keys [16 w, 16 w + 16) of each of its
-// tiles, with its own m, l, O and its own ring of cp.async stages: inside a segment no warp waits for another, and
-// loads of the next segment are in flight while one ends.  At a segment's end the four warps merge
-// in shared memory.  A whole item is written at once; a part goes to the workspace (at most two per
-// CTA), and the CTA that finishes an item's last part (a counter, left at zero again) joins all
-// parts in the order of the line.  Nothing waits, and the order of the sums is fixed by the lengths.
+// tiles, with its own m, l, O and its own ring of cp.async stages: inside a segment no warp waits
+// for another, and loads of the next segment are in flight while one ends.  At a segment's end the
+// four warps merge in shared memory.  A whole item is written at once; a part goes to the workspace (at
+// most two per CTA), and the CTA that finishes an item's last part (a counter, left at zero again)
+// joins all parts in the order of the line.  Nothing waits, and the order of the sums is fixed by
+// the lengths.
 //
 // e4m3 rows are widened to fp16 (exact) in registers; q is brought to fp16 by a power of two per row
-// that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products run in
-// fp16.  Weights are rounded to the products' 16-bit type (2^-9 / 2^-12 relative, half a step; they meet V there), l sums
+// that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products
+// run in fp16.  Weights are rounded to the products' 16-bit type (half a step) to meet V there; l sums
 // them unrounded in fp32.
 namespace paged {
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kRows = 16;
-constexpr int kRing = 65536;  // bytes of cp.async stages per CTA; two CTAs per SM
-template <bool Fp8, int D>
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kMaxRows = 16;
+template <bool Fp8, int D, int NB>
 struct Shape {
+  static constexpr int kRows = 8 * NB;                   // query heads of an item
   static constexpr int kRowBytes = D * (Fp8 ? 1 : 2);
   static constexpr int kHalf = kKeys * kRowBytes;        // one warp's K (or V) rows of a stage
-  static constexpr int kFit = kRing / (kWarps * 2 * kHalf);
-  static constexpr int kStages = kFit > 6 ? 6 : kFit;    // 2 (16-bit, d 128) to 6
+  // CTAs per SM, and the stages that fit: 64 KB of ring at two CTAs, 48 KB at three.
+  // 8-bit rows spend their time on widening and want more warps, 16-bit rows wait for HBM.
+  static constexpr int kCtas = Fp8 && NB == 1 ? 3 : 2;
+  static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * 2 * kHalf);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
   static constexpr int kMergeOff = kStages * kWarps * 2 * kHalf;
   static constexpr int kMlOff = kMergeOff + kWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kMlOff + kWarps * kRows * 2 * 4;
+  static constexpr int kPart = kRows * (D + 2);          // floats of a segment's part: O, then m and l
 };
 }  // namespace paged
 
-constexpr int kPagedMaxCtas = 512;
+constexpr int kPagedMaxCtas = 640;
 
 struct PagedParams {
   CacheArgs c;
@@ -119,9 +126,9 @@ struct PagedParams {
   long long q_seq, q_head, out_seq, out_head;  // bytes
   const int* table;
   const int* lengths;
-  float* part;        // [CTA][2][16 rows][D + 2]: O, m, l of a segment
+  float* part;        // [CTA][2][rows][D + 2]: O, m, l of a segment
   unsigned* counter;  // [item]: segments done
-  int max_pages, batch, heads, group, blocks;  // blocks: groups of 16 query heads per kv head
+  int max_pages, batch, heads, group, blocks;  // blocks: items per kv head
   uint32_t div_mul, div_shift;  // row / page_size
   float sl2;          // scale * log2(e)
   int window, sinks;
@@ -194,11 +201,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 values (the low 16 bits) as fp16, exactly.
-__device__ __forceinline__ uint32_t widen_e4m3(uint32_t v) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(v));
-  return d;
+// Four e4m3 values as two pairs of fp16, exactly.
+__device__ __forceinline__ void widen_e4m3(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(v));
 }
 
 // Where a CTA stands on the line of tiles.
@@ -210,28 +216,36 @@ struct PagedAt {
   Visible vis;  // of this sequence
 };
 
-template <class T, bool Fp8, int D>
-__global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedParams p) {
+// The transpose of an 8 x 8 matrix of 16-bit elements, a row's pair per thread.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+template <class T, bool Fp8, int D, int NB>
+__global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kCtas)) paged_kernel(const PagedParams p) {
   using namespace paged;
-  using S = Shape<Fp8, D>;
+  using S = Shape<Fp8, D, NB>;
   using M = typename std::conditional<Fp8, __half, T>::type;  // the products' type
-  constexpr int kSteps = D / 16, kStages = S::kStages;
+  constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_sum[kThreads + 1];
+  __shared__ long long s_sum[kThreads], s_warp[kWarps];
+  __shared__ float s_max[kMaxRows];
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int subs = p.c.kv_heads * p.blocks;
 
   // ---------------------------------------------------------------- plan
-  // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk).
+  // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk); s_sum holds the sums inside a warp.
   const int chunk = (p.batch + kThreads - 1) / kThreads;
   {
-    long long mine = 0;
+    long long sum = 0;
     for (int i = 0; i < chunk; ++i) {
       const int b = static_cast<int>(threadIdx.x) * chunk + i;
       if (b >= p.batch) break;
       const int count = visible_rows(paged_length(p, b, blockIdx.x == 0), p.window, p.sinks).count;
-      mine += paged_tiles(count);
+      sum += paged_tiles(count);
       if (count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
         for (int h = 0; h < p.heads; ++h) {
           uint4* o = reinterpret_cast<uint4*>(p.out + b * p.out_seq + h * p.out_head);
@@ -240,22 +254,19 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
         }
       }
     }
-    long long sum = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, sum, x);
       if (lane >= x) sum += o;
     }
-    if (lane == 31) s_sum[warp] = sum;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    __syncthreads();
-    s_sum[threadIdx.x + 1] = before + sum;
-    if (threadIdx.x == 0) s_sum[0] = 0;
+    s_sum[threadIdx.x] = sum;
+    if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
   }
-  const long long total = s_sum[kThreads] * subs;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += s_warp[w];
+  total *= subs;
   const long long per = (total + gridDim.x - 1) / gridDim.x;
   const long long first = per * blockIdx.x;
   const long long last = first + per < total ? first + per : total;
@@ -265,13 +276,13 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
   PagedAt at;
   long long item_begin;  // position on the line of the current item's first tile
   {
-    int lo = 0, hi = kThreads;  // the thread whose sequences hold `first`
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s_sum[mid] * subs <= first) lo = mid; else hi = mid;
-    }
-    long long pos = s_sum[lo] * subs;
-    at.b = lo * chunk;
+    // the warp, then the thread, whose sequences hold `first`
+    long long pos = 0;
+    int w = 0;
+    while (pos + s_warp[w] * subs <= first) pos += s_warp[w++] * subs;
+    const int i = __popc(__ballot_sync(0xffffffffu, pos + s_sum[32 * w + lane] * subs <= first));
+    if (i > 0) pos += s_sum[32 * w + i - 1] * subs;
+    at.b = (32 * w + i) * chunk;
     for (;;) {
       at.vis = visible_rows(paged_length(p, at.b, false), p.window, p.sinks);
       at.tiles = paged_tiles(at.vis.count);
@@ -298,26 +309,29 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
   };
 
   // ---------------------------------------------------------------- loads
-  // The rows of a step are looked up (page table) one step before they are loaded; lane l < 16 (and
-  // l + 16) holds key l's.  `mask` has a bit for each key that is there.
+  // The rows of a step are looked up (page table) one step before they are loaded; lanes l and
+  // l + 16 hold key l's.  A stage's mask has a bit for each key that is there.
   PagedAt load_at = at;
   int step_loaded = 0;  // steps issued
   long long row_off = 0;
   bool row_ok = false;
   auto look_up = [&]() {
     row_ok = false;
+    row_off = 0;
     if (step_loaded >= nsteps) return;
     const int i = load_at.tile * kTile + warp * kKeys + (lane & 15);
     if (i < load_at.vis.count) {
       const int row = i < load_at.vis.head ? i : i + load_at.vis.skip;
       const uint32_t pg = (__umulhi(static_cast<uint32_t>(row), p.div_mul) + row) >> p.div_shift;
       const int page = __ldg(p.table + static_cast<long long>(load_at.b) * p.max_pages + pg);
-      row_ok = page >= 0 && page < p.c.num_pages;
-      if (!row_ok) report_index(p.status, static_cast<unsigned long long>(load_at.b));
-      row_off = page * p.c.page_stride + (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
-                (load_at.sub / p.blocks) * p.c.head_stride;
+      if (page >= 0 && page < p.c.num_pages) {
+        row_ok = true;
+        row_off = page * p.c.page_stride + (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
+                  (load_at.sub / p.blocks) * p.c.head_stride;
+      } else {
+        report_index(p.status, static_cast<unsigned long long>(load_at.b));
+      }
     }
-    if (!row_ok) row_off = 0;
   };
   const uint32_t ring = smem_u32(smem) + warp * (2 * S::kHalf);
   auto stage_addr = [&](int s) { return ring + s * (kWarps * 2 * S::kHalf); };
@@ -333,7 +347,7 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
         const int key = j * kPer + lane / kChunks;
         const long long off = __shfl_sync(0xffffffffu, row_off, key) + c * 16;
         const uint32_t bytes = (mask >> key) & 1u ? 16u : 0u;  // 0: filled with zeros, nothing is read
-        uint32_t ck, cv;
+        uint32_t ck, cv;  // 16-byte chunks are permuted within a row so that no read below conflicts
         if constexpr (!Fp8) {
           ck = cv = key * S::kRowBytes + ((c ^ (key & 7)) << 4);
         } else if constexpr (D == 128) {
@@ -354,8 +368,9 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
   };
 
   // ---------------------------------------------------------------- the running state of a segment
-  float o[D / 8][4], m[2], l[2], sc[2];
-  uint32_t qf[kSteps][4];
+  // Columns are query heads: thread (g, t) holds those of 8 b + 2t and 8 b + 2t + 1.
+  float o[D / 16][NB][4], m[NB][2], l[NB][2], sc[NB][2];
+  uint32_t qf[kSteps][NB][2];
   look_up();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) issue(s, masks[s]);
@@ -365,16 +380,15 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
     // a segment: this CTA's tiles of one item
     const int seg_tile = at.tile;
     const int seg = nsteps - step < at.tiles - at.tile ? nsteps - step : at.tiles - at.tile;
-    const int hk = at.sub / p.blocks, h0 = hk * p.group + (at.sub - hk * p.blocks) * kRows;
-    const int rows = p.group - (at.sub - hk * p.blocks) * kRows < kRows ? p.group - (at.sub - hk * p.blocks) * kRows : kRows;
-    // Q fragments of rows g and g + 8 (zero past the group)
+    const int hk = at.sub / p.blocks, r0 = (at.sub - hk * p.blocks) * kRows, h0 = hk * p.group + r0;
+    const int rows = p.group - r0 < kRows ? p.group - r0 : kRows;
+    // q as the products' B: column g of block b (zero past the group)
+    const float sl2 = Fp8 && p.c.k_scale ? p.sl2 * __ldg(p.c.k_scale + hk) : p.sl2;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool there = g + 8 * r < rows;
-      const uint8_t* qp = p.q + at.b * p.q_seq + (h0 + g + 8 * r) * p.q_head;
-      sc[r] = p.sl2;
+    for (int b = 0; b < NB; ++b) {
+      const bool there = g + 8 * b < rows;
+      const uint8_t* qp = p.q + at.b * p.q_seq + (h0 + g + 8 * b) * p.q_head;
       if constexpr (Fp8) {
-        if (p.c.k_scale) sc[r] *= __ldg(p.c.k_scale + hk);
         float top = 0.f;
         float2 x[kSteps * 2];
 #pragma unroll
@@ -395,26 +409,32 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
         int e = static_cast<int>(__float_as_uint(top) >> 23);
         e = e < 2 ? 2 : e > 252 ? 252 : e;
         const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        sc[r] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+        sc[b][0] = sl2 * __shfl_sync(0xffffffffu, up, 8 * t);      // column 2t lives in lanes g = 2t
+        sc[b][1] = sl2 * __shfl_sync(0xffffffffu, up, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          qf[i][r] = from_f32x2<__half>(x[2 * i].x * down, x[2 * i].y * down);
-          qf[i][2 + r] = from_f32x2<__half>(x[2 * i + 1].x * down, x[2 * i + 1].y * down);
+          qf[i][b][0] = from_f32x2<__half>(x[2 * i].x * down, x[2 * i].y * down);
+          qf[i][b][1] = from_f32x2<__half>(x[2 * i + 1].x * down, x[2 * i + 1].y * down);
         }
       } else {
+        sc[b][0] = sc[b][1] = sl2;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          qf[i][r] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 2 * t) * 2)) : 0u;
-          qf[i][2 + r] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 8 + 2 * t) * 2)) : 0u;
+          qf[i][b][0] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 2 * t) * 2)) : 0u;
+          qf[i][b][1] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + (16 * i + 8 + 2 * t) * 2)) : 0u;
         }
       }
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[b][j] = -INFINITY;
+        l[b][j] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][b][j] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
     for (int i = 0; i < seg; ++i, ++step) {
       // the stage of step - 1 is free (every lane has read it): fill it with step + kStages - 1
@@ -430,86 +450,92 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
-      float x[2][4];  // scores of keys 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1; rows g (0, 1) and g + 8 (2, 3)
+      float x[NB][4];  // scores of keys g (0, 1) and g + 8 (2, 3) at columns 2t, 2t + 1
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
-      if constexpr (!Fp8) {
-        const int key = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t b[4];
-          ldsm4(b, sk + key * S::kRowBytes + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
-          mma16816<M>(x[0], qf[k], b[0], b[1]);
-          mma16816<M>(x[1], qf[k], b[2], b[3]);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int key = 8 * n + g, c = 4 * h + t;
-            const uint4 w = lds128(sk + key * S::kRowBytes + ((D == 128 ? c ^ ((key & 1) << 2) : c) << 4));
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma16816<M>(x[n], qf[4 * h + k], widen_e4m3(v[k]), widen_e4m3(v[k] >> 16));
-          }
-      }
-      // scale, mask, running maximum
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool there = (mask >> (8 * n + 2 * t + (j & 1))) & 1u;
-          x[n][j] = there ? x[n][j] * sc[j >> 1] : -INFINITY;
-          top[j >> 1] = fmaxf(top[j >> 1], x[n][j]);
-        }
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-        moved |= top[r] > m[r];
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float mn = fmaxf(m[r], top[r]);
-          const float keep = mn == -INFINITY ? 0.f : ex2_approx(m[r] - mn);
-          m[r] = mn;
-          l[r] *= keep;
-#pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[d][2 * r] *= keep;
-            o[d][2 * r + 1] *= keep;
-          }
-        }
-      }
-      uint32_t pf[4];  // the weights as the next product's A: rows g, g + 8 of keys 2t.., then of 8 + 2t..
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float w0 = ex2_approx(x[n][2 * r] - base), w1 = ex2_approx(x[n][2 * r + 1] - base);
-          l[r] += w0 + w1;
-          pf[2 * n + r] = from_f32x2<M>(w0, w1);
-        }
-      }
+        for (int j = 0; j < 4; ++j) x[b][j] = 0.f;
       if constexpr (!Fp8) {
         const int key = lane & 15;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          uint32_t b[4];
-          ldsm4t(b, sv + key * S::kRowBytes + (((2 * d + (lane >> 4)) ^ (key & 7)) << 4));
-          mma16816<M>(o[2 * d], pf, b[0], b[1]);
-          mma16816<M>(o[2 * d + 1], pf, b[2], b[3]);
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          ldsm4(a, sk + key * S::kRowBytes + (((2 * k + (lane >> 4)) ^ (key & 7)) << 4));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<M>(x[b], a, qf[k][b][0], qf[k][b][1]);
         }
       } else {
-        // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8): transposed bytewise, so
-        // that column g of product n is head dim g D/8 + n
+        // 16 bytes per thread and row: k index 2t, 2t + 1, 8 + 2t, 9 + 2t of step (h, k) is head dim
+        // 64 h + 16 t + 4 k + 0..3, for q above likewise
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const int c = 4 * h + t;
+          const uint4 u = lds128(sk + g * S::kRowBytes + ((D == 128 ? c ^ ((g & 1) << 2) : c) << 4));
+          const uint4 w = lds128(sk + (g + 8) * S::kRowBytes + ((D == 128 ? c ^ ((g & 1) << 2) : c) << 4));
+          const uint32_t lo[4] = {u.x, u.y, u.z, u.w}, hi[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a[4];
+            widen_e4m3(lo[k], a[0], a[2]);
+            widen_e4m3(hi[k], a[1], a[3]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<M>(x[b], a, qf[4 * h + k][b][0], qf[4 * h + k][b][1]);
+          }
+        }
+      }
+      bool moved = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[b][j] *= sc[b][j & 1];
+          if (mask != 0xffffu && !((mask >> (g + 8 * (j >> 1))) & 1u)) x[b][j] = -INFINITY;
+          moved |= x[b][j] > m[b][j & 1] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(x[b][j], x[b][j + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float mn = fmaxf(m[b][j], top);
+            const float keep = mn == -INFINITY ? 0.f : ex2_approx(m[b][j] - mn);
+            m[b][j] = mn;
+            l[b][j] *= keep;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              o[d][b][j] *= keep;
+              o[d][b][j + 2] *= keep;
+            }
+          }
+      }
+      uint32_t pf[NB][2];  // the weights as the next product's B: keys by pairs in a column of queries
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = ex2_approx(x[b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
+          l[b][j & 1] += w[j];
+        }
+        pf[b][0] = transpose8x8(from_f32x2<M>(w[0], w[1]));
+        pf[b][1] = transpose8x8(from_f32x2<M>(w[2], w[3]));
+      }
+      if constexpr (!Fp8) {
+        const int key = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t a[4];
+          ldsm4t(a, sv + key * S::kRowBytes + (((2 * d + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<M>(o[d][b], a, pf[b][0], pf[b][1]);
+        }
+      } else {
+        // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8), transposed bytewise: rows
+        // g and g + 8 of product n are head dims g D/8 + 2n and + 2n + 1
         constexpr int kW = D / 32;  // words
         uint32_t w[4][kW];
 #pragma unroll
@@ -528,15 +554,15 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
           }
         }
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
+        for (int i = 0; i < kW; ++i)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const uint32_t lo = __byte_perm(w[0][i], w[1][i], z ? 0x7362 : 0x5140);
-            const uint32_t hi = __byte_perm(w[2][i], w[3][i], z ? 0x7362 : 0x5140);
-            mma16816<M>(o[4 * i + 2 * z], pf, widen_e4m3(lo), widen_e4m3(hi));
-            mma16816<M>(o[4 * i + 2 * z + 1], pf, widen_e4m3(lo >> 16), widen_e4m3(hi >> 16));
+            uint32_t a[4];
+            widen_e4m3(__byte_perm(w[0][i], w[1][i], z ? 0x7362 : 0x5140), a[0], a[1]);
+            widen_e4m3(__byte_perm(w[2][i], w[3][i], z ? 0x7362 : 0x5140), a[2], a[3]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<M>(o[2 * i + z][b], a, pf[b][0], pf[b][1]);
           }
-        }
       }
     }
 
@@ -544,28 +570,31 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
     float* merge = reinterpret_cast<float*>(smem + S::kMergeOff);
     float2* ml = reinterpret_cast<float2*>(smem + S::kMlOff);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = g + 8 * r;
-      if (row < rows) {
-        float* dst = merge + (warp * kRows + row) * S::kPitch;
-        if (t == 0) ml[warp * kRows + row] = make_float2(m[r], l[r]);
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          if constexpr (!Fp8) {
-            *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-          } else {
-            dst[2 * t * (D / 8) + n] = o[n][2 * r];
-            dst[(2 * t + 1) * (D / 8) + n] = o[n][2 * r + 1];
+      for (int j = 0; j < 2; ++j) {
+        l[b][j] += __shfl_xor_sync(0xffffffffu, l[b][j], 4);
+        l[b][j] += __shfl_xor_sync(0xffffffffu, l[b][j], 8);
+        l[b][j] += __shfl_xor_sync(0xffffffffu, l[b][j], 16);
+        const int row = 8 * b + 2 * t + j;
+        if (row < rows) {
+          float* dst = merge + (warp * kRows + row) * S::kPitch;
+          if (g == 0) ml[warp * kRows + row] = make_float2(m[b][j], l[b][j]);
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            if constexpr (!Fp8) {
+              dst[16 * n + g] = o[n][b][j];
+              dst[16 * n + g + 8] = o[n][b][j + 2];
+            } else {
+              *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * n) = make_float2(o[n][b][j], o[n][b][j + 2]);
+            }
           }
         }
       }
-    }
     __syncthreads();
     const bool whole = seg == at.tiles;
     const int vecs = rows * (D / 4);  // float4s of the merged rows
-    float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_tile ? 0 : 1)) * (kRows * (D + 2));
+    float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_tile ? 0 : 1)) * S::kPart;
     const float vs = Fp8 && p.c.v_scale ? __ldg(p.c.v_scale + hk) : 1.f;
     auto write_out = [&](int row, int d, float4 v, float mm, float ll) {
       const float inv = ll == 0.f ? 0.f : vs / ll;
@@ -574,6 +603,12 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
           make_uint2(from_f32x2<T>(v.x * inv, v.y * inv), from_f32x2<T>(v.z * inv, v.w * inv));
       if (p.lse && d == 0)
         p.lse[static_cast<long long>(at.b) * p.heads + h] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+    };
+    auto add = [](float4& acc, float f, const float4& v) {
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
     };
     for (int i = threadIdx.x; i < vecs; i += kThreads) {
       const int row = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -586,12 +621,8 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
       for (int w = 0; w < kWarps; ++w) {
         const float2 z = ml[w * kRows + row];
         const float f = ex2_approx(z.x - base);
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * S::kPitch + d);
         ll += f * z.y;
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
+        add(acc, f, *reinterpret_cast<const float4*>(merge + (w * kRows + row) * S::kPitch + d));
       }
       if (whole) {
         write_out(row, d, acc, mm, ll);
@@ -614,26 +645,47 @@ __global__ void __launch_bounds__(paged::kThreads, 2) paged_kernel(const PagedPa
       }
       __syncthreads();
       if (s_last) {
-        auto slot = [&](int c) { return p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * (kRows * (D + 2)); };
-        for (int i = threadIdx.x; i < vecs; i += kThreads) {
-          const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-          float mm = -INFINITY, ll = 0.f;
+        auto slot = [&](int c) { return p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * S::kPart; };
+        for (int row = warp; row < rows; row += kWarps) {  // a row's maximum over all parts
+          float mm = -INFINITY;
+          for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(slot(c) + kRows * D + 2 * row));
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+          if (lane == 0) s_max[row] = mm;
+        }
+        __syncthreads();
+        // Few rows leave threads over: `teams` of them share the parts of a row, added up at the end.
+        const int teams = vecs < kThreads ? kThreads / vecs : 1;
+        for (int i0 = 0; i0 < vecs * teams; i0 += kThreads) {
+          const int i = i0 + threadIdx.x, team = teams > 1 ? i / vecs : 0, v = i - team * vecs;
+          const bool mine = i < vecs * teams;
+          const int row = v / (D / 4), d = (v % (D / 4)) * 4;
+          float ll = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (mine) {
+            const float base = s_max[row] == -INFINITY ? 0.f : s_max[row];
 #pragma unroll 8
-          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(slot(c) + kRows * D + 2 * row));
-          const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 8
-          for (int c = c0; c <= c1; ++c) {
-            const float2 z = __ldcg(reinterpret_cast<const float2*>(slot(c) + kRows * D + 2 * row));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c) + row * D + d));
-            const float f = ex2_approx(z.x - base);
-            ll += f * z.y;
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+            for (int c = c0 + team; c <= c1; c += teams) {
+              const float2 z = __ldcg(reinterpret_cast<const float2*>(slot(c) + kRows * D + 2 * row));
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(slot(c) + row * D + d));
+              const float f = ex2_approx(z.x - base);
+              ll += f * z.y;
+              add(acc, f, u);
+            }
           }
-          write_out(row, d, acc, mm, ll);
+          if (teams > 1) {  // one round (vecs * teams <= kThreads); the merged rows are not needed any more
+            float* hold = merge + threadIdx.x * 8;
+            *reinterpret_cast<float4*>(hold) = acc;
+            hold[4] = ll;
+            __syncthreads();
+            if (mine && team == 0)
+              for (int x = 1; x < teams; ++x) {
+                const float* other = merge + (threadIdx.x + x * vecs) * 8;
+                add(acc, 1.f, *reinterpret_cast<const float4*>(other));
+                ll += other[4];
+              }
+          }
+          if (mine && team == 0) write_out(row, d, acc, s_max[row], ll);
         }
       }
     }
@@ -724,8 +776,11 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
 }
 
 // Workspace: the parts of split items (two per CTA of the largest grid), then one counter per item.
-static int paged_blocks(int heads, int kv_heads) { return (heads / kv_heads + paged::kRows - 1) / paged::kRows; }
-static size_t paged_part_bytes(int d) { return align256(static_cast<size_t>(kPagedMaxCtas) * 2 * paged::kRows * (d + 2) * 4); }
+static int paged_rows(int heads, int kv_heads) { return heads / kv_heads > 8 ? 16 : 8; }  // query heads of an item
+static int paged_blocks(int heads, int kv_heads) {
+  return (heads / kv_heads + paged_rows(heads, kv_heads) - 1) / paged_rows(heads, kv_heads);
+}
+static size_t paged_part_bytes(int d) { return align256(static_cast<size_t>(kPagedMaxCtas) * 2 * paged::kMaxRows * (d + 2) * 4); }
 
 extern "C" size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d) {
   if (batch < 0 || batch > 4096 || !heads_ok(heads, kv_heads, d)) return 0;
@@ -781,16 +836,18 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
   const long long most = batch * static_cast<long long>(cache->kv_heads) * p.blocks * (cap / paged::kTile + 1);
-  long long grid = 2LL * ctx->ctas < kPagedMaxCtas ? 2LL * ctx->ctas : kPagedMaxCtas;
-  if (grid > most) grid = most;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
-    using S = paged::Shape<decltype(fp8)::value, decltype(d)::value>;
-    auto kern = paged_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return static_cast<int>(TL_ERR_CUDA);
-    }
-    kern<<<static_cast<unsigned>(grid), paged::kThreads, S::kSmem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched();
+    auto launch = [&](auto nb) {
+      using S = paged::Shape<decltype(fp8)::value, decltype(d)::value, decltype(nb)::value>;
+      auto kern = paged_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value, decltype(nb)::value>;
+      static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may use its shared memory
+      if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), S::kSmem)) return static_cast<int>(TL_ERR_CUDA);
+      long long grid = static_cast<long long>(S::kCtas) * ctx->ctas;
+      if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+      if (grid > most) grid = most;
+      kern<<<static_cast<unsigned>(grid), paged::kThreads, S::kSmem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+      return launched();
+    };
+    return p.group > 8 ? launch(std::integral_constant<int, 2>{}) : launch(std::integral_constant<int, 1>{});
   });
 }

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "tl_host.h"
 
 namespace tl {
@@ -39,6 +41,18 @@ template <>
 __device__ __forceinline__ uint32_t from_f32x2<__half>(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device (a bit of `ready` each).
+inline bool smem_ready(std::atomic<unsigned long long>& ready, int device, const void* kern, int bytes) {
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device < 64 && (ready.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  ready.fetch_or(device < 64 ? bit : 0, std::memory_order_release);
+  return true;
 }
 
 inline bool esize_ok(long long stride, int esize) { return stride >= 0 && (stride * esize) % 16 == 0; }
