@@ -102,9 +102,10 @@ struct Shape {
   static constexpr int kRows = 8 * NB;                   // query heads of an item
   static constexpr int kRowBytes = D * (Fp8 ? 1 : 2);
   static constexpr int kHalf = kKeys * kRowBytes;        // one warp's K (or V) rows of a stage
-  // CTAs per SM, and the stages that fit: 64 KB of ring at two CTAs, 48 KB at three.
-  // 8-bit rows spend their time on widening and want more warps, 16-bit rows wait for HBM.
-  static constexpr int kCtas = Fp8 && NB == 1 ? 3 : 2;
+  // CTAs per SM, and the stages that fit: 64 KB of ring at two CTAs, 48 KB at three.  A step of
+  // 8-bit or short rows brings few bytes for its instructions and wants the warps; the registers
+  // allow three CTAs there.
+  static constexpr int kCtas = D == 64 || (Fp8 && NB == 1) ? 3 : 2;
   static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * 2 * kHalf);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   using M = typename std::conditional<Fp8, __half, T>::type;  // the products' type
   constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_sum[kThreads], s_warp[kWarps];
+  __shared__ uint32_t s_sum[kThreads], s_warp[kWarps];
   __shared__ float s_max[kMaxRows];
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk); s_sum holds the sums inside a warp.
   const int chunk = (p.batch + kThreads - 1) / kThreads;
   {
-    long long sum = 0;
+    uint32_t sum = 0;
     for (int i = 0; i < chunk; ++i) {
       const int b = static_cast<int>(threadIdx.x) * chunk + i;
       if (b >= p.batch) break;
@@ -256,28 +257,27 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     }
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, sum, x);
+      const uint32_t o = __shfl_up_sync(0xffffffffu, sum, x);
       if (lane >= x) sum += o;
     }
     s_sum[threadIdx.x] = sum;
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
   }
-  long long total = 0;
+  uint32_t total = 0;  // below 2^31 (the host checks)
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += s_warp[w];
   total *= subs;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long first = per * blockIdx.x;
-  const long long last = first + per < total ? first + per : total;
-  if (first >= last) return;
-  const int nsteps = static_cast<int>(last - first);
+  const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
+  const uint32_t first = per * blockIdx.x;  // at most total + grid^2
+  if (first >= total) return;
+  const int nsteps = static_cast<int>(per < total - first ? per : total - first);
 
   PagedAt at;
-  long long item_begin;  // position on the line of the current item's first tile
+  uint32_t item_begin;  // position on the line of the current item's first tile
   {
     // the warp, then the thread, whose sequences hold `first`
-    long long pos = 0;
+    uint32_t pos = 0;
     int w = 0;
     while (pos + s_warp[w] * subs <= first) pos += s_warp[w++] * subs;
     const int i = __popc(__ballot_sync(0xffffffffu, pos + s_sum[32 * w + lane] * subs <= first));
@@ -286,13 +286,13 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     for (;;) {
       at.vis = visible_rows(paged_length(p, at.b, false), p.window, p.sinks);
       at.tiles = paged_tiles(at.vis.count);
-      const long long here = static_cast<long long>(at.tiles) * subs;
+      const uint32_t here = static_cast<uint32_t>(at.tiles) * subs;
       if (first < pos + here) break;
       pos += here;
       ++at.b;
     }
-    at.sub = static_cast<int>((first - pos) / at.tiles);
-    at.tile = static_cast<int>((first - pos) - static_cast<long long>(at.sub) * at.tiles);
+    at.sub = static_cast<int>((first - pos) / static_cast<uint32_t>(at.tiles));
+    at.tile = static_cast<int>(first - pos) - at.sub * at.tiles;
     item_begin = first - at.tile;
   }
   // One tile on; past the last one of the CTA's range the position is not used.
@@ -634,9 +634,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     if (!whole) {
       // the item's parts lie in CTAs [c0, c1]: the first in slot 1 (it starts the item), the others in slot 0
       const int c0 = static_cast<int>(item_begin / per), c1 = static_cast<int>((item_begin + at.tiles - 1) / per);
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
+        __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
         unsigned* ctr = p.counter + static_cast<size_t>(at.b) * subs + at.sub;
         const unsigned done = atomicAdd(ctr, 1u) + 1u;
         s_last = done == static_cast<unsigned>(c1 - c0 + 1);
@@ -645,10 +645,16 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       }
       __syncthreads();
       if (s_last) {
-        auto slot = [&](int c) { return p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * S::kPart; };
+        // Part c of c0 + 1.. is `stride` floats after part c - 1; the first one lies apart.
+        constexpr int kStride = 2 * S::kPart;
+        const float* one = p.part + (static_cast<size_t>(c0) * 2 + 1) * S::kPart;
+        const float* rest = p.part + static_cast<size_t>(c0 + 1) * kStride;
+        const int more = c1 - c0;  // parts after the first
         for (int row = warp; row < rows; row += kWarps) {  // a row's maximum over all parts
-          float mm = -INFINITY;
-          for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(slot(c) + kRows * D + 2 * row));
+          float mm = lane == 0 ? __ldcg(one + kRows * D + 2 * row) : -INFINITY;
+          const float* src = rest + static_cast<size_t>(lane) * kStride + kRows * D + 2 * row;
+#pragma unroll 2
+          for (int c = lane; c < more; c += 32, src += 32 * kStride) mm = fmaxf(mm, __ldcg(src));
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
           if (lane == 0) s_max[row] = mm;
@@ -664,13 +670,31 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           if (mine) {
             const float base = s_max[row] == -INFINITY ? 0.f : s_max[row];
-#pragma unroll 8
-            for (int c = c0 + team; c <= c1; c += teams) {
-              const float2 z = __ldcg(reinterpret_cast<const float2*>(slot(c) + kRows * D + 2 * row));
-              const float4 u = __ldcg(reinterpret_cast<const float4*>(slot(c) + row * D + d));
+            auto fold = [&](const float2& z, const float4& u) {
               const float f = ex2_approx(z.x - base);
               ll += f * z.y;
               add(acc, f, u);
+            };
+            if (team == 0)
+              fold(__ldcg(reinterpret_cast<const float2*>(one + kRows * D + 2 * row)),
+                   __ldcg(reinterpret_cast<const float4*>(one + row * D + d)));
+            const float* src = rest + static_cast<size_t>(team) * kStride;
+            const int step_floats = teams * kStride;
+            constexpr int kBatch = 8;  // a round trip to L2, often the other die's, each
+            for (int c = team; c < more; c += kBatch * teams) {
+              float2 z[kBatch];
+              float4 u[kBatch];
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x, src += step_floats) {
+                z[x] = make_float2(-INFINITY, 0.f);
+                u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + x * teams < more) {
+                  z[x] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * row));
+                  u[x] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x) fold(z[x], u[x]);
             }
           }
           if (teams > 1) {  // one round (vecs * teams <= kThreads); the merged rows are not needed any more
@@ -836,6 +860,7 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
   const long long most = batch * static_cast<long long>(cache->kv_heads) * p.blocks * (cap / paged::kTile + 1);
+  if (most >= (1LL << 31)) return TL_ERR_INVALID;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
     auto launch = [&](auto nb) {
       using S = paged::Shape<decltype(fp8)::value, decltype(d)::value, decltype(nb)::value>;

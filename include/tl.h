@@ -468,7 +468,8 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * workspace: tl_paged_attention_workspace_bytes(): partial results of sequences split over several
  * CTAs, and one counter per sequence, kv head and group of 16 query heads.
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
- * page_size < 2^31; scale finite and > 0.  batch == 0 or heads == 0 is a no-op.
+ * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
+ * batch == 0 or heads == 0 is a no-op.
  * The result does not depend on what else runs, and is bit-identical run to run on one device.
  */
 size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d);
