@@ -186,10 +186,20 @@ def _ptrs(ts):
     return arr
 
 
-def _stream(stream) -> int:
+_raw_stream = None
+
+
+def _stream(stream, device: int | None = None) -> int:
     if stream is None:
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the handle without a Stream object around it: 0.1 us instead of 3
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+        if device is not None and _raw_stream:
+            return _raw_stream(device)
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return int(torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -437,7 +447,8 @@ def _vec(t, n: int, dtype_name: str, what: str) -> int:
     """The pointer of an optional contiguous CUDA tensor of n entries."""
     if t is None:
         return 0
-    _need(t, dtype_name, what)
+    if t.dtype is not _dtypes.get(dtype_name) or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype_name, what)
     if t.numel() != n:
         raise ValueError(f"{what} must have {n} entries (got {tuple(t.shape)})")
     return t.data_ptr()
@@ -445,11 +456,12 @@ def _vec(t, n: int, dtype_name: str, what: str) -> int:
 
 def _cache(k_cache, v_cache, k_scale, v_scale) -> PagedCache:
     code = _code(k_cache, "k_cache")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or not v_cache.is_cuda:
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_cuda:
         raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
-    pages, page, heads, d = k_cache.shape
-    a, b, c, one = k_cache.stride()
-    if v_cache.stride() != (a, b, c, one) or one != 1:
+    pages, page, heads, d = shape
+    a, b, c, one = strides
+    if v_cache.stride() != strides or one != 1:
         raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
     return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _vec(k_scale, heads, "f32", "k_scale"),
                       _vec(v_scale, heads, "f32", "v_scale"), a if pages > 1 else 0, b if page > 1 else 0,
@@ -468,7 +480,7 @@ def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_sc
     n = k.shape[0]
     sp = _vec(slots, n, "i32", "slots")
     rc = lib().tl_kv_append(ctx.handle, ctypes.byref(cache), code, k.data_ptr(), v.data_ptr(), *_rows(k, "k"),
-                            *_rows(v, "v"), sp, n, _stream(stream))
+                            *_rows(v, "v"), sp, n, _stream(stream, ctx.device))
     _check(rc, "tl_kv_append")
 
 
@@ -495,7 +507,7 @@ def tl_paged_attention(ctx: Context, q, k_cache, v_cache, page_table, lengths, o
     rc = lib().tl_paged_attention(ctx.handle, ctypes.byref(cache), code, q.data_ptr(), *_rows(q, "q"), tp, pages, lp,
                                   out.data_ptr(), *_rows(out, "out"), _vec(lse, batch * heads, "f32", "lse"), batch,
                                   heads, d ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
-                                  workspace.numel(), _stream(stream))
+                                  workspace.numel(), _stream(stream, ctx.device))
     _check(rc, "tl_paged_attention")
 
 
@@ -519,7 +531,7 @@ def tl_window_attention(ctx: Context, q, k, v, cu_q, cu_k, out, lse=None, scale=
                                    _vec(cu_k, batch + 1, "i32", "cu_k"), out.data_ptr(), *_rows(out, "out"),
                                    _vec(lse, total_q * heads, "f32", "lse"), batch, total_q, k.shape[0], heads,
                                    k.shape[1], d, d ** -0.5 if scale is None else scale, window, sinks,
-                                   _stream(stream))
+                                   _stream(stream, ctx.device))
     _check(rc, "tl_window_attention")
 
 
@@ -531,18 +543,19 @@ def tl_moe_tokens(ctx: Context, x, logits, topk: int, w_gate, w_up, w_down, out,
                   gates_out=None, stream=None) -> None:
     """tl_moe_combine's layer for the few tokens (at most 128) of a decoding step: out fp32 [T, H];
     experts_out int32 and gates_out fp32 [T, topk] are optional."""
-    _need(x, "bf16", "x"); _need(logits, "f32", "logits"); _need(w_gate, "bf16", "w_gate")
-    _need(w_up, "bf16", "w_up"); _need(w_down, "bf16", "w_down"); _need(out, "f32", "out")
-    _need(workspace, "u8", "workspace")
+    _need(x, "bf16", "x")
     T, H = x.shape
     E, _, F = w_gate.shape
-    if logits.shape != (T, E) or w_gate.shape != (E, H, F) or w_up.shape != (E, H, F) or \
-            w_down.shape != (E, F, H) or out.shape != (T, H):
+    if logits.shape != (T, E) or w_gate.shape != (E, H, F) or w_up.shape != w_gate.shape or \
+            w_down.shape != (E, F, H) or out.shape != x.shape:
         raise ValueError("inconsistent shapes")
-    rc = lib().tl_moe_tokens(ctx.handle, x.data_ptr(), logits.data_ptr(), topk, w_gate.data_ptr(), w_up.data_ptr(),
-                             w_down.data_ptr(), out.data_ptr(), _vec(experts_out, T * topk, "i32", "experts_out"),
+    _need(workspace, "u8", "workspace")
+    rc = lib().tl_moe_tokens(ctx.handle, x.data_ptr(), _vec(logits, T * E, "f32", "logits"), topk,
+                             _vec(w_gate, E * H * F, "bf16", "w_gate"), _vec(w_up, E * H * F, "bf16", "w_up"),
+                             _vec(w_down, E * F * H, "bf16", "w_down"), _vec(out, T * H, "f32", "out"),
+                             _vec(experts_out, T * topk, "i32", "experts_out"),
                              _vec(gates_out, T * topk, "f32", "gates_out"), workspace.data_ptr(), workspace.numel(),
-                             T, H, E, F, _stream(stream))
+                             T, H, E, F, _stream(stream, ctx.device))
     _check(rc, "tl_moe_tokens")
 
 
