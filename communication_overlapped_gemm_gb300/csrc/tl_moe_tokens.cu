@@ -1,132 +1,481 @@
 // The MoE layer for the few tokens of a decoding step.
+//
+//   h_a = SiLU(x_t Wg_e) * (x_t Wu_e),   out_t = sum_j gate_tj h_a Wd_e,   a = (t, j), e the expert of a
+// With a handful of tokens at each expert the weights are read once and meet one or two tokens, so
+// HBM bounds the layer: 6 H F bytes for each distinct expert, 6 H F flops for each assignment.  Two
+// launches, one per product; the second is a dependent launch whose CTAs fit beside the first's, so
+// its weights are already being loaded while the first ends.
+//
+// Each CTA (one per SM and kernel) works out the routing by itself, so nothing has to pass between
+// CTAs before the first load: the topk of every token, the assignments in the order (expert, t, j),
+// and the items: an expert with up to 8 NT of its assignments.  (item, 64 or 128 columns, 64 rows
+// of the weights) is a unit of 16 KB; all units form one line, cut into equal ranges, one per CTA:
+// even work for any routing.  One warp keeps a ring of TMA loads full, four warps multiply.
+//
+// The products run on mma.sync m16n8k16: columns of the weights are its 16 rows (transposed by ldmatrix from
+// the 128-byte-swizzled tile), the tokens its 8 columns, which wastes least for 1 to 8 tokens; a
+// tcgen05 tile would be 128 rows of tokens.  The k order inside 32 rows is permuted so
+// that a thread's part of x is 16 contiguous bytes and ldmatrix rows fall in different banks: thread t
+// holds k = 8 t .. 8 t + 7 as four pairs, and pair (i + t) mod 4 is its i-th.
+// h goes to the second product as a sum of three bf16 (24 bits), three products for one load of
+// the weights, so the layer keeps fp32 precision between the two.
+//
+// Tiles whose units lie in several CTAs: each CTA stores its fp32 sums, and the one that finishes
+// last (a counter, left at zero again) adds them in the order of the line.  In the second product
+// the last item of a column block to finish combines the block's rows, sum over j in order.  The order of
+// every sum is fixed by the routing; nothing waits on another CTA.
+#include <type_traits>
+
 #include "tl_serve.cuh"
 
 namespace tl {
 
 namespace moet {
-constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk;
-}
+constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk, kMaxCtas = 512;
+constexpr int kMmaWarps = 4, kMmaThreads = 32 * kMmaWarps, kThreads = kMmaThreads + 32;
+constexpr int kUnitBytes = 16384, kStages = 6;  // both kernels' rings fit in one SM together
+constexpr int kTileOff = 0;
+constexpr int kBarOff = kStages * kUnitBytes;
+constexpr int kSmem = kBarOff + 2 * kStages * 8 + 1024;  // 1024: the ring's alignment
+}  // namespace moet
 
 struct MoeTokParams {
+  CUtensorMap w0;  // gate, or down: {columns, rows, E}, box {64, 64, 1}
+  CUtensorMap w1;  // up
+  Common common;
   const __nv_bfloat16* x;
   const float* logits;
-  const __nv_bfloat16* w_gate;
-  const __nv_bfloat16* w_up;
-  const __nv_bfloat16* w_down;
   float* out;
   int* experts_out;
   float* gates_out;
-  int* experts;  // [T topk]
-  float* gates;  // [T topk]
-  float* h;      // [T topk][F]
+  __nv_bfloat16* h;    // [3][T topk][F]: h = h0 + h1 + h2, rows in the order (expert, t, j)
+  float* y;            // [T topk][H]
+  float* part;         // [CTA][2][128 threads][8 NT] sums of a cut tile
+  float* gates;        // [T topk]
+  unsigned* cut_ctr;   // [CTA]: CTAs done with the cut tile that starts in this one
+  unsigned* col_ctr;   // [column block]: items done (second product)
   int T, H, E, F, topk, renorm;
 };
 
-// The routing of one token by one warp: the topk largest logits (ties to the lower expert, NaN
-// the lowest), and the softmax over all E logits taken at them.
-__device__ __forceinline__ void route_token(const float* row, int E, int topk, int renorm, int lane, int* experts,
-                                            float* gates) {
+// What a CTA derives from the logits.
+struct MoeTables {
+  uint8_t expert[moet::kMaxA];   // of assignment a = t topk + j
+  uint16_t at[moet::kMaxA];      // row of assignment a
+  uint16_t order[moet::kMaxA];   // assignment of a row
+  uint16_t start[moet::kMaxE + 1];  // rows of expert e: [start[e], start[e + 1])
+  uint16_t item_expert[moet::kMaxA];
+  uint16_t item_row[moet::kMaxA];   // first row
+  int items;
+  unsigned last;
+};
+
+// An order-preserving key of a logit; NaN is the lowest, as -inf.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  const uint32_t b = __float_as_uint(v == v ? v + 0.f : -INFINITY);  // + 0: -0 equals 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One warp: the topk experts of a token, best first, ties to the lower index.  Lane l holds
+// experts l, l + 32, ...; key 0 marks "none" (below the key of -inf).
+__device__ __forceinline__ void route_token(const float* row, int E, int topk, int lane, uint8_t* experts) {
   constexpr int kPer = moet::kMaxE / 32;
-  float v[kPer], mx = -INFINITY, s = 0.f;
+  uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < E ? row[e] : -INFINITY;
-    mx = fmaxf(mx, v[i]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < E) s += expf(v[i] - mx);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  uint32_t taken = 0;
-  float sum = 0.f;
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? logit_key(__ldg(row + lane + 32 * i)) : 0u;
   for (int j = 0; j < topk; ++j) {
-    // order key: NaN -> -inf; a free expert always beats "none" (index beyond every expert)
-    float bv = -INFINITY;
-    int bi = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      const float x = v[i] == v[i] ? v[i] : -INFINITY;
-      if (e < E && !(taken & (1u << i)) && (x > bv || (x == bv && e < bi))) {
-        bv = x;
-        bi = e;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (ov > bv || (ov == bv && oi < bi)) {
-        bv = ov;
-        bi = oi;
-      }
-    }
-    float mine = 0.f;
+    uint32_t best = 0u;
+    int at = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i == bi) {
-        taken |= 1u << i;
-        mine = v[i];
+      if (32 * i < E && key[i] > best) {
+        best = key[i];
+        at = i;
       }
-    const float g = expf(__shfl_sync(0xffffffffu, mine, bi & 31) - mx) / s;
-    sum += g;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0xffffffffu);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
+    if (lane == 0) experts[j] = static_cast<uint8_t>(e);
+  }
+}
+
+// All threads of the CTA: routing, order and items (groups of `group` rows of an expert).
+__device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb, int group) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.topk;
+  for (int t = warp; t < p.T; t += moet::kThreads / 32)
+    route_token(p.logits + static_cast<size_t>(t) * p.E, p.E, p.topk, lane, tb.expert + t * p.topk);
+  for (int a = n + static_cast<int>(threadIdx.x); a < ((n + 3) & ~3); a += moet::kThreads) tb.expert[a] = 0xff;  // never an assignment below
+  __syncthreads();
+  // counts, then rows, of the experts of this thread: a byte compare over all assignments.  (E = 256
+  // uses 0xff too, so entries past n are cut off by index.)
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(tb.expert);
+  for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
+    int c = 0;
+    for (int w = 0; 4 * w < n; ++w) {
+      const uint32_t eq = __vcmpeq4(words[w], e * 0x01010101u);
+      c += __popc((4 * w + 4 <= n ? eq : eq & ((1u << (8 * (n - 4 * w))) - 1u)) & 0x01010101u);
+    }
+    tb.start[e + 1] = static_cast<uint16_t>(c);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int rows = 0, items = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int c = e0 + lane < p.E ? tb.start[e0 + lane + 1] : 0, k = (c + group - 1) / group;
+      int sr = c, si = k;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int r = __shfl_up_sync(0xffffffffu, sr, x), i = __shfl_up_sync(0xffffffffu, si, x);
+        if (lane >= x) {
+          sr += r;
+          si += i;
+        }
+      }
+      __syncwarp();
+      if (e0 + lane < p.E) tb.start[e0 + lane + 1] = static_cast<uint16_t>(rows + sr);
+      for (int i = 0; i < k; ++i) {
+        tb.item_expert[items + si - k + i] = static_cast<uint16_t>(e0 + lane);
+        tb.item_row[items + si - k + i] = static_cast<uint16_t>(rows + sr - c + i * group);
+      }
+      rows += __shfl_sync(0xffffffffu, sr, 31);
+      items += __shfl_sync(0xffffffffu, si, 31);
+    }
     if (lane == 0) {
-      experts[j] = bi;
-      gates[j] = g;
+      tb.start[0] = 0;
+      tb.items = items;
     }
   }
-  __syncwarp();
-  if (renorm)
-    for (int j = lane; j < topk; j += 32) gates[j] /= sum;
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
+    int r = tb.start[e];
+    if (r == tb.start[e + 1]) continue;
+    for (int w = 0; 4 * w < n; ++w) {
+      uint32_t eq = __vcmpeq4(words[w], e * 0x01010101u) & 0x01010101u;
+      for (; eq; eq &= eq - 1) {
+        const int a = 4 * w + ((__ffs(eq) - 1) >> 3);
+        if (a >= n) break;
+        tb.at[a] = static_cast<uint16_t>(r);
+        tb.order[r++] = static_cast<uint16_t>(a);
+      }
+    }
+  }
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(128) moet_route_kernel(const MoeTokParams p) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= p.T) return;
-  route_token(p.logits + static_cast<size_t>(t) * p.E, p.E, p.topk, p.renorm, lane, p.experts + t * p.topk,
-              p.gates + t * p.topk);
-  __syncwarp();
-  for (int j = lane; j < p.topk; j += 32) {
-    if (p.experts_out) p.experts_out[t * p.topk + j] = p.experts[t * p.topk + j];
-    if (p.gates_out) p.gates_out[t * p.topk + j] = p.gates[t * p.topk + j];
+// Four pairs of a 16-byte part of x (or h) in the order that thread t uses them: pair (i + t) mod 4 i-th.
+__device__ __forceinline__ void rotate_pairs(const uint4& v, int t, uint32_t (&r)[4]) {
+  const uint32_t a0 = t & 1 ? v.y : v.x, a1 = t & 1 ? v.z : v.y, a2 = t & 1 ? v.w : v.z, a3 = t & 1 ? v.x : v.w;
+  r[0] = t & 2 ? a2 : a0;
+  r[1] = t & 2 ? a3 : a1;
+  r[2] = t & 2 ? a0 : a2;
+  r[3] = t & 2 ? a1 : a3;
+}
+
+// A 16-byte load that another kernel's writes may precede (not through the read-only path).
+__device__ __forceinline__ uint4 ld_global128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// One warp: the gates of a token, the softmax over all E logits taken at its experts.
+__device__ __forceinline__ void token_gates(const MoeTokParams& p, const MoeTables& tb, int tok, int lane) {
+  const float* row = p.logits + static_cast<size_t>(tok) * p.E;
+  float top = -INFINITY, sum = 0.f;
+  for (int e = lane; e < p.E; e += 32) top = fmaxf(top, row[e]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int e = lane; e < p.E; e += 32) sum += expf(row[e] - top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float gate = lane < p.topk ? expf(row[tb.expert[tok * p.topk + lane]] - top) / sum : 0.f;
+  if (p.renorm) {
+    float all = gate;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);  // topk <= 8
+    gate /= all;
+  }
+  if (lane < p.topk) {
+    p.gates[tok * p.topk + lane] = gate;
+    if (p.gates_out) p.gates_out[tok * p.topk + lane] = gate;
   }
 }
 
-// h = SiLU(x Wg) * (x Wu): one thread per column of F, one CTA row per assignment.
-__global__ void __launch_bounds__(64) moet_up_kernel(const MoeTokParams p) {
-  const int a = blockIdx.y, f = blockIdx.x * 64 + threadIdx.x;
-  if (f >= p.F) return;
-  const size_t w0 = static_cast<size_t>(p.experts[a]) * p.H * p.F + f;
-  const __nv_bfloat16* x = p.x + static_cast<size_t>(a / p.topk) * p.H;
-  float g = 0.f, u = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < p.H; ++k) {
-    const float xv = __bfloat162float(x[k]);
-    g += xv * __bfloat162float(p.w_gate[w0 + static_cast<size_t>(k) * p.F]);
-    u += xv * __bfloat162float(p.w_up[w0 + static_cast<size_t>(k) * p.F]);
+// Down: false for the first product (gate and up, 64 columns of each), true for the second (down,
+// 128 columns).  NT: groups of 8 tokens in an item.
+template <bool Down, int NT>
+__global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_constant__ MoeTokParams p) {
+  using namespace moet;
+  constexpr int kParts = Down ? 3 : 1;            // 16-bit terms of the left operand
+  constexpr int kCols = Down ? 128 : 64;          // columns of a tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ MoeTables tb;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kBarOff);
+  uint64_t* empty = full + kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kMmaWarps);
+    }
+    fence_mbar_init();
+    tma_prefetch_map(&p.w0);
+    if (!Down) tma_prefetch_map(&p.w1);
   }
-  p.h[static_cast<size_t>(a) * p.F + f] = g / (1.f + expf(-g)) * u;
-}
+  if (!Down) grid_dep_launch();
+  moet_tables(p, tb, 8 * NT);
+  const int K = Down ? p.F : p.H, N = Down ? p.H : p.F;
+  const int nk = (K + 63) / 64, nc = (N + kCols - 1) / kCols;
+  // the line of units: the first product item by item, the second column block by column block, so
+  // that blocks are combined while others are still multiplied
+  const uint32_t tiles = static_cast<uint32_t>(tb.items) * nc, total = tiles * nk;
+  const uint32_t per = (total + gridDim.x - 1) / gridDim.x, first = per * blockIdx.x;
+  const int n = first >= total ? 0 : static_cast<int>(per < total - first ? per : total - first);
+  const int item0 = n ? (Down ? (first / nk) % tb.items : first / nk / nc) : 0;
+  const int col0 = n ? (Down ? first / nk / tb.items : (first / nk) % nc) : 0;
+  const int k0 = n ? first % nk : 0;
+  auto next_tile = [&](int& item, int& col) {
+    if (Down) {
+      if (++item == tb.items) {
+        item = 0;
+        ++col;
+      }
+    } else if (++col == nc) {
+      col = 0;
+      ++item;
+    }
+  };
 
-// out = sum_j gate_j h_j Wd: one thread per column of H, one CTA row per token.
-__global__ void __launch_bounds__(64) moet_down_kernel(const MoeTokParams p) {
-  const int t = blockIdx.y, c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= p.H) return;
-  float out = 0.f;
-  for (int j = 0; j < p.topk; ++j) {
-    const int a = t * p.topk + j;
-    const size_t w0 = static_cast<size_t>(p.experts[a]) * p.F * p.H + c;
-    const float* h = p.h + static_cast<size_t>(a) * p.F;
-    float y = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < p.F; ++k) y += h[k] * __bfloat162float(p.w_down[w0 + static_cast<size_t>(k) * p.H]);
-    out += p.gates[a] * y;
+  if (warp == kMmaWarps) {
+    // ------------------------------------------------------------ loads (they wait for no other kernel)
+    if (lane == 0) {
+      int item = item0, col = col0, k = k0, i = 0;
+      bool ok = true;
+      for (; i < n && ok; ++i) {
+        const int s = i % kStages;
+        ok = mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, p.common, kSiteEmpty);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&full[s], kUnitBytes);
+        const int e = tb.item_expert[item];
+        uint8_t* dst = ring + s * kUnitBytes;
+        tma_load_3d(dst, &p.w0, &full[s], col * kCols, k * 64, e);
+        tma_load_3d(dst + kUnitBytes / 2, Down ? &p.w0 : &p.w1, &full[s], col * kCols + (Down ? 64 : 0), k * 64, e);
+        if (++k == nk) {
+          k = 0;
+          next_tile(item, col);
+        }
+      }
+      if (!ok)  // gave up: what was issued has landed before the CTA ends
+        for (int j = i > kStages ? i - kStages : 0; j < i; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1, p.common, kSiteDrain);
+    }
+    __syncwarp();
+    if (!Down)
+      for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) token_gates(p, tb, tok, lane);
+    return;
   }
-  p.out[static_cast<size_t>(t) * p.H + c] = out;
+
+  // -------------------------------------------------------------- products
+  const int g = lane >> 2, t = lane & 3;
+  if (Down) grid_dep_wait();  // h is written
+  if (!Down && blockIdx.x == 0 && p.experts_out)
+    for (int a = threadIdx.x; a < p.T * p.topk; a += kMmaThreads) p.experts_out[a] = tb.expert[a];
+  int item = item0, col = col0, k = k0;
+  float acc[2][NT][4];
+  uint4 xv[kParts][NT][2];  // this thread's part of the left operand for the next unit
+  int rows = 0, row0 = 0;
+  const __nv_bfloat16* src[NT];
+  auto new_tile = [&]() {
+    row0 = tb.item_row[item];
+    const int end = tb.start[tb.item_expert[item] + 1];
+    rows = end - row0 < 8 * NT ? end - row0 : 8 * NT;
+#pragma unroll
+    for (int b = 0; b < NT; ++b) {
+      src[b] = nullptr;
+      if (8 * b + g < rows) {
+        const int r = row0 + 8 * b + g;
+        src[b] = Down ? p.h + static_cast<size_t>(r) * p.F : p.x + static_cast<size_t>(tb.order[r] / p.topk) * p.H;
+      }
+    }
+  };
+  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  auto load_x = [&]() {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
+          const int at = k * 64 + 32 * w + 8 * t;
+          if (8 * b < rows && src[b] && at < K)
+            xv[q][b][w] = Down ? ld_global128(src[b] + q * plane + at) : __ldg(reinterpret_cast<const uint4*>(src[b] + at));
+        }
+  };
+  if (n) {
+    new_tile();
+    load_x();
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
+  // ldmatrix rows: lane l gives row l & 7 of matrix l >> 3; matrices 0, 1: k pairs 2s, columns 0-7 and
+  // 8-15; matrices 2, 3: k pairs 2s + 1
+  const int lt = (lane & 7) >> 1, lbit = lane & 1, lhi = lane >> 4, lcol = (lane >> 3) & 1;
+  int seg0 = k0;  // first unit of the current tile that is this CTA's
+  bool ok = true;
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kStages;
+    if (ok) ok = mbar_wait(&full[s], (i / kStages) & 1, p.common, kSiteFull);  // after a timeout: on, without waits
+    const uint32_t w = smem_u32(ring + s * kUnitBytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t xr[kParts][NT][4];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) rotate_pairs(xv[q][b][h], t, xr[q][b]);
+#pragma unroll
+      for (int s2 = 0; s2 < 2; ++s2) {
+        const int kr = 32 * h + 8 * lt + 2 * ((2 * s2 + lhi + lt) & 3) + lbit;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          // first product: m = gate, up, columns 16 warp of each; second: columns 32 warp + 16 m
+          const int chunk = (Down ? 4 * (warp & 1) + 2 * m : 2 * warp) + lcol;
+          const uint32_t box = w + (Down ? (warp >> 1) : m) * (kUnitBytes / 2);
+          uint32_t a[4];
+          ldsm4t(a, box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+            if (8 * b < rows)
+#pragma unroll
+              for (int q = 0; q < kParts; ++q) mma16816<__nv_bfloat16>(acc[m][b], a, xr[q][b][2 * s2], xr[q][b][2 * s2 + 1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    const int this_k = k, this_col = col, this_rows = rows, this_row0 = row0;
+    if (++k == nk) {
+      k = 0;
+      next_tile(item, col);
+    }
+    if (i + 1 < n) {
+      if (k == 0) new_tile();
+      load_x();
+    }
+    if (this_k + 1 != nk && i + 1 != n) continue;
+
+    // ------------------------------------------------------------ the end of a tile, or of the CTA's part of it
+    const uint32_t tile = (first + i) / nk;
+    bool mine = true;
+    if (seg0 != 0 || this_k + 1 != nk) {
+      const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
+      constexpr int kSlot = kMmaThreads * 8 * NT;
+      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg0 ? 0 : 1)) * kSlot + threadIdx.x * 4;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+          if (8 * b < this_rows)
+            *reinterpret_cast<float4*>(part + (m * NT + b) * kMmaThreads * 4) =
+                make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
+      named_bar_sync(1, kMmaThreads);
+      if (threadIdx.x == 0) {
+        __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
+        const unsigned done = atomicAdd(p.cut_ctr + c0, 1u) + 1u;
+        tb.last = done == c1 - c0 + 1;
+        if (tb.last) p.cut_ctr[c0] = 0u;
+        __threadfence();
+      }
+      named_bar_sync(1, kMmaThreads);
+      mine = tb.last != 0;
+      if (mine) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+            if (8 * b < this_rows) {
+              float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+              for (uint32_t c = c0; c <= c1; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                    p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kSlot + (m * NT + b) * kMmaThreads * 4 + threadIdx.x * 4));
+                sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+              }
+              acc[m][b][0] = sum.x;
+              acc[m][b][1] = sum.y;
+              acc[m][b][2] = sum.z;
+              acc[m][b][3] = sum.w;
+            }
+      }
+    }
+    if (mine) {
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 8 * b + 2 * t + (j & 1);  // columns of the products are rows of the item
+          if (r >= this_rows) continue;
+          if constexpr (!Down) {
+            const int f = this_col * 64 + warp * 16 + g + 8 * (j >> 1);
+            if (f < N) {
+              const float a = acc[0][b][j], v = a / (1.f + expf(-a)) * acc[1][b][j];
+              const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
+              const float r1 = v - __bfloat162float(h0);
+              const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
+              const size_t at = static_cast<size_t>(this_row0 + r) * p.F + f;
+              p.h[at] = h0;
+              p.h[plane + at] = h1;
+              p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+            }
+          } else {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const int c = this_col * 128 + warp * 32 + m * 16 + g + 8 * (j >> 1);
+              if (c < N) p.y[static_cast<size_t>(this_row0 + r) * p.H + c] = acc[m][b][j];
+            }
+          }
+        }
+      if constexpr (Down) {
+        // the block's last item combines its rows
+        named_bar_sync(1, kMmaThreads);
+        if (threadIdx.x == 0) {
+          __threadfence();
+          const unsigned done = atomicAdd(p.col_ctr + this_col, 1u) + 1u;
+          tb.last = done == static_cast<unsigned>(tb.items);
+          if (tb.last) p.col_ctr[this_col] = 0u;
+          __threadfence();
+        }
+        named_bar_sync(1, kMmaThreads);
+        if (tb.last) {
+          for (int v = threadIdx.x; v < p.T * 32; v += kMmaThreads) {
+            const int tok = v >> 5, c = this_col * 128 + (v & 31) * 4;
+            if (c >= N) continue;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.topk; ++j) {
+              const int a = tok * p.topk + j;
+              const float gate = __ldcg(p.gates + a);
+              const float4 u = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[a]) * p.H + c));
+              sum = make_float4(sum.x + gate * u.x, sum.y + gate * u.y, sum.z + gate * u.z, sum.w + gate * u.w);
+            }
+            *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+          }
+        }
+      }
+    }
+    seg0 = 0;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
+  }
 }
 
 }  // namespace tl
@@ -135,13 +484,52 @@ using namespace tl;
 
 static bool moet_shape_ok(int T, int H, int E, int F, int topk) {
   return T >= 1 && T <= moet::kMaxT && topk >= 1 && topk <= moet::kMaxTopk && E >= topk && E <= moet::kMaxE && H > 0 &&
-         F > 0 && H % 8 == 0 && F % 8 == 0 && H <= (1 << 20) && F <= (1 << 20);
+         F > 0 && H % 8 == 0 && F % 8 == 0 && H <= 32768 && F <= 32768;
+}
+
+// Tokens in an item, in eights: an expert with more of them is read again (from L2).  Most experts have
+// one or two tokens whatever T; the sums of 32 tokens are what the registers hold.
+static int moet_eights(int T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+
+struct MoetLayout {
+  size_t gates, h, y, part, total;
+};
+static MoetLayout moet_layout(int T, int H, int F, int topk) {
+  const size_t a = static_cast<size_t>(T) * topk;
+  MoetLayout L;
+  L.gates = kCounterBytes;
+  L.h = L.gates + align256(a * 4);
+  L.y = L.h + align256(3 * a * F * 2);
+  L.part = L.y + align256(a * H * 4);
+  L.total = L.part + static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kMmaThreads * 8 * moet_eights(T) * 4;
+  return L;
 }
 
 extern "C" size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int topk) {
   if (!moet_shape_ok(T, H, E, F, topk)) return 0;
-  const size_t a = static_cast<size_t>(T) * topk;
-  return 2 * align256(a * 4) + align256(a * F * 4);
+  return moet_layout(T, H, F, topk).total;
+}
+
+template <bool Down, int NT>
+static int moet_launch(tl_ctx* ctx, const MoeTokParams& p, cudaStream_t st) {
+  auto kern = moet_kernel<Down, NT>;
+  static std::atomic<unsigned long long> ready{0};
+  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), moet::kSmem)) return TL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctx->ctas < moet::kMaxCtas ? ctx->ctas : moet::kMaxCtas, 1, 1);
+  cfg.blockDim = dim3(moet::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = moet::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = Down ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return TL_ERR_CUDA;
+  }
+  return TL_OK;
 }
 
 extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, const void* w_gate,
@@ -152,22 +540,31 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   for (const void* q : {x, static_cast<const void*>(logits), w_gate, w_up, w_down, static_cast<const void*>(out),
                         static_cast<const void*>(workspace)})
     if (!aligned16(q)) return TL_ERR_INVALID;
-  if (workspace_bytes < tl_moe_tokens_workspace_bytes(T, H, E, F, topk)) return TL_ERR_WORKSPACE;
+  const MoetLayout L = moet_layout(T, H, F, topk);
+  if (workspace_bytes < L.total) return TL_ERR_WORKSPACE;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
-  const size_t a = static_cast<size_t>(T) * topk;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeTokParams p;
+  std::memset(&p, 0, sizeof(p));
+  CUtensorMap down;
+  const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!tmap_3d(&p.w0, BF, 2, w_gate, F, H, E, 64, 64, 1) || !tmap_3d(&p.w1, BF, 2, w_up, F, H, E, 64, 64, 1) ||
+      !tmap_3d(&down, BF, 2, w_down, H, F, E, 64, 64, 1))
+    return TL_ERR_CUDA;
+  p.common = make_common(ctx);
+  p.common.trace_hdr = nullptr;  // these kernels record no trace spans
+  p.common.trace = nullptr;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.logits = logits;
-  p.w_gate = static_cast<const __nv_bfloat16*>(w_gate);
-  p.w_up = static_cast<const __nv_bfloat16*>(w_up);
-  p.w_down = static_cast<const __nv_bfloat16*>(w_down);
   p.out = out;
   p.experts_out = experts_out;
   p.gates_out = gates_out;
-  p.experts = reinterpret_cast<int*>(ws);
-  p.gates = reinterpret_cast<float*>(ws + align256(a * 4));
-  p.h = reinterpret_cast<float*>(ws + 2 * align256(a * 4));
+  p.cut_ctr = reinterpret_cast<unsigned*>(ws);
+  p.col_ctr = reinterpret_cast<unsigned*>(ws) + kCutCounters;
+  p.gates = reinterpret_cast<float*>(ws + L.gates);
+  p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  p.y = reinterpret_cast<float*>(ws + L.y);
+  p.part = reinterpret_cast<float*>(ws + L.part);
   p.T = T;
   p.H = H;
   p.E = E;
@@ -175,8 +572,15 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   p.topk = topk;
   p.renorm = ctx->cfg.moe_renorm;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  moet_route_kernel<<<(T + 3) / 4, 128, 0, st>>>(p);
-  moet_up_kernel<<<dim3((F + 63) / 64, T * topk), 64, 0, st>>>(p);
-  moet_down_kernel<<<dim3((H + 63) / 64, T), 64, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ERR_CUDA;
+  auto both = [&](auto nt) {
+    const int rc = moet_launch<false, decltype(nt)::value>(ctx, p, st);
+    if (rc != TL_OK) return rc;
+    p.w0 = down;
+    return moet_launch<true, decltype(nt)::value>(ctx, p, st);
+  };
+  switch (moet_eights(T)) {
+    case 1: return both(std::integral_constant<int, 1>{});
+    case 2: return both(std::integral_constant<int, 2>{});
+    default: return both(std::integral_constant<int, 4>{});
+  }
 }

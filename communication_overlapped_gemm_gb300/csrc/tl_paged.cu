@@ -116,7 +116,7 @@ struct Shape {
 };
 }  // namespace paged
 
-constexpr int kPagedMaxCtas = 640;
+constexpr int kPagedMaxCtas = kCutCounters;
 
 struct PagedParams {
   CacheArgs c;
@@ -128,7 +128,7 @@ struct PagedParams {
   const int* table;
   const int* lengths;
   float* part;        // [CTA][2][rows][D + 2]: O, m, l of a segment
-  unsigned* counter;  // [item]: segments done
+  unsigned* counter;  // [CTA]: segments done of the split item that starts in this one
   int max_pages, batch, heads, group, blocks;  // blocks: items per kv head
   uint32_t div_mul, div_shift;  // row / page_size
   float sl2;          // scale * log2(e)
@@ -174,14 +174,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -191,16 +183,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
-}
-// d += a b: 16 x 8 x 16, fp32 sums.
-template <class T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Four e4m3 values as two pairs of fp16, exactly.
 __device__ __forceinline__ void widen_e4m3(uint32_t v, uint32_t& lo, uint32_t& hi) {
@@ -637,7 +619,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       __syncthreads();
       if (threadIdx.x == 0) {
         __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
-        unsigned* ctr = p.counter + static_cast<size_t>(at.b) * subs + at.sub;
+        unsigned* ctr = p.counter + c0;
         const unsigned done = atomicAdd(ctr, 1u) + 1u;
         s_last = done == static_cast<unsigned>(c1 - c0 + 1);
         if (s_last) *ctr = 0u;
@@ -799,16 +781,15 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
   });
 }
 
-// Workspace: the parts of split items (two per CTA of the largest grid), then one counter per item.
+// Workspace: the counters, then the parts of split items (two per CTA of the largest grid).
 static int paged_rows(int heads, int kv_heads) { return heads / kv_heads > 8 ? 16 : 8; }  // query heads of an item
 static int paged_blocks(int heads, int kv_heads) {
   return (heads / kv_heads + paged_rows(heads, kv_heads) - 1) / paged_rows(heads, kv_heads);
 }
-static size_t paged_part_bytes(int d) { return align256(static_cast<size_t>(kPagedMaxCtas) * 2 * paged::kMaxRows * (d + 2) * 4); }
 
 extern "C" size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d) {
   if (batch < 0 || batch > 4096 || !heads_ok(heads, kv_heads, d)) return 0;
-  return paged_part_bytes(d) + align256(static_cast<size_t>(batch) * kv_heads * paged_blocks(heads, kv_heads) * 4 + 4);
+  return kCounterBytes + static_cast<size_t>(kPagedMaxCtas) * 2 * paged_rows(heads, kv_heads) * (d + 2) * 4;
 }
 
 extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* q,
@@ -847,8 +828,8 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   p.heads = heads;
   p.group = heads / cache->kv_heads;
   p.blocks = paged_blocks(heads, cache->kv_heads);
-  p.part = static_cast<float*>(workspace);
-  p.counter = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + paged_part_bytes(cache->d));
+  p.counter = static_cast<unsigned*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
   p.sl2 = scale * kLog2E;
   p.window = window;
   p.sinks = sinks;

@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "tl_host.h"
 
@@ -43,6 +44,25 @@ __device__ __forceinline__ uint32_t from_f32x2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// d += a b: 16 x 8 x 16, fp32 sums.
+template <class T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Lets a kernel use `bytes` of dynamic shared memory, once per device (a bit of `ready` each).
 inline bool smem_ready(std::atomic<unsigned long long>& ready, int device, const void* kern, int bytes) {
   const unsigned long long bit = 1ull << (device & 63);
@@ -54,6 +74,13 @@ inline bool smem_ready(std::atomic<unsigned long long>& ready, int device, const
   ready.fetch_or(device < 64 ? bit : 0, std::memory_order_release);
   return true;
 }
+
+// The first 8 KB of a serving operator's workspace: counters that every call leaves at zero, whatever its
+// shape.  A CTA's range of work starts at most one piece that goes on in other CTAs, so the counter
+// of a cut piece is that of the CTA it starts in.
+constexpr int kCutCounters = 1024;  // by CTA: the largest grid
+constexpr int kColCounters = 1024;
+constexpr size_t kCounterBytes = (kCutCounters + kColCounters) * 4;
 
 inline bool esize_ok(long long stride, int esize) { return stride >= 0 && (stride * esize) % 16 == 0; }
 

@@ -415,7 +415,10 @@ int tl_ag_gemm_static_scratch(tl_ctx* ctx, int W, int rank, const void* const* a
  * passed as it is.
  * Indices read on the device (slots, page numbers, lengths) are checked there: an entry out of
  * range is left out, nothing outside the buffers is read or written, and tl_ctx_check returns
- * TL_ERR_INDEX.  These four entry points wait on nothing and can be captured into a graph.
+ * TL_ERR_INDEX.  No CTA of these four entry points waits for another; all can be captured into a graph.
+ * Workspaces: the first 8 KB hold counters that each call leaves at zero again.  So one workspace,
+ * zero-filled once, serves calls of tl_paged_attention and tl_moe_tokens of any shapes, in order; after
+ * another operator used it, its first 8 KB have to be zero-filled again.
  */
 #define TL_BF16 0
 #define TL_FP16 1
@@ -465,8 +468,8 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * overlap q).  cache: dtype or TL_E4M3.  page_table: int32 [batch x max_pages], dense; only the entries
  * of visible rows are read.  lengths: int32 [batch]; a length over max_pages * page_size is cut to
  * that and reported, a page out of range is left out (its rows are not visible) and reported.
- * workspace: tl_paged_attention_workspace_bytes(): partial results of sequences split over several
- * CTAs, and one counter per sequence, kv head and group of 16 query heads.
+ * workspace: tl_paged_attention_workspace_bytes(): counters, and partial results of sequences split
+ * over several CTAs.
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
  * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
  * batch == 0 or heads == 0 is a no-op.
@@ -514,7 +517,7 @@ int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token
  * out: fp32 [T x H].  experts_out (int32 [T x topk]) and gates_out (fp32 [T x topk]) are optional: the
  * chosen experts, best first, and their gates.  NaN logits count as the lowest (the gates are NaN).
  * workspace: tl_moe_tokens_workspace_bytes().
- * Shapes: 1 <= T <= 128; 1 <= topk <= 8; topk <= E <= 256; H % 8 == 0; F % 8 == 0.
+ * Shapes: 1 <= T <= 128; 1 <= topk <= 8; topk <= E <= 256; H % 8 == 0; F % 8 == 0; H, F <= 32768.
  */
 size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int topk);
 int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, const void* w_gate, const void* w_up,
