@@ -8,9 +8,10 @@
 //
 // Each CTA (one per SM and kernel) works out the routing by itself, so nothing has to pass between
 // CTAs before the first load: the topk of every token, the assignments in the order (expert, t, j),
-// and the items: an expert with up to 8 NT of its assignments.  (item, 64 or 128 columns, 64 rows
+// and the items: an expert with up to 8 NT (8 or 16) of its assignments.  (item, 64 or 128 columns, 64 rows
 // of the weights) is a unit of 16 KB; all units form one line, cut into equal ranges, one per CTA:
-// even work for any routing.  One warp keeps a ring of TMA loads full, four warps multiply.
+// even work for any routing.  One warp keeps a ring of TMA loads full, two groups of four
+// warps multiply, a unit each in turn.
 //
 // The products run on mma.sync m16n8k16: columns of the weights are its 16 rows (transposed by ldmatrix from
 // the 128-byte-swizzled tile), the tokens its 8 columns, which wastes least for 1 to 8 tokens; a
@@ -32,11 +33,22 @@ namespace tl {
 
 namespace moet {
 constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk, kMaxCtas = 512;
-constexpr int kMmaWarps = 4, kMmaThreads = 32 * kMmaWarps, kThreads = kMmaThreads + 32;
-constexpr int kUnitBytes = 16384, kStages = 6;  // both kernels' rings fit in one SM together
-constexpr int kTileOff = 0;
-constexpr int kBarOff = kStages * kUnitBytes;
-constexpr int kSmem = kBarOff + 2 * kStages * 8 + 1024;  // 1024: the ring's alignment
+// Two groups of four warps take every other unit: one group's loads of x and products hide the other's.
+constexpr int kGroup = 128, kThreads = 2 * kGroup + 32;
+constexpr int kUnitBytes = 16384;
+// Stages: an even number, so that a stage always serves the same group.  (With an odd one, a group could
+// be a whole ring ahead of a load that the other one still waits for, and take the barrier's
+// phase before it for its own.)  For up to 8 tokens the second product's CTAs fit beside the first's
+// (registers too) with four.
+template <bool Down, int NT>
+struct Ring {
+  static constexpr int kStages = Down && NT == 1 ? 4 : 6;
+  static_assert(kStages % 2 == 0, "a stage belongs to one group");
+  static constexpr int kBarOff = kStages * kUnitBytes;
+  static constexpr int kHandOff = kBarOff + 128;  // group 1's sums: [2][8 NT][128 threads] floats
+  static_assert(2 * kStages * 8 <= 128, "barriers");
+  static constexpr int kSmem = kHandOff + 2 * kGroup * 8 * NT * 4 + 1024;  // 1024: the ring's alignment
+};
 }  // namespace moet
 
 struct MoeTokParams {
@@ -50,7 +62,7 @@ struct MoeTokParams {
   float* gates_out;
   __nv_bfloat16* h;    // [3][T topk][F]: h = h0 + h1 + h2, rows in the order (expert, t, j)
   float* y;            // [T topk][H]
-  float* part;         // [CTA][2][128 threads][8 NT] sums of a cut tile
+  float* part;         // [CTA][2][8 NT][128 threads] sums of a cut tile
   float* gates;        // [T topk]
   unsigned* cut_ctr;   // [CTA]: CTAs done with the cut tile that starts in this one
   unsigned* col_ctr;   // [column block]: items done (second product)
@@ -207,18 +219,20 @@ __device__ __forceinline__ void token_gates(const MoeTokParams& p, const MoeTabl
 template <bool Down, int NT>
 __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_constant__ MoeTokParams p) {
   using namespace moet;
+  using R = Ring<Down, NT>;
+  constexpr int kStages = R::kStages;
   constexpr int kParts = Down ? 3 : 1;            // 16-bit terms of the left operand
   constexpr int kCols = Down ? 128 : 64;          // columns of a tile
   extern __shared__ uint8_t smem_raw[];
   __shared__ MoeTables tb;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kBarOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + R::kBarOff);
   uint64_t* empty = full + kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kMmaWarps);
+      mbar_init(&empty[s], 4);  // the warps of one group
     }
     fence_mbar_init();
     tma_prefetch_map(&p.w0);
@@ -248,7 +262,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
     }
   };
 
-  if (warp == kMmaWarps) {
+  if (warp == 2 * kGroup / 32) {
     // ------------------------------------------------------------ loads (they wait for no other kernel)
     if (lane == 0) {
       int item = item0, col = col0, k = k0, i = 0;
@@ -277,29 +291,41 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   }
 
   // -------------------------------------------------------------- products
-  const int g = lane >> 2, t = lane & 3;
+  const int grp = warp >> 2, wq = warp & 3, tid = threadIdx.x & (kGroup - 1), g = lane >> 2, t = lane & 3;
   if (Down) grid_dep_wait();  // h is written
   if (!Down && blockIdx.x == 0 && p.experts_out)
-    for (int a = threadIdx.x; a < p.T * p.topk; a += kMmaThreads) p.experts_out[a] = tb.expert[a];
-  int item = item0, col = col0, k = k0;
-  float acc[2][NT][4];
-  uint4 xv[kParts][NT][2];  // this thread's part of the left operand for the next unit
-  int rows = 0, row0 = 0;
-  const __nv_bfloat16* src[NT];
-  auto new_tile = [&]() {
+    for (int a = threadIdx.x; a < p.T * p.topk; a += 2 * kGroup) p.experts_out[a] = tb.expert[a];
+  // the rows of an item
+  auto item_rows = [&](int item, int& row0) {
     row0 = tb.item_row[item];
     const int end = tb.start[tb.item_expert[item] + 1];
-    rows = end - row0 < 8 * NT ? end - row0 : 8 * NT;
+    return end - row0 < 8 * NT ? end - row0 : 8 * NT;
+  };
+  // this thread's part of the left operand for the next unit of its group, loaded a unit ahead
+  int x_item = item0, x_col = col0, x_k = k0, x_rows = 0;
+  uint4 xv[kParts][NT][2];
+  const __nv_bfloat16* src[NT];
+  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  auto x_tile = [&]() {
+    int row0;
+    x_rows = item_rows(x_item, row0);
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
       src[b] = nullptr;
-      if (8 * b + g < rows) {
+      if (8 * b + g < x_rows) {
         const int r = row0 + 8 * b + g;
         src[b] = Down ? p.h + static_cast<size_t>(r) * p.F : p.x + static_cast<size_t>(tb.order[r] / p.topk) * p.H;
       }
     }
   };
-  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  auto x_step = [&]() {
+    if (++x_k == nk) {
+      x_k = 0;
+      next_tile(x_item, x_col);
+      return true;
+    }
+    return false;
+  };
   auto load_x = [&]() {
 #pragma unroll
     for (int q = 0; q < kParts; ++q)
@@ -308,173 +334,196 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
-          const int at = k * 64 + 32 * w + 8 * t;
-          if (8 * b < rows && src[b] && at < K)
+          const int at = x_k * 64 + 32 * w + 8 * t;
+          if (8 * b < x_rows && src[b] && at < K)
             xv[q][b][w] = Down ? ld_global128(src[b] + q * plane + at) : __ldg(reinterpret_cast<const uint4*>(src[b] + at));
         }
   };
-  if (n) {
-    new_tile();
+  if (grp && n > 1) x_step();
+  if (grp < n) {
+    x_tile();
     load_x();
   }
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
   // ldmatrix rows: lane l gives row l & 7 of matrix l >> 3; matrices 0, 1: k pairs 2s, columns 0-7 and
   // 8-15; matrices 2, 3: k pairs 2s + 1
   const int lt = (lane & 7) >> 1, lbit = lane & 1, lhi = lane >> 4, lcol = (lane >> 3) & 1;
-  int seg0 = k0;  // first unit of the current tile that is this CTA's
+  float* hand = reinterpret_cast<float*>(ring + R::kHandOff) + tid * 4;
+  float acc[2][NT][4];
   bool ok = true;
-  for (int i = 0; i < n; ++i) {
-    const int s = i % kStages;
-    if (ok) ok = mbar_wait(&full[s], (i / kStages) & 1, p.common, kSiteFull);  // after a timeout: on, without waits
-    const uint32_t w = smem_u32(ring + s * kUnitBytes);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t xr[kParts][NT][4];
-#pragma unroll
-      for (int q = 0; q < kParts; ++q)
-#pragma unroll
-        for (int b = 0; b < NT; ++b) rotate_pairs(xv[q][b][h], t, xr[q][b]);
-#pragma unroll
-      for (int s2 = 0; s2 < 2; ++s2) {
-        const int kr = 32 * h + 8 * lt + 2 * ((2 * s2 + lhi + lt) & 3) + lbit;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          // first product: m = gate, up, columns 16 warp of each; second: columns 32 warp + 16 m
-          const int chunk = (Down ? 4 * (warp & 1) + 2 * m : 2 * warp) + lcol;
-          const uint32_t box = w + (Down ? (warp >> 1) : m) * (kUnitBytes / 2);
-          uint32_t a[4];
-          ldsm4t(a, box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
-            if (8 * b < rows)
-#pragma unroll
-              for (int q = 0; q < kParts; ++q) mma16816<__nv_bfloat16>(acc[m][b], a, xr[q][b][2 * s2], xr[q][b][2 * s2 + 1]);
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-    const int this_k = k, this_col = col, this_rows = rows, this_row0 = row0;
-    if (++k == nk) {
-      k = 0;
-      next_tile(item, col);
-    }
-    if (i + 1 < n) {
-      if (k == 0) new_tile();
-      load_x();
-    }
-    if (this_k + 1 != nk && i + 1 != n) continue;
-
-    // ------------------------------------------------------------ the end of a tile, or of the CTA's part of it
-    const uint32_t tile = (first + i) / nk;
-    bool mine = true;
-    if (seg0 != 0 || this_k + 1 != nk) {
-      const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
-      constexpr int kSlot = kMmaThreads * 8 * NT;
-      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg0 ? 0 : 1)) * kSlot + threadIdx.x * 4;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int b = 0; b < NT; ++b)
-          if (8 * b < this_rows)
-            *reinterpret_cast<float4*>(part + (m * NT + b) * kMmaThreads * 4) =
-                make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
-      named_bar_sync(1, kMmaThreads);
-      if (threadIdx.x == 0) {
-        __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
-        const unsigned done = atomicAdd(p.cut_ctr + c0, 1u) + 1u;
-        tb.last = done == c1 - c0 + 1;
-        if (tb.last) p.cut_ctr[c0] = 0u;
-        __threadfence();
-      }
-      named_bar_sync(1, kMmaThreads);
-      mine = tb.last != 0;
-      if (mine) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
-            if (8 * b < this_rows) {
-              float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-              for (uint32_t c = c0; c <= c1; ++c) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kSlot + (m * NT + b) * kMmaThreads * 4 + threadIdx.x * 4));
-                sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
-              }
-              acc[m][b][0] = sum.x;
-              acc[m][b][1] = sum.y;
-              acc[m][b][2] = sum.z;
-              acc[m][b][3] = sum.w;
-            }
-      }
-    }
-    if (mine) {
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 8 * b + 2 * t + (j & 1);  // columns of the products are rows of the item
-          if (r >= this_rows) continue;
-          if constexpr (!Down) {
-            const int f = this_col * 64 + warp * 16 + g + 8 * (j >> 1);
-            if (f < N) {
-              const float a = acc[0][b][j], v = a / (1.f + expf(-a)) * acc[1][b][j];
-              const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
-              const float r1 = v - __bfloat162float(h0);
-              const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
-              const size_t at = static_cast<size_t>(this_row0 + r) * p.F + f;
-              p.h[at] = h0;
-              p.h[plane + at] = h1;
-              p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
-            }
-          } else {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const int c = this_col * 128 + warp * 32 + m * 16 + g + 8 * (j >> 1);
-              if (c < N) p.y[static_cast<size_t>(this_row0 + r) * p.H + c] = acc[m][b][j];
-            }
-          }
-        }
-      if constexpr (Down) {
-        // the block's last item combines its rows
-        named_bar_sync(1, kMmaThreads);
-        if (threadIdx.x == 0) {
-          __threadfence();
-          const unsigned done = atomicAdd(p.col_ctr + this_col, 1u) + 1u;
-          tb.last = done == static_cast<unsigned>(tb.items);
-          if (tb.last) p.col_ctr[this_col] = 0u;
-          __threadfence();
-        }
-        named_bar_sync(1, kMmaThreads);
-        if (tb.last) {
-          for (int v = threadIdx.x; v < p.T * 32; v += kMmaThreads) {
-            const int tok = v >> 5, c = this_col * 128 + (v & 31) * 4;
-            if (c >= N) continue;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < p.topk; ++j) {
-              const int a = tok * p.topk + j;
-              const float gate = __ldcg(p.gates + a);
-              const float4 u = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[a]) * p.H + c));
-              sum = make_float4(sum.x + gate * u.x, sum.y + gate * u.y, sum.z + gate * u.z, sum.w + gate * u.w);
-            }
-            *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
-          }
-        }
-      }
-    }
-    seg0 = 0;
+  int item = item0, col = col0;
+  for (int begin = 0, seg = 0; begin < n; ++seg) {
+    // this CTA's units [begin, end) of one tile
+    const uint32_t tile = (first + begin) / nk;
+    const int left = static_cast<int>((tile + 1) * nk - (first + begin));
+    const int end = left < n - begin ? begin + left : n;
+    int row0;
+    const int rows = item_rows(item, row0);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
+    for (int i = begin + ((begin ^ grp) & 1); i < end; i += 2) {
+      uint32_t xr[2][kParts][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int b = 0; b < NT; ++b) rotate_pairs(xv[q][b][h], t, xr[h][q][b]);
+      if (i + 2 < n) {
+        const bool one = x_step(), two = x_step();
+        if (one || two) x_tile();
+        load_x();
+      }
+      const int s = i % kStages;
+      if (ok) ok = mbar_wait(&full[s], (i / kStages) & 1, p.common, kSiteFull);  // after a timeout: on, without waits
+      const uint32_t w = smem_u32(ring + s * kUnitBytes);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2) {
+          const int kr = 32 * h + 8 * lt + 2 * ((2 * s2 + lhi + lt) & 3) + lbit;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            // first product: m = gate, up, columns 16 wq of each; second: columns 32 wq + 16 m
+            const int chunk = (Down ? 4 * (wq & 1) + 2 * m : 2 * wq) + lcol;
+            const uint32_t box = w + (Down ? (wq >> 1) : m) * (kUnitBytes / 2);
+            uint32_t a[4];
+            ldsm4t(a, box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+              if (8 * b < rows)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q)
+                  mma16816<__nv_bfloat16>(acc[m][b], a, xr[h][q][b][2 * s2], xr[h][q][b][2 * s2 + 1]);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ------------------------------------------------------------ the end of a tile, or of the CTA's part of it
+    // Group 1 hands its sums over (two buffers: it cannot pass the next barrier before group 0 has read
+    // these) and goes on with the next tile; group 0 adds and finishes.
+    const int this_col = col;
+    const uint32_t seg_first = first + begin;
+    begin = end;
+    next_tile(item, col);
+    float* buf = hand + (seg & 1) * kGroup * 8 * NT;
+    if (grp) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+          if (8 * b < rows)
+            *reinterpret_cast<float4*>(buf + (m * NT + b) * kGroup * 4) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
+    }
+    named_bar_sync(1, 2 * kGroup);
+    if (grp) continue;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+        if (8 * b < rows) {
+          const float4 v = *reinterpret_cast<const float4*>(buf + (m * NT + b) * kGroup * 4);
+          acc[m][b][0] += v.x;
+          acc[m][b][1] += v.y;
+          acc[m][b][2] += v.z;
+          acc[m][b][3] += v.w;
+        }
+    const bool starts = seg_first == tile * nk, ends = first + end == (tile + 1) * nk;
+    if (!starts || !ends) {
+      const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
+      constexpr int kSlot = kGroup * 8 * NT;
+      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * kSlot + tid * 4;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+          if (8 * b < rows)
+            *reinterpret_cast<float4*>(part + (m * NT + b) * kGroup * 4) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
+      named_bar_sync(2, kGroup);
+      if (tid == 0) {
+        __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
+        const unsigned done = atomicAdd(p.cut_ctr + c0, 1u) + 1u;
+        tb.last = done == c1 - c0 + 1;
+        if (tb.last) p.cut_ctr[c0] = 0u;
+        __threadfence();
+      }
+      named_bar_sync(2, kGroup);
+      if (!tb.last) continue;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+          if (8 * b < rows) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (uint32_t c = c0; c <= c1; ++c) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                  p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kSlot + (m * NT + b) * kGroup * 4 + tid * 4));
+              sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+            }
+            acc[m][b][0] = sum.x;
+            acc[m][b][1] = sum.y;
+            acc[m][b][2] = sum.z;
+            acc[m][b][3] = sum.w;
+          }
+    }
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 8 * b + 2 * t + (j & 1);  // columns of the products are rows of the item
+        if (r >= rows) continue;
+        if constexpr (!Down) {
+          const int f = this_col * 64 + wq * 16 + g + 8 * (j >> 1);
+          if (f < N) {
+            const float a = acc[0][b][j], v = a / (1.f + expf(-a)) * acc[1][b][j];
+            const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
+            const float r1 = v - __bfloat162float(h0);
+            const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
+            const size_t at = static_cast<size_t>(row0 + r) * p.F + f;
+            p.h[at] = h0;
+            p.h[plane + at] = h1;
+            p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int c = this_col * 128 + wq * 32 + m * 16 + g + 8 * (j >> 1);
+            if (c < N) p.y[static_cast<size_t>(row0 + r) * p.H + c] = acc[m][b][j];
+          }
+        }
+      }
+    if constexpr (Down) {
+      // the block's last item combines its rows
+      named_bar_sync(2, kGroup);
+      if (tid == 0) {
+        __threadfence();
+        const unsigned done = atomicAdd(p.col_ctr + this_col, 1u) + 1u;
+        tb.last = done == static_cast<unsigned>(tb.items);
+        if (tb.last) p.col_ctr[this_col] = 0u;
+        __threadfence();
+      }
+      named_bar_sync(2, kGroup);
+      if (tb.last) {
+        for (int v = tid; v < p.T * 32; v += kGroup) {
+          const int tok = v >> 5, c = this_col * 128 + (v & 31) * 4;
+          if (c >= N) continue;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int j = 0; j < p.topk; ++j) {
+            const int a = tok * p.topk + j;
+            const float gate = __ldcg(p.gates + a);
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[a]) * p.H + c));
+            sum = make_float4(sum.x + gate * u.x, sum.y + gate * u.y, sum.z + gate * u.z, sum.w + gate * u.w);
+          }
+          *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+        }
+      }
+    }
   }
 }
 
@@ -487,9 +536,9 @@ static bool moet_shape_ok(int T, int H, int E, int F, int topk) {
          F > 0 && H % 8 == 0 && F % 8 == 0 && H <= 32768 && F <= 32768;
 }
 
-// Tokens in an item, in eights: an expert with more of them is read again (from L2).  Most experts have
-// one or two tokens whatever T; the sums of 32 tokens are what the registers hold.
-static int moet_eights(int T) { return T <= 8 ? 1 : T <= 16 ? 2 : 4; }
+// Tokens in an item, in eights: an expert with more of them is read again, from L2.  Most experts have
+// one or two tokens whatever T, and 16 tokens' operands are what the registers hold twice.
+static int moet_eights(int T) { return T <= 8 ? 1 : 2; }
 
 struct MoetLayout {
   size_t gates, h, y, part, total;
@@ -501,7 +550,7 @@ static MoetLayout moet_layout(int T, int H, int F, int topk) {
   L.h = L.gates + align256(a * 4);
   L.y = L.h + align256(3 * a * F * 2);
   L.part = L.y + align256(a * H * 4);
-  L.total = L.part + static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kMmaThreads * 8 * moet_eights(T) * 4;
+  L.total = L.part + static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 8 * moet_eights(T) * 4;
   return L;
 }
 
@@ -514,11 +563,11 @@ template <bool Down, int NT>
 static int moet_launch(tl_ctx* ctx, const MoeTokParams& p, cudaStream_t st) {
   auto kern = moet_kernel<Down, NT>;
   static std::atomic<unsigned long long> ready{0};
-  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), moet::kSmem)) return TL_ERR_CUDA;
+  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), moet::Ring<Down, NT>::kSmem)) return TL_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctx->ctas < moet::kMaxCtas ? ctx->ctas : moet::kMaxCtas, 1, 1);
   cfg.blockDim = dim3(moet::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = moet::kSmem;
+  cfg.dynamicSmemBytes = moet::Ring<Down, NT>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -578,9 +627,5 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
     p.w0 = down;
     return moet_launch<true, decltype(nt)::value>(ctx, p, st);
   };
-  switch (moet_eights(T)) {
-    case 1: return both(std::integral_constant<int, 1>{});
-    case 2: return both(std::integral_constant<int, 2>{});
-    default: return both(std::integral_constant<int, 4>{});
-  }
+  return moet_eights(T) == 1 ? both(std::integral_constant<int, 1>{}) : both(std::integral_constant<int, 2>{});
 }
