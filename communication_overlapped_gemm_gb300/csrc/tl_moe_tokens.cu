@@ -1,30 +1,33 @@
-// The MoE layer for the few tokens of a decoding step.
+// The MoE layer for the few tokens of a decoding step, in one launch.
 //
 //   h_a = SiLU(x_t Wg_e) * (x_t Wu_e),   out_t = sum_j gate_tj h_a Wd_e,   a = (t, j), e the expert of a
 // With a handful of tokens at each expert the weights are read once and meet one or two tokens, so
-// HBM bounds the layer: 6 H F bytes for each distinct expert, 6 H F flops for each assignment.  Two
-// launches, one per product; the second is a dependent launch whose CTAs fit beside the first's, so
-// its weights are already being loaded while the first ends.
+// HBM bounds the layer: 6 H F bytes for each distinct expert, 6 H F flops for each assignment.
 //
-// Each CTA (one per SM and kernel) works out the routing by itself, so nothing has to pass between
-// CTAs before the first load: the topk of every token, the assignments in the order (expert, t, j),
-// and the items: an expert with up to 8 NT (8 or 16) of its assignments.  (item, 64 or 128 columns, 64 rows
-// of the weights) is a unit of 16 KB; all units form one line, cut into equal ranges, one per CTA:
-// even work for any routing.  One warp keeps a ring of TMA loads full, two groups of four
-// warps multiply, a unit each in turn.
+// Each CTA (one per SM, a cooperative launch) works out the routing by itself, so nothing has to
+// pass between CTAs before the first load: the topk of every token, the assignments in the order
+// (expert, t, j), and the items: an expert with up to 8 NT (8 or 16) of its assignments.  (item, 64
+// columns of gate and up or 128 of down, 64 rows) is a unit of 16 KB; all units of a product form one
+// line, cut into equal ranges, one per CTA: even work for any routing.  A CTA takes its range of
+// the first product, then its range of the second.  One warp keeps a ring of TMA loads full across
+// both; two groups of four warps multiply, a unit each in turn.
 //
-// The products run on mma.sync m16n8k16: columns of the weights are its 16 rows (transposed by ldmatrix from
-// the 128-byte-swizzled tile), the tokens its 8 columns, which wastes least for 1 to 8 tokens; a
-// tcgen05 tile would be 128 rows of tokens.  The k order inside 32 rows is permuted so
-// that a thread's part of x is 16 contiguous bytes and ldmatrix rows fall in different banks: thread t
+// The second product of an item waits (bounded) until its h is complete.  No unit of the first waits
+// for anything, every CTA is resident, and both lines are item by item, so the h that a CTA needs comes
+// from itself and its neighbours; its weights are in the ring by then.
+//
+// The products run on mma.sync m16n8k16: columns of the weights are its 16 rows (transposed by
+// ldmatrix from the 128-byte-swizzled tile), the tokens its 8 columns, which wastes least for 1 to 8
+// tokens; a tcgen05 tile would be 128 rows of tokens.  The k order inside 32 rows is permuted so that
+// a thread's part of x is 16 contiguous bytes and ldmatrix rows fall in different banks: thread t
 // holds k = 8 t .. 8 t + 7 as four pairs, and pair (i + t) mod 4 is its i-th.
 // h goes to the second product as a sum of three bf16 (24 bits), three products for one load of
 // the weights, so the layer keeps fp32 precision between the two.
 //
 // Tiles whose units lie in several CTAs: each CTA stores its fp32 sums, and the one that finishes
-// last (a counter, left at zero again) adds them in the order of the line.  In the second product
-// the last item of a column block to finish combines the block's rows, sum over j in order.  The order of
-// every sum is fixed by the routing; nothing waits on another CTA.
+// last (a counter) adds them in the order of the line.  The last of a token's topk rows to be finished
+// in a block of 128 columns adds them up, in the order j = 0, 1, ...  So the order of every sum is
+// fixed by the routing.  Every counter is left at zero.
 #include <type_traits>
 
 #include "tl_serve.cuh"
@@ -38,22 +41,20 @@ constexpr int kGroup = 128, kThreads = 2 * kGroup + 32;
 constexpr int kUnitBytes = 16384;
 // Stages: an even number, so that a stage always serves the same group.  (With an odd one, a group could
 // be a whole ring ahead of a load that the other one still waits for, and take the barrier's
-// phase before it for its own.)  For up to 8 tokens the second product's CTAs fit beside the first's
-// (registers too) with four.
-template <bool Down, int NT>
+// phase before it for its own.)  192 KB in flight per SM: with 96 KB the loop ran at 0.7 of HBM.
+template <int NT>
 struct Ring {
-  static constexpr int kStages = Down && NT == 1 ? 4 : 6;
+  static constexpr int kStages = 12;
   static_assert(kStages % 2 == 0, "a stage belongs to one group");
   static constexpr int kBarOff = kStages * kUnitBytes;
-  static constexpr int kHandOff = kBarOff + 128;  // group 1's sums: [2][8 NT][128 threads] floats
-  static_assert(2 * kStages * 8 <= 128, "barriers");
+  static constexpr int kHandOff = kBarOff + 256;  // group 1's sums: [2][8 NT][128 threads] floats
+  static_assert(2 * kStages * 8 <= 256, "barriers");
   static constexpr int kSmem = kHandOff + 2 * kGroup * 8 * NT * 4 + 1024;  // 1024: the ring's alignment
 };
 }  // namespace moet
 
 struct MoeTokParams {
-  CUtensorMap w0;  // gate, or down: {columns, rows, E}, box {64, 64, 1}
-  CUtensorMap w1;  // up
+  CUtensorMap gate, up, down;  // {columns, rows, E}, box {64, 64, 1}
   Common common;
   const __nv_bfloat16* x;
   const float* logits;
@@ -63,22 +64,22 @@ struct MoeTokParams {
   __nv_bfloat16* h;    // [3][T topk][F]: h = h0 + h1 + h2, rows in the order (expert, t, j)
   float* y;            // [T topk][H]
   float* part;         // [CTA][2][8 NT][128 threads] sums of a cut tile
-  float* gates;        // [T topk]
   unsigned* cut_ctr;   // [CTA]: CTAs done with the cut tile that starts in this one
-  unsigned* col_ctr;   // [column block]: items done (second product)
+  unsigned* item_ctr;  // [item]: tiles done, of both products
+  unsigned* tok_ctr;   // [token][column block]: rows done
   int T, H, E, F, topk, renorm;
 };
 
 // What a CTA derives from the logits.
 struct MoeTables {
-  uint8_t expert[moet::kMaxA];   // of assignment a = t topk + j
+  alignas(16) uint8_t expert[moet::kMaxA];  // of assignment a = t topk + j
   uint16_t at[moet::kMaxA];      // row of assignment a
   uint16_t order[moet::kMaxA];   // assignment of a row
   uint16_t start[moet::kMaxE + 1];  // rows of expert e: [start[e], start[e + 1])
   uint16_t item_expert[moet::kMaxA];
   uint16_t item_row[moet::kMaxA];   // first row
   int items;
-  unsigned last;
+  uint32_t last;
 };
 
 // An order-preserving key of a logit; NaN is the lowest, as -inf.
@@ -87,46 +88,78 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One warp: the topk experts of a token, best first, ties to the lower index.  Lane l holds
-// experts l, l + 32, ...; key 0 marks "none" (below the key of -inf).
-__device__ __forceinline__ void route_token(const float* row, int E, int topk, int lane, uint8_t* experts) {
+// One warp: the topk experts of tokens t, t + step, .. (kBatch of them, below T), best first, ties to
+// the lower index.  Lane l holds experts l, l + 32, ...; key 0 marks "none" (below the key of -inf).
+// Several tokens at a time, because each is a chain of loads and reductions.
+template <int kBatch>
+__device__ __forceinline__ void route_tokens(const MoeTokParams& p, int t, int step, int lane, uint8_t* experts) {
   constexpr int kPer = moet::kMaxE / 32;
-  uint32_t key[kPer];
+  uint32_t key[kBatch][kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? logit_key(__ldg(row + lane + 32 * i)) : 0u;
-  for (int j = 0; j < topk; ++j) {
-    uint32_t best = 0u;
-    int at = 0;
+  for (int i = 0; i < kPer; ++i)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (32 * i < E && key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0xffffffffu);
+    for (int b = 0; b < kBatch; ++b) {
+      key[b][i] = 0u;
+      if (32 * i < p.E && lane + 32 * i < p.E && t + b * step < p.T)
+        key[b][i] = logit_key(__ldg(p.logits + static_cast<size_t>(t + b * step) * p.E + lane + 32 * i));
+    }
+  for (int j = 0; j < p.topk; ++j) {
+    uint32_t best[kBatch], e[kBatch];
+    int at[kBatch];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (static_cast<uint32_t>(lane + 32 * i) == e) key[i] = 0u;
-    if (lane == 0) experts[j] = static_cast<uint8_t>(e);
+    for (int b = 0; b < kBatch; ++b) {
+      best[b] = key[b][0];
+      at[b] = 0;
+    }
+#pragma unroll
+    for (int i = 1; i < kPer; ++i)
+      if (32 * i < p.E)
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (key[b][i] > best[b]) {
+            best[b] = key[b][i];
+            at[b] = i;
+          }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best[b]);
+      e[b] = __reduce_min_sync(0xffffffffu, best[b] == top ? lane + 32 * at[b] : 0xffffffffu);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (static_cast<uint32_t>(lane + 32 * i) == e[b]) key[b][i] = 0u;
+      if (lane == 0 && t + b * step < p.T) experts[(t + b * step) * p.topk + j] = static_cast<uint8_t>(e[b]);
+    }
   }
+}
+
+// Bytes of the 16 experts from assignment a0 on that are e, a bit each (bit 8 i of word w: a0 + 4 w + i).
+__device__ __forceinline__ uint32_t same_expert(uint32_t word, uint32_t e4, int left) {
+  const uint32_t eq = __vcmpeq4(word, e4) & 0x01010101u;
+  return left >= 4 ? eq : left <= 0 ? 0u : eq & ((1u << (8 * left)) - 1u);
 }
 
 // All threads of the CTA: routing, order and items (groups of `group` rows of an expert).
 __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb, int group) {
+  constexpr int kWarps = moet::kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.topk;
-  for (int t = warp; t < p.T; t += moet::kThreads / 32)
-    route_token(p.logits + static_cast<size_t>(t) * p.E, p.E, p.topk, lane, tb.expert + t * p.topk);
-  for (int a = n + static_cast<int>(threadIdx.x); a < ((n + 3) & ~3); a += moet::kThreads) tb.expert[a] = 0xff;  // never an assignment below
+  if (p.T <= kWarps) {
+    if (warp < p.T) route_tokens<1>(p, warp, kWarps, lane, tb.expert);
+  } else {
+    for (int t = warp; t < p.T; t += 4 * kWarps) route_tokens<4>(p, t, kWarps, lane, tb.expert);
+  }
   __syncthreads();
-  // counts, then rows, of the experts of this thread: a byte compare over all assignments.  (E = 256
-  // uses 0xff too, so entries past n are cut off by index.)
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(tb.expert);
+  // the count of each expert: a byte compare over all assignments, 16 at a time
+  const uint4* words = reinterpret_cast<const uint4*>(tb.expert);
   for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
+    const uint32_t e4 = e * 0x01010101u;
     int c = 0;
-    for (int w = 0; 4 * w < n; ++w) {
-      const uint32_t eq = __vcmpeq4(words[w], e * 0x01010101u);
-      c += __popc((4 * w + 4 <= n ? eq : eq & ((1u << (8 * (n - 4 * w))) - 1u)) & 0x01010101u);
+    for (int a = 0; a < n; a += 16) {
+      const uint4 w = words[a >> 4];
+      c += __popc(same_expert(w.x, e4, n - a)) + __popc(same_expert(w.y, e4, n - a - 4)) +
+           __popc(same_expert(w.z, e4, n - a - 8)) + __popc(same_expert(w.w, e4, n - a - 12));
     }
     tb.start[e + 1] = static_cast<uint16_t>(c);
   }
@@ -144,7 +177,6 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
           si += i;
         }
       }
-      __syncwarp();
       if (e0 + lane < p.E) tb.start[e0 + lane + 1] = static_cast<uint16_t>(rows + sr);
       for (int i = 0; i < k; ++i) {
         tb.item_expert[items + si - k + i] = static_cast<uint16_t>(e0 + lane);
@@ -161,15 +193,18 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
     int r = tb.start[e];
-    if (r == tb.start[e + 1]) continue;
-    for (int w = 0; 4 * w < n; ++w) {
-      uint32_t eq = __vcmpeq4(words[w], e * 0x01010101u) & 0x01010101u;
-      for (; eq; eq &= eq - 1) {
-        const int a = 4 * w + ((__ffs(eq) - 1) >> 3);
-        if (a >= n) break;
-        tb.at[a] = static_cast<uint16_t>(r);
-        tb.order[r++] = static_cast<uint16_t>(a);
-      }
+    const int end = tb.start[e + 1];
+    const uint32_t e4 = e * 0x01010101u;
+    for (int a = 0; r < end; a += 16) {
+      const uint4 w = words[a >> 4];
+      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        for (uint32_t eq = same_expert(in[x], e4, n - a - 4 * x); eq; eq &= eq - 1) {
+          const int at = a + 4 * x + ((__ffs(eq) - 1) >> 3);
+          tb.at[at] = static_cast<uint16_t>(r);
+          tb.order[r++] = static_cast<uint16_t>(at);
+        }
     }
   }
   __syncthreads();
@@ -184,117 +219,120 @@ __device__ __forceinline__ void rotate_pairs(const uint4& v, int t, uint32_t (&r
   r[3] = t & 2 ? a1 : a3;
 }
 
-// A 16-byte load that another kernel's writes may precede (not through the read-only path).
-__device__ __forceinline__ uint4 ld_global128(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
-}
-
-// One warp: the gates of a token, the softmax over all E logits taken at its experts.
-__device__ __forceinline__ void token_gates(const MoeTokParams& p, const MoeTables& tb, int tok, int lane) {
+// One warp: the gates of a token (lane j < topk has gate j), the softmax over all E logits taken at
+// its experts.
+__device__ __forceinline__ float token_gate(const MoeTokParams& p, const MoeTables& tb, int tok, int lane) {
   const float* row = p.logits + static_cast<size_t>(tok) * p.E;
   float top = -INFINITY, sum = 0.f;
-  for (int e = lane; e < p.E; e += 32) top = fmaxf(top, row[e]);
+  for (int e = lane; e < p.E; e += 32) top = fmaxf(top, __ldg(row + e));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  for (int e = lane; e < p.E; e += 32) sum += expf(row[e] - top);
+  for (int e = lane; e < p.E; e += 32) sum += expf(__ldg(row + e) - top);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  float gate = lane < p.topk ? expf(row[tb.expert[tok * p.topk + lane]] - top) / sum : 0.f;
+  float gate = lane < p.topk ? expf(__ldg(row + tb.expert[tok * p.topk + lane]) - top) / sum : 0.f;
   if (p.renorm) {
     float all = gate;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);  // topk <= 8
     gate /= all;
   }
-  if (lane < p.topk) {
-    p.gates[tok * p.topk + lane] = gate;
-    if (p.gates_out) p.gates_out[tok * p.topk + lane] = gate;
-  }
+  return gate;
 }
 
-// Down: false for the first product (gate and up, 64 columns of each), true for the second (down,
-// 128 columns).  NT: groups of 8 tokens in an item.
-template <bool Down, int NT>
-__global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_constant__ MoeTokParams p) {
-  using namespace moet;
-  using R = Ring<Down, NT>;
-  constexpr int kStages = R::kStages;
-  constexpr int kParts = Down ? 3 : 1;            // 16-bit terms of the left operand
-  constexpr int kCols = Down ? 128 : 64;          // columns of a tile
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ MoeTables tb;
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + R::kBarOff);
-  uint64_t* empty = full + kStages;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);  // the warps of one group
-    }
-    fence_mbar_init();
-    tma_prefetch_map(&p.w0);
-    if (!Down) tma_prefetch_map(&p.w1);
-  }
-  if (!Down) grid_dep_launch();
-  moet_tables(p, tb, 8 * NT);
-  const int K = Down ? p.F : p.H, N = Down ? p.H : p.F;
-  const int nk = (K + 63) / 64, nc = (N + kCols - 1) / kCols;
-  // the line of units: the first product item by item, the second column block by column block, so
-  // that blocks are combined while others are still multiplied
-  const uint32_t tiles = static_cast<uint32_t>(tb.items) * nc, total = tiles * nk;
-  const uint32_t per = (total + gridDim.x - 1) / gridDim.x, first = per * blockIdx.x;
-  const int n = first >= total ? 0 : static_cast<int>(per < total - first ? per : total - first);
-  const int item0 = n ? (Down ? (first / nk) % tb.items : first / nk / nc) : 0;
-  const int col0 = n ? (Down ? first / nk / tb.items : (first / nk) % nc) : 0;
-  const int k0 = n ? first % nk : 0;
-  auto next_tile = [&](int& item, int& col) {
-    if (Down) {
-      if (++item == tb.items) {
-        item = 0;
-        ++col;
+// Adds to a counter, releasing what this thread has seen and acquiring what others released; the sum.
+__device__ __forceinline__ unsigned count_up(unsigned* ctr) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
+  return old + 1u;
+}
+
+// Wait (bounded) until an item's h is complete; one lane polls.
+__device__ __forceinline__ bool wait_item(const unsigned* ctr, unsigned want, const Common& c, int lane) {
+  bool ok = true;
+  if (lane == 0) {
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+      if (v >= want) break;
+      if (globaltimer() - t0 > c.timeout_ns) {
+        report_timeout(c.status, kSiteSignal, 0);
+        ok = false;
+        break;
       }
-    } else if (++col == nc) {
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// A CTA's range of one product's line of units (item by item, column block by column block, k).
+template <bool Down>
+struct MoeLine {
+  static constexpr int kCols = Down ? 128 : 64;  // columns of a tile
+  int K, N, nk, nc, n;
+  uint32_t per, first;
+  int item0, col0, k0;
+  __device__ __forceinline__ MoeLine(const MoeTokParams& p, int items) {
+    K = Down ? p.F : p.H;
+    N = Down ? p.H : p.F;
+    nk = (K + 63) / 64;
+    nc = (N + kCols - 1) / kCols;
+    const uint32_t total = static_cast<uint32_t>(items) * nc * nk;
+    per = (total + gridDim.x - 1) / gridDim.x;
+    first = per * blockIdx.x;
+    n = first >= total ? 0 : static_cast<int>(per < total - first ? per : total - first);
+    const uint32_t tile = n ? first / nk : 0;
+    k0 = n ? first % nk : 0;
+    item0 = tile / nc;
+    col0 = tile % nc;
+  }
+  __device__ __forceinline__ void next_tile(int& item, int& col) const {
+    if (++col == nc) {
       col = 0;
       ++item;
     }
-  };
-
-  if (warp == 2 * kGroup / 32) {
-    // ------------------------------------------------------------ loads (they wait for no other kernel)
-    if (lane == 0) {
-      int item = item0, col = col0, k = k0, i = 0;
-      bool ok = true;
-      for (; i < n && ok; ++i) {
-        const int s = i % kStages;
-        ok = mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, p.common, kSiteEmpty);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&full[s], kUnitBytes);
-        const int e = tb.item_expert[item];
-        uint8_t* dst = ring + s * kUnitBytes;
-        tma_load_3d(dst, &p.w0, &full[s], col * kCols, k * 64, e);
-        tma_load_3d(dst + kUnitBytes / 2, Down ? &p.w0 : &p.w1, &full[s], col * kCols + (Down ? 64 : 0), k * 64, e);
-        if (++k == nk) {
-          k = 0;
-          next_tile(item, col);
-        }
-      }
-      if (!ok)  // gave up: what was issued has landed before the CTA ends
-        for (int j = i > kStages ? i - kStages : 0; j < i; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1, p.common, kSiteDrain);
-    }
-    __syncwarp();
-    if (!Down)
-      for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) token_gates(p, tb, tok, lane);
-    return;
   }
+};
 
-  // -------------------------------------------------------------- products
-  const int grp = warp >> 2, wq = warp & 3, tid = threadIdx.x & (kGroup - 1), g = lane >> 2, t = lane & 3;
-  if (Down) grid_dep_wait();  // h is written
-  if (!Down && blockIdx.x == 0 && p.experts_out)
-    for (int a = threadIdx.x; a < p.T * p.topk; a += 2 * kGroup) p.experts_out[a] = tb.expert[a];
+// The loads of a line, by one thread; u counts units over both lines.
+template <bool Down, int kStages>
+__device__ __forceinline__ bool moet_load(const MoeTokParams& p, const MoeTables& tb, uint8_t* ring, uint64_t* full,
+                                          uint64_t* empty, int& u) {
+  using namespace moet;
+  const MoeLine<Down> ln(p, tb.items);
+  int item = ln.item0, col = ln.col0, k = ln.k0;
+  for (int i = 0; i < ln.n; ++i, ++u) {
+    const int s = u % kStages;
+    if (!mbar_wait(&empty[s], ((u / kStages) & 1) ^ 1, p.common, kSiteEmpty)) return false;
+    mbar_arrive_expect_tx(&full[s], kUnitBytes);
+    const int e = tb.item_expert[item];
+    uint8_t* dst = ring + s * kUnitBytes;
+    tma_load_3d(dst, Down ? &p.down : &p.gate, &full[s], col * ln.kCols, k * 64, e);
+    tma_load_3d(dst + kUnitBytes / 2, Down ? &p.down : &p.up, &full[s], col * ln.kCols + (Down ? 64 : 0), k * 64, e);
+    if (++k == ln.nk) {
+      k = 0;
+      ln.next_tile(item, col);
+    }
+  }
+  return true;
+}
+
+// The products of a line, by the two groups; u0: units of the line before it.
+template <bool Down, int NT>
+__device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& tb, uint8_t* ring, uint64_t* full,
+                                              uint64_t* empty, int u0, int& segs, bool& ok) {
+  using namespace moet;
+  using R = Ring<NT>;
+  constexpr int kStages = R::kStages;
+  constexpr int kParts = Down ? 3 : 1;  // 16-bit terms of the left operand
+  const MoeLine<Down> ln(p, tb.items);
+  const int nk = ln.nk, K = ln.K, N = ln.N, n = ln.n;
+  const uint32_t per = ln.per, first = ln.first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wq = warp & 3, tid = threadIdx.x & (kGroup - 1), g = lane >> 2, t = lane & 3;
+  const int grp = warp >> 2, par = (u0 ^ grp) & 1;  // this group's units are those with i & 1 == par
+  const int nc1 = Down ? (p.F + 63) / 64 : 0;       // tiles of an item in the first product
   // the rows of an item
   auto item_rows = [&](int item, int& row0) {
     row0 = tb.item_row[item];
@@ -302,11 +340,14 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
     return end - row0 < 8 * NT ? end - row0 : 8 * NT;
   };
   // this thread's part of the left operand for the next unit of its group, loaded a unit ahead
-  int x_item = item0, x_col = col0, x_k = k0, x_rows = 0;
+  int x_item = ln.item0, x_col = ln.col0, x_k = ln.k0, x_rows = 0, x_seen = -1;
   uint4 xv[kParts][NT][2];
   const __nv_bfloat16* src[NT];
   const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
   auto x_tile = [&]() {
+    if (x_item == x_seen) return;
+    x_seen = x_item;
+    if (Down && ok) ok = wait_item(p.item_ctr + x_item, nc1, p.common, lane);
     int row0;
     x_rows = item_rows(x_item, row0);
 #pragma unroll
@@ -321,10 +362,8 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   auto x_step = [&]() {
     if (++x_k == nk) {
       x_k = 0;
-      next_tile(x_item, x_col);
-      return true;
+      ln.next_tile(x_item, x_col);
     }
-    return false;
   };
   auto load_x = [&]() {
 #pragma unroll
@@ -335,12 +374,14 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
         for (int w = 0; w < 2; ++w) {
           xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
           const int at = x_k * 64 + 32 * w + 8 * t;
+          // h from L2: a line of L1 could hold a neighbour row that is not written yet
           if (8 * b < x_rows && src[b] && at < K)
-            xv[q][b][w] = Down ? ld_global128(src[b] + q * plane + at) : __ldg(reinterpret_cast<const uint4*>(src[b] + at));
+            xv[q][b][w] = Down ? __ldcg(reinterpret_cast<const uint4*>(src[b] + q * plane + at))
+                               : __ldg(reinterpret_cast<const uint4*>(src[b] + at));
         }
   };
-  if (grp && n > 1) x_step();
-  if (grp < n) {
+  if (par && n > 1) x_step();
+  if (par < n) {
     x_tile();
     load_x();
   }
@@ -349,9 +390,8 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   const int lt = (lane & 7) >> 1, lbit = lane & 1, lhi = lane >> 4, lcol = (lane >> 3) & 1;
   float* hand = reinterpret_cast<float*>(ring + R::kHandOff) + tid * 4;
   float acc[2][NT][4];
-  bool ok = true;
-  int item = item0, col = col0;
-  for (int begin = 0, seg = 0; begin < n; ++seg) {
+  int item = ln.item0, col = ln.col0;
+  for (int begin = 0; begin < n; ++segs) {
     // this CTA's units [begin, end) of one tile
     const uint32_t tile = (first + begin) / nk;
     const int left = static_cast<int>((tile + 1) * nk - (first + begin));
@@ -364,7 +404,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
       for (int b = 0; b < NT; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
-    for (int i = begin + ((begin ^ grp) & 1); i < end; i += 2) {
+    for (int i = begin + ((begin ^ par) & 1); i < end; i += 2) {
       uint32_t xr[2][kParts][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -373,12 +413,14 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
 #pragma unroll
           for (int b = 0; b < NT; ++b) rotate_pairs(xv[q][b][h], t, xr[h][q][b]);
       if (i + 2 < n) {
-        const bool one = x_step(), two = x_step();
-        if (one || two) x_tile();
+        x_step();
+        x_step();
+        x_tile();
         load_x();
       }
-      const int s = i % kStages;
-      if (ok) ok = mbar_wait(&full[s], (i / kStages) & 1, p.common, kSiteFull);  // after a timeout: on, without waits
+      const int s = (u0 + i) % kStages;
+      if (ok)  // the same in all lanes; after a timeout: on, without waits
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ((u0 + i) / kStages) & 1, p.common, kSiteFull));
       const uint32_t w = smem_u32(ring + s * kUnitBytes);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -407,11 +449,11 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
     // ------------------------------------------------------------ the end of a tile, or of the CTA's part of it
     // Group 1 hands its sums over (two buffers: it cannot pass the next barrier before group 0 has read
     // these) and goes on with the next tile; group 0 adds and finishes.
-    const int this_col = col;
+    const int this_col = col, this_item = item;
     const uint32_t seg_first = first + begin;
     begin = end;
-    next_tile(item, col);
-    float* buf = hand + (seg & 1) * kGroup * 8 * NT;
+    ln.next_tile(item, col);
+    float* buf = hand + (segs & 1) * kGroup * 8 * NT;
     if (grp) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -433,11 +475,10 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
           acc[m][b][2] += v.z;
           acc[m][b][3] += v.w;
         }
-    const bool starts = seg_first == tile * nk, ends = first + end == (tile + 1) * nk;
-    if (!starts || !ends) {
+    if (seg_first != tile * nk || first + end != (tile + 1) * nk) {
       const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
       constexpr int kSlot = kGroup * 8 * NT;
-      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * kSlot + tid * 4;
+      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot + tid * 4;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -445,12 +486,9 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
           if (8 * b < rows)
             *reinterpret_cast<float4*>(part + (m * NT + b) * kGroup * 4) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
       named_bar_sync(2, kGroup);
-      if (tid == 0) {
-        __threadfence();  // the CTA's part, seen by this thread through the barrier, before the count
-        const unsigned done = atomicAdd(p.cut_ctr + c0, 1u) + 1u;
-        tb.last = done == c1 - c0 + 1;
+      if (tid == 0) {  // releases the whole CTA's part, which it has seen through the barrier
+        tb.last = count_up(p.cut_ctr + c0) == c1 - c0 + 1;
         if (tb.last) p.cut_ctr[c0] = 0u;
-        __threadfence();
       }
       named_bar_sync(2, kGroup);
       if (!tb.last) continue;
@@ -458,19 +496,37 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
-          if (8 * b < rows) {
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (uint32_t c = c0; c <= c1; ++c) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                  p.part + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kSlot + (m * NT + b) * kGroup * 4 + tid * 4));
-              sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
+      const float* from = p.part + (static_cast<size_t>(c0) * 2 + 1) * kSlot + tid * 4;  // slot 1 starts a tile
+      for (uint32_t c = c0; c <= c1;) {
+        constexpr int kBatch = 4;
+        float4 v[kBatch][2][NT];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+              v[x][m][b] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (c + x <= c1 && 8 * b < rows)
+                v[x][m][b] = __ldcg(reinterpret_cast<const float4*>(from + (m * NT + b) * kGroup * 4));
             }
-            acc[m][b][0] = sum.x;
-            acc[m][b][1] = sum.y;
-            acc[m][b][2] = sum.z;
-            acc[m][b][3] = sum.w;
-          }
+          from += c + x == c0 ? kSlot : 2 * kSlot;
+        }
+        c += kBatch;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+              acc[m][b][0] += v[x][m][b].x;
+              acc[m][b][1] += v[x][m][b].y;
+              acc[m][b][2] += v[x][m][b].z;
+              acc[m][b][3] += v[x][m][b].w;
+            }
+      }
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b)
@@ -498,33 +554,88 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
           }
         }
       }
-    if constexpr (Down) {
-      // the block's last item combines its rows
-      named_bar_sync(2, kGroup);
-      if (tid == 0) {
-        __threadfence();
-        const unsigned done = atomicAdd(p.col_ctr + this_col, 1u) + 1u;
-        tb.last = done == static_cast<unsigned>(tb.items);
-        if (tb.last) p.col_ctr[this_col] = 0u;
-        __threadfence();
+    named_bar_sync(2, kGroup);
+    if constexpr (!Down) {
+      if (tid == 0) count_up(p.item_ctr + this_item);
+    } else {
+      // A token's topk rows of this block: the last one to be finished adds them up.  The item's last
+      // tile sets the item's counter back: nothing waits on it any more.
+      if (wq == 0) {
+        bool done = false;
+        if (lane < rows) {
+          unsigned* ctr = p.tok_ctr + (tb.order[row0 + lane] / p.topk) * ln.nc + this_col;
+          done = count_up(ctr) == static_cast<unsigned>(p.topk);
+          if (done) *ctr = 0u;
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, done);
+        if (lane == 0) {
+          tb.last = mask;
+          if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
+        }
       }
       named_bar_sync(2, kGroup);
-      if (tb.last) {
-        for (int v = tid; v < p.T * 32; v += kGroup) {
-          const int tok = v >> 5, c = this_col * 128 + (v & 31) * 4;
-          if (c >= N) continue;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j = 0; j < p.topk; ++j) {
-            const int a = tok * p.topk + j;
-            const float gate = __ldcg(p.gates + a);
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[a]) * p.H + c));
-            sum = make_float4(sum.x + gate * u.x, sum.y + gate * u.y, sum.z + gate * u.z, sum.w + gate * u.w);
-          }
-          *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+      uint32_t mask = tb.last;
+      for (int x = 0; mask; ++x, mask &= mask - 1) {
+        if ((x & 3) != wq) continue;
+        const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * 128 + lane * 4;
+        float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kMaxTopk; ++j) {
+          v[j] = sum;
+          if (j < p.topk && c < N)
+            v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[tok * p.topk + j]) * p.H + c));
+        }
+        const float gate = token_gate(p, tb, tok, lane);
+#pragma unroll
+        for (int j = 0; j < kMaxTopk; ++j) {
+          const float f = __shfl_sync(0xffffffffu, gate, j);
+          if (j < p.topk) sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
+        }
+        if (c < N) *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+        if (this_col == 0 && lane < p.topk) {
+          if (p.experts_out) p.experts_out[tok * p.topk + lane] = tb.expert[tok * p.topk + lane];
+          if (p.gates_out) p.gates_out[tok * p.topk + lane] = gate;
         }
       }
     }
   }
+}
+
+// NT: groups of 8 tokens in an item.
+template <int NT>
+__global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_constant__ MoeTokParams p) {
+  using namespace moet;
+  using R = Ring<NT>;
+  constexpr int kStages = R::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ MoeTables tb;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + R::kBarOff);
+  uint64_t* empty = full + kStages;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);  // the warps of one group
+    }
+    fence_mbar_init();
+    tma_prefetch_map(&p.gate);
+    tma_prefetch_map(&p.up);
+    tma_prefetch_map(&p.down);
+  }
+  moet_tables(p, tb, 8 * NT);
+  if (threadIdx.x >= 2 * kGroup) {
+    if (threadIdx.x == 2 * kGroup) {
+      int u = 0;
+      const bool ok = moet_load<false, kStages>(p, tb, ring, full, empty, u) && moet_load<true, kStages>(p, tb, ring, full, empty, u);
+      if (!ok)  // gave up: what was issued has landed before the CTA ends
+        for (int j = u > kStages ? u - kStages : 0; j < u; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1, p.common, kSiteDrain);
+    }
+    return;
+  }
+  int segs = 0;
+  bool ok = true;
+  moet_multiply<false, NT>(p, tb, ring, full, empty, 0, segs, ok);
+  moet_multiply<true, NT>(p, tb, ring, full, empty, MoeLine<false>(p, tb.items).n, segs, ok);
 }
 
 }  // namespace tl
@@ -541,13 +652,12 @@ static bool moet_shape_ok(int T, int H, int E, int F, int topk) {
 static int moet_eights(int T) { return T <= 8 ? 1 : 2; }
 
 struct MoetLayout {
-  size_t gates, h, y, part, total;
+  size_t h, y, part, total;
 };
 static MoetLayout moet_layout(int T, int H, int F, int topk) {
   const size_t a = static_cast<size_t>(T) * topk;
   MoetLayout L;
-  L.gates = kCounterBytes;
-  L.h = L.gates + align256(a * 4);
+  L.h = kCounterBytes;
   L.y = L.h + align256(3 * a * F * 2);
   L.part = L.y + align256(a * H * 4);
   L.total = L.part + static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 8 * moet_eights(T) * 4;
@@ -559,24 +669,25 @@ extern "C" size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int 
   return moet_layout(T, H, F, topk).total;
 }
 
-template <bool Down, int NT>
+template <int NT>
 static int moet_launch(tl_ctx* ctx, const MoeTokParams& p, cudaStream_t st) {
-  auto kern = moet_kernel<Down, NT>;
+  auto kern = moet_kernel<NT>;
   static std::atomic<unsigned long long> ready{0};
-  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), moet::Ring<Down, NT>::kSmem)) return TL_ERR_CUDA;
+  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), moet::Ring<NT>::kSmem)) return TL_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctx->ctas < moet::kMaxCtas ? ctx->ctas : moet::kMaxCtas, 1, 1);
   cfg.blockDim = dim3(moet::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = moet::Ring<Down, NT>::kSmem;
+  cfg.dynamicSmemBytes = moet::Ring<NT>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: the second product waits on the first
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = Down ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) {
     (void)cudaGetLastError();
-    return TL_ERR_CUDA;
+    return e == cudaErrorCooperativeLaunchTooLarge ? TL_ERR_UNSUPPORTED : TL_ERR_CUDA;
   }
   return TL_OK;
 }
@@ -595,13 +706,12 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeTokParams p;
   std::memset(&p, 0, sizeof(p));
-  CUtensorMap down;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!tmap_3d(&p.w0, BF, 2, w_gate, F, H, E, 64, 64, 1) || !tmap_3d(&p.w1, BF, 2, w_up, F, H, E, 64, 64, 1) ||
-      !tmap_3d(&down, BF, 2, w_down, H, F, E, 64, 64, 1))
+  if (!tmap_3d(&p.gate, BF, 2, w_gate, F, H, E, 64, 64, 1) || !tmap_3d(&p.up, BF, 2, w_up, F, H, E, 64, 64, 1) ||
+      !tmap_3d(&p.down, BF, 2, w_down, H, F, E, 64, 64, 1))
     return TL_ERR_CUDA;
   p.common = make_common(ctx);
-  p.common.trace_hdr = nullptr;  // these kernels record no trace spans
+  p.common.trace_hdr = nullptr;  // this kernel records no trace spans
   p.common.trace = nullptr;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.logits = logits;
@@ -609,8 +719,8 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   p.experts_out = experts_out;
   p.gates_out = gates_out;
   p.cut_ctr = reinterpret_cast<unsigned*>(ws);
-  p.col_ctr = reinterpret_cast<unsigned*>(ws) + kCutCounters;
-  p.gates = reinterpret_cast<float*>(ws + L.gates);
+  p.item_ctr = p.cut_ctr + kCutCounters;
+  p.tok_ctr = p.item_ctr + kItemCounters;
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.part = reinterpret_cast<float*>(ws + L.part);
@@ -621,11 +731,5 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   p.topk = topk;
   p.renorm = ctx->cfg.moe_renorm;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  auto both = [&](auto nt) {
-    const int rc = moet_launch<false, decltype(nt)::value>(ctx, p, st);
-    if (rc != TL_OK) return rc;
-    p.w0 = down;
-    return moet_launch<true, decltype(nt)::value>(ctx, p, st);
-  };
-  return moet_eights(T) == 1 ? both(std::integral_constant<int, 1>{}) : both(std::integral_constant<int, 2>{});
+  return moet_eights(T) == 1 ? moet_launch<1>(ctx, p, st) : moet_launch<2>(ctx, p, st);
 }

@@ -75,12 +75,14 @@ inline bool smem_ready(std::atomic<unsigned long long>& ready, int device, const
   return true;
 }
 
-// The first 8 KB of a serving operator's workspace: counters that every call leaves at zero, whatever its
+// The first bytes of a serving operator's workspace: counters that every call leaves at zero, whatever its
 // shape.  A CTA's range of work starts at most one piece that goes on in other CTAs, so the counter
 // of a cut piece is that of the CTA it starts in.
-constexpr int kCutCounters = 1024;  // by CTA: the largest grid
-constexpr int kColCounters = 1024;
-constexpr size_t kCounterBytes = (kCutCounters + kColCounters) * 4;
+constexpr int kCutCounters = 1024;         // by CTA: the largest grid
+constexpr int kItemCounters = 1024;        // MoE: by item, at most 128 tokens x topk 8
+constexpr int kTokenCounters = 128 * 256;  // MoE: by token and block of 128 of at most 32768 columns
+constexpr size_t kCounterBytes = (kCutCounters + kItemCounters + kTokenCounters) * 4;
+static_assert(kCounterBytes == TL_SERVE_COUNTER_BYTES, "header");
 
 inline bool esize_ok(long long stride, int esize) { return stride >= 0 && (stride * esize) % 16 == 0; }
 

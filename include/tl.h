@@ -415,11 +415,12 @@ int tl_ag_gemm_static_scratch(tl_ctx* ctx, int W, int rank, const void* const* a
  * passed as it is.
  * Indices read on the device (slots, page numbers, lengths) are checked there: an entry out of
  * range is left out, nothing outside the buffers is read or written, and tl_ctx_check returns
- * TL_ERR_INDEX.  No CTA of these four entry points waits for another; all can be captured into a graph.
- * Workspaces: the first 8 KB hold counters that each call leaves at zero again.  So one workspace,
- * zero-filled once, serves calls of tl_paged_attention and tl_moe_tokens of any shapes, in order; after
- * another operator used it, its first 8 KB have to be zero-filled again.
+ * TL_ERR_INDEX.  All four can be captured into a graph and replayed.
+ * Workspaces: the first TL_SERVE_COUNTER_BYTES hold counters that each call leaves at zero again.  So one
+ * workspace, zero-filled once, serves calls of tl_paged_attention and tl_moe_tokens of any shapes, in
+ * order; after another operator used it, those bytes have to be zero-filled again.
  */
+#define TL_SERVE_COUNTER_BYTES 139264
 #define TL_BF16 0
 #define TL_FP16 1
 #define TL_E4M3 2
@@ -516,7 +517,8 @@ int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token
  * x: bf16 [T x H]; logits: fp32 [T x E]; w_gate, w_up: bf16 [E x H x F]; w_down: bf16 [E x F x H];
  * out: fp32 [T x H].  experts_out (int32 [T x topk]) and gates_out (fp32 [T x topk]) are optional: the
  * chosen experts, best first, and their gates.  NaN logits count as the lowest (the gates are NaN).
- * workspace: tl_moe_tokens_workspace_bytes().
+ * workspace: tl_moe_tokens_workspace_bytes().  One cooperative launch of one CTA per SM:
+ * TL_ERR_UNSUPPORTED if the device cannot hold it at once.
  * Shapes: 1 <= T <= 128; 1 <= topk <= 8; topk <= E <= 256; H % 8 == 0; F % 8 == 0; H, F <= 32768.
  */
 size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int topk);
