@@ -35,7 +35,7 @@
 namespace tl {
 
 namespace moet {
-constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk, kMaxCtas = 512;
+constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk, kMaxCtas = 256;
 // Two groups of four warps take every other unit: one group's loads of x and products hide the other's.
 constexpr int kGroup = 128, kThreads = 2 * kGroup + 32;
 constexpr int kUnitBytes = 16384;
@@ -51,6 +51,7 @@ struct Ring {
   static_assert(2 * kStages * 8 <= 256, "barriers");
   static constexpr int kSmem = kHandOff + 2 * kGroup * 8 * NT * 4 + 1024;  // 1024: the ring's alignment
 };
+static_assert(2 * kMaxCtas <= kCutCounters, "a counter per product and CTA");
 }  // namespace moet
 
 struct MoeTokParams {
@@ -63,8 +64,8 @@ struct MoeTokParams {
   float* gates_out;
   __nv_bfloat16* h;    // [3][T topk][F]: h = h0 + h1 + h2, rows in the order (expert, t, j)
   float* y;            // [T topk][H]
-  float* part;         // [CTA][2][8 NT][128 threads] sums of a cut tile
-  unsigned* cut_ctr;   // [CTA]: CTAs done with the cut tile that starts in this one
+  float* part;         // [product][CTA][2][8 NT][128 threads] sums of a cut tile
+  unsigned* cut_ctr;   // [product][CTA]: CTAs done with the cut tile that starts in this one
   unsigned* item_ctr;  // [item]: tiles done, of both products
   unsigned* tok_ctr;   // [token][column block]: rows done
   int T, H, E, F, topk, renorm;
@@ -247,6 +248,10 @@ __device__ __forceinline__ unsigned count_up(unsigned* ctr) {
   return old + 1u;
 }
 
+__device__ __forceinline__ void count_up_async(unsigned* ctr) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
+}
+
 // Wait (bounded) until an item's h is complete; one lane polls.
 __device__ __forceinline__ bool wait_item(const unsigned* ctr, unsigned want, const Common& c, int lane) {
   bool ok = true;
@@ -339,11 +344,14 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     const int end = tb.start[tb.item_expert[item] + 1];
     return end - row0 < 8 * NT ? end - row0 : 8 * NT;
   };
-  // this thread's part of the left operand for the next unit of its group, loaded a unit ahead
+  // This thread's part of the left operand for the next unit of its group, loaded a unit ahead.
+  // Columns past the item's rows hold whatever row 0 has: a column of the products depends on no
+  // other, and those are not stored.
   int x_item = ln.item0, x_col = ln.col0, x_k = ln.k0, x_rows = 0, x_seen = -1;
   uint4 xv[kParts][NT][2];
-  const __nv_bfloat16* src[NT];
-  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  uint32_t src[NT];  // elements, below 2^27
+  const __nv_bfloat16* base = Down ? p.h : p.x;
+  const uint32_t plane = static_cast<uint32_t>(p.T) * p.topk * p.F;
   auto x_tile = [&]() {
     if (x_item == x_seen) return;
     x_seen = x_item;
@@ -352,11 +360,8 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     x_rows = item_rows(x_item, row0);
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
-      src[b] = nullptr;
-      if (8 * b + g < x_rows) {
-        const int r = row0 + 8 * b + g;
-        src[b] = Down ? p.h + static_cast<size_t>(r) * p.F : p.x + static_cast<size_t>(tb.order[r] / p.topk) * p.H;
-      }
+      const int r = row0 + (8 * b + g < x_rows ? 8 * b + g : 0);
+      src[b] = (Down ? r : tb.order[r] / p.topk) * static_cast<uint32_t>(K) + 8 * t;
     }
   };
   auto x_step = [&]() {
@@ -366,19 +371,21 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     }
   };
   auto load_x = [&]() {
+    const int left = K - x_k * 64 - 8 * t;  // the last unit's rows past K meet zero weights, and have to be finite
 #pragma unroll
-    for (int q = 0; q < kParts; ++q)
+    for (int b = 0; b < NT; ++b)
+      if (8 * b < x_rows)
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+        for (int q = 0; q < kParts; ++q)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
-          const int at = x_k * 64 + 32 * w + 8 * t;
-          // h from L2: a line of L1 could hold a neighbour row that is not written yet
-          if (8 * b < x_rows && src[b] && at < K)
-            xv[q][b][w] = Down ? __ldcg(reinterpret_cast<const uint4*>(src[b] + q * plane + at))
-                               : __ldg(reinterpret_cast<const uint4*>(src[b] + at));
-        }
+          for (int w = 0; w < 2; ++w) {
+            // h from L2: a line of L1 could hold a neighbour row that is not written yet
+            const uint4* at = reinterpret_cast<const uint4*>(base + (src[b] + q * plane + x_k * 64 + 32 * w));
+            if (32 * w < left)
+              xv[q][b][w] = Down ? __ldcg(at) : __ldg(at);
+            else
+              xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
+          }
   };
   if (par && n > 1) x_step();
   if (par < n) {
@@ -407,11 +414,21 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     for (int i = begin + ((begin ^ par) & 1); i < end; i += 2) {
       uint32_t xr[2][kParts][NT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int b = 0; b < NT; ++b)
+        if (8 * b < rows)
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int b = 0; b < NT; ++b) rotate_pairs(xv[q][b][h], t, xr[h][q][b]);
+            for (int q = 0; q < kParts; ++q) {
+              if constexpr (Down) {  // h is stored in the order of use
+                xr[h][q][b][0] = xv[q][b][h].x;
+                xr[h][q][b][1] = xv[q][b][h].y;
+                xr[h][q][b][2] = xv[q][b][h].z;
+                xr[h][q][b][3] = xv[q][b][h].w;
+              } else {
+                rotate_pairs(xv[q][b][h], t, xr[h][q][b]);
+              }
+            }
       if (i + 2 < n) {
         x_step();
         x_step();
@@ -427,43 +444,48 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2) {
           const int kr = 32 * h + 8 * lt + 2 * ((2 * s2 + lhi + lt) & 3) + lbit;
+          uint32_t a[2][4];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             // first product: m = gate, up, columns 16 wq of each; second: columns 32 wq + 16 m
             const int chunk = (Down ? 4 * (wq & 1) + 2 * m : 2 * wq) + lcol;
             const uint32_t box = w + (Down ? (wq >> 1) : m) * (kUnitBytes / 2);
-            uint32_t a[4];
-            ldsm4t(a, box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-              if (8 * b < rows)
-#pragma unroll
-                for (int q = 0; q < kParts; ++q)
-                  mma16816<__nv_bfloat16>(acc[m][b], a, xr[h][q][b][2 * s2], xr[h][q][b][2 * s2 + 1]);
+            ldsm4t(a[m], box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
           }
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+            if (8 * b < rows)
+#pragma unroll
+              for (int q = 0; q < kParts; ++q)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                  mma16816<__nv_bfloat16>(acc[m][b], a[m], xr[h][q][b][2 * s2], xr[h][q][b][2 * s2 + 1]);
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
 
     // ------------------------------------------------------------ the end of a tile, or of the CTA's part of it
-    // Group 1 hands its sums over (two buffers: it cannot pass the next barrier before group 0 has read
-    // these) and goes on with the next tile; group 0 adds and finishes.
+    // The groups finish tiles in turn: the other one hands its sums over and goes on with the next
+    // tile.  Two buffers and two barriers: it cannot reach the tile after next, and write this buffer
+    // again, before the finisher, which hands over the next one, has read this one.
     const int this_col = col, this_item = item;
     const uint32_t seg_first = first + begin;
     begin = end;
     ln.next_tile(item, col);
     float* buf = hand + (segs & 1) * kGroup * 8 * NT;
-    if (grp) {
+    const uint32_t bar = 1 + (segs & 1);
+    if ((segs & 1) != grp) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
           if (8 * b < rows)
             *reinterpret_cast<float4*>(buf + (m * NT + b) * kGroup * 4) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
+      named_bar_arrive(bar, 2 * kGroup);
+      continue;
     }
-    named_bar_sync(1, 2 * kGroup);
-    if (grp) continue;
+    named_bar_sync(bar, 2 * kGroup);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -476,21 +498,25 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           acc[m][b][3] += v.w;
         }
     if (seg_first != tile * nk || first + end != (tile + 1) * nk) {
+      // (each product has parts and counters of its own: a CTA is in the second one while its
+      // neighbour still works on their common tile of the first)
       const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
       constexpr int kSlot = kGroup * 8 * NT;
-      float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot + tid * 4;
+      float* parts = p.part + (Down ? static_cast<size_t>(kMaxCtas) * 2 * kSlot : 0);
+      unsigned* ctr = p.cut_ctr + (Down ? kMaxCtas : 0) + c0;
+      float* part = parts + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot + tid * 4;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
           if (8 * b < rows)
             *reinterpret_cast<float4*>(part + (m * NT + b) * kGroup * 4) = make_float4(acc[m][b][0], acc[m][b][1], acc[m][b][2], acc[m][b][3]);
-      named_bar_sync(2, kGroup);
+      named_bar_sync(3, kGroup);
       if (tid == 0) {  // releases the whole CTA's part, which it has seen through the barrier
-        tb.last = count_up(p.cut_ctr + c0) == c1 - c0 + 1;
-        if (tb.last) p.cut_ctr[c0] = 0u;
+        tb.last = count_up(ctr) == c1 - c0 + 1;
+        if (tb.last) *ctr = 0u;
       }
-      named_bar_sync(2, kGroup);
+      named_bar_sync(3, kGroup);
       if (!tb.last) continue;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -498,7 +524,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
         for (int b = 0; b < NT; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
-      const float* from = p.part + (static_cast<size_t>(c0) * 2 + 1) * kSlot + tid * 4;  // slot 1 starts a tile
+      const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + tid * 4;  // slot 1 starts a tile
       for (uint32_t c = c0; c <= c1;) {
         constexpr int kBatch = 4;
         float4 v[kBatch][2][NT];
@@ -541,7 +567,8 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
             const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
             const float r1 = v - __bfloat162float(h0);
             const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
-            const size_t at = static_cast<size_t>(row0 + r) * p.F + f;
+            // pair (k / 2) mod 4 of part (k / 8) mod 4 of 32 lies where that thread uses it
+            const size_t at = static_cast<size_t>(row0 + r) * p.F + ((f & ~7) | ((((f >> 1) - (f >> 3)) & 3) << 1) | (f & 1));
             p.h[at] = h0;
             p.h[plane + at] = h1;
             p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
@@ -554,9 +581,9 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           }
         }
       }
-    named_bar_sync(2, kGroup);
+    named_bar_sync(3, kGroup);
     if constexpr (!Down) {
-      if (tid == 0) count_up(p.item_ctr + this_item);
+      if (tid == 0) count_up_async(p.item_ctr + this_item);
     } else {
       // A token's topk rows of this block: the last one to be finished adds them up.  The item's last
       // tile sets the item's counter back: nothing waits on it any more.
@@ -573,7 +600,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
         }
       }
-      named_bar_sync(2, kGroup);
+      named_bar_sync(3, kGroup);
       uint32_t mask = tb.last;
       for (int x = 0; mask; ++x, mask &= mask - 1) {
         if ((x & 3) != wq) continue;
@@ -660,7 +687,7 @@ static MoetLayout moet_layout(int T, int H, int F, int topk) {
   L.h = kCounterBytes;
   L.y = L.h + align256(3 * a * F * 2);
   L.part = L.y + align256(a * H * 4);
-  L.total = L.part + static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 8 * moet_eights(T) * 4;
+  L.total = L.part + 2 * static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 8 * moet_eights(T) * 4;
   return L;
 }
 

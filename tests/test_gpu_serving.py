@@ -462,6 +462,27 @@ def test_moe_tokens_repeats_bit_for_bit_in_one_workspace(tl, ctx):
             assert all(torch.equal(a, b) for a, b in zip(first, run_moe(tl, ctx, *case, 2, w)))
 
 
+@pytest.mark.parametrize("T", [1, 8, 64])
+def test_moe_tokens_repeats_at_the_size_of_a_layer(tl, ctx, T):
+    """Every CTA has units of both products, and tiles cut between neighbours in both: no run differs."""
+    H, E, F = 2048, 64, 1408
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    w = [(torch.randn(s, generator=gen, device="cuda") * 0.02).bfloat16() for s in ((E, H, F), (E, H, F), (E, F, H))]
+    x, lg = torch.randn((T, H), generator=gen, device="cuda").bfloat16(), torch.randn((T, E), generator=gen, device="cuda")
+    work = ws(tl.tl_moe_tokens_workspace_bytes(T, H, E, F, 2))
+    first = run_moe(tl, ctx, x, lg, *w, 2, work)
+    for _ in range(60):
+        again = run_moe(tl, ctx, x, lg, *w, 2, work)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    assert ctx.check() == tl.TL_OK
+    h = torch.stack([torch.nn.functional.silu(a @ w[0][e].double()) * (a @ w[1][e].double())
+                     for a, row in zip(x.double(), first[1].tolist()) for e in row])
+    y = torch.stack([v @ w[2][e].double() for v, e in zip(h, first[1].flatten().tolist())]).view(T, 2, H)
+    want = (torch.softmax(lg.double(), -1).gather(1, first[1].long())[:, :, None] * y).sum(1)
+    # sums of 2048 and 1408 terms in fp32: a relative 2^-23 each time, at random signs sqrt(2048) of them, doubled for the chain
+    assert (first[0] - want).norm() <= 2 * math.sqrt(2048) * 2.0 ** -23 * want.norm()
+
+
 def test_moe_tokens_in_a_graph_on_another_stream(tl, ctx):
     x, lg, *w = moe_case(6, 256, 8, 128, seed=20)
     out, work = torch.empty((6, 256), device="cuda"), ws(tl.tl_moe_tokens_workspace_bytes(6, 256, 8, 128, 2))
