@@ -6,11 +6,14 @@
 //
 // Each CTA (one per SM, a cooperative launch) works out the routing by itself, so nothing has to
 // pass between CTAs before the first load: the topk of every token, the assignments in the order
-// (expert, t, j), and the items: an expert with up to 8 NT (8 or 16) of its assignments.  (item, 64
-// columns of gate and up or 128 of down, 64 rows) is a unit of 16 KB; all units of a product form one
+// (expert, t, j), and the items: an expert with up to 8 NT (8 or 16) of its assignments.  (item, 128
+// columns of gate and up or 256 of down, 32 rows) is a unit of 16 KB; all units of a product form one
 // line, cut into equal ranges, one per CTA: even work for any routing.  A CTA takes its range of
-// the first product, then its range of the second.  One warp keeps a ring of TMA loads full across
-// both; two groups of four warps multiply, a unit each in turn.
+// the first product, then its range of the second.  One warp keeps a ring of TMA loads of the
+// weights full across both, a second one copies the tokens' parts of x (then h) beside them; two
+// groups of four warps multiply, a unit each in turn.  (With the parts of x loaded by the multiplying
+// warps from L2 a unit ahead, 64 tokens took 251 us against 194 without those loads.  Boxes
+// side by side read 256 or 512 bytes of a row at a time: 128 bytes reached 0.8 of HBM.)
 //
 // The second product of an item waits (bounded) until its h is complete.  No unit of the first waits
 // for anything, every CTA is resident, and both lines are item by item, so the h that a CTA needs comes
@@ -18,9 +21,7 @@
 //
 // The products run on mma.sync m16n8k16: columns of the weights are its 16 rows (transposed by
 // ldmatrix from the 128-byte-swizzled tile), the tokens its 8 columns, which wastes least for 1 to 8
-// tokens; a tcgen05 tile would be 128 rows of tokens.  The k order inside 32 rows is permuted so that
-// a thread's part of x is 16 contiguous bytes and ldmatrix rows fall in different banks: thread t
-// holds k = 8 t .. 8 t + 7 as four pairs, and pair (i + t) mod 4 is its i-th.
+// tokens; a tcgen05 tile would be 128 rows of tokens.
 // h goes to the second product as a sum of three bf16 (24 bits), three products for one load of
 // the weights, so the layer keeps fp32 precision between the two.
 //
@@ -37,25 +38,28 @@ namespace tl {
 namespace moet {
 constexpr int kMaxT = 128, kMaxTopk = 8, kMaxE = 256, kMaxA = kMaxT * kMaxTopk, kMaxCtas = 256;
 // Two groups of four warps take every other unit: one group's loads of x and products hide the other's.
-constexpr int kGroup = 128, kThreads = 2 * kGroup + 32;
-constexpr int kUnitBytes = 16384;
+constexpr int kGroup = 128, kThreads = 2 * kGroup + 64;
+constexpr int kRows = 32, kBox = 4096, kUnitBytes = 4 * kBox;  // rows of a unit; 64 columns of them; 4 boxes
+constexpr int kXPitch = 80;  // bytes from a token's 32 values to the next one's: ldmatrix rows in different banks
 // Stages: an even number, so that a stage always serves the same group.  (With an odd one, a group could
 // be a whole ring ahead of a load that the other one still waits for, and take the barrier's
-// phase before it for its own.)  192 KB in flight per SM: with 96 KB the loop ran at 0.7 of HBM.
+// phase before it for its own.)
 template <int NT>
 struct Ring {
-  static constexpr int kStages = 12;
+  static constexpr int kStages = NT == 1 ? 10 : 8;
   static_assert(kStages % 2 == 0, "a stage belongs to one group");
-  static constexpr int kBarOff = kStages * kUnitBytes;
-  static constexpr int kHandOff = kBarOff + 256;  // group 1's sums: [2][8 NT][128 threads] floats
+  static constexpr int kXPart = 8 * NT * kXPitch;  // one 16-bit term of the tokens' 32 values
+  static constexpr int kStageBytes = (kUnitBytes + 3 * kXPart + 1023) / 1024 * 1024;
+  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kHandOff = kBarOff + 256;  // sums handed over: [2][16 NT][128 threads] floats
   static_assert(2 * kStages * 8 <= 256, "barriers");
-  static constexpr int kSmem = kHandOff + 2 * kGroup * 8 * NT * 4 + 1024;  // 1024: the ring's alignment
+  static constexpr int kSmem = kHandOff + 2 * kGroup * 16 * NT * 4 + 1024;  // 1024: the ring's alignment
 };
 static_assert(2 * kMaxCtas <= kCutCounters, "a counter per product and CTA");
 }  // namespace moet
 
 struct MoeTokParams {
-  CUtensorMap gate, up, down;  // {columns, rows, E}, box {64, 64, 1}
+  CUtensorMap gate, up, down;  // {columns, rows, E}, box {64, 32, 1}
   Common common;
   const __nv_bfloat16* x;
   const float* logits;
@@ -64,7 +68,7 @@ struct MoeTokParams {
   float* gates_out;
   __nv_bfloat16* h;    // [3][T topk][F]: h = h0 + h1 + h2, rows in the order (expert, t, j)
   float* y;            // [T topk][H]
-  float* part;         // [product][CTA][2][8 NT][128 threads] sums of a cut tile
+  float* part;         // [product][CTA][2][16 NT][128 threads] sums of a cut tile
   unsigned* cut_ctr;   // [product][CTA]: CTAs done with the cut tile that starts in this one
   unsigned* item_ctr;  // [item]: tiles done, of both products
   unsigned* tok_ctr;   // [token][column block]: rows done
@@ -211,15 +215,6 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
   __syncthreads();
 }
 
-// Four pairs of a 16-byte part of x (or h) in the order that thread t uses them: pair (i + t) mod 4 i-th.
-__device__ __forceinline__ void rotate_pairs(const uint4& v, int t, uint32_t (&r)[4]) {
-  const uint32_t a0 = t & 1 ? v.y : v.x, a1 = t & 1 ? v.z : v.y, a2 = t & 1 ? v.w : v.z, a3 = t & 1 ? v.x : v.w;
-  r[0] = t & 2 ? a2 : a0;
-  r[1] = t & 2 ? a3 : a1;
-  r[2] = t & 2 ? a0 : a2;
-  r[3] = t & 2 ? a1 : a3;
-}
-
 // One warp: the gates of a token (lane j < topk has gate j), the softmax over all E logits taken at
 // its experts.
 __device__ __forceinline__ float token_gate(const MoeTokParams& p, const MoeTables& tb, int tok, int lane) {
@@ -274,14 +269,14 @@ __device__ __forceinline__ bool wait_item(const unsigned* ctr, unsigned want, co
 // A CTA's range of one product's line of units (item by item, column block by column block, k).
 template <bool Down>
 struct MoeLine {
-  static constexpr int kCols = Down ? 128 : 64;  // columns of a tile
+  static constexpr int kCols = Down ? 256 : 128;  // columns of a tile
   int K, N, nk, nc, n;
   uint32_t per, first;
   int item0, col0, k0;
   __device__ __forceinline__ MoeLine(const MoeTokParams& p, int items) {
     K = Down ? p.F : p.H;
     N = Down ? p.H : p.F;
-    nk = (K + 63) / 64;
+    nk = (K + moet::kRows - 1) / moet::kRows;
     nc = (N + kCols - 1) / kCols;
     const uint32_t total = static_cast<uint32_t>(items) * nc * nk;
     per = (total + gridDim.x - 1) / gridDim.x;
@@ -300,21 +295,81 @@ struct MoeLine {
   }
 };
 
-// The loads of a line, by one thread; u counts units over both lines.
-template <bool Down, int kStages>
-__device__ __forceinline__ bool moet_load(const MoeTokParams& p, const MoeTables& tb, uint8_t* ring, uint64_t* full,
-                                          uint64_t* empty, int& u) {
+// The rows of an item.
+template <int NT>
+__device__ __forceinline__ int item_rows(const MoeTables& tb, int item, int& row0) {
+  row0 = tb.item_row[item];
+  const int end = tb.start[tb.item_expert[item] + 1];
+  return end - row0 < 8 * NT ? end - row0 : 8 * NT;
+}
+
+// The loads of a line's weights, by one thread; u counts units over both lines.
+template <bool Down, int NT>
+__device__ __forceinline__ bool moet_load_w(const MoeTokParams& p, const MoeTables& tb, uint8_t* ring, uint64_t* full,
+                                            uint64_t* empty, int& u) {
   using namespace moet;
+  using R = Ring<NT>;
   const MoeLine<Down> ln(p, tb.items);
   int item = ln.item0, col = ln.col0, k = ln.k0;
   for (int i = 0; i < ln.n; ++i, ++u) {
-    const int s = u % kStages;
-    if (!mbar_wait(&empty[s], ((u / kStages) & 1) ^ 1, p.common, kSiteEmpty)) return false;
+    const int s = u % R::kStages;
+    if (!mbar_wait(&empty[s], ((u / R::kStages) & 1) ^ 1, p.common, kSiteEmpty)) return false;
     mbar_arrive_expect_tx(&full[s], kUnitBytes);
-    const int e = tb.item_expert[item];
-    uint8_t* dst = ring + s * kUnitBytes;
-    tma_load_3d(dst, Down ? &p.down : &p.gate, &full[s], col * ln.kCols, k * 64, e);
-    tma_load_3d(dst + kUnitBytes / 2, Down ? &p.down : &p.up, &full[s], col * ln.kCols + (Down ? 64 : 0), k * 64, e);
+    const int e = tb.item_expert[item], x = col * ln.kCols, y = k * kRows;
+    uint8_t* dst = ring + s * R::kStageBytes;
+#pragma unroll
+    for (int box = 0; box < 4; ++box)
+      tma_load_3d(dst + box * kBox, Down ? &p.down : box < 2 ? &p.gate : &p.up, &full[s], x + 64 * (Down ? box : box & 1), y, e);
+    if (++k == ln.nk) {
+      k = 0;
+      ln.next_tile(item, col);
+    }
+  }
+  return true;
+}
+
+// Bytes of global to shared memory (both 16-byte aligned, a multiple of 16 of them), counted on a barrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The tokens' 32 values of x, or of the three terms of h, for each unit, by one warp.
+template <bool Down, int NT>
+__device__ __forceinline__ bool moet_load_x(const MoeTokParams& p, const MoeTables& tb, uint8_t* ring, uint64_t* full,
+                                            uint64_t* empty, int& u) {
+  using namespace moet;
+  using R = Ring<NT>;
+  const MoeLine<Down> ln(p, tb.items);
+  const int lane = threadIdx.x & 31, r = lane & 15, q0 = lane >> 4;
+  const int nc1 = (p.F + MoeLine<false>::kCols - 1) / MoeLine<false>::kCols;  // tiles of an item in the first product
+  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  int item = ln.item0, col = ln.col0, k = ln.k0, seen = -1, rows = 0;
+  const __nv_bfloat16* src = nullptr;
+  for (int i = 0; i < ln.n; ++i, ++u) {
+    if (item != seen) {
+      seen = item;
+      if (Down) {
+        if (!wait_item(p.item_ctr + item, nc1, p.common, lane)) return false;
+        fence_proxy_async_global();  // h was written by ordinary stores, and is read by bulk copies
+      }
+      int row0;
+      rows = item_rows<NT>(tb, item, row0);
+      const int row = row0 + (r < rows ? r : 0);
+      src = Down ? p.h + static_cast<size_t>(row) * p.F : p.x + static_cast<size_t>(tb.order[row] / p.topk) * p.H;
+    }
+    const int s = u % R::kStages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / R::kStages) & 1) ^ 1, p.common, kSiteEmpty))) return false;
+    const int left = ln.K - k * kRows;
+    const uint32_t bytes = 2 * (left < kRows ? left : kRows);
+    uint8_t* dst = ring + s * R::kStageBytes + kUnitBytes;
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], rows * (Down ? 3 : 1) * bytes);
+    __syncwarp();
+    if (r < rows)
+#pragma unroll
+      for (int q = q0; q < (Down ? 3 : 1); q += 2)
+        bulk_load(dst + q * R::kXPart + r * kXPitch, src + q * plane + k * kRows, bytes, &full[s]);
     if (++k == ln.nk) {
       k = 0;
       ln.next_tile(item, col);
@@ -332,135 +387,69 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
   constexpr int kStages = R::kStages;
   constexpr int kParts = Down ? 3 : 1;  // 16-bit terms of the left operand
   const MoeLine<Down> ln(p, tb.items);
-  const int nk = ln.nk, K = ln.K, N = ln.N, n = ln.n;
+  const int nk = ln.nk, N = ln.N, n = ln.n;
   const uint32_t per = ln.per, first = ln.first;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wq = warp & 3, tid = threadIdx.x & (kGroup - 1), g = lane >> 2, t = lane & 3;
   const int grp = warp >> 2, par = (u0 ^ grp) & 1;  // this group's units are those with i & 1 == par
-  const int nc1 = Down ? (p.F + 63) / 64 : 0;       // tiles of an item in the first product
-  // the rows of an item
-  auto item_rows = [&](int item, int& row0) {
-    row0 = tb.item_row[item];
-    const int end = tb.start[tb.item_expert[item] + 1];
-    return end - row0 < 8 * NT ? end - row0 : 8 * NT;
-  };
-  // This thread's part of the left operand for the next unit of its group, loaded a unit ahead.
-  // Columns past the item's rows hold whatever row 0 has: a column of the products depends on no
-  // other, and those are not stored.
-  int x_item = ln.item0, x_col = ln.col0, x_k = ln.k0, x_rows = 0, x_seen = -1;
-  uint4 xv[kParts][NT][2];
-  uint32_t src[NT];  // elements, below 2^27
-  const __nv_bfloat16* base = Down ? p.h : p.x;
-  const uint32_t plane = static_cast<uint32_t>(p.T) * p.topk * p.F;
-  auto x_tile = [&]() {
-    if (x_item == x_seen) return;
-    x_seen = x_item;
-    if (Down && ok) ok = wait_item(p.item_ctr + x_item, nc1, p.common, lane);
-    int row0;
-    x_rows = item_rows(x_item, row0);
+  const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
+  // Weights, 16 columns m of this warp: rows k are lines of 128 bytes, their 16-byte chunks permuted by k
+  // mod 8; ldmatrix matrices 0, 1: rows 0-7, columns 0-7 and 8-15; 2, 3: rows 8-15.  First product:
+  // m = 0, 1 gate, 2, 3 up, columns 32 wq of the tile on; second: columns 64 wq on.
+  uint32_t w_off[4];
 #pragma unroll
-    for (int b = 0; b < NT; ++b) {
-      const int r = row0 + (8 * b + g < x_rows ? 8 * b + g : 0);
-      src[b] = (Down ? r : tb.order[r] / p.topk) * static_cast<uint32_t>(K) + 8 * t;
-    }
-  };
-  auto x_step = [&]() {
-    if (++x_k == nk) {
-      x_k = 0;
-      ln.next_tile(x_item, x_col);
-    }
-  };
-  auto load_x = [&]() {
-    const int left = K - x_k * 64 - 8 * t;  // the last unit's rows past K meet zero weights, and have to be finite
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-      if (8 * b < x_rows)
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            // h from L2: a line of L1 could hold a neighbour row that is not written yet
-            const uint4* at = reinterpret_cast<const uint4*>(base + (src[b] + q * plane + x_k * 64 + 32 * w));
-            if (32 * w < left)
-              xv[q][b][w] = Down ? __ldcg(at) : __ldg(at);
-            else
-              xv[q][b][w] = make_uint4(0u, 0u, 0u, 0u);
-          }
-  };
-  if (par && n > 1) x_step();
-  if (par < n) {
-    x_tile();
-    load_x();
+  for (int m = 0; m < 4; ++m) {
+    const int box = Down ? wq : (wq >> 1) + (m & 2), chunk = (Down ? 2 * m : 4 * (wq & 1) + 2 * (m & 1)) + ((lane >> 3) & 1);
+    w_off[m] = box * kBox + ((lane & 7) + ((lane >> 4) << 3)) * 128 + ((chunk ^ (lane & 7)) << 4);
   }
-  // ldmatrix rows: lane l gives row l & 7 of matrix l >> 3; matrices 0, 1: k pairs 2s, columns 0-7 and
-  // 8-15; matrices 2, 3: k pairs 2s + 1
-  const int lt = (lane & 7) >> 1, lbit = lane & 1, lhi = lane >> 4, lcol = (lane >> 3) & 1;
+  const uint32_t x_off = kUnitBytes + (lane & 7) * kXPitch + (lane >> 3) * 16;  // tokens 0-7, 8 of the 32 values per matrix
   float* hand = reinterpret_cast<float*>(ring + R::kHandOff) + tid * 4;
-  float acc[2][NT][4];
+  float acc[4][NT][4];
   int item = ln.item0, col = ln.col0;
   for (int begin = 0; begin < n; ++segs) {
     // this CTA's units [begin, end) of one tile
     const uint32_t tile = (first + begin) / nk;
-    const int left = static_cast<int>((tile + 1) * nk - (first + begin));
+    const int k0 = static_cast<int>(first + begin - tile * nk), left = nk - k0;
     const int end = left < n - begin ? begin + left : n;
     int row0;
-    const int rows = item_rows(item, row0);
+    const int rows = item_rows<NT>(tb, item, row0);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
     for (int i = begin + ((begin ^ par) & 1); i < end; i += 2) {
-      uint32_t xr[2][kParts][NT][4];
+      const int s = (u0 + i) % kStages;
+      if (ok)  // the same in all lanes; after a timeout: on, without waits
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ((u0 + i) / kStages) & 1, p.common, kSiteFull));
+      const uint32_t st = smem_u32(ring + s * R::kStageBytes);
+      uint32_t x[NT][kParts][4];
 #pragma unroll
       for (int b = 0; b < NT; ++b)
         if (8 * b < rows)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int q = 0; q < kParts; ++q) {
+            ldsm4(x[b][q], st + x_off + q * R::kXPart + b * 8 * kXPitch);
+            const int there = ln.K - (k0 + i - begin) * kRows;  // the last unit's values past K: not copied, meet zero weights
+            if (there < kRows)
 #pragma unroll
-            for (int q = 0; q < kParts; ++q) {
-              if constexpr (Down) {  // h is stored in the order of use
-                xr[h][q][b][0] = xv[q][b][h].x;
-                xr[h][q][b][1] = xv[q][b][h].y;
-                xr[h][q][b][2] = xv[q][b][h].z;
-                xr[h][q][b][3] = xv[q][b][h].w;
-              } else {
-                rotate_pairs(xv[q][b][h], t, xr[h][q][b]);
-              }
-            }
-      if (i + 2 < n) {
-        x_step();
-        x_step();
-        x_tile();
-        load_x();
-      }
-      const int s = (u0 + i) % kStages;
-      if (ok)  // the same in all lanes; after a timeout: on, without waits
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ((u0 + i) / kStages) & 1, p.common, kSiteFull));
-      const uint32_t w = smem_u32(ring + s * kUnitBytes);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2) {
-          const int kr = 32 * h + 8 * lt + 2 * ((2 * s2 + lhi + lt) & 3) + lbit;
-          uint32_t a[2][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            // first product: m = gate, up, columns 16 wq of each; second: columns 32 wq + 16 m
-            const int chunk = (Down ? 4 * (wq & 1) + 2 * m : 2 * wq) + lcol;
-            const uint32_t box = w + (Down ? (wq >> 1) : m) * (kUnitBytes / 2);
-            ldsm4t(a[m], box + kr * 128 + ((chunk ^ (kr & 7)) << 4));
+              for (int j = 1; j < 4; ++j)
+                if (8 * j >= there) x[b][q][j] = 0u;
           }
 #pragma unroll
-          for (int b = 0; b < NT; ++b)
-            if (8 * b < rows)
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[4][4];
 #pragma unroll
-              for (int q = 0; q < kParts; ++q)
+        for (int m = 0; m < 4; ++m) ldsm4t(a[m], st + w_off[m] + h * 2048);
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  mma16816<__nv_bfloat16>(acc[m][b], a[m], xr[h][q][b][2 * s2], xr[h][q][b][2 * s2 + 1]);
-        }
+        for (int b = 0; b < NT; ++b)
+          if (8 * b < rows)
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) mma16816<__nv_bfloat16>(acc[m][b], a[m], x[b][q][2 * h], x[b][q][2 * h + 1]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
@@ -473,11 +462,11 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     const uint32_t seg_first = first + begin;
     begin = end;
     ln.next_tile(item, col);
-    float* buf = hand + (segs & 1) * kGroup * 8 * NT;
+    float* buf = hand + (segs & 1) * kGroup * 16 * NT;
     const uint32_t bar = 1 + (segs & 1);
     if ((segs & 1) != grp) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
           if (8 * b < rows)
@@ -487,7 +476,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     }
     named_bar_sync(bar, 2 * kGroup);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int b = 0; b < NT; ++b)
         if (8 * b < rows) {
@@ -501,12 +490,12 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
       // (each product has parts and counters of its own: a CTA is in the second one while its
       // neighbour still works on their common tile of the first)
       const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
-      constexpr int kSlot = kGroup * 8 * NT;
+      constexpr int kSlot = kGroup * 16 * NT;
       float* parts = p.part + (Down ? static_cast<size_t>(kMaxCtas) * 2 * kSlot : 0);
       unsigned* ctr = p.cut_ctr + (Down ? kMaxCtas : 0) + c0;
       float* part = parts + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot + tid * 4;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
           if (8 * b < rows)
@@ -519,40 +508,35 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
       named_bar_sync(3, kGroup);
       if (!tb.last) continue;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int b = 0; b < NT; ++b)
+        if (8 * b < rows) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
+          for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
-      const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + tid * 4;  // slot 1 starts a tile
-      for (uint32_t c = c0; c <= c1;) {
-        constexpr int kBatch = 4;
-        float4 v[kBatch][2][NT];
+            for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
+          const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + b * kGroup * 4 + tid * 4;  // slot 1 starts a tile
+          for (uint32_t c = c0; c <= c1;) {
+            constexpr int kBatch = 4;
+            float4 v[kBatch][4];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
+            for (int x = 0; x < kBatch; ++x) {
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int b = 0; b < NT; ++b) {
-              v[x][m][b] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (c + x <= c1 && 8 * b < rows)
-                v[x][m][b] = __ldcg(reinterpret_cast<const float4*>(from + (m * NT + b) * kGroup * 4));
+              for (int m = 0; m < 4; ++m)
+                v[x][m] = c + x <= c1 ? __ldcg(reinterpret_cast<const float4*>(from + m * NT * kGroup * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              from += c + x == c0 ? kSlot : 2 * kSlot;
             }
-          from += c + x == c0 ? kSlot : 2 * kSlot;
+            c += kBatch;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                acc[m][b][0] += v[x][m].x;
+                acc[m][b][1] += v[x][m].y;
+                acc[m][b][2] += v[x][m].z;
+                acc[m][b][3] += v[x][m].w;
+              }
+          }
         }
-        c += kBatch;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int b = 0; b < NT; ++b) {
-              acc[m][b][0] += v[x][m][b].x;
-              acc[m][b][1] += v[x][m][b].y;
-              acc[m][b][2] += v[x][m][b].z;
-              acc[m][b][3] += v[x][m][b].w;
-            }
-      }
     }
 #pragma unroll
     for (int b = 0; b < NT; ++b)
@@ -561,22 +545,24 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
         const int r = 8 * b + 2 * t + (j & 1);  // columns of the products are rows of the item
         if (r >= rows) continue;
         if constexpr (!Down) {
-          const int f = this_col * 64 + wq * 16 + g + 8 * (j >> 1);
-          if (f < N) {
-            const float a = acc[0][b][j], v = a / (1.f + expf(-a)) * acc[1][b][j];
-            const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
-            const float r1 = v - __bfloat162float(h0);
-            const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
-            // pair (k / 2) mod 4 of part (k / 8) mod 4 of 32 lies where that thread uses it
-            const size_t at = static_cast<size_t>(row0 + r) * p.F + ((f & ~7) | ((((f >> 1) - (f >> 3)) & 3) << 1) | (f & 1));
-            p.h[at] = h0;
-            p.h[plane + at] = h1;
-            p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int f = this_col * ln.kCols + wq * 32 + m * 16 + g + 8 * (j >> 1);
+            if (f < N) {
+              const float a = acc[m][b][j], v = a / (1.f + expf(-a)) * acc[2 + m][b][j];
+              const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
+              const float r1 = v - __bfloat162float(h0);
+              const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
+              const size_t at = static_cast<size_t>(row0 + r) * p.F + f;
+              p.h[at] = h0;
+              p.h[plane + at] = h1;
+              p.h[2 * plane + at] = __float2bfloat16_rn(r1 - __bfloat162float(h1));
+            }
           }
         } else {
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const int c = this_col * 128 + wq * 32 + m * 16 + g + 8 * (j >> 1);
+          for (int m = 0; m < 4; ++m) {
+            const int c = this_col * ln.kCols + wq * 64 + m * 16 + g + 8 * (j >> 1);
             if (c < N) p.y[static_cast<size_t>(row0 + r) * p.H + c] = acc[m][b][j];
           }
         }
@@ -595,6 +581,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           if (done) *ctr = 0u;
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, done);
+        const int nc1 = (p.F + MoeLine<false>::kCols - 1) / MoeLine<false>::kCols;
         if (lane == 0) {
           tb.last = mask;
           if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
@@ -602,9 +589,9 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
       }
       named_bar_sync(3, kGroup);
       uint32_t mask = tb.last;
-      for (int x = 0; mask; ++x, mask &= mask - 1) {
-        if ((x & 3) != wq) continue;
-        const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * 128 + lane * 4;
+      for (int x = 0; mask; ++x, mask &= mask - 1) {  // two tokens at a time, half a block per warp
+        if ((x & 1) != (wq >> 1)) continue;
+        const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * ln.kCols + (wq & 1) * 128 + lane * 4;
         float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < kMaxTopk; ++j) {
@@ -619,7 +606,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           if (j < p.topk) sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
         }
         if (c < N) *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
-        if (this_col == 0 && lane < p.topk) {
+        if (this_col == 0 && (wq & 1) == 0 && lane < p.topk) {
           if (p.experts_out) p.experts_out[tok * p.topk + lane] = tb.expert[tok * p.topk + lane];
           if (p.gates_out) p.gates_out[tok * p.topk + lane] = gate;
         }
@@ -641,7 +628,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   uint64_t* empty = full + kStages;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);   // weights, x
       mbar_init(&empty[s], 4);  // the warps of one group
     }
     fence_mbar_init();
@@ -651,11 +638,17 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   }
   moet_tables(p, tb, 8 * NT);
   if (threadIdx.x >= 2 * kGroup) {
-    if (threadIdx.x == 2 * kGroup) {
-      int u = 0;
-      const bool ok = moet_load<false, kStages>(p, tb, ring, full, empty, u) && moet_load<true, kStages>(p, tb, ring, full, empty, u);
-      if (!ok)  // gave up: what was issued has landed before the CTA ends
-        for (int j = u > kStages ? u - kStages : 0; j < u; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1, p.common, kSiteDrain);
+    int u = 0;
+    bool ok = true;
+    const bool one = (threadIdx.x & 31) == 0;
+    if (threadIdx.x >= 2 * kGroup + 32)
+      ok = moet_load_x<false, NT>(p, tb, ring, full, empty, u) && moet_load_x<true, NT>(p, tb, ring, full, empty, u);
+    else if (one)
+      ok = moet_load_w<false, NT>(p, tb, ring, full, empty, u) && moet_load_w<true, NT>(p, tb, ring, full, empty, u);
+    if (!ok && one) {
+      // Gave up: what was issued lands before the CTA ends (bounded: the other warp may not have joined
+      // in a stage's barrier, and then the wait runs out long after the copies are in).
+      for (int j = u > kStages ? u - kStages : 0; j < u; ++j) mbar_wait(&full[j % kStages], (j / kStages) & 1, p.common, kSiteDrain);
     }
     return;
   }
@@ -687,7 +680,7 @@ static MoetLayout moet_layout(int T, int H, int F, int topk) {
   L.h = kCounterBytes;
   L.y = L.h + align256(3 * a * F * 2);
   L.part = L.y + align256(a * H * 4);
-  L.total = L.part + 2 * static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 8 * moet_eights(T) * 4;
+  L.total = L.part + 2 * static_cast<size_t>(moet::kMaxCtas) * 2 * moet::kGroup * 16 * moet_eights(T) * 4;
   return L;
 }
 
@@ -734,8 +727,8 @@ extern "C" int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, in
   MoeTokParams p;
   std::memset(&p, 0, sizeof(p));
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!tmap_3d(&p.gate, BF, 2, w_gate, F, H, E, 64, 64, 1) || !tmap_3d(&p.up, BF, 2, w_up, F, H, E, 64, 64, 1) ||
-      !tmap_3d(&p.down, BF, 2, w_down, H, F, E, 64, 64, 1))
+  if (!tmap_3d(&p.gate, BF, 2, w_gate, F, H, E, 64, moet::kRows, 1) || !tmap_3d(&p.up, BF, 2, w_up, F, H, E, 64, moet::kRows, 1) ||
+      !tmap_3d(&p.down, BF, 2, w_down, H, F, E, 64, moet::kRows, 1))
     return TL_ERR_CUDA;
   p.common = make_common(ctx);
   p.common.trace_hdr = nullptr;  // this kernel records no trace spans
