@@ -53,6 +53,7 @@ struct Ring {
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kHandOff = kBarOff + 256;  // sums handed over: [2][16 NT][128 threads] floats
   static_assert(2 * kStages * 8 <= 256, "barriers");
+  static_assert(2 * kGroup * 16 * NT * 4 >= kMaxA / 32 * kMaxE * 2, "the routing's counts go there first");
   static constexpr int kSmem = kHandOff + 2 * kGroup * 16 * NT * 4 + 1024;  // 1024: the ring's alignment
 };
 static_assert(2 * kMaxCtas <= kCutCounters, "a counter per product and CTA");
@@ -78,6 +79,8 @@ struct MoeTokParams {
 // What a CTA derives from the logits.
 struct MoeTables {
   alignas(16) uint8_t expert[moet::kMaxA];  // of assignment a = t topk + j
+  uint8_t rank[moet::kMaxA];     // among the assignments of the same expert in its group of 32
+  float gate[moet::kMaxA];       // of assignment a
   uint16_t at[moet::kMaxA];      // row of assignment a
   uint16_t order[moet::kMaxA];   // assignment of a row
   uint16_t start[moet::kMaxE + 1];  // rows of expert e: [start[e], start[e + 1])
@@ -94,79 +97,106 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 }
 
 // One warp: the topk experts of tokens t, t + step, .. (kBatch of them, below T), best first, ties to
-// the lower index.  Lane l holds experts l, l + 32, ...; key 0 marks "none" (below the key of -inf).
-// Several tokens at a time, because each is a chain of loads and reductions.
-template <int kBatch>
-__device__ __forceinline__ void route_tokens(const MoeTokParams& p, int t, int step, int lane, uint8_t* experts) {
-  constexpr int kPer = moet::kMaxE / 32;
+// the lower index, and their gates: the softmax over all E logits taken there.  Lane l holds experts
+// l, l + 32, ...; key 0 marks "none" (below the key of -inf).  Several tokens at a time, because each
+// is a chain of loads and reductions.
+template <int kBatch, int kPer>
+__device__ __forceinline__ void route_tokens(const MoeTokParams& p, int t, int step, int lane, MoeTables& tb) {
   uint32_t key[kBatch][kPer];
+  float top[kBatch], sum[kBatch], all[kBatch];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
+  for (int b = 0; b < kBatch; ++b) {
+    float v[kPer];
+    const float* row = p.logits + static_cast<size_t>(t + b * step < p.T ? t + b * step : t) * p.E;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      key[b][i] = 0u;
-      if (32 * i < p.E && lane + 32 * i < p.E && t + b * step < p.T)
-        key[b][i] = logit_key(__ldg(p.logits + static_cast<size_t>(t + b * step) * p.E + lane + 32 * i));
+    for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < p.E ? __ldg(row + lane + 32 * i) : 0.f;
+    top[b] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      key[b][i] = lane + 32 * i < p.E ? logit_key(v[i]) : 0u;
+      if (lane + 32 * i < p.E) top[b] = fmaxf(top[b], v[i]);
     }
-  for (int j = 0; j < p.topk; ++j) {
-    uint32_t best[kBatch], e[kBatch];
-    int at[kBatch];
+    sum[b] = 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < p.E) sum[b] += expf(v[i] - top[b]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
+    all[b] = 0.f;
+  }
+  for (int j = 0; j < p.topk; ++j)
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      best[b] = key[b][0];
-      at[b] = 0;
-    }
+      uint32_t best = key[b][0];
+      int at = 0;
 #pragma unroll
-    for (int i = 1; i < kPer; ++i)
-      if (32 * i < p.E)
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-          if (key[b][i] > best[b]) {
-            best[b] = key[b][i];
-            at[b] = i;
-          }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best[b]);
-      e[b] = __reduce_min_sync(0xffffffffu, best[b] == top ? lane + 32 * at[b] : 0xffffffffu);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
+      for (int i = 1; i < kPer; ++i)
+        if (key[b][i] > best) {
+          best = key[b][i];
+          at = i;
+        }
+      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+      const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : 0xffffffffu);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (static_cast<uint32_t>(lane + 32 * i) == e[b]) key[b][i] = 0u;
-      if (lane == 0 && t + b * step < p.T) experts[(t + b * step) * p.topk + j] = static_cast<uint8_t>(e[b]);
+        if (static_cast<uint32_t>(lane + 32 * i) == e) key[b][i] = 0u;
+      const float v = __uint_as_float(high & 0x80000000u ? high & 0x7fffffffu : ~high);  // of the key (NaN: the sum is NaN too)
+      const float gate = expf(v - top[b]) / sum[b];
+      all[b] += gate;
+      if (lane == 0 && t + b * step < p.T) {
+        tb.expert[(t + b * step) * p.topk + j] = static_cast<uint8_t>(e);
+        tb.gate[(t + b * step) * p.topk + j] = gate;
+      }
     }
+  if (p.renorm) {
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (lane < p.topk && t + b * step < p.T) tb.gate[(t + b * step) * p.topk + lane] /= all[b];
   }
 }
 
-// Bytes of the 16 experts from assignment a0 on that are e, a bit each (bit 8 i of word w: a0 + 4 w + i).
-__device__ __forceinline__ uint32_t same_expert(uint32_t word, uint32_t e4, int left) {
-  const uint32_t eq = __vcmpeq4(word, e4) & 0x01010101u;
-  return left >= 4 ? eq : left <= 0 ? 0u : eq & ((1u << (8 * left)) - 1u);
+template <int kPer>
+__device__ __forceinline__ void route_all(const MoeTokParams& p, int warp, int lane, MoeTables& tb) {
+  constexpr int kWarps = moet::kThreads / 32, kBatch = 8 / kPer;
+  if (p.T <= kWarps) {
+    if (warp < p.T) route_tokens<1, kPer>(p, warp, kWarps, lane, tb);
+  } else {
+    for (int t = warp; t < p.T; t += kBatch * kWarps) route_tokens<kBatch, kPer>(p, t, kWarps, lane, tb);
+  }
 }
 
-// All threads of the CTA: routing, order and items (groups of `group` rows of an expert).
-__device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb, int group) {
-  constexpr int kWarps = moet::kThreads / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.topk;
-  if (p.T <= kWarps) {
-    if (warp < p.T) route_tokens<1>(p, warp, kWarps, lane, tb.expert);
-  } else {
-    for (int t = warp; t < p.T; t += 4 * kWarps) route_tokens<4>(p, t, kWarps, lane, tb.expert);
+// All threads of the CTA: routing, order and items (groups of `group` rows of an expert).  `seen`:
+// a count for each 32 assignments and expert, 16 KB of shared memory that nothing else uses yet.
+__device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb, uint16_t* seen, int group) {
+  using namespace moet;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.topk, chunks = (n + 31) / 32;
+  for (int i = threadIdx.x; i < chunks * p.E; i += kThreads) seen[i] = 0;
+  if (p.E <= 64)
+    route_all<2>(p, warp, lane, tb);
+  else
+    route_all<8>(p, warp, lane, tb);
+  __syncthreads();
+  for (int c = warp; c < chunks; c += kThreads / 32) {
+    const int a = 32 * c + lane;
+    const uint32_t same = __match_any_sync(0xffffffffu, a < n ? static_cast<uint32_t>(tb.expert[a]) : 0x100u + lane);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (a < n) {
+      tb.rank[a] = static_cast<uint8_t>(rank);
+      if (rank == 0) seen[c * p.E + tb.expert[a]] = static_cast<uint16_t>(__popc(same));
+    }
   }
   __syncthreads();
-  // the count of each expert: a byte compare over all assignments, 16 at a time
-  const uint4* words = reinterpret_cast<const uint4*>(tb.expert);
-  for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
-    const uint32_t e4 = e * 0x01010101u;
-    int c = 0;
-    for (int a = 0; a < n; a += 16) {
-      const uint4 w = words[a >> 4];
-      c += __popc(same_expert(w.x, e4, n - a)) + __popc(same_expert(w.y, e4, n - a - 4)) +
-           __popc(same_expert(w.z, e4, n - a - 8)) + __popc(same_expert(w.w, e4, n - a - 12));
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {  // counts become the rows before each group of 32
+    int sum = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int here = seen[c * p.E + e];
+      seen[c * p.E + e] = static_cast<uint16_t>(sum);
+      sum += here;
     }
-    tb.start[e + 1] = static_cast<uint16_t>(c);
+    tb.start[e + 1] = static_cast<uint16_t>(sum);
   }
   __syncthreads();
   if (warp == 0) {
@@ -196,44 +226,12 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += moet::kThreads) {
-    int r = tb.start[e];
-    const int end = tb.start[e + 1];
-    const uint32_t e4 = e * 0x01010101u;
-    for (int a = 0; r < end; a += 16) {
-      const uint4 w = words[a >> 4];
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        for (uint32_t eq = same_expert(in[x], e4, n - a - 4 * x); eq; eq &= eq - 1) {
-          const int at = a + 4 * x + ((__ffs(eq) - 1) >> 3);
-          tb.at[at] = static_cast<uint16_t>(r);
-          tb.order[r++] = static_cast<uint16_t>(at);
-        }
-    }
+  for (int a = threadIdx.x; a < n; a += kThreads) {
+    const int e = tb.expert[a], row = tb.start[e] + seen[(a >> 5) * p.E + e] + tb.rank[a];
+    tb.at[a] = static_cast<uint16_t>(row);
+    tb.order[row] = static_cast<uint16_t>(a);
   }
   __syncthreads();
-}
-
-// One warp: the gates of a token (lane j < topk has gate j), the softmax over all E logits taken at
-// its experts.
-__device__ __forceinline__ float token_gate(const MoeTokParams& p, const MoeTables& tb, int tok, int lane) {
-  const float* row = p.logits + static_cast<size_t>(tok) * p.E;
-  float top = -INFINITY, sum = 0.f;
-  for (int e = lane; e < p.E; e += 32) top = fmaxf(top, __ldg(row + e));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  for (int e = lane; e < p.E; e += 32) sum += expf(__ldg(row + e) - top);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  float gate = lane < p.topk ? expf(__ldg(row + tb.expert[tok * p.topk + lane]) - top) / sum : 0.f;
-  if (p.renorm) {
-    float all = gate;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);  // topk <= 8
-    gate /= all;
-  }
-  return gate;
 }
 
 // Adds to a counter, releasing what this thread has seen and acquiring what others released; the sum.
@@ -328,48 +326,47 @@ __device__ __forceinline__ bool moet_load_w(const MoeTokParams& p, const MoeTabl
   return true;
 }
 
-// Bytes of global to shared memory (both 16-byte aligned, a multiple of 16 of them), counted on a barrier.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// Arrive on a barrier (one of its counted arrivals) once this thread's earlier cp.async have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The tokens' 32 values of x, or of the three terms of h, for each unit, by one warp.
+// The tokens' 32 values of x, or of the three terms of h, for each unit, by one warp: lane l copies
+// 16 bytes, values 8 (l mod 4) on, of rows l / 4 and l / 4 + 8.
 template <bool Down, int NT>
 __device__ __forceinline__ bool moet_load_x(const MoeTokParams& p, const MoeTables& tb, uint8_t* ring, uint64_t* full,
                                             uint64_t* empty, int& u) {
   using namespace moet;
   using R = Ring<NT>;
   const MoeLine<Down> ln(p, tb.items);
-  const int lane = threadIdx.x & 31, r = lane & 15, q0 = lane >> 4;
+  const int lane = threadIdx.x & 31, r = lane >> 2, ch = lane & 3;
   const int nc1 = (p.F + MoeLine<false>::kCols - 1) / MoeLine<false>::kCols;  // tiles of an item in the first product
   const size_t plane = static_cast<size_t>(p.T) * p.topk * p.F;
   int item = ln.item0, col = ln.col0, k = ln.k0, seen = -1, rows = 0;
-  const __nv_bfloat16* src = nullptr;
+  const __nv_bfloat16* src[NT];
   for (int i = 0; i < ln.n; ++i, ++u) {
     if (item != seen) {
       seen = item;
-      if (Down) {
-        if (!wait_item(p.item_ctr + item, nc1, p.common, lane)) return false;
-        fence_proxy_async_global();  // h was written by ordinary stores, and is read by bulk copies
-      }
+      if (Down && !wait_item(p.item_ctr + item, nc1, p.common, lane)) return false;
       int row0;
       rows = item_rows<NT>(tb, item, row0);
-      const int row = row0 + (r < rows ? r : 0);
-      src = Down ? p.h + static_cast<size_t>(row) * p.F : p.x + static_cast<size_t>(tb.order[row] / p.topk) * p.H;
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        const int row = row0 + (r + 8 * b < rows ? r + 8 * b : 0);
+        src[b] = (Down ? p.h + static_cast<size_t>(row) * p.F : p.x + static_cast<size_t>(tb.order[row] / p.topk) * p.H) + 8 * ch;
+      }
     }
     const int s = u % R::kStages;
     if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((u / R::kStages) & 1) ^ 1, p.common, kSiteEmpty))) return false;
-    const int left = ln.K - k * kRows;
-    const uint32_t bytes = 2 * (left < kRows ? left : kRows);
-    uint8_t* dst = ring + s * R::kStageBytes + kUnitBytes;
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], rows * (Down ? 3 : 1) * bytes);
-    __syncwarp();
-    if (r < rows)
+    const uint32_t dst = smem_u32(ring + s * R::kStageBytes + kUnitBytes) + r * kXPitch + ch * 16;
+    const uint32_t bytes = k * kRows + 8 * ch < ln.K ? 16u : 0u;  // past K: zeros, nothing is read
 #pragma unroll
-      for (int q = q0; q < (Down ? 3 : 1); q += 2)
-        bulk_load(dst + q * R::kXPart + r * kXPitch, src + q * plane + k * kRows, bytes, &full[s]);
+    for (int b = 0; b < NT; ++b)
+      if (r + 8 * b < rows)
+#pragma unroll
+        for (int q = 0; q < (Down ? 3 : 1); ++q)
+          cp_async16(dst + q * R::kXPart + b * 8 * kXPitch, src[b] + (bytes ? q * plane + k * kRows : 0), bytes);
+    cp_async_arrive(&full[s]);
     if (++k == ln.nk) {
       k = 0;
       ln.next_tile(item, col);
@@ -409,7 +406,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
   for (int begin = 0; begin < n; ++segs) {
     // this CTA's units [begin, end) of one tile
     const uint32_t tile = (first + begin) / nk;
-    const int k0 = static_cast<int>(first + begin - tile * nk), left = nk - k0;
+    const int left = static_cast<int>((tile + 1) * nk - (first + begin));
     const int end = left < n - begin ? begin + left : n;
     int row0;
     const int rows = item_rows<NT>(tb, item, row0);
@@ -431,11 +428,6 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
             ldsm4(x[b][q], st + x_off + q * R::kXPart + b * 8 * kXPitch);
-            const int there = ln.K - (k0 + i - begin) * kRows;  // the last unit's values past K: not copied, meet zero weights
-            if (there < kRows)
-#pragma unroll
-              for (int j = 1; j < 4; ++j)
-                if (8 * j >= there) x[b][q][j] = 0u;
           }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -516,7 +508,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
             for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
           const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + b * kGroup * 4 + tid * 4;  // slot 1 starts a tile
           for (uint32_t c = c0; c <= c1;) {
-            constexpr int kBatch = 4;
+            constexpr int kBatch = NT == 1 ? 8 : 4;
             float4 v[kBatch][4];
 #pragma unroll
             for (int x = 0; x < kBatch; ++x) {
@@ -581,34 +573,33 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           if (done) *ctr = 0u;
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, done);
+        if (lane == 0) tb.last = mask;
+      } else if (tid == kGroup - 1) {
         const int nc1 = (p.F + MoeLine<false>::kCols - 1) / MoeLine<false>::kCols;
-        if (lane == 0) {
-          tb.last = mask;
-          if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
-        }
+        if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
       }
       named_bar_sync(3, kGroup);
       uint32_t mask = tb.last;
       for (int x = 0; mask; ++x, mask &= mask - 1) {  // two tokens at a time, half a block per warp
         if ((x & 1) != (wq >> 1)) continue;
         const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * ln.kCols + (wq & 1) * 128 + lane * 4;
-        float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < N) {
+          float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < kMaxTopk; ++j) {
-          v[j] = sum;
-          if (j < p.topk && c < N)
-            v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[tok * p.topk + j]) * p.H + c));
-        }
-        const float gate = token_gate(p, tb, tok, lane);
+          for (int j = 0; j < kMaxTopk; ++j)
+            if (j < p.topk)
+              v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[tok * p.topk + j]) * p.H + c));
 #pragma unroll
-        for (int j = 0; j < kMaxTopk; ++j) {
-          const float f = __shfl_sync(0xffffffffu, gate, j);
-          if (j < p.topk) sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
+          for (int j = 0; j < kMaxTopk; ++j)
+            if (j < p.topk) {
+              const float f = tb.gate[tok * p.topk + j];
+              sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
+            }
+          *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
         }
-        if (c < N) *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
         if (this_col == 0 && (wq & 1) == 0 && lane < p.topk) {
           if (p.experts_out) p.experts_out[tok * p.topk + lane] = tb.expert[tok * p.topk + lane];
-          if (p.gates_out) p.gates_out[tok * p.topk + lane] = gate;
+          if (p.gates_out) p.gates_out[tok * p.topk + lane] = tb.gate[tok * p.topk + lane];
         }
       }
     }
@@ -628,7 +619,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
   uint64_t* empty = full + kStages;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 2);   // weights, x
+      mbar_init(&full[s], 1 + 32);  // weights, a lane's x each
       mbar_init(&empty[s], 4);  // the warps of one group
     }
     fence_mbar_init();
@@ -636,7 +627,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
     tma_prefetch_map(&p.up);
     tma_prefetch_map(&p.down);
   }
-  moet_tables(p, tb, 8 * NT);
+  moet_tables(p, tb, reinterpret_cast<uint16_t*>(ring + R::kHandOff), 8 * NT);
   if (threadIdx.x >= 2 * kGroup) {
     int u = 0;
     bool ok = true;
@@ -645,6 +636,7 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
       ok = moet_load_x<false, NT>(p, tb, ring, full, empty, u) && moet_load_x<true, NT>(p, tb, ring, full, empty, u);
     else if (one)
       ok = moet_load_w<false, NT>(p, tb, ring, full, empty, u) && moet_load_w<true, NT>(p, tb, ring, full, empty, u);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && one) {
       // Gave up: what was issued lands before the CTA ends (bounded: the other warp may not have joined
       // in a stage's barrier, and then the wait runs out long after the copies are in).

@@ -166,9 +166,6 @@ __device__ __forceinline__ int paged_length(const PagedParams& p, int b, bool re
 }
 __device__ __forceinline__ int paged_tiles(int count) { return (count + paged::kTile - 1) / paged::kTile; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
