@@ -97,64 +97,82 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 }
 
 // One warp: the topk experts of tokens t, t + step, .. (kBatch of them, below T), best first, ties to
-// the lower index, and their gates: the softmax over all E logits taken there.  Lane l holds experts
-// l, l + 32, ...; key 0 marks "none" (below the key of -inf).  Several tokens at a time, because each
-// is a chain of loads and reductions.
+// the lower index.  Lane l holds experts l, l + 32, ...; key 0 marks "none" (below the key of -inf).
+// Each token is a chain of loads and reductions, so several go side by side, without a branch between them.
 template <int kBatch, int kPer>
 __device__ __forceinline__ void route_tokens(const MoeTokParams& p, int t, int step, int lane, MoeTables& tb) {
-  uint32_t key[kBatch][kPer];
-  float top[kBatch], sum[kBatch], all[kBatch];
+  uint32_t key[kBatch][kPer], mine[kBatch];
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
-    float v[kPer];
     const float* row = p.logits + static_cast<size_t>(t + b * step < p.T ? t + b * step : t) * p.E;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < p.E ? __ldg(row + lane + 32 * i) : 0.f;
-    top[b] = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      key[b][i] = lane + 32 * i < p.E ? logit_key(v[i]) : 0u;
-      if (lane + 32 * i < p.E) top[b] = fmaxf(top[b], v[i]);
-    }
-    sum[b] = 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < p.E) sum[b] += expf(v[i] - top[b]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
-    all[b] = 0.f;
+    for (int i = 0; i < kPer; ++i) key[b][i] = lane + 32 * i < p.E ? logit_key(__ldg(row + lane + 32 * i)) : 0u;
   }
-  for (int j = 0; j < p.topk; ++j)
+  for (int j = 0; j < p.topk; ++j) {
+    uint32_t best[kBatch], e[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      uint32_t best = key[b][0];
-      int at = 0;
+      best[b] = key[b][0];
+      e[b] = lane;
 #pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (key[b][i] > best) {
-          best = key[b][i];
-          at = i;
-        }
-      const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : 0xffffffffu);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (static_cast<uint32_t>(lane + 32 * i) == e) key[b][i] = 0u;
-      const float v = __uint_as_float(high & 0x80000000u ? high & 0x7fffffffu : ~high);  // of the key (NaN: the sum is NaN too)
-      const float gate = expf(v - top[b]) / sum[b];
-      all[b] += gate;
-      if (lane == 0 && t + b * step < p.T) {
-        tb.expert[(t + b * step) * p.topk + j] = static_cast<uint8_t>(e);
-        tb.gate[(t + b * step) * p.topk + j] = gate;
+      for (int i = 1; i < kPer; ++i) {
+        e[b] = key[b][i] > best[b] ? lane + 32 * i : e[b];
+        best[b] = max(best[b], key[b][i]);
       }
     }
-  if (p.renorm) {
-    __syncwarp();
+    uint32_t high[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (lane < p.topk && t + b * step < p.T) tb.gate[(t + b * step) * p.topk + lane] /= all[b];
+    for (int b = 0; b < kBatch; ++b) high[b] = __reduce_max_sync(0xffffffffu, best[b]);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) e[b] = __reduce_min_sync(0xffffffffu, best[b] == high[b] ? e[b] : 0xffffffffu);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      mine[b] = lane == j ? e[b] : mine[b];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) key[b][i] = lane + 32 * i == static_cast<int>(e[b]) ? 0u : key[b][i];
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b)
+    if (lane < p.topk && t + b * step < p.T) tb.expert[(t + b * step) * p.topk + lane] = static_cast<uint8_t>(mine[b]);
+}
+
+// One warp: the gates of kBatch tokens (as above), the softmax over all E logits taken at the chosen experts.
+template <int kBatch>
+__device__ __forceinline__ void token_gates(const MoeTokParams& p, int t, int step, int lane, MoeTables& tb) {
+  const float* row[kBatch];
+  float top[kBatch], sum[kBatch], gate[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    row[b] = p.logits + static_cast<size_t>(t + b * step < p.T ? t + b * step : t) * p.E;
+    top[b] = -INFINITY;
+    sum[b] = 0.f;
+  }
+  for (int e = lane; e < p.E; e += 32)
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) top[b] = fmaxf(top[b], __ldg(row[b] + e));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], o));
+  for (int e = lane; e < p.E; e += 32)
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) sum[b] += expf(__ldg(row[b] + e) - top[b]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int a = (t + b * step < p.T ? t + b * step : t) * p.topk + (lane < p.topk ? lane : 0);
+    gate[b] = lane < p.topk ? expf(__ldg(row[b] + tb.expert[a]) - top[b]) / sum[b] : 0.f;
+    if (p.renorm) {
+      float all = gate[b];
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);  // topk <= 8
+      gate[b] /= all;
+    }
+    if (lane < p.topk && t + b * step < p.T) tb.gate[a] = gate[b];
   }
 }
 
@@ -644,6 +662,8 @@ __global__ void __launch_bounds__(moet::kThreads, 1) moet_kernel(const __grid_co
     }
     return;
   }
+  // the gates, while the first loads are under way; a tile's barriers lie between here and their first use
+  for (int t = threadIdx.x >> 5; t < p.T; t += 4 * (2 * kGroup / 32)) token_gates<4>(p, t, 2 * kGroup / 32, threadIdx.x & 31, tb);
   int segs = 0;
   bool ok = true;
   moet_multiply<false, NT>(p, tb, ring, full, empty, 0, segs, ok);
