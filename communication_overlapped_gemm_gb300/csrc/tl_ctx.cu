@@ -59,6 +59,14 @@ bool tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base
   return encode(m, dt, 3, base, dims, strides, box);
 }
 
+bool tmap_3d_strided(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t stride1, uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2) {
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {stride1, stride2};
+  cuuint32_t box[3] = {b0, b1, b2};
+  return encode(m, dt, 3, base, dims, strides, box);
+}
+
 int set_smem_attr(const void* kern) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
     (void)cudaGetLastError();

@@ -30,6 +30,9 @@ bool tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base
              uint64_t outer, uint32_t box_inner, uint32_t box_outer);
 bool tmap_3d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, uint64_t d0, uint64_t d1,
              uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2);
+// The same with the strides given (bytes, multiples of 16): views whose dimensions lie in any order.
+bool tmap_3d_strided(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t stride1, uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,10 +1,62 @@
-// Causal attention of packed prompts with a sliding window and sinks.
+// Causal attention of packed prompts with a sliding window and sinks, on the tensor cores.
+//
+//   S = sl2 Q K^T,  P = 2^(S - m),  O = P V,  l = sum P,  out = O / l,  lse = ln 2 (m + log2 l)
+// over the keys that each query sees, with the running maximum m of a row (base 2).
+//
+// A tile is 128 rows: the G = heads / kv_heads query heads of one kv head for 128 / G consecutive tokens
+// (TMA reads them as one box), so short prompts fill tiles, a tile's window is narrow, and K and V
+// are read once for all G heads.  An item is two tiles side by side of one sequence and kv head, which
+// share every K and V block in shared memory; persistent CTAs take items in turn, those that
+// end a sequence (the longest without a window) first.  An item's keys are walked in blocks of 128:
+// first the sinks that lie before its windows, then from the first window's start to its last
+// query.  Blocks start anywhere (a TMA row coordinate has no alignment), so a window of 1024 takes 9.
+//
+//   warp 0    TMA: Q of both tiles, K and V blocks through a ring
+//   warp 1    TMEM and the MMAs (one thread), tcgen05.mma M = 128:
+//               S_t = Q_t K^T        N = 128 keys, K = head dim, both K-major from shared memory
+//               O_t += P_t V         N = head dim, K = 128 keys, P_t from TMEM, V MN-major
+//   warps 4-7, 8-11   softmax of tile 0 and 1, one row per thread
+// TMEM: S_0, S_1 (128 columns each; P_t as 16-bit pairs takes the first 64 of S_t once they are
+// read), O_0, O_1.  MMAs are issued as S_0 S_1 | PV_0 S_0' PV_1 S_1' | ..: while one tile is in its
+// softmax the tensor cores work for the other.  MMAs of a thread complete in order, so S_t' needs
+// no wait for PV_t before it, and "S_t' is there" also says that PV_t is complete: the softmax
+// rescales O_t then, and only when a row's maximum grew by more than 2^8 (until then weights
+// stay below 2^8 and the stale maximum cancels in O / l).
+// P is rounded to the 16-bit type of V (half a step each); l sums it unrounded in fp32.
+//
+// A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
+// reach the row through the product.  So a row with a non-finite result is computed once more by
+// its warp from the keys that it sees alone (window_row).
+#include <atomic>
+
 #include "tl_serve.cuh"
+#include "tl_softmax.cuh"
 
 namespace tl {
 
+namespace win {
+constexpr int kKeys = 128, kMaxBatch = 1024;
+constexpr int kThreads = 384;          // warps 0-3 (two of them idle), softmax warpgroups 4-7 and 8-11
+constexpr float kRescale = 8.f;
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;             // 64-column SW128 boxes of a row
+  static constexpr int kBox = 128 * 128;             // 128 rows of 64 columns
+  static constexpr int kTileBytes = kHalves * kBox;  // Q of a tile, a K block, a V block
+  static constexpr int kSlots = D == 128 ? 4 : 8;    // K and V blocks in flight (128 KB)
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kCumOff = kBarOff + 256;
+  static constexpr int kSmem = 1024 + kCumOff + (kMaxBatch + 1) * 4;
+};
+constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S_t at 128 t, O_t at 256 + 128 t
+}  // namespace win
+
 struct WindowParams {
-  DevStatus* status;
+  CUtensorMap tq;  // {d, heads, total_q}, box {64, G, 128 / G}
+  CUtensorMap tk;  // {d, kv_heads, total_k}, box {64, 1, 128}
+  CUtensorMap tv;
+  Common common;
   const uint8_t* q;
   const uint8_t* k;
   const uint8_t* v;
@@ -13,7 +65,8 @@ struct WindowParams {
   long long q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;  // bytes
   const int* cu_q;
   const int* cu_k;
-  int batch, total_q, total_k, heads, group;
+  int batch, total_q, total_k, heads, kv_heads, group;
+  int tokens;  // of a tile: 128 / group
   float sl2;  // scale * log2(e)
   int window, sinks;
 };
@@ -68,25 +121,412 @@ __device__ __forceinline__ void window_row(const WindowParams& p, int token, int
     p.lse[static_cast<long long>(token) * p.heads + h] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-// A warp per (query, head).
+// A sequence's bounds, as rows of q and k; nothing (n = 0) if they are out of order or range.
+struct WinSeq {
+  int q0, k0, n, off;  // first rows, queries, position of the first query
+};
+__device__ __forceinline__ WinSeq win_seq(const WindowParams& p, int b, bool report) {
+  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+  WinSeq s;
+  if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) {
+    if (report) report_index(p.common.status, static_cast<unsigned long long>(b));
+    s.q0 = s.k0 = s.n = s.off = 0;
+  } else {
+    s.q0 = q0;
+    s.k0 = k0;
+    s.n = q1 - q0;
+    s.off = (k1 - k0) - s.n;
+  }
+  return s;
+}
+
+// An item and the key blocks it walks.
+struct WinItem {
+  WinSeq s;
+  int hk, i0;     // kv head, first query
+  bool two;       // its second tile has queries
+  int lo;         // first key of the blocks after the sinks'
+  int sinks;      // keys [0, sinks) of the sinks' blocks
+  int nh, nb;     // blocks of sinks, all blocks
+};
+__device__ __forceinline__ WinItem win_item(const WindowParams& p, const int* cum, int idx) {
+  // the sequence that holds item idx: cum[b] <= idx < cum[b + 1]
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= idx) lo = mid; else hi = mid;
+  }
+  WinItem w;
+  w.s = win_seq(p, lo, false);
+  const int in = idx - cum[lo], tiles = (cum[lo + 1] - cum[lo]) / p.kv_heads;
+  w.hk = in % p.kv_heads;
+  w.i0 = (tiles - 1 - in / p.kv_heads) * 2 * p.tokens;
+  w.two = w.i0 + p.tokens < w.s.n;
+  const int end = min(w.i0 + 2 * p.tokens, w.s.n);  // one past the last query
+  const int first = w.s.off + w.i0, last = w.s.off + end - 1;  // positions
+  w.lo = p.window == 0 || first < p.window ? 0 : first - p.window + 1;
+  w.sinks = min(p.sinks, w.lo);
+  w.nh = (w.sinks + win::kKeys - 1) / win::kKeys;
+  w.nb = last < 0 ? 0 : w.nh + (last - w.lo) / win::kKeys + 1;
+  if (last < 0) w.nh = 0;
+  return w;
+}
+__device__ __forceinline__ int win_start(const WinItem& w, int j) {
+  return j < w.nh ? j * win::kKeys : w.lo + (j - w.nh) * win::kKeys;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16, one CTA.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The first n of 32 bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 template <class T, int D>
-__global__ void __launch_bounds__(256) window_kernel(const WindowParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long n = static_cast<long long>(p.total_q) * p.heads;
-  for (long long i = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < n;
-       i += (static_cast<long long>(gridDim.x) * blockDim.x) >> 5) {
-    const int token = static_cast<int>(i / p.heads), h = static_cast<int>(i % p.heads);
-    for (int b = 0; b < p.batch; ++b) {
-      const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k) {
-        if (lane == 0) report_index(p.status, static_cast<unsigned long long>(b));
-        continue;
+__global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_constant__ WindowParams p) {
+  using namespace win;
+  using S = Shape<D>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  // operand formats: bits 7-9 and 10-12, 0 fp16, 1 bf16
+  constexpr uint32_t kFormat = kBf16 ? 0u : (1u << 7) | (1u << 10);
+  constexpr uint32_t kDescS = umma_idesc_bf16(128, kKeys, false) & ~kFormat;
+  constexpr uint32_t kDescO = umma_idesc_bf16(128, D, true) & ~kFormat;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(base + S::kBarOff);
+  uint64_t* qempty = qfull + 1;
+  uint64_t* full = qfull + 2;              // [kSlots] a K or V block is there
+  uint64_t* empty = full + S::kSlots;      // [kSlots] both tiles' MMAs have read it
+  uint64_t* sfull = empty + S::kSlots;     // [2] S_t is there, every MMA before it complete
+  uint64_t* pready = sfull + 2;            // [2] P_t is there (and O_t rescaled)
+  uint64_t* ofull = pready + 2;            // [2] the item's last PV_t is complete
+  uint64_t* drain = ofull + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* cum = reinterpret_cast<int*>(base + S::kCumOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Common& c = p.common;
+
+  // items before each sequence
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+    const WinSeq s = win_seq(p, b, blockIdx.x == 0);
+    cum[b + 1] = (s.n + 2 * p.tokens - 1) / (2 * p.tokens) * p.kv_heads;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pready[t], 4);
+      mbar_init(&ofull[t], 1);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_map(&p.tq);
+    tma_prefetch_map(&p.tk);
+    tma_prefetch_map(&p.tv);
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      int v = b0 + lane < p.batch ? cum[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x) v += o;
       }
-      if (token < q0 || token >= q1) continue;
-      window_row<T, D>(p, token, h, (k1 - k0) - (q1 - q0) + (token - q0), k0, lane);
-      break;
+      if (b0 + lane < p.batch) cum[b0 + lane + 1] = sum + v;
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) cum[0] = 0;
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int items = cum[p.batch];
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      bool ok = true;
+      int u = 0, nq = 0;  // blocks and items loaded
+      const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.group) * 128 * S::kHalves;
+      for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+        const WinItem w = win_item(p, cum, idx);
+        if (w.nb == 0) continue;
+        ok = mbar_wait(qempty, (nq & 1) ^ 1, c, kSiteEmpty);
+        if (!ok) break;
+        mbar_arrive_expect_tx(qfull, q_bytes * (w.two ? 2 : 1));
+        for (int t = 0; t < (w.two ? 2 : 1); ++t)
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(base + t * S::kTileBytes + h * S::kBox, &p.tq, qfull, 64 * h, w.hk * p.group,
+                        w.s.q0 + w.i0 + t * p.tokens);
+        ++nq;
+        for (int j = 0; j < w.nb && ok; ++j)
+          for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+            const int s = u % S::kSlots;
+            ok = mbar_wait(&empty[s], ((u / S::kSlots) & 1) ^ 1, c, kSiteEmpty);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[s], S::kTileBytes);
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_3d(base + S::kRingOff + s * S::kTileBytes + h * S::kBox, kv ? &p.tv : &p.tk, &full[s], 64 * h, w.hk,
+                          w.s.k0 + win_start(w, j));
+          }
+      }
+      // every load has landed before the CTA ends (at once, unless a wait ran out)
+      if (nq) mbar_wait(qfull, (nq - 1) & 1, c, kSiteDrain);
+      for (int j = u > S::kSlots ? u - S::kSlots : 0; j < u; ++j) mbar_wait(&full[j % S::kSlots], (j / S::kSlots) & 1, c, kSiteDrain);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      const uint32_t q0 = smem_u32(base), ring = q0 + S::kRingOff;
+      bool ok = true;
+      int u = 0, nq = 0, np[2] = {0, 0};  // blocks read, items, P blocks consumed
+      auto wait_block = [&](int j) { return mbar_wait(&full[j % S::kSlots], (j / S::kSlots) & 1, c, kSiteFull); };
+      auto mma_s = [&](int t, int slot) {  // S_t = Q_t K^T
+        const uint64_t a0 = umma_desc_sw128(q0 + t * S::kTileBytes, 16, 1024);
+        const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * S::kBox + (k & 3) * 32) >> 4;
+          umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, kDescS, k ? 1u : 0u);
+        }
+        umma_commit(&sfull[t]);
+      };
+      auto mma_o = [&](int t, int slot, bool acc) {  // O_t += P_t V
+        const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, S::kBox, 1024);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + k * 8, b0 + ((k * 2048) >> 4), kDescO, (acc || k) ? 1u : 0u);
+      };
+      for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+        const WinItem w = win_item(p, cum, idx);
+        if (w.nb == 0) continue;
+        const int nt = w.two ? 2 : 1;
+        ok = mbar_wait(qfull, nq & 1, c, kSiteFull) && wait_block(u);
+        if (!ok) break;
+        ++nq;
+        tc_fence_after();
+        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots);
+        umma_commit(&empty[u % S::kSlots]);
+        if (w.nb == 1) umma_commit(qempty);
+        for (int j = 0; j < w.nb && ok; ++j) {
+          // slots u: K of block j (read), u + 1: V of block j, u + 2: K of block j + 1
+          ok = wait_block(u + 1);
+          for (int t = 0; t < nt && ok; ++t) {
+            ok = mbar_wait(&pready[t], np[t] & 1, c, kSiteTmemFull);
+            if (!ok) break;
+            ++np[t];
+            tc_fence_after();
+            mma_o(t, (u + 1) % S::kSlots, j > 0);
+            if (t == nt - 1) umma_commit(&empty[(u + 1) % S::kSlots]);
+            if (j + 1 < w.nb) {
+              if (t == 0) {
+                ok = wait_block(u + 2);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              mma_s(t, (u + 2) % S::kSlots);
+              if (t == nt - 1) {
+                umma_commit(&empty[(u + 2) % S::kSlots]);
+                if (j + 2 == w.nb) umma_commit(qempty);
+              }
+            } else {
+              umma_commit(&ofull[t]);
+            }
+          }
+          u += 2;
+        }
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, c, kSiteDrain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + kColS + 128 * t + lanes, to = tmem + kColO + 128 * t + lanes;
+    const int tok = row / p.group, hg = row - tok * p.group;
+    bool ok = true;
+    int ns = 0, no = 0;  // S blocks and items seen
+    for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+      const WinItem w = win_item(p, cum, idx);
+      if (t && !w.two) continue;
+      const int i = w.i0 + t * p.tokens + tok;  // this row's query
+      const bool live = tok < p.tokens && i < w.s.n;
+      const int pos = live ? w.s.off + i : -1;
+      const int from = p.window == 0 || pos < p.window ? 0 : pos - p.window + 1;  // first key of its window
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < w.nb && ok; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[t], ns & 1, c, kSiteTmemFull));
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        // the keys of this block that the row sees: [a, z), or before s2
+        const int start = win_start(w, j);
+        const bool head = j < w.nh;
+        // (rows without a query are not cut: what they compute goes nowhere)
+        const int z = !live ? kKeys : (head ? min(w.sinks, pos + 1) : pos + 1) - start;
+        const int a = head || !live ? 0 : from - start, s2 = head ? 0 : p.sinks - start;
+        const bool cut = __any_sync(0xffffffffu, z < kKeys || (a > 0 && s2 < kKeys));
+        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (cut)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) seen[q] = low_bits(z - 32 * q) & (~low_bits(a - 32 * q) | low_bits(s2 - 32 * q));
+        // the block's maximum, 32 columns at a time
+        float top = -INFINITY;
+        {
+          uint32_t r[2][32];
+          tmem_ld32_issue(ts, r[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait(r[q & 1]);
+            if (q < 3) tmem_ld32_issue(ts + 32 * (q + 1), r[(q + 1) & 1]);
+            float x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[q & 1][k]);
+            if (cut)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = (seen[q] >> k) & 1u ? x[k] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = fmax3(x[k], x[k + 8], x[k + 16]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = fmaxf(x[k], x[k + 24]);
+            top = fmax3(fmax3(top, x[0], x[1]), fmax3(x[2], x[3], x[4]), fmax3(x[5], x[6], x[7]));
+          }
+          top *= p.sl2;  // positive
+        }
+        if (__any_sync(0xffffffffu, top > m + kRescale)) {
+          const float mn = fmaxf(m, top), keep = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+          m = mn;
+          l *= keep;
+          if (j > 0) {  // PV_t of the blocks before is complete (it precedes this S_t)
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              float o[32];
+              tmem_ld32(to + 32 * q, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= keep;
+              tmem_st32(to + 32 * q, o);
+            }
+          }
+        }
+        // weights, 32 columns at a time; P's columns lie over scores that are read
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const unsigned long long sl2x2 = f2(p.sl2, p.sl2), nmx2 = f2(nm, nm);
+        unsigned long long sum[2] = {0ull, 0ull};
+        {
+          uint32_t r[2][32], pk[32];
+          tmem_ld32_issue(ts, r[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait(r[q & 1]);
+            if (q < 3) tmem_ld32_issue(ts + 32 * (q + 1), r[(q + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0 = __uint_as_float(r[q & 1][2 * k]), x1 = __uint_as_float(r[q & 1][2 * k + 1]);
+              if (cut) {
+                x0 = (seen[q] >> (2 * k)) & 1u ? x0 : -INFINITY;
+                x1 = (seen[q] >> (2 * k + 1)) & 1u ? x1 : -INFINITY;
+              }
+              float y0, y1;
+              f2_split(ffma2(f2(x0, x1), sl2x2, nmx2), y0, y1);
+              const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+              sum[k & 1] = fadd2(sum[k & 1], f2(e0, e1));
+              pk[16 * (q & 1) + k] = from_f32x2<T>(e0, e1);
+            }
+            if (q == 1) tmem_st32_raw(ts, pk);  // over scores 0-31; those from 64 on are still to be read
+          }
+          tmem_st32_raw(ts + 32, pk);
+        }
+        {
+          float a0, a1;
+          f2_split(fadd2(sum[0], sum[1]), a0, a1);
+          l += a0 + a1;
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[t]);
+      }
+      if (!ok) break;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool bad = !(l <= 3.0e38f);
+      T* dst = reinterpret_cast<T*>(p.out + (w.s.q0 + i) * p.out_token + (w.hk * p.group + hg) * p.out_head);
+      if (w.nb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ofull[t], no & 1, c, kSiteTmemFull));
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        if (w.nb) {
+          tmem_ld32(to + 32 * q, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          bad |= !(fabsf(o[k]) <= 3.0e38f);
+          o[k] *= inv;
+        }
+        if (live)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            reinterpret_cast<uint4*>(dst)[4 * q + v] =
+                make_uint4(from_f32x2<T>(o[8 * v], o[8 * v + 1]), from_f32x2<T>(o[8 * v + 2], o[8 * v + 3]),
+                           from_f32x2<T>(o[8 * v + 4], o[8 * v + 5]), from_f32x2<T>(o[8 * v + 6], o[8 * v + 7]));
+      }
+      if (live && p.lse)
+        p.lse[static_cast<long long>(w.s.q0 + i) * p.heads + w.hk * p.group + hg] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      tc_fence_before();
+      // rows with a non-finite result, once more from what they see
+      for (uint32_t again = __ballot_sync(0xffffffffu, bad && live); again; again &= again - 1) {
+        const int x = __ffs(again) - 1;
+        window_row<T, D>(p, __shfl_sync(0xffffffffu, w.s.q0 + i, x), w.hk * p.group + __shfl_sync(0xffffffffu, hg, x),
+                         __shfl_sync(0xffffffffu, pos, x), w.s.k0, lane);
+      }
+      __syncwarp();
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <class T, int D>
+static int window_launch(tl_ctx* ctx, const WindowParams& p, cudaStream_t st) {
+  auto kern = window_kernel<T, D>;
+  static std::atomic<unsigned long long> ready{0};
+  if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), win::Shape<D>::kSmem)) return TL_ERR_CUDA;
+  const long long most = (p.total_q / (2LL * p.tokens) + p.batch) * p.kv_heads;  // items there can be
+  const int grid = most < ctx->ctas ? static_cast<int>(most) : ctx->ctas;
+  kern<<<grid, win::kThreads, win::Shape<D>::kSmem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ERR_CUDA;
 }
 
 }  // namespace tl
@@ -108,11 +548,15 @@ extern "C" int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long l
                       out_token_stride, out_head_stride})
     if (!esize_ok(s, 2)) return TL_ERR_INVALID;
   if (total_q == 0 || heads == 0 || batch == 0) return TL_OK;
+  // (a row read as another one, by a stride of 0, is refused: a tensor map has none)
+  if ((total_q > 1 && !q_token_stride) || (heads > 1 && !q_head_stride)) return TL_ERR_INVALID;
+  if ((total_k > 1 && (!k_token_stride || !v_token_stride)) || (total_k > 0 && kv_heads > 1 && (!k_head_stride || !v_head_stride)))
+    return TL_ERR_INVALID;
   if (!q || !out || !cu_q || !cu_k || !aligned16(q) || !aligned16(out)) return TL_ERR_INVALID;
   if (total_k > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return TL_ERR_INVALID;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
   WindowParams p;
-  p.status = ctx->status;
+  std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const uint8_t*>(q);
   p.k = static_cast<const uint8_t*>(k);
   p.v = static_cast<const uint8_t*>(v);
@@ -136,15 +580,23 @@ extern "C" int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long l
   p.sl2 = scale * kLog2E;
   p.window = window;
   p.sinks = sinks;
-  const long long need = (static_cast<long long>(total_q) * heads + 7) / 8, most = 64LL * ctx->sms;
-  const unsigned grid = static_cast<unsigned>(need < most ? need : most);
+  p.kv_heads = kv_heads;
+  p.tokens = 128 / p.group;
+  const auto dt = dtype == TL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  // a dimension of one entry has any stride; a map wants a valid one
+  auto stride = [&](long long bytes, int n) { return static_cast<uint64_t>(n > 1 ? bytes : 2 * d); };
+  const int rows_k = total_k > 0 ? total_k : 1, heads_k = total_k > 0 ? kv_heads : 1;  // (no keys: a map of q, never read)
+  if (!tmap_3d_strided(&p.tq, dt, q, d, heads, total_q, stride(p.q_head, heads), stride(p.q_token, total_q), 64, p.group,
+                       p.tokens) ||
+      !tmap_3d_strided(&p.tk, dt, total_k > 0 ? k : q, d, heads_k, rows_k, stride(p.k_head, heads_k),
+                       stride(p.k_token, total_k), 64, 1, win::kKeys) ||
+      !tmap_3d_strided(&p.tv, dt, total_k > 0 ? v : q, d, heads_k, rows_k, stride(p.v_head, heads_k),
+                       stride(p.v_token, total_k), 64, 1, win::kKeys))
+    return TL_ERR_CUDA;
+  p.common = make_common(ctx);
+  p.common.trace_hdr = nullptr;  // this kernel records no trace spans
+  p.common.trace = nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == TL_BF16) {
-    if (d == 64) window_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(p);
-    else window_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (d == 64) window_kernel<__half, 64><<<grid, 256, 0, st>>>(p);
-    else window_kernel<__half, 128><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ERR_CUDA;
+  if (dtype == TL_BF16) return d == 64 ? window_launch<__nv_bfloat16, 64>(ctx, p, st) : window_launch<__nv_bfloat16, 128>(ctx, p, st);
+  return d == 64 ? window_launch<__half, 64>(ctx, p, st) : window_launch<__half, 128>(ctx, p, st);
 }

@@ -498,6 +498,7 @@ int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, cons
  * left alone); a bound out of order or range leaves that sequence out and is reported.
  * Shapes: batch <= 1024; heads % kv_heads == 0, heads / kv_heads <= 128; d 64 or 128; window, sinks >= 0;
  * scale finite and > 0; total_q * heads < 2^31.
+ * strides of q, k and v > 0 where the dimension has more than one entry.
  * total_q == 0, heads == 0 or batch == 0 is a no-op.  No workspace.
  */
 int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride,
