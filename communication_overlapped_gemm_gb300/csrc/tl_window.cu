@@ -185,6 +185,34 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 
+// 16 fp32 columns of this warp's lanes, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// The register share of this warpgroup, of those that the CTA was launched with.
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // The first n of 32 bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -204,8 +232,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   uint64_t* full = qfull + 2;              // [kSlots] a K or V block is there
   uint64_t* empty = full + S::kSlots;      // [kSlots] both tiles' MMAs have read it
   uint64_t* sfull = empty + S::kSlots;     // [2] S_t is there, every MMA before it complete
-  uint64_t* pready = sfull + 2;            // [2] P_t is there (and O_t rescaled)
-  uint64_t* ofull = pready + 2;            // [2] the item's last PV_t is complete
+  uint64_t* pready = sfull + 2;            // [2][2] the first, the second 64 keys of P_t are there (and O_t rescaled)
+  uint64_t* ofull = pready + 4;            // [2] the item's last PV_t is complete
   uint64_t* drain = ofull + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   int* cum = reinterpret_cast<int*>(base + S::kCumOff);
@@ -226,7 +254,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[t], 4);
+      mbar_init(&pready[2 * t], 4);
+      mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&ofull[t], 1);
     }
     mbar_init(drain, 1);
@@ -259,7 +288,9 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const int items = cum[p.batch];
-
+  // Registers: 128 x 88 + 256 x 208 = 384 x 168, what the CTA has at launch.
+  if (warp < 4) {
+    regs_down<88>();
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
@@ -310,11 +341,13 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         }
         umma_commit(&sfull[t]);
       };
-      auto mma_o = [&](int t, int slot, bool acc) {  // O_t += P_t V
+      auto mma_o = [&](int t, int slot, int half, bool acc) {  // O_t += P_t V over 64 keys
         const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, S::kBox, 1024);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + k * 8, b0 + ((k * 2048) >> 4), kDescO, (acc || k) ? 1u : 0u);
+        for (int k = 0; k < kKeys / 32; ++k) {
+          const int kk = half * (kKeys / 32) + k;
+          umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, b0 + ((kk * 2048) >> 4), kDescO, (acc || kk) ? 1u : 0u);
+        }
       };
       for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
         const WinItem w = win_item(p, cum, idx);
@@ -331,11 +364,14 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
           // slots u: K of block j (read), u + 1: V of block j, u + 2: K of block j + 1
           ok = wait_block(u + 1);
           for (int t = 0; t < nt && ok; ++t) {
-            ok = mbar_wait(&pready[t], np[t] & 1, c, kSiteTmemFull);
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = mbar_wait(&pready[2 * t + half], np[t] & 1, c, kSiteTmemFull);
+              if (!ok) break;
+              tc_fence_after();
+              mma_o(t, (u + 1) % S::kSlots, half, j > 0);
+            }
             if (!ok) break;
             ++np[t];
-            tc_fence_after();
-            mma_o(t, (u + 1) % S::kSlots, j > 0);
             if (t == nt - 1) umma_commit(&empty[(u + 1) % S::kSlots]);
             if (j + 1 < w.nb) {
               if (t == 0) {
@@ -359,8 +395,10 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       mbar_wait(drain, 0, c, kSiteDrain);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
     // ------------------------------------------------------------ softmax
+    regs_up<208>();
     const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * t + lanes, to = tmem + kColO + 128 * t + lanes;
@@ -391,81 +429,69 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         if (cut)
 #pragma unroll
           for (int q = 0; q < 4; ++q) seen[q] = low_bits(z - 32 * q) & (~low_bits(a - 32 * q) | low_bits(s2 - 32 * q));
-        // the block's maximum, 32 columns at a time
-        float top = -INFINITY;
-        {
-          uint32_t r[2][32];
-          tmem_ld32_issue(ts, r[0]);
+        // all 128 scores at once
+        uint32_t r[4][32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait(r[q & 1]);
-            if (q < 3) tmem_ld32_issue(ts + 32 * (q + 1), r[(q + 1) & 1]);
-            float x[32];
+        for (int q = 0; q < 4; ++q) tmem_ld32_issue(ts + 32 * q, r[q]);
+        tmem_ld_wait(r[0]);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[q & 1][k]);
-            if (cut)
+        for (int q = 1; q < 4; ++q) tmem_ld_after(r[q]);
+        if (cut)
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = (seen[q] >> k) & 1u ? x[k] : -INFINITY;
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fmax3(x[k], x[k + 8], x[k + 16]);
+            for (int k = 0; k < 32; ++k) r[q][k] = (seen[q] >> k) & 1u ? r[q][k] : 0xff800000u;  // -inf
+        float mx[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fmaxf(x[k], x[k + 24]);
-            top = fmax3(fmax3(top, x[0], x[1]), fmax3(x[2], x[3], x[4]), fmax3(x[5], x[6], x[7]));
-          }
-          top *= p.sl2;  // positive
-        }
+        for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(r[0][k]);
+#pragma unroll
+        for (int i = 8; i < 120; i += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx[k] = fmax3(mx[k], __uint_as_float(r[(i + k) >> 5][(i + k) & 31]), __uint_as_float(r[(i + 8 + k) >> 5][(i + 8 + k) & 31]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(r[3][24 + k]));
+        const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.sl2;  // sl2 > 0
         if (__any_sync(0xffffffffu, top > m + kRescale)) {
           const float mn = fmaxf(m, top), keep = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
           m = mn;
           l *= keep;
           if (j > 0) {  // PV_t of the blocks before is complete (it precedes this S_t)
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              float o[32];
-              tmem_ld32(to + 32 * q, o);
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * q, o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= keep;
-              tmem_st32(to + 32 * q, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+              tmem_st16(to + 16 * q, o);
             }
           }
         }
-        // weights, 32 columns at a time; P's columns lie over scores that are read
+        // weights, 64 keys at a time; P's columns lie over scores that are read
         const float nm = m == -INFINITY ? 0.f : -m;
         const unsigned long long sl2x2 = f2(p.sl2, p.sl2), nmx2 = f2(nm, nm);
         unsigned long long sum[2] = {0ull, 0ull};
-        {
-          uint32_t r[2][32], pk[32];
-          tmem_ld32_issue(ts, r[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait(r[q & 1]);
-            if (q < 3) tmem_ld32_issue(ts + 32 * (q + 1), r[(q + 1) & 1]);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x0 = __uint_as_float(r[q & 1][2 * k]), x1 = __uint_as_float(r[q & 1][2 * k + 1]);
-              if (cut) {
-                x0 = (seen[q] >> (2 * k)) & 1u ? x0 : -INFINITY;
-                x1 = (seen[q] >> (2 * k + 1)) & 1u ? x1 : -INFINITY;
-              }
-              float y0, y1;
-              f2_split(ffma2(f2(x0, x1), sl2x2, nmx2), y0, y1);
-              const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
-              sum[k & 1] = fadd2(sum[k & 1], f2(e0, e1));
-              pk[16 * (q & 1) + k] = from_f32x2<T>(e0, e1);
-            }
-            if (q == 1) tmem_st32_raw(ts, pk);  // over scores 0-31; those from 64 on are still to be read
+          for (int k = 0; k < 32; ++k) {
+            const int i = 64 * half + 2 * k;
+            float y0, y1;
+            f2_split(ffma2(f2(__uint_as_float(r[i >> 5][i & 31]), __uint_as_float(r[i >> 5][(i & 31) + 1])), sl2x2, nmx2), y0, y1);
+            const float e0 = ex2_approx(y0), e1 = ex2_approx(y1);
+            sum[k & 1] = fadd2(sum[k & 1], f2(e0, e1));
+            pk[k] = from_f32x2<T>(e0, e1);
           }
-          tmem_st32_raw(ts + 32, pk);
+          tmem_st32_raw(ts + 32 * half, pk);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pready[2 * t + half]);
         }
-        {
-          float a0, a1;
-          f2_split(fadd2(sum[0], sum[1]), a0, a1);
-          l += a0 + a1;
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[t]);
+        float a0, a1;
+        f2_split(fadd2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
       }
       if (!ok) break;
       const float inv = l == 0.f ? 0.f : 1.f / l;
