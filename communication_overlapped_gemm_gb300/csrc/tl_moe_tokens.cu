@@ -267,12 +267,13 @@ __device__ __forceinline__ void count_up_async(unsigned* ctr) {
 __device__ __forceinline__ bool wait_item(const unsigned* ctr, unsigned want, const Common& c, int lane) {
   bool ok = true;
   if (lane == 0) {
-    const uint64_t t0 = globaltimer();
-    for (;;) {
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
       unsigned v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
       if (v >= want) break;
-      if (globaltimer() - t0 > c.timeout_ns) {
+      if (i == 64) t0 = globaltimer();  // (a read of the timer costs as much as the load)
+      if (i > 64 && (i & 15) == 0 && globaltimer() - t0 > c.timeout_ns) {
         report_timeout(c.status, kSiteSignal, 0);
         ok = false;
         break;

@@ -185,6 +185,13 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // 16 fp32 columns of this warp's lanes, waited for.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   const int items = cum[p.batch];
   // Registers: 128 x 88 + 256 x 208 = 384 x 168, what the CTA has at launch.
   if (warp < 4) {
@@ -326,72 +333,74 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    // The whole warp walks along and one elected thread issues each group of MMAs.
+    {
       const uint32_t q0 = smem_u32(base), ring = q0 + S::kRingOff;
       bool ok = true;
       int u = 0, nq = 0, np[2] = {0, 0};  // blocks read, items, P blocks consumed
-      auto wait_block = [&](int j) { return mbar_wait(&full[j % S::kSlots], (j / S::kSlots) & 1, c, kSiteFull); };
-      auto mma_s = [&](int t, int slot) {  // S_t = Q_t K^T
+      auto wait = [&](uint64_t* bar, int n, unsigned site) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, c, site)) != 0; };
+      auto wait_block = [&](int j) { return wait(&full[j % S::kSlots], j / S::kSlots, kSiteFull); };
+      // S_t = Q_t K^T; then, for the last tile, the slot (and with the item's last block, Q) is free
+      auto mma_s = [&](int t, int slot, bool last_tile, bool last_block) {
         const uint64_t a0 = umma_desc_sw128(q0 + t * S::kTileBytes, 16, 1024);
         const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * S::kBox + (k & 3) * 32) >> 4;
-          umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, kDescS, k ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * S::kBox + (k & 3) * 32) >> 4;
+            umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, kDescS, k ? 1u : 0u);
+          }
+          umma_commit(&sfull[t]);
+          if (last_tile) {
+            umma_commit(&empty[slot]);
+            if (last_block) umma_commit(qempty);
+          }
         }
-        umma_commit(&sfull[t]);
+        __syncwarp();
       };
-      auto mma_o = [&](int t, int slot, int half, bool acc) {  // O_t += P_t V over 64 keys
+      // O_t += P_t V over 64 keys; after the second half the slot is free (last tile), O_t complete (last block)
+      auto mma_o = [&](int t, int slot, int half, bool acc, bool last_tile, bool last_block) {
         const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, S::kBox, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kKeys / 32; ++k) {
-          const int kk = half * (kKeys / 32) + k;
-          umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, b0 + ((kk * 2048) >> 4), kDescO, (acc || kk) ? 1u : 0u);
+          for (int k = 0; k < kKeys / 32; ++k) {
+            const int kk = half * (kKeys / 32) + k;
+            umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, b0 + ((kk * 2048) >> 4), kDescO, (acc || kk) ? 1u : 0u);
+          }
+          if (half && last_tile) umma_commit(&empty[slot]);
+          if (half && last_block) umma_commit(&ofull[t]);
         }
+        __syncwarp();
       };
       for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
         const WinItem w = win_item(p, cum, idx);
         if (w.nb == 0) continue;
         const int nt = w.two ? 2 : 1;
-        ok = mbar_wait(qfull, nq & 1, c, kSiteFull) && wait_block(u);
+        ok = wait(qfull, nq, kSiteFull) && wait_block(u);
         if (!ok) break;
         ++nq;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots);
-        umma_commit(&empty[u % S::kSlots]);
-        if (w.nb == 1) umma_commit(qempty);
+        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots, t == nt - 1, w.nb == 1);
         for (int j = 0; j < w.nb && ok; ++j) {
           // slots u: K of block j (read), u + 1: V of block j, u + 2: K of block j + 1
-          ok = wait_block(u + 1);
+          const bool more = j + 1 < w.nb;
+          ok = wait_block(u + 1) && (!more || wait_block(u + 2));
           for (int t = 0; t < nt && ok; ++t) {
+            const bool last = t == nt - 1;
             for (int half = 0; half < 2 && ok; ++half) {
-              ok = mbar_wait(&pready[2 * t + half], np[t] & 1, c, kSiteTmemFull);
+              ok = wait(&pready[2 * t + half], np[t], kSiteTmemFull);
               if (!ok) break;
               tc_fence_after();
-              mma_o(t, (u + 1) % S::kSlots, half, j > 0);
+              mma_o(t, (u + 1) % S::kSlots, half, j > 0, last, !more);
             }
             if (!ok) break;
             ++np[t];
-            if (t == nt - 1) umma_commit(&empty[(u + 1) % S::kSlots]);
-            if (j + 1 < w.nb) {
-              if (t == 0) {
-                ok = wait_block(u + 2);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              mma_s(t, (u + 2) % S::kSlots);
-              if (t == nt - 1) {
-                umma_commit(&empty[(u + 2) % S::kSlots]);
-                if (j + 2 == w.nb) umma_commit(qempty);
-              }
-            } else {
-              umma_commit(&ofull[t]);
-            }
+            if (more) mma_s(t, (u + 2) % S::kSlots, last, j + 2 == w.nb);
           }
           u += 2;
         }
       }
-      umma_commit(drain);
+      if (elect_one()) umma_commit(drain);
       mbar_wait(drain, 0, c, kSiteDrain);
     }
     __syncwarp();
