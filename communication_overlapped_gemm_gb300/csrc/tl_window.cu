@@ -8,8 +8,8 @@
 // are read once for all G heads.  An item is two tiles side by side of one sequence and kv head, which
 // share every K and V block in shared memory; persistent CTAs take items in turn, those that
 // end a sequence (the longest without a window) first.  An item's keys are walked in blocks of 128:
-// first the sinks that lie before its windows, then from the first window's start to its last
-// query.  Blocks start anywhere (a TMA row coordinate has no alignment), so a window of 1024 takes 9.
+// first the sinks that lie before its windows (up to 32 of them as a block of 32), then from
+// the first window's start to its last query.  Blocks start anywhere (a TMA row coordinate has no alignment), so a window of 1024 takes 9.
 //
 //   warp 0    TMA: Q of both tiles, K and V blocks through a ring
 //   warp 1    TMEM and the MMAs (one thread), tcgen05.mma M = 128:
@@ -35,7 +35,7 @@
 namespace tl {
 
 namespace win {
-constexpr int kKeys = 128, kMaxBatch = 1024;
+constexpr int kKeys = 128, kNarrow = 32, kMaxBatch = 1024;
 constexpr int kThreads = 384;          // warps 0-3 (two of them idle), softmax warpgroups 4-7 and 8-11
 constexpr float kRescale = 8.f;
 template <int D>
@@ -148,6 +148,7 @@ struct WinItem {
   int lo;         // first key of the blocks after the sinks'
   int sinks;      // keys [0, sinks) of the sinks' blocks
   int nh, nb;     // blocks of sinks, all blocks
+  bool narrow;    // the sinks fit in kNarrow keys: their block is that wide
 };
 __device__ __forceinline__ WinItem win_item(const WindowParams& p, const int* cum, int idx) {
   // the sequence that holds item idx: cum[b] <= idx < cum[b + 1]
@@ -169,6 +170,7 @@ __device__ __forceinline__ WinItem win_item(const WindowParams& p, const int* cu
   w.nh = (w.sinks + win::kKeys - 1) / win::kKeys;
   w.nb = last < 0 ? 0 : w.nh + (last - w.lo) / win::kKeys + 1;
   if (last < 0) w.nh = 0;
+  w.narrow = w.nh == 1 && w.sinks <= win::kNarrow;
   return w;
 }
 __device__ __forceinline__ int win_start(const WinItem& w, int j) {
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   // operand formats: bits 7-9 and 10-12, 0 fp16, 1 bf16
   constexpr uint32_t kFormat = kBf16 ? 0u : (1u << 7) | (1u << 10);
   constexpr uint32_t kDescS = umma_idesc_bf16(128, kKeys, false) & ~kFormat;
+  constexpr uint32_t kDescNarrow = umma_idesc_bf16(128, kNarrow, false) & ~kFormat;
   constexpr uint32_t kDescO = umma_idesc_bf16(128, D, true) & ~kFormat;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -341,14 +344,14 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       auto wait = [&](uint64_t* bar, int n, unsigned site) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, c, site)) != 0; };
       auto wait_block = [&](int j) { return wait(&full[j % S::kSlots], j / S::kSlots, kSiteFull); };
       // S_t = Q_t K^T; then, for the last tile, the slot (and with the item's last block, Q) is free
-      auto mma_s = [&](int t, int slot, bool last_tile, bool last_block) {
+      auto mma_s = [&](int t, int slot, uint32_t desc, bool last_tile, bool last_block) {
         const uint64_t a0 = umma_desc_sw128(q0 + t * S::kTileBytes, 16, 1024);
         const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, 16, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * S::kBox + (k & 3) * 32) >> 4;
-            umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, kDescS, k ? 1u : 0u);
+            umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, desc, k ? 1u : 0u);
           }
           umma_commit(&sfull[t]);
           if (last_tile) {
@@ -358,13 +361,14 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         }
         __syncwarp();
       };
-      // O_t += P_t V over 64 keys; after the second half the slot is free (last tile), O_t complete (last block)
-      auto mma_o = [&](int t, int slot, int half, bool acc, bool last_tile, bool last_block) {
+      // O_t += P_t V over 64 keys (kNarrow and none of a narrow block); after the second half the slot is free (last tile), O_t complete (last block)
+      auto mma_o = [&](int t, int slot, int half, int steps, bool acc, bool last_tile, bool last_block) {
         const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, S::kBox, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kKeys / 32; ++k) {
             const int kk = half * (kKeys / 32) + k;
+            if (kk >= steps) break;
             umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, b0 + ((kk * 2048) >> 4), kDescO, (acc || kk) ? 1u : 0u);
           }
           if (half && last_tile) umma_commit(&empty[slot]);
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         if (!ok) break;
         ++nq;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots, t == nt - 1, w.nb == 1);
+        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots, w.narrow ? kDescNarrow : kDescS, t == nt - 1, w.nb == 1);
         for (int j = 0; j < w.nb && ok; ++j) {
           // slots u: K of block j (read), u + 1: V of block j, u + 2: K of block j + 1
           const bool more = j + 1 < w.nb;
@@ -391,11 +395,11 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
               ok = wait(&pready[2 * t + half], np[t], kSiteTmemFull);
               if (!ok) break;
               tc_fence_after();
-              mma_o(t, (u + 1) % S::kSlots, half, j > 0, last, !more);
+              mma_o(t, (u + 1) % S::kSlots, half, w.narrow && j == 0 ? kNarrow / 16 : kKeys / 16, j > 0, last, !more);
             }
             if (!ok) break;
             ++np[t];
-            if (more) mma_s(t, (u + 2) % S::kSlots, last, j + 2 == w.nb);
+            if (more) mma_s(t, (u + 2) % S::kSlots, kDescS, last, j + 2 == w.nb);
           }
           u += 2;
         }
@@ -433,6 +437,34 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         // (rows without a query are not cut: what they compute goes nowhere)
         const int z = !live ? kKeys : (head ? min(w.sinks, pos + 1) : pos + 1) - start;
         const int a = head || !live ? 0 : from - start, s2 = head ? 0 : p.sinks - start;
+        if (w.narrow && j == 0) {  // the sinks, in kNarrow columns; an item's first block
+          uint32_t r[kNarrow], pk[kNarrow / 2];
+          tmem_ld32_issue(ts, r);
+          tmem_ld_wait(r);
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kNarrow; ++k) {
+            if (k >= z) r[k] = 0xff800000u;
+            top = fmaxf(top, __uint_as_float(r[k]));
+          }
+          m = top * p.sl2;
+          const float nm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+          for (int k = 0; k < kNarrow / 2; ++k) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(r[2 * k]), p.sl2, nm));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(r[2 * k + 1]), p.sl2, nm));
+            l += e0 + e1;
+            pk[k] = from_f32x2<T>(e0, e1);
+          }
+          tmem_st16(ts, pk);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&pready[2 * t]);
+            mbar_arrive(&pready[2 * t + 1]);
+          }
+          continue;
+        }
         const bool cut = __any_sync(0xffffffffu, z < kKeys || (a > 0 && s2 < kKeys));
         uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (cut)
@@ -505,13 +537,19 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       if (!ok) break;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       bool bad = !(l <= 3.0e38f);
-      T* dst = reinterpret_cast<T*>(p.out + (w.s.q0 + i) * p.out_token + (w.hk * p.group + hg) * p.out_head);
       if (w.nb) {
         ok = __all_sync(0xffffffffu, mbar_wait(&ofull[t], no & 1, c, kSiteTmemFull));
         if (!ok) break;
         ++no;
         tc_fence_after();
       }
+      // Four lanes hold four rows; they exchange 16-byte pieces so that a store covers 64 bytes of each of
+      // eight rows instead of 16 of 32.  Lane 4 r + x then stores piece x of rows 4 r .. 4 r + 3.
+      const long long mine = (w.s.q0 + i) * p.out_token + (w.hk * p.group + hg) * p.out_head;
+      const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      uint8_t* dst[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) dst[x] = p.out + __shfl_sync(0xffffffffu, mine, (lane & ~3) + x) + 16 * (lane & 3);
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float o[32];
@@ -521,22 +559,36 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
+        uint32_t v[4][4];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          bad |= !(fabsf(o[k]) <= 3.0e38f);
-          o[k] *= inv;
+        for (int k = 0; k < 16; ++k) {
+          bad |= !(fabsf(o[2 * k]) <= 3.0e38f) || !(fabsf(o[2 * k + 1]) <= 3.0e38f);
+          v[k >> 2][k & 3] = from_f32x2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
         }
-        if (live)
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            reinterpret_cast<uint4*>(dst)[4 * q + v] =
-                make_uint4(from_f32x2<T>(o[8 * v], o[8 * v + 1]), from_f32x2<T>(o[8 * v + 2], o[8 * v + 3]),
-                           from_f32x2<T>(o[8 * v + 4], o[8 * v + 5]), from_f32x2<T>(o[8 * v + 6], o[8 * v + 7]));
+        for (int h = 0; h < 2; ++h) {  // the transpose, by pairs at distance 1, then 2
+          const bool up = (lane >> h) & 1;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int lo = h ? x : 2 * x, hi = lo + (1 << h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[lo][k] : v[hi][k], 1 << h);
+              if (up) v[lo][k] = got;
+              else v[hi][k] = got;
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if ((lives >> ((lane & ~3) + x)) & 1u)
+            *reinterpret_cast<uint4*>(dst[x] + 64 * q) = make_uint4(v[x][0], v[x][1], v[x][2], v[x][3]);
       }
       if (live && p.lse)
         p.lse[static_cast<long long>(w.s.q0 + i) * p.heads + w.hk * p.group + hg] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
       tc_fence_before();
-      // rows with a non-finite result, once more from what they see
+      // rows with a non-finite result, once more from what they see (after the stores above, of other lanes)
+      __syncwarp();
       for (uint32_t again = __ballot_sync(0xffffffffu, bad && live); again; again &= again - 1) {
         const int x = __ffs(again) - 1;
         window_row<T, D>(p, __shfl_sync(0xffffffffu, w.s.q0 + i, x), w.hk * p.group + __shfl_sync(0xffffffffu, hg, x),
