@@ -15,8 +15,15 @@ struct CacheArgs {
   int num_pages, page_size, kv_heads;
 };
 
+// n / d for n < 2^31 as (umulhi(n, mul) + n) >> shift, exact.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
 // ---------------------------------------------------------------------------- append
-// One thread per 8 elements of a K and of a V row: 16 bytes read and 16 (8 for e4m3) written.
+// Each thread copies 16 bytes of a K and of a V row (8 bytes written for e4m3), two rows at a time so that
+// four loads are in flight.
 struct AppendParams {
   CacheArgs c;
   DevStatus* status;
@@ -24,10 +31,12 @@ struct AppendParams {
   const uint8_t* v;
   long long k_token, k_head, v_token, v_head;  // bytes
   const int* slots;
-  int tokens;
+  FastDiv by_heads, by_page;
+  uint32_t rows;  // tokens * kv_heads
 };
 
-// 8 elements of T divided by the scale, as e4m3 (nearest even, saturating; NaN stays NaN).
+// 8 elements of T divided by the scale, as e4m3 (nearest even, saturating; NaN stays NaN).  (A
+// multiplication by the reciprocal with the quotient only near a tie measured no faster.)
 template <class T>
 __device__ __forceinline__ uint2 quantise8(uint4 x, float scale) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
@@ -42,29 +51,40 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, float scale) {
 
 template <class T, bool Fp8, int D>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  constexpr int kVec = D / 8;
-  const long long n = static_cast<long long>(p.tokens) * p.c.kv_heads * kVec;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int vec = static_cast<int>(i % kVec);
-    const long long th = i / kVec;
-    const int h = static_cast<int>(th % p.c.kv_heads), t = static_cast<int>(th / p.c.kv_heads);
-    const int slot = p.slots[t];
-    if (slot < 0) continue;
-    const int page = slot / p.c.page_size;
-    if (page >= p.c.num_pages) {
-      if (h == 0 && vec == 0) report_index(p.status, static_cast<unsigned long long>(t));
-      continue;
+  constexpr int kVec = D / 8, kRowsCta = 256 / kVec, kBatch = 2;
+  const int vec = threadIdx.x % kVec;
+  for (uint32_t r0 = blockIdx.x * kRowsCta + threadIdx.x / kVec; r0 < p.rows; r0 += gridDim.x * (kRowsCta * kBatch)) {
+    uint4 k[kBatch], v[kBatch];
+    long long at[kBatch];
+    int head[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t r = r0 + b * gridDim.x * kRowsCta;
+      at[b] = -1;
+      if (r >= p.rows) continue;
+      const uint32_t t = divide(r, p.by_heads), h = r - t * p.c.kv_heads;
+      const int slot = __ldg(p.slots + t);
+      if (slot < 0) continue;
+      const uint32_t page = divide(static_cast<uint32_t>(slot), p.by_page);
+      if (page >= static_cast<uint32_t>(p.c.num_pages)) {
+        if (h == 0 && vec == 0) report_index(p.status, t);
+        continue;
+      }
+      head[b] = static_cast<int>(h);
+      at[b] = page * p.c.page_stride + (slot - static_cast<int>(page) * p.c.page_size) * p.c.row_stride + h * p.c.head_stride;
+      k[b] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + vec);
+      v[b] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + vec);
     }
-    const long long at = page * p.c.page_stride + (slot - page * p.c.page_size) * p.c.row_stride + h * p.c.head_stride;
-    const uint4 k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + vec);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + vec);
-    if constexpr (Fp8) {
-      reinterpret_cast<uint2*>(p.c.k + at)[vec] = quantise8<T>(k, p.c.k_scale ? p.c.k_scale[h] : 1.f);
-      reinterpret_cast<uint2*>(p.c.v + at)[vec] = quantise8<T>(v, p.c.v_scale ? p.c.v_scale[h] : 1.f);
-    } else {
-      reinterpret_cast<uint4*>(p.c.k + at)[vec] = k;
-      reinterpret_cast<uint4*>(p.c.v + at)[vec] = v;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (at[b] < 0) continue;
+      if constexpr (Fp8) {
+        reinterpret_cast<uint2*>(p.c.k + at[b])[vec] = quantise8<T>(k[b], p.c.k_scale ? __ldg(p.c.k_scale + head[b]) : 1.f);
+        reinterpret_cast<uint2*>(p.c.v + at[b])[vec] = quantise8<T>(v[b], p.c.v_scale ? __ldg(p.c.v_scale + head[b]) : 1.f);
+      } else {
+        reinterpret_cast<uint4*>(p.c.k + at[b])[vec] = k[b];
+        reinterpret_cast<uint4*>(p.c.v + at[b])[vec] = v[b];
+      }
     }
   }
 }
@@ -130,7 +150,7 @@ struct PagedParams {
   float* part;        // [CTA][2][rows][D + 2]: O, m, l of a segment
   unsigned* counter;  // [CTA]: segments done of the split item that starts in this one
   int max_pages, batch, heads, group, blocks;  // blocks: items per kv head
-  uint32_t div_mul, div_shift;  // row / page_size
+  FastDiv by_page;
   float sl2;          // scale * log2(e)
   int window, sinks;
 };
@@ -301,7 +321,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     const int i = load_at.tile * kTile + warp * kKeys + (lane & 15);
     if (i < load_at.vis.count) {
       const int row = i < load_at.vis.head ? i : i + load_at.vis.skip;
-      const uint32_t pg = (__umulhi(static_cast<uint32_t>(row), p.div_mul) + row) >> p.div_shift;
+      const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
       const int page = __ldg(p.table + static_cast<long long>(load_at.b) * p.max_pages + pg);
       if (page >= 0 && page < p.c.num_pages) {
         row_ok = true;
@@ -728,6 +748,14 @@ static CacheArgs cache_args(const tl_paged_cache* c) {
   return a;
 }
 
+static FastDiv fast_div(int d) {
+  FastDiv f;
+  f.shift = 0;
+  while ((1ull << f.shift) < static_cast<unsigned long long>(d)) ++f.shift;
+  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+
 static int launched() {
   if (cudaGetLastError() != cudaSuccess) return TL_ERR_CUDA;
   return TL_OK;
@@ -756,6 +784,7 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
       !esize_ok(v_head_stride, 2))
     return TL_ERR_INVALID;
   if (tokens == 0 || cache->kv_heads == 0) return TL_OK;
+  if (static_cast<long long>(tokens) * cache->kv_heads >= (1LL << 30)) return TL_ERR_INVALID;
   if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return TL_ERR_INVALID;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
   AppendParams p;
@@ -768,9 +797,11 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
   p.v_token = 2 * v_token_stride;
   p.v_head = 2 * v_head_stride;
   p.slots = slots;
-  p.tokens = tokens;
-  const long long n = static_cast<long long>(tokens) * cache->kv_heads * (cache->d / 8);
-  const long long need = (n + 255) / 256, most = 8LL * ctx->sms;
+  p.rows = static_cast<uint32_t>(tokens) * cache->kv_heads;
+  p.by_heads = fast_div(cache->kv_heads);
+  p.by_page = fast_div(cache->page_size);
+  const long long per_cta = 256 / (cache->d / 8);
+  const long long need = (p.rows + per_cta - 1) / per_cta, most = 16LL * ctx->sms;  // two rounds of a full GPU
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
     append_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>
         <<<static_cast<unsigned>(need < most ? need : most), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
@@ -830,10 +861,7 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   p.sl2 = scale * kLog2E;
   p.window = window;
   p.sinks = sinks;
-  // row / page_size as (umulhi(row, mul) + row) >> shift, exact for row < 2^31
-  p.div_shift = 0;
-  while ((1ull << p.div_shift) < static_cast<unsigned long long>(cache->page_size)) ++p.div_shift;
-  p.div_mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << p.div_shift) - cache->page_size)) / cache->page_size + 1);
+  p.by_page = fast_div(cache->page_size);
   // no more CTAs than tiles there can be
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;

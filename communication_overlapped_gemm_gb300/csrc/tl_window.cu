@@ -177,6 +177,18 @@ __device__ __forceinline__ int win_start(const WinItem& w, int j) {
   return j < w.nh ? j * win::kKeys : w.lo + (j - w.nh) * win::kKeys;
 }
 
+// A CTA's items: one of each round of gridDim.x, forwards and backwards in turn, so that the one with the
+// longest item of a round has the shortest of the next.  (Forwards always: 127 us against 110 on two
+// causal prompts of 3 and 4 thousand tokens.)
+__device__ __forceinline__ int win_next(int idx, int items) {
+  const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  for (int round = idx < 0 ? 0 : idx / grid + 1; round * grid < items; ++round) {
+    const int next = round * grid + (round & 1 ? grid - 1 - cta : cta);
+    if (next < items) return next;
+  }
+  return items;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16, one CTA.
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       bool ok = true;
       int u = 0, nq = 0;  // blocks and items loaded
       const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.group) * 128 * S::kHalves;
-      for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+      for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
         const WinItem w = win_item(p, cum, idx);
         if (w.nb == 0) continue;
         ok = mbar_wait(qempty, (nq & 1) ^ 1, c, kSiteEmpty);
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         }
         __syncwarp();
       };
-      for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+      for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
         const WinItem w = win_item(p, cum, idx);
         if (w.nb == 0) continue;
         const int nt = w.two ? 2 : 1;
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     const int tok = row / p.group, hg = row - tok * p.group;
     bool ok = true;
     int ns = 0, no = 0;  // S blocks and items seen
-    for (int idx = blockIdx.x; idx < items && ok; idx += gridDim.x) {
+    for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
       const WinItem w = win_item(p, cum, idx);
       if (t && !w.two) continue;
       const int i = w.i0 + t * p.tokens + tok;  // this row's query

@@ -449,7 +449,7 @@ typedef struct tl_paged_cache {
  * A cache of the activations' type takes the rows as they are.  An e4m3 cache takes
  * k / k_scale[h], computed in fp32, rounded to nearest even and saturated at +-448 (infinities
  * too; NaN stays NaN).
- * Shapes: d 64 or 128; num_pages * page_size < 2^31.  tokens == 0 or kv_heads == 0 is a no-op.
+ * Shapes: d 64 or 128; num_pages * page_size < 2^31; tokens * kv_heads < 2^30.  tokens == 0 or kv_heads == 0 is a no-op.
  */
 int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* k, const void* v,
                  long long k_token_stride, long long k_head_stride, long long v_token_stride,

@@ -85,6 +85,24 @@ def test_append(tl, ctx, dtype, tokens, heads, d, page, head_major, cache):
         assert np.array_equal(f64(pool), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_e4m3_rounds_every_value_as_the_quotient_does(tl, ctx, dtype):
+    """Every finite 16-bit value over scales of all sizes (powers of two give exact ties), against the
+    fp32 quotient rounded by torch on the CPU."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(DT[dtype])
+    rows = torch.where(torch.isfinite(bits), bits, torch.zeros((), dtype=DT[dtype])).view(16, 64, 64)
+    for k, base in enumerate((1.0, 0.0137, 3.3e-5, 2.0 ** -20, 700.0, 1e-33, 2e32)):
+        scale = torch.from_numpy(np.random.default_rng(k).uniform(0.6, 1.6, 64)).float() * base
+        scale[:4] = torch.tensor([base, base * 3, base / 7, base * 1.1])
+        pool = [torch.zeros((2, 16, 64, 64), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+        dev = rows.cuda()
+        tl.tl_kv_append(ctx, dev, dev, *pool, torch.arange(16, dtype=torch.int32, device="cuda"), k_scale=scale.cuda(),
+                        v_scale=scale.cuda())
+        want = (rows.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        for p in pool:
+            assert torch.equal(p[0].cpu().view(torch.uint8), want)
+
+
 def test_append_reports_slots_out_of_range_and_leaves_them_out(tl, ctx):
     k = draws(1, 4, 2, 64).bfloat16().cuda()
     guard = torch.zeros((8, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
