@@ -6,8 +6,8 @@
 // A tile is 128 rows: the G = heads / kv_heads query heads of one kv head for 128 / G consecutive tokens
 // (TMA reads them as one box), so short prompts fill tiles, a tile's window is narrow, and K and V
 // are read once for all G heads.  An item is two tiles side by side of one sequence and kv head, which
-// share every K and V block in shared memory; persistent CTAs take items in turn, those that
-// end a sequence (the longest without a window) first.  An item's keys are walked in blocks of 128:
+// share every K and V block in shared memory; persistent CTAs take items in turn, the longest
+// first (WinPlan).  An item's keys are walked in blocks of 128:
 // first the sinks that lie before its windows (up to 32 of them as a block of 32), then from
 // the first window's start to its last query.  Blocks start anywhere (a TMA row coordinate has no alignment), so a window of 1024 takes 9.
 //
@@ -36,6 +36,7 @@ namespace tl {
 
 namespace win {
 constexpr int kKeys = 128, kNarrow = 32, kMaxBatch = 1024;
+constexpr int kLevels = 256, kSorted = 32, kHeld = 32;  // order of items: see WinPlan
 constexpr int kThreads = 384;          // warps 0-3 (two of them idle), softmax warpgroups 4-7 and 8-11
 constexpr float kRescale = 8.f;
 template <int D>
@@ -47,7 +48,9 @@ struct Shape {
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
   static constexpr int kCumOff = kBarOff + 256;
-  static constexpr int kSmem = 1024 + kCumOff + (kMaxBatch + 1) * 4;
+  static constexpr int kPlanOff = kCumOff + (kMaxBatch + 4) * 4;
+  static constexpr int kHeldOff = kPlanOff + (kLevels + 4 + 2 * kSorted) * 4;
+  static constexpr int kSmem = 1024 + kHeldOff + kHeld * 64;
 };
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S_t at 128 t, O_t at 256 + 128 t
 }  // namespace win
@@ -140,8 +143,25 @@ __device__ __forceinline__ WinSeq win_seq(const WindowParams& p, int b, bool rep
   return s;
 }
 
+// The order of the items.  Of 2 to 32 sequences with several items a CTA, those whose tiles stand further into their keys come first,
+// in 256 levels of `gran` positions, so that a round of CTAs has items of about the same length; otherwise
+// sequence by sequence, the last tiles first.
+struct WinPlan {
+  bool sorted;
+  int* cum;    // [batch + 1]: items before each sequence (if not sorted)
+  int* above;  // [kLevels + 1]: above[0] all pairs of tiles, above[v + 1] those that start at (v + 1) gran or later
+  int* off;    // [kSorted]: position of a sequence's first query
+  int* pairs;  // [kSorted]: its pairs of tiles
+  int gran, items;
+};
+// Of a sequence's pairs of tiles, those that start at position x or later.
+__device__ __forceinline__ int pairs_from(int pairs, int off, int step, int x) {
+  const int first = x <= off ? 0 : (x - off + step - 1) / step;
+  return first < pairs ? pairs - first : 0;
+}
+
 // An item and the key blocks it walks.
-struct WinItem {
+struct alignas(16) WinItem {
   WinSeq s;
   int hk, i0;     // kv head, first query
   bool two;       // its second tile has queries
@@ -150,20 +170,46 @@ struct WinItem {
   int nh, nb;     // blocks of sinks, all blocks
   bool narrow;    // the sinks fit in kNarrow keys: their block is that wide
 };
-__device__ __forceinline__ WinItem win_item(const WindowParams& p, const int* cum, int idx) {
-  // the sequence that holds item idx: cum[b] <= idx < cum[b + 1]
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= idx) lo = mid; else hi = mid;
-  }
+// (a whole warp at once)
+__device__ __forceinline__ WinItem win_item(const WindowParams& p, const WinPlan& plan, int idx, int lane) {
+  const int step = 2 * p.tokens;
   WinItem w;
-  w.s = win_seq(p, lo, false);
-  const int in = idx - cum[lo], tiles = (cum[lo + 1] - cum[lo]) / p.kv_heads;
-  w.hk = in % p.kv_heads;
-  w.i0 = (tiles - 1 - in / p.kv_heads) * 2 * p.tokens;
+  int b, pair;
+  if (plan.sorted) {
+    const int rank = idx / p.kv_heads;
+    w.hk = idx - rank * p.kv_heads;
+    int lo = 0, hi = win::kLevels;  // the level v with above[v + 1] <= rank < above[v]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (plan.above[mid + 1] <= rank) hi = mid; else lo = mid + 1;
+    }
+    const int n = lane < p.batch ? plan.pairs[lane] : 0, off = lane < p.batch ? plan.off[lane] : 0;
+    const int after = pairs_from(n, off, step, (lo + 1) * plan.gran);
+    const int here = (lo ? pairs_from(n, off, step, lo * plan.gran) : n) - after;
+    int sum = here;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, x);
+      if (lane >= x) sum += o;
+    }
+    const int in = rank - plan.above[lo + 1];
+    b = __popc(__ballot_sync(0xffffffffu, sum <= in));
+    pair = __shfl_sync(0xffffffffu, n - after - 1 - (in - (sum - here)), b);
+  } else {
+    int lo = 0, hi = p.batch;  // the sequence that holds the item: cum[b] <= idx < cum[b + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (plan.cum[mid] <= idx) lo = mid; else hi = mid;
+    }
+    b = lo;
+    const int in = idx - plan.cum[lo], pairs = (plan.cum[lo + 1] - plan.cum[lo]) / p.kv_heads;
+    w.hk = in % p.kv_heads;
+    pair = pairs - 1 - in / p.kv_heads;
+  }
+  w.s = win_seq(p, b, false);
+  w.i0 = pair * step;
   w.two = w.i0 + p.tokens < w.s.n;
-  const int end = min(w.i0 + 2 * p.tokens, w.s.n);  // one past the last query
+  const int end = min(w.i0 + step, w.s.n);  // one past the last query
   const int first = w.s.off + w.i0, last = w.s.off + end - 1;  // positions
   w.lo = p.window == 0 || first < p.window ? 0 : first - p.window + 1;
   w.sinks = min(p.sinks, w.lo);
@@ -177,16 +223,12 @@ __device__ __forceinline__ int win_start(const WinItem& w, int j) {
   return j < w.nh ? j * win::kKeys : w.lo + (j - w.nh) * win::kKeys;
 }
 
-// A CTA's items: one of each round of gridDim.x, forwards and backwards in turn, so that the one with the
-// longest item of a round has the shortest of the next.  (Forwards always: 127 us against 110 on two
-// causal prompts of 3 and 4 thousand tokens.)
-__device__ __forceinline__ int win_next(int idx, int items) {
+// A CTA's k-th item: one of each round of gridDim.x, forwards and backwards in turn, so that the one with the
+// longest item of a round has the shortest of the next (one causal prompt of 8k: 408 us forwards, 370 so).
+// From `items` on there is none.
+__device__ __forceinline__ int win_index(int k) {
   const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  for (int round = idx < 0 ? 0 : idx / grid + 1; round * grid < items; ++round) {
-    const int next = round * grid + (round & 1 ? grid - 1 - cta : cta);
-    if (next < items) return next;
-  }
-  return items;
+  return k * grid + (k & 1 ? grid - 1 - cta : cta);
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16, one CTA.
@@ -258,14 +300,22 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   uint64_t* ofull = pready + 4;            // [2] the item's last PV_t is complete
   uint64_t* drain = ofull + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
-  int* cum = reinterpret_cast<int*>(base + S::kCumOff);
+  WinPlan plan;
+  plan.cum = reinterpret_cast<int*>(base + S::kCumOff);
+  plan.above = reinterpret_cast<int*>(base + S::kPlanOff);
+  plan.off = plan.above + kLevels + 1;
+  plan.pairs = plan.off + kSorted;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Common& c = p.common;
 
-  // items before each sequence
   for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     const WinSeq s = win_seq(p, b, blockIdx.x == 0);
-    cum[b + 1] = (s.n + 2 * p.tokens - 1) / (2 * p.tokens) * p.kv_heads;
+    const int pairs = (s.n + 2 * p.tokens - 1) / (2 * p.tokens);
+    plan.cum[b + 1] = pairs * p.kv_heads;
+    if (b < kSorted) {
+      plan.off[b] = s.off;
+      plan.pairs[b] = pairs;
+    }
   }
   if (threadIdx.x == 0) {
     mbar_init(qfull, 1);
@@ -292,46 +342,75 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  plan.gran = kKeys;
+  plan.sorted = false;
+  if (p.batch > 1 && p.batch <= kSorted) {  // in every warp alike
+    int end = lane < p.batch ? plan.off[lane] + plan.pairs[lane] * 2 * p.tokens : 0, all = lane < p.batch ? plan.pairs[lane] : 0;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+      end = max(end, __shfl_xor_sync(0xffffffffu, end, x));
+      all += __shfl_xor_sync(0xffffffffu, all, x);
+    }
+    plan.gran = max(plan.gran, (end + kLevels - 1) / kLevels);
+    plan.sorted = all * p.kv_heads > static_cast<int>(gridDim.x);
+  }
+  if (plan.sorted) {
+    for (int v = threadIdx.x; v <= kLevels; v += kThreads) {
+      int sum = 0;
+      for (int b = 0; b < p.batch; ++b)
+        sum += v ? pairs_from(plan.pairs[b], plan.off[b], 2 * p.tokens, v * plan.gran) : plan.pairs[b];
+      plan.above[v] = sum;
+    }
+  } else if (warp == 0) {
     int sum = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      int v = b0 + lane < p.batch ? cum[b0 + lane + 1] : 0;
+      int v = b0 + lane < p.batch ? plan.cum[b0 + lane + 1] : 0;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, v, x);
         if (lane >= x) v += o;
       }
-      if (b0 + lane < p.batch) cum[b0 + lane + 1] = sum + v;
+      if (b0 + lane < p.batch) plan.cum[b0 + lane + 1] = sum + v;
       sum += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) cum[0] = 0;
+    if (lane == 0) plan.cum[0] = 0;
   }
   __syncthreads();
+  const int items = plan.sorted ? plan.above[0] * p.kv_heads : plan.cum[p.batch];
+  // the CTA's first items, looked up by all warps at once; later ones by each warp as it comes to them
+  WinItem* held = reinterpret_cast<WinItem*>(base + S::kHeldOff);
+  static_assert(sizeof(WinItem) <= 64, "room");
+  for (int k = warp; k < kHeld && win_index(k) < items; k += kThreads / 32) {
+    const WinItem w = win_item(p, plan, win_index(k), lane);
+    if (lane == 0) held[k] = w;
+  }
+  __syncthreads();
+  auto item = [&](int k) { return k < kHeld ? held[k] : win_item(p, plan, win_index(k), lane); };
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
-  const int items = cum[p.batch];
   // Registers: 128 x 88 + 256 x 208 = 384 x 168, what the CTA has at launch.
   if (warp < 4) {
     regs_down<88>();
   if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      bool ok = true;
-      int u = 0, nq = 0;  // blocks and items loaded
-      const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.group) * 128 * S::kHalves;
-      for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
-        const WinItem w = win_item(p, cum, idx);
-        if (w.nb == 0) continue;
+    // ------------------------------------------------------------ loads (lane 0; the whole warp finds the items)
+    bool ok = true;
+    int u = 0, nq = 0;  // blocks and items loaded
+    const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.group) * 128 * S::kHalves;
+    for (int k = 0; ok && win_index(k) < items; ++k) {
+      const WinItem w = item(k);
+      if (w.nb == 0) continue;
+      if (lane == 0) {
         ok = mbar_wait(qempty, (nq & 1) ^ 1, c, kSiteEmpty);
-        if (!ok) break;
-        mbar_arrive_expect_tx(qfull, q_bytes * (w.two ? 2 : 1));
-        for (int t = 0; t < (w.two ? 2 : 1); ++t)
-          for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(base + t * S::kTileBytes + h * S::kBox, &p.tq, qfull, 64 * h, w.hk * p.group,
-                        w.s.q0 + w.i0 + t * p.tokens);
-        ++nq;
+        if (ok) {
+          mbar_arrive_expect_tx(qfull, q_bytes * (w.two ? 2 : 1));
+          for (int t = 0; t < (w.two ? 2 : 1); ++t)
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_load_3d(base + t * S::kTileBytes + h * S::kBox, &p.tq, qfull, 64 * h, w.hk * p.group,
+                          w.s.q0 + w.i0 + t * p.tokens);
+          ++nq;
+        }
         for (int j = 0; j < w.nb && ok; ++j)
-          for (int kv = 0; kv < 2 && ok; ++kv, ++u) {
+          for (int kv = 0; kv < 2 && ok; ++kv) {
             const int s = u % S::kSlots;
             ok = mbar_wait(&empty[s], ((u / S::kSlots) & 1) ^ 1, c, kSiteEmpty);
             if (!ok) break;
@@ -339,9 +418,13 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
             for (int h = 0; h < S::kHalves; ++h)
               tma_load_3d(base + S::kRingOff + s * S::kTileBytes + h * S::kBox, kv ? &p.tv : &p.tk, &full[s], 64 * h, w.hk,
                           w.s.k0 + win_start(w, j));
+            ++u;
           }
       }
-      // every load has landed before the CTA ends (at once, unless a wait ran out)
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+    // every load has landed before the CTA ends (at once, unless a wait ran out)
+    if (lane == 0) {
       if (nq) mbar_wait(qfull, (nq - 1) & 1, c, kSiteDrain);
       for (int j = u > S::kSlots ? u - S::kSlots : 0; j < u; ++j) mbar_wait(&full[j % S::kSlots], (j / S::kSlots) & 1, c, kSiteDrain);
     }
@@ -388,8 +471,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         }
         __syncwarp();
       };
-      for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
-        const WinItem w = win_item(p, cum, idx);
+      for (int it = 0; ok && win_index(it) < items; ++it) {
+        const WinItem w = item(it);
         if (w.nb == 0) continue;
         const int nt = w.two ? 2 : 1;
         ok = wait(qfull, nq, kSiteFull) && wait_block(u);
@@ -430,8 +513,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     const int tok = row / p.group, hg = row - tok * p.group;
     bool ok = true;
     int ns = 0, no = 0;  // S blocks and items seen
-    for (int idx = win_next(-1, items); idx < items && ok; idx = win_next(idx, items)) {
-      const WinItem w = win_item(p, cum, idx);
+    for (int it = 0; ok && win_index(it) < items; ++it) {
+      const WinItem w = item(it);
       if (t && !w.two) continue;
       const int i = w.i0 + t * p.tokens + tok;  // this row's query
       const bool live = tok < p.tokens && i < w.s.n;
