@@ -100,13 +100,16 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 // a tcgen05 instruction, and CUDA cores alone would need G fused multiply-adds per element, 27 T/s
 // at G = 8 and full HBM rate of the 39 T/s that the SMs have.
 //
-// Work: an item is (sequence, kv head, block of 8 or 16 query heads), a tile 64 of its visible keys.  All tiles of
+// Work: an item is (sequence, kv head, block of 8 or 16 query heads), a tile 64 of its visible keys.
+// (Rows of less than 256 bytes that lie side by side, the heads of a token, are read together: an item
+// is then `wh` kv heads, 2 or 4, and a tile 64 / wh keys; a warp has one of the heads.  With pieces of 128
+// bytes read far apart HBM gave 0.80 of its copy rate, with 64 bytes 0.45.)  All tiles of
 // all items form one line, cut into equal ranges, one per CTA, so ragged batches are even and few
 // long sequences are spread over all SMs.  Each CTA derives the plan from the lengths by a prefix
 // sum.  A CTA's part of an item is a segment; warp w takes keys [16 w, 16 w + 16) of each of its
 // tiles, with its own m, l, O and its own ring of cp.async stages: inside a segment no warp waits
 // for another, and loads of the next segment are in flight while one ends.  At a segment's end the
-// four warps merge in shared memory.  A whole item is written at once; a part goes to the workspace (at
+// warps of a head merge in shared memory.  A whole item is written at once; a part goes to the workspace (at
 // most two per CTA), and the CTA that finishes an item's last part (a counter, left at zero again)
 // joins all parts in the order of the line.  Nothing waits, and the order of the sums is fixed by
 // the lengths.
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 // run in fp16.  Weights are rounded to the products' 16-bit type (half a step) to meet V there; l sums
 // them unrounded in fp32.
 namespace paged {
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kMaxRows = 16;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kMaxRows = 32;
 template <bool Fp8, int D, int NB>
 struct Shape {
   static constexpr int kRows = 8 * NB;                   // query heads of an item
@@ -132,11 +135,13 @@ struct Shape {
   static constexpr int kMergeOff = kStages * kWarps * 2 * kHalf;
   static constexpr int kMlOff = kMergeOff + kWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kMlOff + kWarps * kRows * 2 * 4;
-  static constexpr int kPart = kRows * (D + 2);          // floats of a segment's part: O, then m and l
+  static constexpr int kPartRows = NB == 1 ? 32 : 16;    // query heads of an item's kv heads, at most
+  static constexpr int kPart = kPartRows * (D + 2);      // floats of a segment's part: O, then m and l
 };
 }  // namespace paged
 
-constexpr int kPagedMaxCtas = kCutCounters;
+constexpr int kPagedMaxCtas = 640;
+static_assert(kPagedMaxCtas <= kCutCounters, "a counter per CTA");
 
 struct PagedParams {
   CacheArgs c;
@@ -150,6 +155,7 @@ struct PagedParams {
   float* part;        // [CTA][2][rows][D + 2]: O, m, l of a segment
   unsigned* counter;  // [CTA]: segments done of the split item that starts in this one
   int max_pages, batch, heads, group, blocks;  // blocks: items per kv head
+  int lw;             // log2 of the kv heads of an item
   FastDiv by_page;
   float sl2;          // scale * log2(e)
   int window, sinks;
@@ -184,7 +190,7 @@ __device__ __forceinline__ int paged_length(const PagedParams& p, int b, bool re
   }
   return n;
 }
-__device__ __forceinline__ int paged_tiles(int count) { return (count + paged::kTile - 1) / paged::kTile; }
+__device__ __forceinline__ int paged_tiles(int count, int lw) { return (count + (paged::kTile >> lw) - 1) >> (6 - lw); }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -234,7 +240,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   __shared__ float s_max[kMaxRows];
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int subs = p.c.kv_heads * p.blocks;
+  const int subs = (p.c.kv_heads >> p.lw) * p.blocks;
+  // this warp's kv head of an item's, and its 16 keys of a tile's
+  const int hw = warp & ((1 << p.lw) - 1), kb = warp >> p.lw;
 
   // ---------------------------------------------------------------- plan
   // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk); s_sum holds the sums inside a warp.
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       const int b = static_cast<int>(threadIdx.x) * chunk + i;
       if (b >= p.batch) break;
       const int count = visible_rows(paged_length(p, b, blockIdx.x == 0), p.window, p.sinks).count;
-      sum += paged_tiles(count);
+      sum += paged_tiles(count, p.lw);
       if (count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
         for (int h = 0; h < p.heads; ++h) {
           uint4* o = reinterpret_cast<uint4*>(p.out + b * p.out_seq + h * p.out_head);
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     at.b = (32 * w + i) * chunk;
     for (;;) {
       at.vis = visible_rows(paged_length(p, at.b, false), p.window, p.sinks);
-      at.tiles = paged_tiles(at.vis.count);
+      at.tiles = paged_tiles(at.vis.count, p.lw);
       const uint32_t here = static_cast<uint32_t>(at.tiles) * subs;
       if (first < pos + here) break;
       pos += here;
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     a.sub = 0;
     while (++a.b < p.batch) {
       a.vis = visible_rows(paged_length(p, a.b, false), p.window, p.sinks);
-      a.tiles = paged_tiles(a.vis.count);
+      a.tiles = paged_tiles(a.vis.count, p.lw);
       if (a.tiles > 0) return;
     }
   };
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     row_ok = false;
     row_off = 0;
     if (step_loaded >= nsteps) return;
-    const int i = load_at.tile * kTile + warp * kKeys + (lane & 15);
+    const int i = load_at.tile * (kTile >> p.lw) + kb * kKeys + (lane & 15);
     if (i < load_at.vis.count) {
       const int row = i < load_at.vis.head ? i : i + load_at.vis.skip;
       const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       if (page >= 0 && page < p.c.num_pages) {
         row_ok = true;
         row_off = page * p.c.page_stride + (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
-                  (load_at.sub / p.blocks) * p.c.head_stride;
+                  (((NB == 1 ? load_at.sub : load_at.sub / p.blocks) << p.lw) + hw) * p.c.head_stride;
       } else {
         report_index(p.status, static_cast<unsigned long long>(load_at.b));
       }
@@ -379,7 +387,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     // a segment: this CTA's tiles of one item
     const int seg_tile = at.tile;
     const int seg = nsteps - step < at.tiles - at.tile ? nsteps - step : at.tiles - at.tile;
-    const int hk = at.sub / p.blocks, r0 = (at.sub - hk * p.blocks) * kRows, h0 = hk * p.group + r0;
+    const int hk0 = (NB == 1 ? at.sub : at.sub / p.blocks) << p.lw, hk = hk0 + hw;  // (NB 1: one block)
+    const int r0 = NB == 1 ? 0 : at.sub % p.blocks * kRows, h0 = hk * p.group + r0;
     const int rows = p.group - r0 < kRows ? p.group - r0 : kRows;
     // q as the products' B: column g of block b (zero past the group)
     const float sl2 = Fp8 && p.c.k_scale ? p.sl2 * __ldg(p.c.k_scale + hk) : p.sl2;
@@ -592,12 +601,12 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       }
     __syncthreads();
     const bool whole = seg == at.tiles;
-    const int vecs = rows * (D / 4);  // float4s of the merged rows
+    const int all = rows << p.lw, vecs = all * (D / 4);  // the item's query heads; float4s of them
     float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_tile ? 0 : 1)) * S::kPart;
-    const float vs = Fp8 && p.c.v_scale ? __ldg(p.c.v_scale + hk) : 1.f;
-    auto write_out = [&](int row, int d, float4 v, float mm, float ll) {
-      const float inv = ll == 0.f ? 0.f : vs / ll;
-      const int h = h0 + row;
+    auto head_of = [&](int r) { return NB == 1 ? (r >= rows) + (r >= 2 * rows) + (r >= 3 * rows) : 0; };  // of the item's
+    auto write_out = [&](int r, int d, float4 v, float mm, float ll) {
+      const int head = head_of(r), kv = hk0 + head, h = kv * p.group + r0 + r - head * rows;
+      const float vs = Fp8 && p.c.v_scale ? __ldg(p.c.v_scale + kv) : 1.f, inv = ll == 0.f ? 0.f : vs / ll;
       *reinterpret_cast<uint2*>(p.out + at.b * p.out_seq + h * p.out_head + d * 2) =
           make_uint2(from_f32x2<T>(v.x * inv, v.y * inv), from_f32x2<T>(v.z * inv, v.w * inv));
       if (p.lse && d == 0)
@@ -610,24 +619,23 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       acc.w += f * v.w;
     };
     for (int i = threadIdx.x; i < vecs; i += kThreads) {
-      const int row = i / (D / 4), d = (i % (D / 4)) * 4;
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      const int head = head_of(r), row = r - head * rows;
       float mm = -INFINITY, ll = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + row].x);
+      for (int w = head; w < kWarps; w += 1 << p.lw) mm = fmaxf(mm, ml[w * kRows + row].x);
       const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = head; w < kWarps; w += 1 << p.lw) {
         const float2 z = ml[w * kRows + row];
         const float f = ex2_approx(z.x - base);
         ll += f * z.y;
         add(acc, f, *reinterpret_cast<const float4*>(merge + (w * kRows + row) * S::kPitch + d));
       }
       if (whole) {
-        write_out(row, d, acc, mm, ll);
+        write_out(r, d, acc, mm, ll);
       } else {
-        *reinterpret_cast<float4*>(part + row * D + d) = acc;
-        if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * row) = make_float2(mm, ll);
+        *reinterpret_cast<float4*>(part + r * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(part + S::kPartRows * D + 2 * r) = make_float2(mm, ll);
       }
     }
     if (!whole) {
@@ -649,9 +657,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         const float* one = p.part + (static_cast<size_t>(c0) * 2 + 1) * S::kPart;
         const float* rest = p.part + static_cast<size_t>(c0 + 1) * kStride;
         const int more = c1 - c0;  // parts after the first
-        for (int row = warp; row < rows; row += kWarps) {  // a row's maximum over all parts
-          float mm = lane == 0 ? __ldcg(one + kRows * D + 2 * row) : -INFINITY;
-          const float* src = rest + static_cast<size_t>(lane) * kStride + kRows * D + 2 * row;
+        for (int row = warp; row < all; row += kWarps) {  // a row's maximum over all parts
+          float mm = lane == 0 ? __ldcg(one + S::kPartRows * D + 2 * row) : -INFINITY;
+          const float* src = rest + static_cast<size_t>(lane) * kStride + S::kPartRows * D + 2 * row;
 #pragma unroll 2
           for (int c = lane; c < more; c += 32, src += 32 * kStride) mm = fmaxf(mm, __ldcg(src));
 #pragma unroll
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
               add(acc, f, u);
             };
             if (team == 0)
-              fold(__ldcg(reinterpret_cast<const float2*>(one + kRows * D + 2 * row)),
+              fold(__ldcg(reinterpret_cast<const float2*>(one + S::kPartRows * D + 2 * row)),
                    __ldcg(reinterpret_cast<const float4*>(one + row * D + d)));
             const float* src = rest + static_cast<size_t>(team) * kStride;
             const int step_floats = teams * kStride;
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
                 z[x] = make_float2(-INFINITY, 0.f);
                 u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c + x * teams < more) {
-                  z[x] = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * row));
+                  z[x] = __ldcg(reinterpret_cast<const float2*>(src + S::kPartRows * D + 2 * row));
                   u[x] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
                 }
               }
@@ -817,7 +825,8 @@ static int paged_blocks(int heads, int kv_heads) {
 
 extern "C" size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d) {
   if (batch < 0 || batch > 4096 || !heads_ok(heads, kv_heads, d)) return 0;
-  return kCounterBytes + static_cast<size_t>(kPagedMaxCtas) * 2 * paged_rows(heads, kv_heads) * (d + 2) * 4;
+  const int rows = paged_rows(heads, kv_heads) == 8 ? 32 : 16;  // Shape::kPartRows
+  return kCounterBytes + static_cast<size_t>(kPagedMaxCtas) * 2 * rows * (d + 2) * 4;
 }
 
 extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* q,
@@ -865,7 +874,12 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   // no more CTAs than tiles there can be
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
-  const long long most = batch * static_cast<long long>(cache->kv_heads) * p.blocks * (cap / paged::kTile + 1);
+  // kv heads read together: side by side, as many as make 256 bytes of a token
+  const int es = cache->dtype == TL_E4M3 ? 1 : 2;
+  p.lw = 0;
+  if (p.group <= 8 && cache->head_stride == cache->d)
+    while (p.lw < 2 && ((cache->d * es) << p.lw) < 256 && cache->kv_heads % (2 << p.lw) == 0) ++p.lw;
+  const long long most = batch * static_cast<long long>(cache->kv_heads >> p.lw) * p.blocks * (cap / (paged::kTile >> p.lw) + 1);
   if (most >= (1LL << 31)) return TL_ERR_INVALID;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
     auto launch = [&](auto nb) {

@@ -201,6 +201,22 @@ def test_paged_attention_splits_long_sequences(tl, ctx):
         check_paged(q, pools, table, lengths, out, e)
 
 
+@pytest.mark.parametrize("heads,kv", [(4, 4), (12, 4), (64, 8), (6, 2), (16, 2)])
+@pytest.mark.parametrize("d,dtype,cache", [(64, "bf16", "bf16"), (64, "fp16", "e4m3"), (128, "bf16", "e4m3")])
+def test_paged_attention_heads_side_by_side(tl, ctx, heads, kv, d, dtype, cache):
+    """Short rows of several kv heads that lie side by side, whole sequences and split ones, and the same
+    rows in head-major pages."""
+    for major in (False, True):
+        q, pools, table, lengths = paged_case([3001, 1, 0, 40, 129], heads, kv, d, 16, dtype, cache, major, seed=heads)
+        s = {}
+        if cache == "e4m3":
+            s = dict(k_scale=torch.rand(kv, device="cuda") * 0.02 + 0.01, v_scale=torch.rand(kv, device="cuda") * 0.02 + 0.01)
+        for window, sinks in ((0, 0), (333, 20)):
+            out, e = run_paged(tl, ctx, q, pools, table, lengths, window=window, sinks=sinks, **s)
+            assert ctx.check() == tl.TL_OK
+            check_paged(q, pools, table, lengths, out, e, window, sinks, **s)
+
+
 def test_paged_attention_workspace_serves_calls_of_other_shapes(tl, ctx):
     w = ws(max(tl.tl_paged_attention_workspace_bytes(b, h, kv, d) for b, h, kv, d in
                ((1, 8, 1, 128), (5, 34, 2, 64), (13, 4, 4, 128))))
