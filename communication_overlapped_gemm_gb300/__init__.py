@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -454,34 +455,45 @@ def _vec(t, n: int, dtype_name: str, what: str) -> int:
     return t.data_ptr()
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale) -> PagedCache:
-    code = _code(k_cache, "k_cache")
+_pack_cache = struct.Struct("=4Q3q5i4x").pack  # PagedCache, at half its cost
+assert struct.calcsize("=4Q3q5i4x") == ctypes.sizeof(PagedCache)
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """A tl_paged_cache (as bytes) and its kv heads and d."""
     shape, strides = k_cache.shape, k_cache.stride()
+    code = _codes.get(k_cache.dtype)
+    if code is None or not k_cache.is_cuda:
+        code = _code(k_cache, "k_cache")
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_cuda:
         raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
     pages, page, heads, d = shape
     a, b, c, one = strides
     if v_cache.stride() != strides or one != 1:
         raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _vec(k_scale, heads, "f32", "k_scale"),
-                      _vec(v_scale, heads, "f32", "v_scale"), a if pages > 1 else 0, b if page > 1 else 0,
-                      c if heads > 1 else 0, code, pages, page, heads, d)
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(),
+                       0 if k_scale is None else _vec(k_scale, heads, "f32", "k_scale"),
+                       0 if v_scale is None else _vec(v_scale, heads, "f32", "v_scale"), a if pages > 1 else 0,
+                       b if page > 1 else 0, c if heads > 1 else 0, code, pages, page, heads, d), heads, d
 
 
 def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None) -> None:
     """Write the rows k, v (bf16 or fp16 [tokens, kv_heads, d]) into a paged cache ([pages, page_size,
     kv_heads, d] views of any page, row and head strides; the type of k, or float8_e4m3fn holding
     k / k_scale[h]) at slots (int32 [tokens]: page * page_size + row; negative: skipped)."""
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    code = _code(k, "k")
-    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or not v.is_cuda or \
-            k.shape[1:] != (cache.kv_heads, cache.d):
+    cache, heads, d = _cache(k_cache, v_cache, k_scale, v_scale)
+    code, shape = _code(k, "k"), k.shape
+    if len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or not v.is_cuda or shape[1] != heads or \
+            shape[2] != d:
         raise ValueError("inconsistent shapes")
-    n = k.shape[0]
+    n = shape[0]
     sp = _vec(slots, n, "i32", "slots")
-    rc = lib().tl_kv_append(ctx.handle, ctypes.byref(cache), code, k.data_ptr(), v.data_ptr(), *_rows(k, "k"),
-                            *_rows(v, "v"), sp, n, _stream(stream, ctx.device))
-    _check(rc, "tl_kv_append")
+    ka, kb = _rows(k, "k")
+    va, vb = _rows(v, "v")
+    rc = lib().tl_kv_append(ctx.handle, cache, code, k.data_ptr(), v.data_ptr(), ka, kb, va, vb, sp, n,
+                            _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_kv_append")
 
 
 def tl_paged_attention_workspace_bytes(batch, heads, kv_heads, d) -> int:
@@ -494,21 +506,24 @@ def tl_paged_attention(ctx: Context, q, k_cache, v_cache, page_table, lengths, o
     first lengths[b] rows, with a window only the last `window` and the first `sinks` of them.
     q, out: bf16 or fp16 [batch, heads, d]; caches as tl_kv_append; page_table int32 [batch, max_pages];
     lengths int32 [batch] (the new token's row counted); lse fp32 [batch, heads]; scale: 1/sqrt(d)."""
-    cache = _cache(k_cache, v_cache, k_scale, v_scale)
-    code = _code(q, "q")
-    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or q.shape[2] != cache.d or \
-            page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+    cache, _, d = _cache(k_cache, v_cache, k_scale, v_scale)
+    code, shape, tshape = _code(q, "q"), q.shape, page_table.shape
+    if len(shape) != 3 or out.shape != shape or out.dtype is not q.dtype or not out.is_cuda or shape[2] != d or \
+            len(tshape) != 2 or tshape[0] != shape[0]:
         raise ValueError("inconsistent shapes")
-    batch, heads, d = q.shape
-    pages = page_table.shape[1]
+    batch, heads, _ = shape
+    pages = tshape[1]
     _need(workspace, "u8", "workspace")
     tp = _vec(page_table, batch * pages, "i32", "page_table")
     lp = _vec(lengths, batch, "i32", "lengths")
-    rc = lib().tl_paged_attention(ctx.handle, ctypes.byref(cache), code, q.data_ptr(), *_rows(q, "q"), tp, pages, lp,
-                                  out.data_ptr(), *_rows(out, "out"), _vec(lse, batch * heads, "f32", "lse"), batch,
-                                  heads, d ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
+    qa, qb = _rows(q, "q")
+    oa, ob = _rows(out, "out")
+    rc = lib().tl_paged_attention(ctx.handle, cache, code, q.data_ptr(), qa, qb, tp, pages, lp, out.data_ptr(), oa, ob,
+                                  0 if lse is None else _vec(lse, batch * heads, "f32", "lse"), batch, heads,
+                                  d ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
                                   workspace.numel(), _stream(stream, ctx.device))
-    _check(rc, "tl_paged_attention")
+    if rc:
+        _check(rc, "tl_paged_attention")
 
 
 def tl_window_attention(ctx: Context, q, k, v, cu_q, cu_k, out, lse=None, scale=None, window: int = 0, sinks: int = 0,
@@ -517,22 +532,26 @@ def tl_window_attention(ctx: Context, q, k, v, cu_q, cu_k, out, lse=None, scale=
     rows cu_k[b]..cu_k[b+1], its last query at its last key; with a window a query sees the last
     `window` keys up to its own and the first `sinks` ones.  q, out: bf16 or fp16 [total_q, heads, d];
     k, v: [total_k, kv_heads, d]; cu_q, cu_k: int32 [batch + 1]; lse: fp32 [total_q, heads]."""
-    code = _code(q, "q")
-    if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or v.shape != k.shape or k.shape[2] != q.shape[2] or \
+    code, dtype, shape, kshape = _code(q, "q"), q.dtype, q.shape, k.shape
+    if len(shape) != 3 or len(kshape) != 3 or out.shape != shape or v.shape != kshape or kshape[2] != shape[2] or \
             cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.numel() < 1:
         raise ValueError("inconsistent shapes")
     for t, what in ((k, "k"), (v, "v"), (out, "out")):
-        if t.dtype != q.dtype or not t.is_cuda:
+        if t.dtype is not dtype or not t.is_cuda:
             raise ValueError(f"{what} must be a CUDA tensor of q's type (got {t.dtype}, {t.device})")
-    total_q, heads, d = q.shape
-    batch = cu_q.numel() - 1
-    rc = lib().tl_window_attention(ctx.handle, code, q.data_ptr(), *_rows(q, "q"), k.data_ptr(), *_rows(k, "k"),
-                                   v.data_ptr(), *_rows(v, "v"), _vec(cu_q, batch + 1, "i32", "cu_q"),
-                                   _vec(cu_k, batch + 1, "i32", "cu_k"), out.data_ptr(), *_rows(out, "out"),
-                                   _vec(lse, total_q * heads, "f32", "lse"), batch, total_q, k.shape[0], heads,
-                                   k.shape[1], d, d ** -0.5 if scale is None else scale, window, sinks,
-                                   _stream(stream, ctx.device))
-    _check(rc, "tl_window_attention")
+    total_q, heads, d = shape
+    n = cu_q.numel()
+    qa, qb = _rows(q, "q")
+    ka, kb = _rows(k, "k")
+    va, vb = _rows(v, "v")
+    oa, ob = _rows(out, "out")
+    rc = lib().tl_window_attention(ctx.handle, code, q.data_ptr(), qa, qb, k.data_ptr(), ka, kb, v.data_ptr(), va, vb,
+                                   _vec(cu_q, n, "i32", "cu_q"), _vec(cu_k, n, "i32", "cu_k"), out.data_ptr(), oa, ob,
+                                   0 if lse is None else _vec(lse, total_q * heads, "f32", "lse"), n - 1, total_q,
+                                   kshape[0], heads, kshape[1], d, d ** -0.5 if scale is None else scale, window,
+                                   sinks, _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_window_attention")
 
 
 def tl_moe_tokens_workspace_bytes(T, H, E, F, topk) -> int:
