@@ -24,6 +24,12 @@
 // stay below 2^8 and the stale maximum cancels in O / l).
 // P is rounded to the 16-bit type of V (half a step each); l sums it unrounded in fp32.
 //
+// Bound: the tensor pipe and the softmax in turn.  Of a block of 128 keys a tile's S takes 8 MMAs of 70 cycles
+// (4 at d 64), its softmax 1190, PV 8 MMAs of 108 (A comes from TMEM, which costs the same at any N): the two
+// tiles' MMAs are 2850 cycles (2290 at d 64) of the about 3300 (3000) that a block takes.  Measured (32 heads on 8, bf16, d 128, 8192 tokens): causal 373 us,
+// 1473 TFLOP/s of visible pairs, 0.74 of the peak; window 1024 and 4 sinks 127 us, 1015 TFLOP/s, 9 and a quarter
+// blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16 heads on 2, d 64: 101 us, 790 TFLOP/s.
+//
 // A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
 // reach the row through the product.  So a row with a non-finite result is computed once more by
 // its warp from the keys that it sees alone (window_row).

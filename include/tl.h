@@ -2,7 +2,8 @@
  * tl.h - C ABI of the GB300 (sm_103a) tile-centric communication-overlapped GEMM library.
  *
  * The library computes, on ONE GPU, the four overlapped operators of the pages it is
- * built from, with the W tensor-parallel ranks emulated as W separate HBM buffers:
+ * built from, with the W tensor-parallel ranks emulated as W separate HBM buffers (and, further down,
+ * the operators of a decoder's serving step: cache append, paged and window attention, MoE for few tokens):
  *
  *   tl_ag_gemm      AllGather + GEMM:        C = [A_0; A_1; ...; A_{W-1}] . B
  *   tl_gemm_rs      GEMM + ReduceScatter:    out_o = rows_o( sum_p A_p . B_p )
@@ -513,8 +514,9 @@ int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token
  * few tokens of a decoding step, where reading the chosen experts' weights is all that takes time:
  *   y_(t,j) = (SiLU(x_t . Wg_e) * (x_t . Wu_e)) . Wd_e,   out_t = sum_j gate_(t,j) * y_(t,j)
  * Unlike there, h keeps fp32 precision between the two products, the sums over j are taken in fp32
- * in the order j = 0, 1, ... and each distinct expert's weights are read once; results are
- * bit-identical run to run.
+ * in the order j = 0, 1, ... and each distinct expert's weights are read from HBM once (an expert with more
+ * than 16 of the tokens, more than 8 if T <= 8, reads them again, mostly from L2); results are bit-identical
+ * run to run.
  * x: bf16 [T x H]; logits: fp32 [T x E]; w_gate, w_up: bf16 [E x H x F]; w_down: bf16 [E x F x H];
  * out: fp32 [T x H].  experts_out (int32 [T x topk]) and gates_out (fp32 [T x topk]) are optional: the
  * chosen experts, best first, and their gates.  NaN logits count as the lowest (the gates are NaN).
