@@ -12,23 +12,28 @@
 // the first window's start to its last query.  Blocks start anywhere (a TMA row coordinate has no alignment), so a window of 1024 takes 9.
 //
 //   warp 0    TMA: Q of both tiles, K and V blocks through a ring
-//   warp 1    TMEM and the MMAs (one thread), tcgen05.mma M = 128:
+//   warps 1, 2  the MMAs of tile 0 and 1, tcgen05.mma M = 128, issued by one thread each:
 //               S_t = Q_t K^T        N = 128 keys, K = head dim, both K-major from shared memory
 //               O_t += P_t V         N = head dim, K = 128 keys, P_t from TMEM, V MN-major
 //   warps 4-7, 8-11   softmax of tile 0 and 1, one row per thread
 // TMEM: S_0, S_1 (128 columns each; P_t as 16-bit pairs takes the first 64 of S_t once they are
-// read), O_0, O_1.  MMAs are issued as S_0 S_1 | PV_0 S_0' PV_1 S_1' | ..: while one tile is in its
+// read), O_0, O_1.  The two warps issue in turn, S_0 S_1 | PV_0 S_0' | PV_1 S_1' | ..: while one tile is in its
 // softmax the tensor cores work for the other.  MMAs of a thread complete in order, so S_t' needs
 // no wait for PV_t before it, and "S_t' is there" also says that PV_t is complete: the softmax
 // rescales O_t then, and only when a row's maximum grew by more than 2^8 (until then weights
 // stay below 2^8 and the stale maximum cancels in O / l).
+// (The tensor cores take an MMA in 66 cycles, 35 at N = 64, but an issuing warp whose descriptors are not uniform
+// values needs 45 for it, and several times that while the softmax's long unrolled code has the instruction
+// caches: one warp for both tiles was busy throughout, 3300 cycles a block.  Hence two warps, uniform bases plus
+// constants, predicates in place of branches: causal 8192 tokens 374 -> 333 us.  Without the turns both tiles fall
+// into step, softmax with softmax and MMAs with MMAs: 421 us.)
 // P is rounded to the 16-bit type of V (half a step each); l sums it unrounded in fp32.
 //
-// Bound: the tensor pipe and the softmax in turn.  Of a block of 128 keys a tile's S takes 8 MMAs of 70 cycles
-// (4 at d 64), its softmax 1190, PV 8 MMAs of 108 (A comes from TMEM, which costs the same at any N): the two
-// tiles' MMAs are 2850 cycles (2290 at d 64) of the about 3300 (3000) that a block takes.  Measured (32 heads on 8, bf16, d 128, 8192 tokens): causal 373 us,
-// 1473 TFLOP/s of visible pairs, 0.74 of the peak; window 1024 and 4 sinks 127 us, 1015 TFLOP/s, 9 and a quarter
-// blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16 heads on 2, d 64: 101 us, 790 TFLOP/s.
+// Bound: for a block of 128 keys of both tiles the MMAs take 2100 cycles (1100 at d 64), one tile's chain of
+// softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2900.  Measured (32 heads on 8,
+// bf16, d 128, 8192 tokens): causal 333 us, 1650 TFLOP/s of visible pairs, 0.83 of the peak; window 1024 and 4
+// sinks 119 us, 1088 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
+// heads on 2, d 64: 95 us, 836 TFLOP/s.
 //
 // A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
 // reach the row through the product.  So a row with a non-finite result is computed once more by
@@ -43,14 +48,14 @@ namespace tl {
 namespace win {
 constexpr int kKeys = 128, kNarrow = 32, kMaxBatch = 1024;
 constexpr int kLevels = 256, kSorted = 32, kHeld = 32;  // order of items: see WinPlan
-constexpr int kThreads = 384;          // warps 0-3 (two of them idle), softmax warpgroups 4-7 and 8-11
+constexpr int kThreads = 384;          // warps 0-3 (one of them idle), softmax warpgroups 4-7 and 8-11
 constexpr float kRescale = 8.f;
 template <int D>
 struct Shape {
   static constexpr int kHalves = D / 64;             // 64-column SW128 boxes of a row
   static constexpr int kBox = 128 * 128;             // 128 rows of 64 columns
   static constexpr int kTileBytes = kHalves * kBox;  // Q of a tile, a K block, a V block
-  static constexpr int kSlots = D == 128 ? 4 : 8;    // K and V blocks in flight (128 KB)
+  static constexpr int kSlots = 4;                   // K and V blocks in flight, two of each
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
   static constexpr int kCumOff = kBarOff + 256;
@@ -237,16 +242,43 @@ __device__ __forceinline__ int win_index(int k) {
   return k * grid + (k & 1 ? grid - 1 - cta : cta);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16, one CTA.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// MMAs (kind::f16, one CTA) and commits by the thread of a converged warp that has `lead`: a predicate on each
+// instruction, no branch, so that what they take is computed once a warp.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+// A value that is the same in the whole warp, in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
 
+// umma_desc_sw128 without its address.
+__host__ __device__ constexpr uint64_t umma_desc_base(uint32_t lbo) {
+  return static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
 // True in one thread of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -304,7 +336,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   uint64_t* sfull = empty + S::kSlots;     // [2] S_t is there, every MMA before it complete
   uint64_t* pready = sfull + 2;            // [2][2] the first, the second 64 keys of P_t are there (and O_t rescaled)
   uint64_t* ofull = pready + 4;            // [2] the item's last PV_t is complete
-  uint64_t* drain = ofull + 2;
+  uint64_t* turn = ofull + 2;              // [2] tile t's MMAs may be issued
+  uint64_t* drain = turn + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   WinPlan plan;
   plan.cum = reinterpret_cast<int*>(base + S::kCumOff);
@@ -325,18 +358,19 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   }
   if (threadIdx.x == 0) {
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
+    mbar_init(qempty, 2);
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
       mbar_init(&pready[2 * t], 4);
       mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&ofull[t], 1);
+      mbar_init(&turn[t], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     fence_mbar_init();
     tma_prefetch_map(&p.tq);
     tma_prefetch_map(&p.tk);
@@ -394,9 +428,9 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   auto item = [&](int k) { return k < kHeld ? held[k] : win_item(p, plan, win_index(k), lane); };
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
-  // Registers: 128 x 88 + 256 x 208 = 384 x 168, what the CTA has at launch.
+  // Registers: 128 x 104 + 256 x 200 = 384 x 168, what the CTA has at launch.
   if (warp < 4) {
-    regs_down<88>();
+    regs_down<104>();
   if (warp == 0) {
     // ------------------------------------------------------------ loads (lane 0; the whole warp finds the items)
     bool ok = true;
@@ -435,84 +469,108 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       for (int j = u > S::kSlots ? u - S::kSlots : 0; j < u; ++j) mbar_wait(&full[j % S::kSlots], (j / S::kSlots) & 1, c, kSiteDrain);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     // ------------------------------------------------------------ MMAs
-    // The whole warp walks along and one elected thread issues each group of MMAs.
+    // A warp for each tile.  It walks along as a whole and one thread of it issues; the tiles' MMAs are issued in
+    // turn, S_0 S_1 | PV_0 S_0' | PV_1 S_1' | ..  Descriptors are a uniform base and constants: slots 0 and 2 hold K
+    // blocks, 1 and 3 V blocks.
     {
-      const uint32_t q0 = smem_u32(base), ring = q0 + S::kRingOff;
+      const uint32_t lead = elect_one() ? 1u : 0u, t = uniform(warp - 1), tm = uniform(tmem) + 128 * t;
+      const uint32_t s0 = uniform((smem_u32(base) & 0x3FFFFu) >> 4), q0 = s0 + t * (S::kTileBytes >> 4);
+      const int n_items = uniform(items);
       bool ok = true;
-      int u = 0, nq = 0, np[2] = {0, 0};  // blocks read, items, P blocks consumed
+      int nq = 0, np = 0, nt = 0, g = 0;  // items, P blocks consumed, turns, blocks gone by
       auto wait = [&](uint64_t* bar, int n, unsigned site) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, c, site)) != 0; };
-      auto wait_block = [&](int j) { return wait(&full[j % S::kSlots], j / S::kSlots, kSiteFull); };
-      // S_t = Q_t K^T; then, for the last tile, the slot (and with the item's last block, Q) is free
-      auto mma_s = [&](int t, int slot, uint32_t desc, bool last_tile, bool last_block) {
-        const uint64_t a0 = umma_desc_sw128(q0 + t * S::kTileBytes, 16, 1024);
-        const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, 16, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * S::kBox + (k & 3) * 32) >> 4;
-            umma_bf16(tmem + kColS + 128 * t, a0 + off, b0 + off, desc, k ? 1u : 0u);
-          }
-          umma_commit(&sfull[t]);
-          if (last_tile) {
-            umma_commit(&empty[slot]);
-            if (last_block) umma_commit(qempty);
-          }
-        }
-        __syncwarp();
+      constexpr uint64_t kDescK = umma_desc_base(16), kDescMn = umma_desc_base(S::kBox);
+      auto my_turn = [&](bool two) { return !two || (t == 0 && nt == 0) || wait(&turn[t], t ? nt : nt - 1, kSiteFull); };
+      auto next_turn = [&](bool two) {
+        if (!two) return;
+        ++nt;
+        if (lane == 0) mbar_arrive(&turn[1 - t]);
       };
-      // O_t += P_t V over 64 keys (kNarrow and none of a narrow block); after the second half the slot is free (last tile), O_t complete (last block)
-      auto mma_o = [&](int t, int slot, int half, int steps, bool acc, bool last_tile, bool last_block) {
-        const uint64_t b0 = umma_desc_sw128(ring + slot * S::kTileBytes, S::kBox, 1024);
-        if (elect_one()) {
+      // S_t = Q_t K^T; then this tile needs the slot (and after the item's last block, Q) no more
+      auto mma_s = [&](auto slot, uint32_t desc, bool last_block) {
+        constexpr int kAt = S::kRingOff + decltype(slot)::value * S::kTileBytes;
 #pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k) {
-            const int kk = half * (kKeys / 32) + k;
-            if (kk >= steps) break;
-            umma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + kk * 8, b0 + ((kk * 2048) >> 4), kDescO, (acc || kk) ? 1u : 0u);
-          }
-          if (half && last_tile) umma_commit(&empty[slot]);
-          if (half && last_block) umma_commit(&ofull[t]);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * S::kBox + (k & 3) * 32;
+          mma_ss(lead, tm + kColS, kDescK | (q0 + (off >> 4)), kDescK | (s0 + ((kAt + off) >> 4)), desc, k ? 1u : 0u);
         }
-        __syncwarp();
+        mma_commit(lead, &sfull[t]);
+        mma_commit(lead, &empty[decltype(slot)::value]);
+        if (last_block) mma_commit(lead, qempty);
       };
-      for (int it = 0; ok && win_index(it) < items; ++it) {
+      // O_t += P_t V over 64 keys (kNarrow and none of a narrow block)
+      auto mma_o = [&](auto slot, auto hf, bool narrow, uint32_t onto) {
+        constexpr int kFirst = decltype(hf)::value * (kKeys / 32), kAt = S::kRingOff + decltype(slot)::value * S::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kKeys / 32; ++k) {
+          if (narrow && kFirst + k >= kNarrow / 16) break;
+          mma_ts(lead, tm + kColO, tm + kColS + (kFirst + k) * 8, kDescMn | (s0 + ((kAt + (kFirst + k) * 2048) >> 4)), kDescO,
+                 kFirst + k ? 1u : onto);
+        }
+      };
+      // V of block g is in slot 2 kPar + 1, K of the next in the other K slot
+      auto block = [&](auto par, bool two, bool narrow, uint32_t onto, bool more, bool last_k) {
+        constexpr int kPar = decltype(par)::value;
+        using Next = std::integral_constant<int, 2 * (1 - kPar)>;
+        using V = std::integral_constant<int, 2 * kPar + 1>;
+        if (!wait(&full[V::value], g >> 1, kSiteFull) || !wait(&pready[2 * t], np, kSiteTmemFull) || !my_turn(two)) return false;
+        tc_fence_after();
+        mma_o(V(), std::integral_constant<int, 0>(), narrow, onto);
+        if (!wait(&pready[2 * t + 1], np, kSiteTmemFull)) return false;
+        tc_fence_after();
+        mma_o(V(), std::integral_constant<int, 1>(), narrow, 1u);
+        mma_commit(lead, &empty[V::value]);
+        if (!more) mma_commit(lead, &ofull[t]);
+        ++np;
+        ++g;
+        if (more) {
+          if (!wait(&full[Next::value], g >> 1, kSiteFull)) return false;
+          mma_s(Next(), kDescS, last_k);
+        }
+        next_turn(two);
+        return true;
+      };
+      for (int it = 0; ok && win_index(it) < n_items; ++it) {
         const WinItem w = item(it);
-        if (w.nb == 0) continue;
-        const int nt = w.two ? 2 : 1;
-        ok = wait(qfull, nq, kSiteFull) && wait_block(u);
+        const int nb = uniform(w.nb);
+        const bool two = uniform(w.two) != 0, narrow = uniform(w.narrow) != 0;
+        if (nb == 0) continue;
+        ok = wait(qfull, nq, kSiteFull);
         if (!ok) break;
         ++nq;
-        tc_fence_after();
-        for (int t = 0; t < nt; ++t) mma_s(t, u % S::kSlots, w.narrow ? kDescNarrow : kDescS, t == nt - 1, w.nb == 1);
-        for (int j = 0; j < w.nb && ok; ++j) {
-          // slots u: K of block j (read), u + 1: V of block j, u + 2: K of block j + 1
-          const bool more = j + 1 < w.nb;
-          ok = wait_block(u + 1) && (!more || wait_block(u + 2));
-          for (int t = 0; t < nt && ok; ++t) {
-            const bool last = t == nt - 1;
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = wait(&pready[2 * t + half], np[t], kSiteTmemFull);
-              if (!ok) break;
-              tc_fence_after();
-              mma_o(t, (u + 1) % S::kSlots, half, w.narrow && j == 0 ? kNarrow / 16 : kKeys / 16, j > 0, last, !more);
+        if (t && !two) {  // nothing to do, but the loads go by
+          for (int j = 0; j < nb && ok; ++j, ++g)
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              const int slot = 2 * (g & 1) + kv;
+              ok = wait(&full[slot], g >> 1, kSiteFull);
+              if (ok && lane == 0) mbar_arrive(&empty[slot]);
             }
-            if (!ok) break;
-            ++np[t];
-            if (more) mma_s(t, (u + 2) % S::kSlots, kDescS, last, j + 2 == w.nb);
-          }
-          u += 2;
+          if (lane == 0) mbar_arrive(qempty);
+          continue;
+        }
+        ok = wait(&full[2 * (g & 1)], g >> 1, kSiteFull) && my_turn(two);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t desc = narrow ? kDescNarrow : kDescS;
+        if (g & 1) mma_s(std::integral_constant<int, 2>(), desc, nb == 1);
+        else mma_s(std::integral_constant<int, 0>(), desc, nb == 1);
+        next_turn(two);
+        for (int j = 0; j < nb && ok; ++j) {
+          const bool more = j + 1 < nb, nar = narrow && j == 0, last_k = j + 2 == nb;
+          ok = g & 1 ? block(std::integral_constant<int, 1>(), two, nar, j > 0, more, last_k)
+                     : block(std::integral_constant<int, 0>(), two, nar, j > 0, more, last_k);
         }
       }
-      if (elect_one()) umma_commit(drain);
+      mma_commit(lead, drain);
       mbar_wait(drain, 0, c, kSiteDrain);
     }
     __syncwarp();
   }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_up<208>();
+    regs_up<200>();
     const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * t + lanes, to = tmem + kColO + 128 * t + lanes;
