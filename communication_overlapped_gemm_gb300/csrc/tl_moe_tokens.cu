@@ -4,7 +4,7 @@
 // With a handful of tokens at each expert the weights are read once and meet one or two tokens, so
 // HBM bounds the layer: 6 H F bytes for each distinct expert, 6 H F flops for each assignment.
 // Measured (H 2048, F 1408, 64 experts, top 2): 64 tokens 157 us, 6.1 TB/s, 0.91 of the copy rate; 8 tokens 52;
-// one token, two experts, 20.5 us against 5.1 for its bytes: routing, first loads, the tiles' joins and the
+// one token, two experts, 18.3 us against 5.1 for its bytes: routing, first loads, the tiles' joins and the
 // combine are waited for in turn.
 //
 // Each CTA (one per SM, a cooperative launch) works out the routing by itself, so nothing has to
@@ -30,7 +30,7 @@
 //
 // Tiles whose units lie in several CTAs: each CTA stores its fp32 sums, and the one that finishes
 // last (a counter) adds them in the order of the line.  The last of a token's topk rows to be finished
-// in a block of 128 columns adds them up, in the order j = 0, 1, ...  So the order of every sum is
+// in a block of 256 columns adds them up, in the order j = 0, 1, ...  So the order of every sum is
 // fixed by the routing.  Every counter is left at zero.
 #include <type_traits>
 
@@ -89,6 +89,7 @@ struct MoeTables {
   uint16_t start[moet::kMaxE + 1];  // rows of expert e: [start[e], start[e + 1])
   uint16_t item_expert[moet::kMaxA];
   uint16_t item_row[moet::kMaxA];   // first row
+  uint16_t first_item[moet::kMaxE];  // of an expert
   int items;
   uint32_t last;
 };
@@ -200,6 +201,40 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
   else
     route_all<8>(p, warp, lane, tb);
   __syncthreads();
+  // Up to 8 tokens (kernels of that group): by one warp, a lane per assignment, an item per expert (one token 19.2
+  // -> 18.7 us; also compiled into the other kernels it cost them 0.5).
+  if (group == 8 && n <= 32) {
+    if (warp == 0) {
+      const uint32_t key = lane < n ? tb.expert[lane] * 32u + lane : 0xffffffffu;
+      int row = 0, before = 0;  // assignments, and those of other experts, that come first
+      for (int i = 0; i < n; ++i) {
+        const uint32_t other = __shfl_sync(0xffffffffu, key, i);
+        row += other < key;
+        before += other >> 5 < key >> 5;
+      }
+      const uint32_t same = __match_any_sync(0xffffffffu, key >> 5);
+      const bool lead = lane < n && row == before;
+      int item = 0;
+      for (uint32_t leads = __ballot_sync(0xffffffffu, lead); leads; leads &= leads - 1)
+        item += __shfl_sync(0xffffffffu, key, __ffs(leads) - 1) >> 5 < key >> 5;
+      if (lane < n) {
+        const uint32_t e = key >> 5;
+        tb.at[lane] = static_cast<uint16_t>(row);
+        tb.order[row] = static_cast<uint16_t>(lane);
+        if (lead) {
+          tb.start[e] = static_cast<uint16_t>(row);
+          tb.start[e + 1] = static_cast<uint16_t>(row + __popc(same));
+          tb.first_item[e] = static_cast<uint16_t>(item);
+          tb.item_expert[item] = static_cast<uint16_t>(e);
+          tb.item_row[item] = static_cast<uint16_t>(row);
+        }
+      }
+      const int items = __popc(__ballot_sync(0xffffffffu, lead));
+      if (lane == 0) tb.items = items;
+    }
+    __syncthreads();
+    return;
+  }
   for (int c = warp; c < chunks; c += kThreads / 32) {
     const int a = 32 * c + lane;
     const uint32_t same = __match_any_sync(0xffffffffu, a < n ? static_cast<uint32_t>(tb.expert[a]) : 0x100u + lane);
@@ -234,6 +269,7 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
         }
       }
       if (e0 + lane < p.E) tb.start[e0 + lane + 1] = static_cast<uint16_t>(rows + sr);
+      if (e0 + lane < p.E) tb.first_item[e0 + lane] = static_cast<uint16_t>(items + si - k);
       for (int i = 0; i < k; ++i) {
         tb.item_expert[items + si - k + i] = static_cast<uint16_t>(e0 + lane);
         tb.item_row[items + si - k + i] = static_cast<uint16_t>(rows + sr - c + i * group);
@@ -256,10 +292,10 @@ __device__ __forceinline__ void moet_tables(const MoeTokParams& p, MoeTables& tb
 }
 
 // Adds to a counter, releasing what this thread has seen and acquiring what others released; the sum.
-__device__ __forceinline__ unsigned count_up(unsigned* ctr) {
+__device__ __forceinline__ unsigned count_up(unsigned* ctr, unsigned by = 1u) {
   unsigned old;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
-  return old + 1u;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(ctr), "r"(by) : "memory");
+  return old + by;
 }
 
 __device__ __forceinline__ void count_up_async(unsigned* ctr) {
@@ -397,6 +433,78 @@ __device__ __forceinline__ bool moet_load_x(const MoeTokParams& p, const MoeTabl
   return true;
 }
 
+__device__ __forceinline__ void put_routing(const MoeTokParams& p, const MoeTables& tb, int tok, int col, int lane) {
+  if (col == 0 && lane < p.topk) {
+    if (p.experts_out) p.experts_out[tok * p.topk + lane] = tb.expert[tok * p.topk + lane];
+    if (p.gates_out) p.gates_out[tok * p.topk + lane] = tb.gate[tok * p.topk + lane];
+  }
+}
+
+// By a warp: 64 of a token's 256 columns of a block, the gates times all pieces of its topk rows (whole tiles in
+// y, those of cut ones by CTA), in the order j, then that of the line.
+template <int Slot, int Group>
+__device__ __forceinline__ void add_pieces(const MoeTokParams& p, const MoeTables& tb, const MoeLine<true>& ln,
+                                           const float* parts, int tok, int col, int wq, int lane) {
+  using namespace moet;
+  constexpr int kBatch = 16;
+  const int c = col * ln.kCols + wq * 64 + lane * 2;
+  // lane j: the CTAs with pieces of the token's j-th row, and how many pieces are before theirs
+  uint32_t c0 = 0, pieces = 0, row = 0, in = 0;
+  float gate = 0.f;
+  if (lane < p.topk) {
+    const int a = tok * p.topk + lane, e = tb.expert[a];
+    row = tb.at[a];
+    in = (row - tb.start[e]) % Group;
+    const uint32_t unit = ((tb.first_item[e] + (row - tb.start[e]) / Group) * ln.nc + col) * ln.nk;
+    c0 = unit / ln.per;
+    pieces = (unit + ln.nk - 1) / ln.per - c0 + 1;
+    gate = tb.gate[a];
+  }
+  uint32_t before = pieces;
+#pragma unroll
+  for (int x = 1; x < kMaxTopk; x <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) before += v;
+  }
+  const uint32_t all = __shfl_sync(0xffffffffu, before, kMaxTopk - 1);
+  before -= pieces;
+  float2 sum = make_float2(0.f, 0.f);
+  for (uint32_t q0 = 0; q0 < all; q0 += 32) {
+    // lane q: where piece q0 + q lies, and its gate
+    int j = 0;
+#pragma unroll
+    for (int x = 1; x < kMaxTopk; ++x) {
+      const uint32_t start = __shfl_sync(0xffffffffu, before, x);
+      if (x < p.topk && q0 + lane >= start) j = x;
+    }
+    const uint32_t k = q0 + lane - __shfl_sync(0xffffffffu, before, j), cta = __shfl_sync(0xffffffffu, c0, j) + k;
+    const bool cut = __shfl_sync(0xffffffffu, pieces, j) > 1;
+    const uint32_t r = __shfl_sync(0xffffffffu, in, j), y_row = __shfl_sync(0xffffffffu, row, j);
+    const float f = __shfl_sync(0xffffffffu, gate, j);
+    const float* at = cut ? parts + (static_cast<size_t>(cta) * 2 + (k == 0 ? 1 : 0)) * Slot + r * ln.kCols
+                          : p.y + static_cast<size_t>(y_row) * p.H + col * ln.kCols;
+    const int here = all - q0 < 32 ? all - q0 : 32;
+    for (int q = 0; q < here; q += kBatch) {
+      float2 v[kBatch];
+      float fs[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const auto from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), q + x));
+        fs[x] = __shfl_sync(0xffffffffu, f, q + x);
+        v[x] = q + x < here && c < ln.N ? __ldcg(reinterpret_cast<const float2*>(from + wq * 64 + lane * 2)) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (q + x >= here) break;
+        sum.x = fmaf(fs[x], v[x].x, sum.x);
+        sum.y = fmaf(fs[x], v[x].y, sum.y);
+      }
+    }
+  }
+  if (c < ln.N) *reinterpret_cast<float2*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+  if (wq == 0) put_routing(p, tb, tok, col, lane);
+}
+
 // The products of a line, by the two groups; u0: units of the line before it.
 template <bool Down, int NT>
 __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& tb, uint8_t* ring, uint64_t* full,
@@ -405,6 +513,10 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
   using R = Ring<NT>;
   constexpr int kStages = R::kStages;
   constexpr int kParts = Down ? 3 : 1;  // 16-bit terms of the left operand
+  constexpr int kSlot = kGroup * 16 * NT;  // sums of a tile
+  // Up to 8 tokens: the pieces of the second product's cut tiles are added up with the tokens' rows at once, not
+  // tile by tile before, one hand-over less (one token 20.4 -> 19.2 us, 4 tokens 36.5 -> 34.8; 64 tokens 158 -> 162).
+  constexpr bool kPieces = Down && NT == 1;
   const MoeLine<Down> ln(p, tb.items);
   const int nk = ln.nk, N = ln.N, n = ln.n;
   const uint32_t per = ln.per, first = ln.first;
@@ -513,14 +625,15 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           acc[m][b][2] += v.z;
           acc[m][b][3] += v.w;
         }
-    if (seg_first != tile * nk || first + end != (tile + 1) * nk) {
-      // (each product has parts and counters of its own: a CTA is in the second one while its
-      // neighbour still works on their common tile of the first)
+    const bool whole = seg_first == tile * nk && first + end == (tile + 1) * nk;
+    // (each product has parts and counters of its own: a CTA is in the second one while its
+    // neighbour still works on their common tile of the first)
+    float* parts = p.part + (Down ? static_cast<size_t>(kMaxCtas) * 2 * kSlot : 0);
+    float* mine = parts + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot;  // slot 1 starts a tile
+    if (!kPieces && !whole) {
       const uint32_t c0 = tile * nk / per, c1 = (tile * nk + nk - 1) / per;
-      constexpr int kSlot = kGroup * 16 * NT;
-      float* parts = p.part + (Down ? static_cast<size_t>(kMaxCtas) * 2 * kSlot : 0);
       unsigned* ctr = p.cut_ctr + (Down ? kMaxCtas : 0) + c0;
-      float* part = parts + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first == tile * nk ? 1 : 0)) * kSlot + tid * 4;
+      float* part = mine + tid * 4;
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -541,7 +654,7 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
           for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.f;
-          const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + b * kGroup * 4 + tid * 4;  // slot 1 starts a tile
+          const float* from = parts + (static_cast<size_t>(c0) * 2 + 1) * kSlot + b * kGroup * 4 + tid * 4;
           for (uint32_t c = c0; c <= c1;) {
             constexpr int kBatch = NT == 1 ? 8 : 4;
             float4 v[kBatch][4];
@@ -589,8 +702,9 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
         } else {
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const int c = this_col * ln.kCols + wq * 64 + m * 16 + g + 8 * (j >> 1);
-            if (c < N) p.y[static_cast<size_t>(row0 + r) * p.H + c] = acc[m][b][j];
+            const int c = wq * 64 + m * 16 + g + 8 * (j >> 1), at = this_col * ln.kCols + c;
+            if (kPieces && !whole) mine[r * ln.kCols + c] = acc[m][b][j];
+            else if (at < N) p.y[static_cast<size_t>(row0 + r) * p.H + at] = acc[m][b][j];
           }
         }
       }
@@ -598,43 +712,46 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
     if constexpr (!Down) {
       if (tid == 0) count_up_async(p.item_ctr + this_item);
     } else {
-      // A token's topk rows of this block: the last one to be finished adds them up.  The item's last
-      // tile sets the item's counter back: nothing waits on it any more.
+      // A token's topk rows of this block: who finishes the last of them (kPieces: the last unit) adds them up.
+      // The item's last sets the item's counter back: nothing waits on it any more.
+      const unsigned units = kPieces ? static_cast<unsigned>(first + end - seg_first) : 1u, tile_units = kPieces ? nk : 1;
       if (wq == 0) {
         bool done = false;
         if (lane < rows) {
           unsigned* ctr = p.tok_ctr + (tb.order[row0 + lane] / p.topk) * ln.nc + this_col;
-          done = count_up(ctr) == static_cast<unsigned>(p.topk);
+          done = count_up(ctr, units) == static_cast<unsigned>(p.topk) * tile_units;
           if (done) *ctr = 0u;
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, done);
         if (lane == 0) tb.last = mask;
       } else if (tid == kGroup - 1) {
         const int nc1 = (p.F + MoeLine<false>::kCols - 1) / MoeLine<false>::kCols;
-        if (count_up(p.item_ctr + this_item) == static_cast<unsigned>(nc1 + ln.nc)) p.item_ctr[this_item] = 0u;
+        if (count_up(p.item_ctr + this_item, units) == nc1 + ln.nc * tile_units) p.item_ctr[this_item] = 0u;
       }
       named_bar_sync(3, kGroup);
       uint32_t mask = tb.last;
-      for (int x = 0; mask; ++x, mask &= mask - 1) {  // two tokens at a time, half a block per warp
-        if ((x & 1) != (wq >> 1)) continue;
-        const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * ln.kCols + (wq & 1) * 128 + lane * 4;
-        if (c < N) {
-          float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int j = 0; j < kMaxTopk; ++j)
-            if (j < p.topk)
-              v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[tok * p.topk + j]) * p.H + c));
-#pragma unroll
-          for (int j = 0; j < kMaxTopk; ++j)
-            if (j < p.topk) {
-              const float f = tb.gate[tok * p.topk + j];
-              sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
-            }
-          *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
-        }
-        if (this_col == 0 && (wq & 1) == 0 && lane < p.topk) {
-          if (p.experts_out) p.experts_out[tok * p.topk + lane] = tb.expert[tok * p.topk + lane];
-          if (p.gates_out) p.gates_out[tok * p.topk + lane] = tb.gate[tok * p.topk + lane];
+      if constexpr (kPieces) {
+        for (; mask; mask &= mask - 1)  // a quarter of the block per warp
+          add_pieces<kSlot, 8 * NT>(p, tb, ln, parts, tb.order[row0 + __ffs(mask) - 1] / p.topk, this_col, wq, lane);
+      } else {
+        for (int x = 0; mask; ++x, mask &= mask - 1) {  // two tokens at a time, half a block per warp
+          if ((x & 1) != (wq >> 1)) continue;
+          const int tok = tb.order[row0 + __ffs(mask) - 1] / p.topk, c = this_col * ln.kCols + (wq & 1) * 128 + lane * 4;
+          if (c < N) {
+            float4 v[kMaxTopk], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll
+            for (int j = 0; j < kMaxTopk; ++j)
+              if (j < p.topk)
+                v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(tb.at[tok * p.topk + j]) * p.H + c));
+  #pragma unroll
+            for (int j = 0; j < kMaxTopk; ++j)
+              if (j < p.topk) {
+                const float f = tb.gate[tok * p.topk + j];
+                sum = make_float4(sum.x + f * v[j].x, sum.y + f * v[j].y, sum.z + f * v[j].z, sum.w + f * v[j].w);
+              }
+            *reinterpret_cast<float4*>(p.out + static_cast<size_t>(tok) * p.H + c) = sum;
+          }
+          if ((wq & 1) == 0) put_routing(p, tb, tok, this_col, lane);
         }
       }
     }

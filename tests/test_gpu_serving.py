@@ -454,6 +454,20 @@ def test_moe_tokens(tl, ctx, T, H, E, F, topk):
     check_moe(*case, topk, *got)
 
 
+@pytest.mark.parametrize("T,topk,H,F,E", [(1, 8, 256, 4096, 9), (1, 1, 8, 8192, 1), (4, 8, 264, 1000, 100), (5, 7, 520, 2000, 256),
+                                          (8, 4, 256, 512, 4), (8, 6, 1032, 1000, 12)])
+def test_moe_tokens_cut_into_many_pieces(tl, ctx, T, topk, H, F, E):
+    """Few columns of long sums: a token's rows come in more pieces than a warp has lanes; up to and over 32
+    assignments; one expert for all tokens."""
+    case = moe_case(T, H, E, F, seed=100 + T)
+    w = ws(tl.tl_moe_tokens_workspace_bytes(T, H, E, F, topk))
+    first = run_moe(tl, ctx, *case, topk, w)
+    check_moe(*case, topk, *first)
+    assert all(torch.equal(a, b) for a, b in zip(first, run_moe(tl, ctx, *case, topk, w)))
+    assert ctx.check() == tl.TL_OK
+    assert (w[:139264] == 0).all()  # TL_SERVE_COUNTER_BYTES
+
+
 def test_moe_tokens_all_to_one_expert_and_ties(tl, ctx):
     """Every token at one expert (the longest lists); equal logits go to the lower expert."""
     T, E = 100, 7
