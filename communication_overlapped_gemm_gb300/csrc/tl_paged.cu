@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "tl_serve.cuh"
+#include "tl_softmax.cuh"
 
 namespace tl {
 
@@ -22,10 +23,11 @@ struct FastDiv {
 __device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
 // ---------------------------------------------------------------------------- append
-// Each thread copies 16 bytes of a K and of a V row (8 bytes written for e4m3), two rows at a time so that
-// four loads are in flight.  HBM bounds a prompt's rows (8192 tokens of 8 heads of 128: bf16 12.7 us, 0.79 of
-// the copy rate; into e4m3 15.8 us, where the quotients are as long as the loads), the launch a step's (64
-// tokens: 2.1 us).
+// Each thread copies 16 bytes of a K and of a V row (8 bytes written for e4m3): a row a thread, all threads of an
+// SM resident, the rows' loads beside that of the slot, which only the stores need.  HBM and the ramp of a short
+// launch bound a prompt's rows (8192 tokens of 8 heads of 128: bf16 12.3 us, 0.81 of the copy rate; into e4m3
+// 11.8 us, 0.63; two or four rows a thread 15.3 and 18.6, with the slot first 13.0), the launch a step's (64
+// tokens: 1.8 us).
 struct AppendParams {
   CacheArgs c;
   DevStatus* status;
@@ -37,57 +39,75 @@ struct AppendParams {
   uint32_t rows;  // tokens * kv_heads
 };
 
-// 8 elements of T divided by the scale, as e4m3 (nearest even, saturating; NaN stays NaN).  (A
-// multiplication by the reciprocal with the quotient only near a tie measured no faster.)
+// 8 elements of T divided by the scale, as e4m3 (nearest even, saturating; NaN stays NaN).  The quotient is the
+// IEEE one, from the scale's reciprocal y, which a thread needs once: q += (x - q s) y twice from q = x y.  The first
+// step leaves q within a unit in the last place, and then the second is exact (Markstein 1990: for y the
+// rounded reciprocal and a remainder by a fused multiply-add).  That asks for a positive scale whose reciprocal and
+// remainders do not leave the range (a quotient that small is 0 in e4m3 either way) and finite quotients;
+// anything else is divided.  (With divisions throughout 8192 tokens take 12.8 us instead of 11.8.)
+struct Scale {
+  float s, y;
+  bool plain;
+};
+__device__ __forceinline__ Scale read_scale(const float* scales, int head) {
+  Scale c;
+  c.s = scales ? __ldg(scales + head) : 1.f;
+  c.y = __frcp_rn(c.s);
+  c.plain = c.s >= 0x1p-60f && c.s <= 0x1p60f;
+  return c;
+}
 template <class T>
-__device__ __forceinline__ uint2 quantise8(uint4 x, float scale) {
+__device__ __forceinline__ uint2 quantise8(uint4 x, Scale c) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  const unsigned long long y = f2(c.y, c.y), ms = f2(-c.s, -c.s);
   uint32_t out[4];
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = to_f32x2<T>(in[i]);
-    out[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale)), __NV_SATFINITE, __NV_E4M3);
+    const unsigned long long a = f2(f.x, f.y);
+    unsigned long long q = fmul2(a, y);
+    q = ffma2(ffma2(q, ms, a), y, q);
+    q = ffma2(ffma2(q, ms, a), y, q);
+    float2 d;
+    f2_split(q, d.x, d.y);
+    top = fmax3(top, fabsf(f.x), fabsf(f.y));
+    // (the sum above loses the sign of a zero)
+    out[i] = __nv_cvt_float2_to_fp8x2(make_float2(copysignf(d.x, f.x), copysignf(d.y, f.y)), __NV_SATFINITE, __NV_E4M3);
+  }
+  if (!c.plain || top > 0x1p60f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = to_f32x2<T>(in[i]);
+      out[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f.x, c.s), __fdiv_rn(f.y, c.s)), __NV_SATFINITE, __NV_E4M3);
+    }
   }
   return make_uint2(out[0] | (out[1] << 16), out[2] | (out[3] << 16));
 }
 
 template <class T, bool Fp8, int D>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  constexpr int kVec = D / 8, kRowsCta = 256 / kVec, kBatch = 2;
+__global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
+  constexpr int kVec = D / 8;
   const int vec = threadIdx.x % kVec;
-  for (uint32_t r0 = blockIdx.x * kRowsCta + threadIdx.x / kVec; r0 < p.rows; r0 += gridDim.x * (kRowsCta * kBatch)) {
-    uint4 k[kBatch], v[kBatch];
-    long long at[kBatch];
-    int head[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const uint32_t r = r0 + b * gridDim.x * kRowsCta;
-      at[b] = -1;
-      if (r >= p.rows) continue;
-      const uint32_t t = divide(r, p.by_heads), h = r - t * p.c.kv_heads;
-      const int slot = __ldg(p.slots + t);
-      if (slot < 0) continue;
-      const uint32_t page = divide(static_cast<uint32_t>(slot), p.by_page);
-      if (page >= static_cast<uint32_t>(p.c.num_pages)) {
-        if (h == 0 && vec == 0) report_index(p.status, t);
-        continue;
-      }
-      head[b] = static_cast<int>(h);
-      at[b] = page * p.c.page_stride + (slot - static_cast<int>(page) * p.c.page_size) * p.c.row_stride + h * p.c.head_stride;
-      k[b] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + vec);
-      v[b] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + vec);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (at[b] < 0) continue;
-      if constexpr (Fp8) {
-        reinterpret_cast<uint2*>(p.c.k + at[b])[vec] = quantise8<T>(k[b], p.c.k_scale ? __ldg(p.c.k_scale + head[b]) : 1.f);
-        reinterpret_cast<uint2*>(p.c.v + at[b])[vec] = quantise8<T>(v[b], p.c.v_scale ? __ldg(p.c.v_scale + head[b]) : 1.f);
-      } else {
-        reinterpret_cast<uint4*>(p.c.k + at[b])[vec] = k[b];
-        reinterpret_cast<uint4*>(p.c.v + at[b])[vec] = v[b];
-      }
-    }
+  const uint32_t r = blockIdx.x * (256 / kVec) + threadIdx.x / kVec;
+  if (r >= p.rows) return;
+  const uint32_t t = divide(r, p.by_heads), h = r - t * p.c.kv_heads;
+  const int slot = __ldg(p.slots + t);
+  const uint4 k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + vec);
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + vec);
+  if (slot < 0) return;
+  const uint32_t page = divide(static_cast<uint32_t>(slot), p.by_page);
+  if (page >= static_cast<uint32_t>(p.c.num_pages)) {
+    if (h == 0 && vec == 0) report_index(p.status, t);
+    return;
+  }
+  const long long at = page * p.c.page_stride + (slot - static_cast<int>(page) * p.c.page_size) * p.c.row_stride + h * p.c.head_stride;
+  if constexpr (Fp8) {
+    reinterpret_cast<uint2*>(p.c.k + at)[vec] = quantise8<T>(k, read_scale(p.c.k_scale, h));
+    reinterpret_cast<uint2*>(p.c.v + at)[vec] = quantise8<T>(v, read_scale(p.c.v_scale, h));
+  } else {
+    reinterpret_cast<uint4*>(p.c.k + at)[vec] = k;
+    reinterpret_cast<uint4*>(p.c.v + at)[vec] = v;
   }
 }
 
@@ -814,10 +834,10 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
   p.by_heads = fast_div(cache->kv_heads);
   p.by_page = fast_div(cache->page_size);
   const long long per_cta = 256 / (cache->d / 8);
-  const long long need = (p.rows + per_cta - 1) / per_cta, most = 16LL * ctx->sms;  // two rounds of a full GPU
+  const long long ctas = (p.rows + per_cta - 1) / per_cta;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
     append_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>
-        <<<static_cast<unsigned>(need < most ? need : most), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+        <<<static_cast<unsigned>(ctas), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return launched();
   });
 }

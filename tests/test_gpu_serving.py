@@ -103,6 +103,26 @@ def test_append_e4m3_rounds_every_value_as_the_quotient_does(tl, ctx, dtype):
             assert torch.equal(p[0].cpu().view(torch.uint8), want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_e4m3_of_infinities_zeros_and_scales_at_the_limits(tl, ctx, dtype):
+    """Infinities saturate, NaN stays NaN, zeros keep their sign; scales on both sides of 2^-60 and 2^60, where the
+    quotient is taken in another way, negative ones, zero, infinity and NaN."""
+    big = torch.finfo(DT[dtype]).max
+    rows = torch.cat([torch.tensor([math.inf, -math.inf, math.nan, 0.0, -0.0, big, -big, torch.finfo(DT[dtype]).tiny]),
+                      draws(7, 56).float()]).to(DT[dtype])
+    scale = torch.tensor([2.0 ** -60, 2.0 ** -60 * (1 - 2.0 ** -24), 2.0 ** 60, 2.0 ** 60 * (1 + 2.0 ** -23), -0.37, -2.0 ** -70, 0.0, -0.0,
+                          math.inf, math.nan, 1e-45, 3e38, 0.37, 1.0, 448.0, 2.0 ** -9])
+    dev = rows.expand(1, 16, 64).contiguous().cuda()
+    pool = [torch.zeros((1, 1, 16, 64), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    tl.tl_kv_append(ctx, dev, dev, *pool, torch.zeros(1, dtype=torch.int32, device="cuda"), k_scale=scale.cuda(), v_scale=scale.cuda())
+    quotient = rows.float() / scale[:, None]
+    want = quotient.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for p in pool:
+        got = p[0, 0].cpu()
+        assert torch.equal(torch.isnan(got.float()), torch.isnan(quotient))
+        assert torch.equal(got.view(torch.uint8)[~torch.isnan(quotient)], want[~torch.isnan(quotient)])
+
+
 def test_append_reports_slots_out_of_range_and_leaves_them_out(tl, ctx):
     k = draws(1, 4, 2, 64).bfloat16().cuda()
     guard = torch.zeros((8, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
