@@ -341,34 +341,41 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   };
 
   // ---------------------------------------------------------------- loads
-  // The rows of a step are looked up (page table) one step before they are loaded; lanes l and
-  // l + 16 hold key l's.  A stage's mask has a bit for each key that is there.
+  // The rows of a step are looked up (page table) one step before they are loaded, the first kStages - 1 steps' all at
+  // once; nothing waits for an entry before its loads.  Lanes l and l + 16 hold key l's.  A stage's mask has a
+  // bit for each key that is there.
   PagedAt load_at = at;
   int step_loaded = 0;  // steps issued
-  long long row_off = 0;
-  bool row_ok = false;
-  auto look_up = [&]() {
-    row_ok = false;
-    row_off = 0;
-    if (step_loaded >= nsteps) return;
-    const int i = load_at.tile * (kTile >> p.lw) + kb * kKeys + (lane & 15);
-    if (i < load_at.vis.count) {
-      const int row = i < load_at.vis.head ? i : i + load_at.vis.skip;
+  struct Place {
+    int page;        // as the table has it
+    bool wanted;
+    long long rest;  // from the page's start to the row's
+    int b;
+  };
+  auto look_up = [&](const PagedAt& a, bool more) {
+    Place w;
+    w.page = 0;
+    w.wanted = false;
+    w.rest = 0;
+    w.b = a.b;
+    const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & 15);
+    if (more && i < a.vis.count) {
+      const int row = i < a.vis.head ? i : i + a.vis.skip;
       const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
-      const int page = __ldg(p.table + static_cast<long long>(load_at.b) * p.max_pages + pg);
-      if (page >= 0 && page < p.c.num_pages) {
-        row_ok = true;
-        row_off = page * p.c.page_stride + (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
-                  (((NB == 1 ? load_at.sub : load_at.sub / p.blocks) << p.lw) + hw) * p.c.head_stride;
-      } else {
-        report_index(p.status, static_cast<unsigned long long>(load_at.b));
-      }
+      w.page = __ldg(p.table + static_cast<long long>(a.b) * p.max_pages + pg);
+      w.wanted = true;
+      w.rest = (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
+               (((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw) * p.c.head_stride;
     }
+    return w;
   };
   const uint32_t ring = smem_u32(smem) + warp * (2 * S::kHalf);
   auto stage_addr = [&](int s) { return ring + s * (kWarps * 2 * S::kHalf); };
   uint32_t masks[kStages];  // one per stage, the same in all lanes
-  auto issue = [&](int s, uint32_t& mask) {
+  auto issue = [&](int s, uint32_t& mask, const Place& w) {
+    const bool row_ok = w.wanted && w.page >= 0 && w.page < p.c.num_pages;
+    if (w.wanted && !row_ok) report_index(p.status, static_cast<unsigned long long>(w.b));
+    const long long row_off = row_ok ? w.page * p.c.page_stride + w.rest : 0;
     mask = __ballot_sync(0xffffffffu, row_ok) & 0xffffu;
     if (step_loaded < nsteps) {
       constexpr int kChunks = S::kRowBytes / 16, kPer = 32 / kChunks;  // rows a warp-wide copy covers
@@ -392,20 +399,27 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         cp_async16(sk + ck, p.c.k + off, bytes);
         cp_async16(sv + cv, p.c.v + off, bytes);
       }
-      advance(load_at);
       ++step_loaded;
     }
     cp_async_commit();
-    look_up();
   };
 
   // ---------------------------------------------------------------- the running state of a segment
   // Columns are query heads: thread (g, t) holds those of 8 b + 2t and 8 b + 2t + 1.
   float o[D / 16][NB][4], m[NB][2], l[NB][2], sc[NB][2];
   uint32_t qf[kSteps][NB][2];
-  look_up();
+  Place next;
+  {
+    Place places[kStages - 1];
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s, masks[s]);
+    for (int s = 0; s < kStages - 1; ++s) {
+      places[s] = look_up(load_at, s < nsteps);
+      if (s + 1 < nsteps) advance(load_at);
+    }
+    next = look_up(load_at, kStages - 1 < nsteps);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) issue(s, masks[s], places[s]);
+  }
 
   int step = 0;
   while (step < nsteps) {
@@ -474,7 +488,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       __syncwarp();
       const int s = step % kStages, sn = (step + kStages - 1) % kStages;
       uint32_t mask = 0, fresh;
-      issue(sn, fresh);
+      issue(sn, fresh, next);
+      if (step_loaded < nsteps) advance(load_at);
+      next = look_up(load_at, step_loaded < nsteps);
 #pragma unroll
       for (int x = 0; x < kStages; ++x) {
         if (x == sn) masks[x] = fresh;
