@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
 // run in fp16.  Weights are rounded to the products' 16-bit type (half a step) to meet V there; l sums
 // them unrounded in fp32.
 namespace paged {
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys, kMaxRows = 32;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys;
 template <bool Fp8, int D, int NB>
 struct Shape {
   static constexpr int kRows = 8 * NB;                   // query heads of an item
@@ -262,7 +262,6 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_sum[kThreads], s_warp[kWarps];
-  __shared__ float s_max[kMaxRows];
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int subs = (p.c.kv_heads >> p.lw) * p.blocks;
@@ -697,67 +696,65 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         constexpr int kStride = 2 * S::kPart;
         const float* one = p.part + (static_cast<size_t>(c0) * 2 + 1) * S::kPart;
         const float* rest = p.part + static_cast<size_t>(c0 + 1) * kStride;
-        const int more = c1 - c0;  // parts after the first
-        for (int row = warp; row < all; row += kWarps) {  // a row's maximum over all parts
-          float mm = lane == 0 ? __ldcg(one + S::kPartRows * D + 2 * row) : -INFINITY;
-          const float* src = rest + static_cast<size_t>(lane) * kStride + S::kPartRows * D + 2 * row;
-#pragma unroll 2
-          for (int c = lane; c < more; c += 32, src += 32 * kStride) mm = fmaxf(mm, __ldcg(src));
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-          if (lane == 0) s_max[row] = mm;
-        }
-        __syncthreads();
-        // Few rows leave threads over: `teams` of them share the parts of a row, added up at the end.
+        const int parts = c1 - c0 + 1;
+        // Few rows leave threads over: `teams` of them share the parts of a row, merged at the end.
         const int teams = vecs < kThreads ? kThreads / vecs : 1;
         for (int i0 = 0; i0 < vecs * teams; i0 += kThreads) {
           const int i = i0 + threadIdx.x, team = teams > 1 ? i / vecs : 0, v = i - team * vecs;
           const bool mine = i < vecs * teams;
           const int row = v / (D / 4), d = (v % (D / 4)) * 4;
-          float ll = 0.f;
+          float mm = -INFINITY, ll = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           if (mine) {
-            const float base = s_max[row] == -INFINITY ? 0.f : s_max[row];
-            auto fold = [&](const float2& z, const float4& u) {
-              const float f = ex2_approx(z.x - base);
-              ll += f * z.y;
-              add(acc, f, u);
-            };
-            if (team == 0)
-              fold(__ldcg(reinterpret_cast<const float2*>(one + S::kPartRows * D + 2 * row)),
-                   __ldcg(reinterpret_cast<const float4*>(one + row * D + d)));
-            const float* src = rest + static_cast<size_t>(team) * kStride;
-            const int step_floats = teams * kStride;
-            constexpr int kBatch = 8;  // a round trip to L2, often the other die's, each
-            for (int c = team; c < more; c += kBatch * teams) {
+            constexpr int kBatch = 16;  // a round trip to L2, often the other die's, each
+            for (int c = team; c < parts; c += kBatch * teams) {
               float2 z[kBatch];
               float4 u[kBatch];
 #pragma unroll
-              for (int x = 0; x < kBatch; ++x, src += step_floats) {
+              for (int x = 0; x < kBatch; ++x) {
+                const int k = c + x * teams;
+                const float* src = k == 0 ? one : rest + static_cast<size_t>(k - 1) * kStride;
                 z[x] = make_float2(-INFINITY, 0.f);
                 u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c + x * teams < more) {
+                if (k < parts) {
                   z[x] = __ldcg(reinterpret_cast<const float2*>(src + S::kPartRows * D + 2 * row));
                   u[x] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
                 }
               }
+              float top = mm;
 #pragma unroll
-              for (int x = 0; x < kBatch; ++x) fold(z[x], u[x]);
+              for (int x = 0; x < kBatch; ++x) top = fmaxf(top, z[x].x);
+              const float base = top == -INFINITY ? 0.f : top, keep = ex2_approx(mm - base);
+              acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+              ll *= keep;
+              mm = top;
+#pragma unroll
+              for (int x = 0; x < kBatch; ++x) {
+                const float f = ex2_approx(z[x].x - base);
+                ll += f * z[x].y;
+                add(acc, f, u[x]);
+              }
             }
           }
           if (teams > 1) {  // one round (vecs * teams <= kThreads); the merged rows are not needed any more
             float* hold = merge + threadIdx.x * 8;
             *reinterpret_cast<float4*>(hold) = acc;
-            hold[4] = ll;
+            *reinterpret_cast<float2*>(hold + 4) = make_float2(mm, ll);
             __syncthreads();
-            if (mine && team == 0)
-              for (int x = 1; x < teams; ++x) {
+            if (mine && team == 0) {
+              for (int x = 1; x < teams; ++x) mm = fmaxf(mm, merge[(threadIdx.x + x * vecs) * 8 + 4]);
+              const float base = mm == -INFINITY ? 0.f : mm;
+              acc = make_float4(0.f, 0.f, 0.f, 0.f);
+              ll = 0.f;
+              for (int x = 0; x < teams; ++x) {
                 const float* other = merge + (threadIdx.x + x * vecs) * 8;
-                add(acc, 1.f, *reinterpret_cast<const float4*>(other));
-                ll += other[4];
+                const float f = ex2_approx(other[4] - base);
+                ll += f * other[5];
+                add(acc, f, *reinterpret_cast<const float4*>(other));
               }
+            }
           }
-          if (mine && team == 0) write_out(row, d, acc, s_max[row], ll);
+          if (mine && team == 0) write_out(row, d, acc, mm, ll);
         }
       }
     }
