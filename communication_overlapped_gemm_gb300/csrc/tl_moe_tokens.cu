@@ -3,8 +3,8 @@
 //   h_a = SiLU(x_t Wg_e) * (x_t Wu_e),   out_t = sum_j gate_tj h_a Wd_e,   a = (t, j), e the expert of a
 // With a handful of tokens at each expert the weights are read once and meet one or two tokens, so
 // HBM bounds the layer: 6 H F bytes for each distinct expert, 6 H F flops for each assignment.
-// Measured (H 2048, F 1408, 64 experts, top 2): 64 tokens 157 us, 6.1 TB/s, 0.91 of the copy rate; 8 tokens 52;
-// one token, two experts, 18.3 us against 5.1 for its bytes: routing, first loads, the tiles' joins and the
+// Measured (H 2048, F 1408, 64 experts, top 2): 64 tokens 158 us, 6.1 TB/s, 0.90 of the copy rate; 8 tokens 52;
+// one token, two experts, 18.5 us against 5.1 for its bytes: routing, first loads, the tiles' joins and the
 // combine are waited for in turn.
 //
 // Each CTA (one per SM, a cooperative launch) works out the routing by itself, so nothing has to

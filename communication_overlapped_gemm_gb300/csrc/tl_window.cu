@@ -32,7 +32,7 @@
 // Bound: for a block of 128 keys of both tiles the MMAs take 2100 cycles (1100 at d 64), one tile's chain of
 // softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2900.  Measured (32 heads on 8,
 // bf16, d 128, 8192 tokens): causal 333 us, 1650 TFLOP/s of visible pairs, 0.83 of the peak; window 1024 and 4
-// sinks 119 us, 1088 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
+// sinks 118 us, 1090 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
 // heads on 2, d 64: 95 us, 836 TFLOP/s.
 //
 // A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
