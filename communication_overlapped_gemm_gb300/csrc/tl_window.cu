@@ -15,6 +15,7 @@
 //   warps 1, 2  the MMAs of tile 0 and 1, tcgen05.mma M = 128, issued by one thread each:
 //               S_t = Q_t K^T        N = 128 keys, K = head dim, both K-major from shared memory
 //               O_t += P_t V         N = head dim, K = 128 keys, P_t from TMEM, V MN-major
+//   warp 3    the list of the CTA's items, if it is long
 //   warps 4-7, 8-11   softmax of tile 0 and 1, one row per thread
 // TMEM: S_0, S_1 (128 columns each; P_t as 16-bit pairs takes the first 64 of S_t once they are
 // read), O_0, O_1.  The two warps issue in turn, S_0 S_1 | PV_0 S_0' | PV_1 S_1' | ..: while one tile is in its
@@ -31,9 +32,9 @@
 //
 // Bound: for a block of 128 keys of both tiles the MMAs take 2100 cycles (1100 at d 64), one tile's chain of
 // softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2900.  Measured (32 heads on 8,
-// bf16, d 128, 8192 tokens): causal 333 us, 1650 TFLOP/s of visible pairs, 0.83 of the peak; window 1024 and 4
-// sinks 118 us, 1090 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
-// heads on 2, d 64: 95 us, 836 TFLOP/s.
+// bf16, d 128, 8192 tokens): causal 324 us, 1697 TFLOP/s of visible pairs, 0.85 of the peak; window 1024 and 4
+// sinks 114 us, 1136 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
+// heads on 2, d 64: 93 us, 855 TFLOP/s.
 //
 // A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
 // reach the row through the product.  So a row with a non-finite result is computed once more by
@@ -47,8 +48,9 @@ namespace tl {
 
 namespace win {
 constexpr int kKeys = 128, kNarrow = 32, kMaxBatch = 1024;
-constexpr int kLevels = 256, kSorted = 32, kHeld = 32;  // order of items: see WinPlan
-constexpr int kThreads = 384;          // warps 0-3 (one of them idle), softmax warpgroups 4-7 and 8-11
+constexpr int kLevels = 256, kSorted = 32;  // order of items: see WinPlan
+constexpr int kHeld = 32, kReaders = 11;    // items listed; warps that walk them
+constexpr int kThreads = 384;          // warps 0-3, softmax warpgroups 4-7 and 8-11
 constexpr float kRescale = 8.f;
 template <int D>
 struct Shape {
@@ -337,7 +339,9 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   uint64_t* pready = sfull + 2;            // [2][2] the first, the second 64 keys of P_t are there (and O_t rescaled)
   uint64_t* ofull = pready + 4;            // [2] the item's last PV_t is complete
   uint64_t* turn = ofull + 2;              // [2] tile t's MMAs may be issued
-  uint64_t* drain = turn + 2;
+  uint64_t* listed = turn + 2;             // [2] a half of the list of items is written anew
+  uint64_t* used = listed + 2;             // [2] all warps have read it
+  uint64_t* drain = used + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
   WinPlan plan;
   plan.cum = reinterpret_cast<int*>(base + S::kCumOff);
@@ -369,6 +373,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       mbar_init(&pready[2 * t + 1], 4);
       mbar_init(&ofull[t], 1);
       mbar_init(&turn[t], 1);
+      mbar_init(&listed[t], 1);
+      mbar_init(&used[t], kReaders);
     }
     mbar_init(drain, 2);
     fence_mbar_init();
@@ -417,7 +423,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   }
   __syncthreads();
   const int items = plan.sorted ? plan.above[0] * p.kv_heads : plan.cum[p.batch];
-  // the CTA's first items, looked up by all warps at once; later ones by each warp as it comes to them
+  // The list of the CTA's items: the first kHeld looked up by all warps at once, later ones by warp 3, half a list at a
+  // time.  (Looked up by each warp as it came to them, the code in every role cost 4%: instruction fetch.)
   WinItem* held = reinterpret_cast<WinItem*>(base + S::kHeldOff);
   static_assert(sizeof(WinItem) <= 64, "room");
   for (int k = warp; k < kHeld && win_index(k) < items; k += kThreads / 32) {
@@ -425,7 +432,17 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     if (lane == 0) held[k] = w;
   }
   __syncthreads();
-  auto item = [&](int k) { return k < kHeld ? held[k] : win_item(p, plan, win_index(k), lane); };
+  auto item = [&](int k, bool& ok) {
+    constexpr int kHalf = kHeld / 2;
+    const int h = k / kHalf & 1;
+    if (k >= kHeld && k % kHalf == 0) ok = __all_sync(0xffffffffu, mbar_wait(&listed[h], (k / kHeld - 1) & 1, c, kSiteFull)) != 0;
+    const WinItem w = held[k % kHeld];
+    if (k % kHalf == kHalf - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&used[h]);
+    }
+    return w;
+  };
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
   // Registers: 128 x 104 + 256 x 200 = 384 x 168, what the CTA has at launch.
@@ -437,8 +454,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     int u = 0, nq = 0;  // blocks and items loaded
     const uint32_t q_bytes = static_cast<uint32_t>(p.tokens * p.group) * 128 * S::kHalves;
     for (int k = 0; ok && win_index(k) < items; ++k) {
-      const WinItem w = item(k);
-      if (w.nb == 0) continue;
+      const WinItem w = item(k, ok);
+      if (w.nb == 0 || !ok) continue;
       if (lane == 0) {
         ok = mbar_wait(qempty, (nq & 1) ^ 1, c, kSiteEmpty);
         if (ok) {
@@ -533,10 +550,10 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         return true;
       };
       for (int it = 0; ok && win_index(it) < n_items; ++it) {
-        const WinItem w = item(it);
+        const WinItem w = item(it, ok);
         const int nb = uniform(w.nb);
         const bool two = uniform(w.two) != 0, narrow = uniform(w.narrow) != 0;
-        if (nb == 0) continue;
+        if (nb == 0 || !ok) continue;
         ok = wait(qfull, nq, kSiteFull);
         if (!ok) break;
         ++nq;
@@ -567,6 +584,21 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       mbar_wait(drain, 0, c, kSiteDrain);
     }
     __syncwarp();
+  } else {
+    // ------------------------------------------------------------ the list of items, from the kHeld-th on
+    constexpr int kHalf = kHeld / 2;
+    bool ok = true;
+    for (int k = kHeld; ok && win_index(k) < items; k += kHalf) {
+      const int h = k / kHalf & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&used[h], (k / kHeld - 1) & 1, c, kSiteEmpty)) != 0;
+      if (!ok) break;
+      for (int x = k; x < k + kHalf && win_index(x) < items; ++x) {
+        const WinItem w = win_item(p, plan, win_index(x), lane);
+        if (lane == 0) held[x % kHeld] = w;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&listed[h]);
+    }
   }
   } else {
     // ------------------------------------------------------------ softmax
@@ -578,8 +610,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     bool ok = true;
     int ns = 0, no = 0;  // S blocks and items seen
     for (int it = 0; ok && win_index(it) < items; ++it) {
-      const WinItem w = item(it);
-      if (t && !w.two) continue;
+      const WinItem w = item(it, ok);
+      if ((t && !w.two) || !ok) continue;
       const int i = w.i0 + t * p.tokens + tok;  // this row's query
       const bool live = tok < p.tokens && i < w.s.n;
       const int pos = live ? w.s.off + i : -1;

@@ -374,6 +374,18 @@ def test_window_attention_windows(tl, ctx, window, sinks, lens_q, lens_k):
     check_window(q, k, v, cum(lens_q), cum(lens_k), out, e, window, sinks)
 
 
+@pytest.mark.parametrize("lens,heads,kv", [([300] + [i * 7 % 6 for i in range(900)], 16, 16), ([250 + i * 37 % 150 for i in range(32)], 128, 8)])
+def test_window_attention_of_more_items_than_a_list_holds(tl, ctx, lens, heads, kv):
+    """More than 32 items for each CTA, so that the list of them is written anew: up to twice each half for many
+    short sequences, once for 32 (which are ordered by length)."""
+    q, k, v = packed(lens, lens, heads, kv, 64, "bf16", seed=len(lens))
+    out, e = run_window(tl, ctx, q, k, v, cum(lens), cum(lens), window=64, sinks=1)
+    assert ctx.check() == tl.TL_OK
+    check_window(q, k, v, cum(lens), cum(lens), out, e, 64, 1)
+    again, _ = run_window(tl, ctx, q, k, v, cum(lens), cum(lens), window=64, sinks=1)
+    assert torch.equal(out, again)
+
+
 def test_window_attention_queries_before_the_first_key_see_nothing(tl, ctx):
     lens_q, lens_k = [9, 200, 3], [4, 100, 0]
     q, k, v = packed(lens_q, lens_k, 4, 1, 64, "bf16", seed=1)
