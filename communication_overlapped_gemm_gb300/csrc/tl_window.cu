@@ -728,6 +728,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       if (!ok) break;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       bool bad = !(l <= 3.0e38f);
+      unsigned long long zero = 0ull;  // 0 times every sum: NaN if one is not finite
       if (w.nb) {
         ok = __all_sync(0xffffffffu, mbar_wait(&ofull[t], no & 1, c, kSiteTmemFull));
         if (!ok) break;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
         uint32_t v[4][4];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          bad |= !(fabsf(o[2 * k]) <= 3.0e38f) || !(fabsf(o[2 * k + 1]) <= 3.0e38f);
+          zero = ffma2(f2(o[2 * k], o[2 * k + 1]), 0ull, zero);
           v[k >> 2][k & 3] = from_f32x2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
         }
 #pragma unroll
@@ -775,6 +776,9 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
           if ((lives >> ((lane & ~3) + x)) & 1u)
             *reinterpret_cast<uint4*>(dst[x] + 64 * q) = make_uint4(v[x][0], v[x][1], v[x][2], v[x][3]);
       }
+      float z0, z1;
+      f2_split(zero, z0, z1);
+      bad |= !(z0 + z1 == 0.f);
       if (live && p.lse)
         p.lse[static_cast<long long>(w.s.q0 + i) * p.heads + w.hk * p.group + hg] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
       tc_fence_before();
