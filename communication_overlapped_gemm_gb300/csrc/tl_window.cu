@@ -31,9 +31,9 @@
 // P is rounded to the 16-bit type of V (half a step each); l sums it unrounded in fp32.
 //
 // Bound: for a block of 128 keys of both tiles the MMAs take 2100 cycles (1100 at d 64), one tile's chain of
-// softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2900.  Measured (32 heads on 8,
-// bf16, d 128, 8192 tokens): causal 324 us, 1697 TFLOP/s of visible pairs, 0.85 of the peak; window 1024 and 4
-// sinks 114 us, 1136 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
+// softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2700.  Measured (32 heads on 8,
+// bf16, d 128, 8192 tokens): causal 317 to 324 us, 1700 TFLOP/s of visible pairs, 0.85 of the peak; window 1024 and 4
+// sinks 113 us, 1141 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
 // heads on 2, d 64: 93 us, 855 TFLOP/s.
 //
 // A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
