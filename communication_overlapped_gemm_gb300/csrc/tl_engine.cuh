@@ -180,8 +180,10 @@ __device__ __forceinline__ void trace_end(const Common& c) {
   }
 }
 
+// A wait ran out: the first one of a context is kept.  It replaces an index report, which says that workspaces are
+// still valid; after this they are not.
 __device__ __forceinline__ void report_timeout(DevStatus* st, unsigned where, unsigned long long info) {
-  if (atomicCAS(&st->code, 0u, kStatusTimeout) == 0u) {
+  if (atomicExch(&st->code, kStatusTimeout) != kStatusTimeout) {
     st->where = where;
     st->info = info;
   }

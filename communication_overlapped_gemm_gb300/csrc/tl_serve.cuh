@@ -16,7 +16,8 @@ constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // An index read on the device was out of range (the entry is left out): the first report of a
-// context is kept, without the abort flag, since nothing waits on it.
+// context is kept, without the abort flag, since nothing waits on it.  It never replaces a timeout, and a
+// timeout replaces it (report_timeout).
 __device__ __forceinline__ void report_index(DevStatus* st, unsigned long long info) {
   if (atomicCAS(&st->code, 0u, kStatusIndex) == 0u) st->info = info;
 }

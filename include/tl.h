@@ -134,7 +134,8 @@ void tl_ctx_destroy(tl_ctx* ctx);
 /* Read and clear the device status word.  Call after synchronising the streams used with ctx.
  * Returns TL_OK, or TL_ERR_TIMEOUT if a bounded wait ran out (the results of that call are
  * undefined and its workspace must be zero-filled again), or TL_ERR_INDEX if a serving operator
- * met an index out of range (it left that entry out; its workspace stays valid), or TL_ERR_CUDA. */
+ * met an index out of range (it left that entry out; its workspace stays valid), or TL_ERR_CUDA.
+ * If both happened since the last check, in whatever order, it is TL_ERR_TIMEOUT. */
 int tl_ctx_check(tl_ctx* ctx);
 
 /* Human-readable text for a status code (static storage). */
