@@ -684,7 +684,9 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(r[3][24 + k]));
         const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.sl2;  // sl2 > 0
-        if (__any_sync(0xffffffffu, top > m + kRescale)) {
+        // (a row without a query has no vote: what it holds, of another sequence or left by an earlier call, would move
+        // the others' maxima and so their last bits)
+        if (__any_sync(0xffffffffu, live && top > m + kRescale)) {
           const float mn = fmaxf(m, top), keep = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
           m = mn;
           l *= keep;

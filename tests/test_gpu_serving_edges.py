@@ -35,3 +35,24 @@ def test_a_timeout_is_reported_beside_an_index_out_of_range(tl, index_first):
         assert c2.check() == tl.TL_OK
         tl.tl_kv_append(c2, row, row, pool, pool, beyond)
         assert c2.check() == tl.TL_ERR_INDEX and c2.check() == tl.TL_OK
+
+
+# ------------------------------------------------------------------------------------------------ window attention
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 12])
+def test_window_attention_does_not_depend_on_what_ran_before(tl, ctx, group, d):
+    """Heads that do not divide a tile's 128 rows leave rows of it unused: what an earlier call left there has no
+    say in the result.  The earlier call's queries are 0, then 1000 along the one dim in which the keys climb."""
+    n = 600
+    q, k, v = (t.clone() for t in packed([n], [n], group, 1, d, "bf16", seed=group))
+    k[:, 0, 0] = (3 * torch.div(torch.arange(n, device="cuda"), 128, rounding_mode="floor")).bfloat16()
+    q[:, :, 0] = 0.5
+    before = torch.zeros((256, 160, d), dtype=torch.bfloat16, device="cuda")   # an item for every CTA, whole tiles
+    other = draws(5, 256, 160, d).bfloat16().cuda()
+    got = []
+    for far in (0.0, 1000.0):
+        before[:, :, 0] = far
+        run_window(tl, ctx, before, other, other, [0, 256], [0, 256])
+        got.append(run_window(tl, ctx, q, k, v, [0, n], [0, n]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    check_window(q, k, v, [0, n], [0, n], *got[0])
