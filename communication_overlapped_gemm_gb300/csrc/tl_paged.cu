@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
 //
 // e4m3 rows are widened to fp16 (exact) in registers; q is brought to fp16 by a power of two per row
 // that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products
-// run in fp16.  Weights are rounded to the products' 16-bit type (half a step) to meet V there; l sums
-// them unrounded in fp32.
+// run in fp16.  Weights are rounded to the products' 16-bit type (half a step; fp16 ones are held times 2^7,
+// kWeightBits, m being 7 less) to meet V there; l sums them unrounded in fp32.
 namespace paged {
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys;
 template <bool Fp8, int D, int NB>
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         for (int j = 0; j < 4; ++j) {
           x[b][j] *= sc[b][j & 1];
           if (mask != 0xffffu && !((mask >> (g + 8 * (j >> 1))) & 1u)) x[b][j] = -INFINITY;
-          moved |= x[b][j] > m[b][j & 1] + 8.f;
+          moved |= x[b][j] > m[b][j & 1] + (8.f + kWeightBits<M>);
         }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float mn = fmaxf(m[b][j], top);
+            const float mn = fmaxf(m[b][j], top - kWeightBits<M>);
             const float keep = mn == -INFINITY ? 0.f : ex2_approx(m[b][j] - mn);
             m[b][j] = mn;
             l[b][j] *= keep;

@@ -45,6 +45,13 @@ __device__ __forceinline__ uint32_t from_f32x2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Softmax weights that meet V as fp16 are held times 2^7: fp16 has a step of 2^-24 below 2^-14 and nothing below
+// 2^-25, and beside one dominant key the rest of a long sequence may lie there.  The maximum that weights refer to is
+// stale by 2^8 at most, so they stay below 2^15.  The kernels keep m - 7 in place of m, so the factor
+// costs nothing: it is in the weights, their sum and O alike.  bf16 has fp32's range and needs none.
+template <class M>
+constexpr float kWeightBits = std::is_same<M, __half>::value ? 7.f : 0.f;
+
 // 16 bytes to shared memory; with bytes 0, zeros, and nothing is read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

@@ -28,7 +28,8 @@
 // caches: one warp for both tiles was busy throughout, 3300 cycles a block.  Hence two warps, uniform bases plus
 // constants, predicates in place of branches: causal 8192 tokens 374 -> 333 us.  Without the turns both tiles fall
 // into step, softmax with softmax and MMAs with MMAs: 421 us.)
-// P is rounded to the 16-bit type of V (half a step each); l sums it unrounded in fp32.
+// P is rounded to the 16-bit type of V (half a step each; fp16 ones are held times 2^7, kWeightBits, m being 7
+// less); l sums it unrounded in fp32.
 //
 // Bound: for a block of 128 keys of both tiles the MMAs take 2100 cycles (1100 at d 64), one tile's chain of
 // softmax (1200 alone, more beside the other's), barriers and its own MMAs about 2700.  Measured (32 heads on 8,
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
             if (k >= z) r[k] = 0xff800000u;
             top = fmaxf(top, __uint_as_float(r[k]));
           }
-          m = top * p.sl2;
+          m = top * p.sl2 - kWeightBits<T>;
           const float nm = m == -INFINITY ? 0.f : -m;
 #pragma unroll
           for (int k = 0; k < kNarrow / 2; ++k) {
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
             mx[k] = fmax3(mx[k], __uint_as_float(r[(i + k) >> 5][(i + k) & 31]), __uint_as_float(r[(i + 8 + k) >> 5][(i + 8 + k) & 31]));
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(r[3][24 + k]));
-        const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.sl2;  // sl2 > 0
+        const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * p.sl2 - kWeightBits<T>;  // sl2 > 0
         // (a row without a query has no vote: what it holds, of another sequence or left by an earlier call, would move
         // the others' maxima and so their last bits)
         if (__any_sync(0xffffffffu, live && top > m + kRescale)) {

@@ -11,7 +11,7 @@ activations' type (half a step u) and sums in fp32, element by element:
   |lse - exact| <= e + 2^-20 (1 + |lse|).
 
 Weights held in fp16 (fp16 activations, or an e4m3 cache) have a step of 2^-24 below 2^-14, whatever their
-size: 2^-25 more for each key's weight, and 2^-25 for an fp16 output.
+size.  The kernels hold them times 2^7, so it is 2^-32 more for each key's weight; and 2^-25 for an fp16 output.
 """
 from __future__ import annotations
 
@@ -47,7 +47,7 @@ def attend(q, k, v, scale, u, fp16_weights=False):
         e = (d * 2.0 ** -23 * sums.max() + 2.0 ** -21 * np.abs(s[finite] / scale).max()) * scale if sums.size else 0.0
         tol = (u + 2 * e + 2.0 ** -20) * (p @ np.abs(v)) + u * np.abs(out)
         if fp16_weights:
-            tol = tol + 2.0 ** -25 * (np.abs(v).sum(0) / total + 1)
+            tol = tol + 2.0 ** -32 * np.abs(v).sum(0) / total + 2.0 ** -25
     return out, lse, tol, e + 2.0 ** -20 * (1 + abs(lse))
 
 

@@ -56,3 +56,45 @@ def test_window_attention_does_not_depend_on_what_ran_before(tl, ctx, group, d):
         got.append(run_window(tl, ctx, q, k, v, [0, n], [0, n]))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     check_window(q, k, v, [0, n], [0, n], *got[0])
+
+
+# ------------------------------------------------------------------------------------------------ small weights
+def sink_and_tail(n, d, kv):
+    """One key far above the rest whose value is 0, and n others alike whose value is 1: all of the result is
+    their weights, 2^-25.2 each beside the first one's 1.  (As rows [n + 1, kv, d], exact in every type.)"""
+    k, v = torch.zeros((n + 1, kv, d)), torch.ones((n + 1, kv, d))
+    k[0, :, 0], v[0] = 16.0, 0.0
+    return k, v, 17.5 / 16
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_attention_keeps_small_fp16_weights(tl, ctx, d):
+    k, v, scale = sink_and_tail(8192, d, 1)
+    q = torch.zeros((1, 4, d))
+    q[:, :, 0] = 1.0
+    q, k, v = (t.to(torch.float16).cuda() for t in (q, k, v))
+    out, e = run_window(tl, ctx, q, k, v, [0, 1], [0, k.shape[0]], scale=scale)
+    assert ctx.check() == tl.TL_OK
+    check_window(q, k, v, [0, 1], [0, k.shape[0]], out, e, scale=scale)
+    out, e = run_window(tl, ctx, q, k, v, [0, 1], [0, k.shape[0]], scale=scale, window=8000, sinks=1)
+    check_window(q, k, v, [0, 1], [0, k.shape[0]], out, e, 8000, 1, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,cache", [("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+def test_paged_attention_keeps_small_fp16_weights(tl, ctx, dtype, cache, d):
+    """Enough sequences (of the same pages) that none is split: a warp then meets a quarter of the tail with the first key."""
+    kv, batch, page = 8, 64, 64
+    k, v, scale = sink_and_tail(8191, d, kv)
+    pools = [t.view(-1, page, kv, d).to(DT[cache]).cuda() for t in (k, v)]
+    table = torch.arange(pools[0].shape[0], dtype=torch.int32, device="cuda").expand(batch, -1).contiguous()
+    lengths = torch.full((batch,), 8192, dtype=torch.int32, device="cuda")
+    q = torch.zeros((batch, kv, d), dtype=DT[dtype], device="cuda")
+    q[:, :, 0] = 1.0
+    out, e = run_paged(tl, ctx, q, pools, table, lengths, scale=scale)
+    assert ctx.check() == tl.TL_OK
+    u = serving.HALF_STEP[dtype]
+    want, lse, tol, ltol = serving.attend(q[0, 0].cpu().double().numpy(), k[:, 0].double().numpy(), v[:, 0].double().numpy(), scale, u, True)
+    shape = (batch, kv, d)
+    close(f64(out), np.broadcast_to(want, shape), np.broadcast_to(tol, shape), "out")
+    close(f64(e), np.broadcast_to(lse, shape[:2]), np.broadcast_to(ltol, shape[:2]), "lse")
