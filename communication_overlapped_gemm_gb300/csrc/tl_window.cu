@@ -37,10 +37,15 @@
 // sinks 113 us, 1141 TFLOP/s, 9 and a quarter blocks walked for 8 seen.  Two sequences of 4k after 513 keys, 16
 // heads on 2, d 64: 93 us, 855 TFLOP/s.
 //
-// A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V would still
-// reach the row through the product.  So a row with a non-finite result is computed once more by
-// its warp from the keys that it sees alone (window_row).
+// A key that a row does not see gets weight 0 there, but 0 times a NaN or infinity in V still reaches the row
+// through the product.  (One in K does not: the scores of unseen keys are replaced.  So a sum l that is NaN
+// comes from a key that the row sees, and the row is NaN.)  Items with rows whose l is finite and whose result is not are
+// noted, and after the last item, when no other warp waits for anything, their non-finite results are computed once
+// more from what the rows see (window_again).  One prompt of 4096 tokens, 8 heads on 2, d 128, causal, 0.09 ms: with a
+// NaN in K 0.07 ms, with one in V 1.4 ms (row by row and key by key inside the loop it was 56 ms for either), with
+// NaN in a dim of every V 2.6 ms.
 #include <atomic>
+#include <climits>
 
 #include "tl_serve.cuh"
 #include "tl_softmax.cuh"
@@ -64,7 +69,8 @@ struct Shape {
   static constexpr int kCumOff = kBarOff + 256;
   static constexpr int kPlanOff = kCumOff + (kMaxBatch + 4) * 4;
   static constexpr int kHeldOff = kPlanOff + (kLevels + 4 + 2 * kSorted) * 4;
-  static constexpr int kSmem = 1024 + kHeldOff + kHeld * 64;
+  static constexpr int kAgainOff = kHeldOff + kHeld * 64;  // a softmax warp's first and last item for window_again
+  static constexpr int kSmem = 1024 + kAgainOff + 9 * 8;                // (and the plan's numbers for it)
 };
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S_t at 128 t, O_t at 256 + 128 t
 }  // namespace win
@@ -97,45 +103,6 @@ __device__ __forceinline__ Seen seen_keys(int p, int window, int sinks) {
   s.from = window == 0 || p < window ? 0 : p - window + 1;
   s.head = sinks < s.from ? sinks : s.from;
   return s;
-}
-
-// One row (query, head) by one warp: keys in turn, each lane D / 32 of the head dims, with a
-// running maximum and sum in fp32.  Reads the visible keys only.
-template <class T, int D>
-__device__ __forceinline__ void window_row(const WindowParams& p, int token, int h, int pos, int k0, int lane) {
-  constexpr int kPer = D / 32;
-  const int hk = h / p.group;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-  const T* qp = reinterpret_cast<const T*>(p.q + token * p.q_token + h * p.q_head) + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = static_cast<float>(qp[i]);
-    o[i] = 0.f;
-  }
-  const Seen s = seen_keys(pos, p.window, p.sinks);
-  const int count = pos < 0 ? 0 : s.head + pos - s.from + 1;
-  for (int i = 0; i < count; ++i) {
-    const int j = k0 + (i < s.head ? i : i - s.head + s.from);
-    const T* kp = reinterpret_cast<const T*>(p.k + j * p.k_token + hk * p.k_head) + lane * kPer;
-    const T* vp = reinterpret_cast<const T*>(p.v + j * p.v_token + hk * p.v_head) + lane * kPer;
-    float x = 0.f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) x += q[c] * static_cast<float>(kp[c]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= p.sl2;
-    const float mn = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.f : exp2f(m - mn), w = x == -INFINITY ? 0.f : exp2f(x - mn);
-    m = mn;
-    l = l * keep + w;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) o[c] = o[c] * keep + w * static_cast<float>(vp[c]);
-  }
-  T* op = reinterpret_cast<T*>(p.out + token * p.out_token + h * p.out_head) + lane * kPer;
-#pragma unroll
-  for (int c = 0; c < kPer; ++c) op[c] = static_cast<T>(l == 0.f ? 0.f : o[c] / l);
-  if (p.lse && lane == 0)
-    p.lse[static_cast<long long>(token) * p.heads + h] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // A sequence's bounds, as rows of q and k; nothing (n = 0) if they are out of order or range.
@@ -320,6 +287,148 @@ __device__ __forceinline__ void regs_up() {
 // The first n of 32 bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
+// The results of 16 rows of a tile that are not finite, once more by one warp, on mma.sync m16n8k16 with the rows as its
+// rows: 16 keys at a time, of those that any of the rows sees, with a running maximum and sum.  V's elements that are not
+// finite are taken as 0 in the product, and each is then added, times its weight in fp32, to the rows that see its
+// key.  Results that are finite keep their bits.
+template <class T, int D>
+__device__ __forceinline__ void window_again(const WindowParams& p, const WinItem& w, int t, int r0, int lane) {
+  constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;  // all ones: not finite
+  const int g = lane >> 2, c2 = 2 * (lane & 3);  // this thread: rows g and g + 8, columns c2 and c2 + 1 of every 8
+  auto odd = [](uint32_t v) { return (v & kExp) == kExp; };
+  auto load = [](const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); };
+  const uint8_t* qp[2];
+  uint8_t* op[2];
+  bool live[2], any = false;
+  int pos[2], from[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int row = r0 + g + 8 * x, tok = row / p.group, h = w.hk * p.group + row - tok * p.group;
+    const int i = w.i0 + t * p.tokens + tok;
+    live[x] = tok < p.tokens && i < w.s.n;
+    pos[x] = live[x] ? w.s.off + i : -1;
+    from[x] = live[x] ? seen_keys(pos[x], p.window, p.sinks).from : INT_MAX;
+    qp[x] = p.q + (w.s.q0 + i) * p.q_token + h * p.q_head + c2 * 2;
+    op[x] = p.out + (w.s.q0 + i) * p.out_token + h * p.out_head + c2 * 2;
+    if (live[x])
+#pragma unroll 4
+      for (int n = 0; n < D / 8; ++n) {
+        const uint32_t v = load(op[x] + 16 * n);
+        any |= odd(v) || odd(v >> 16);
+      }
+  }
+  if (!__any_sync(0xffffffffu, any)) return;
+  const int last = __reduce_max_sync(0xffffffffu, max(pos[0], pos[1]));
+  const int first = __reduce_min_sync(0xffffffffu, min(from[0], from[1]));
+  const int sinks = p.sinks;
+  auto sees = [&](int x, int j) { return j <= pos[x] && (j >= from[x] || j < sinks); };
+  const uint8_t* kb = p.k + w.s.k0 * p.k_token + w.hk * p.k_head;
+  const uint8_t* vb = p.v + w.s.k0 * p.v_token + w.hk * p.v_head;
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
+  for (int j0 = 0; j0 <= last; j0 += 16) {
+    if (j0 >= sinks && j0 + 16 <= first) j0 = first & ~15;
+    float s[2][4];  // rows g (0, 1) and g + 8 (2, 3), keys c2 and c2 + 1 of both eights
+    const uint8_t* kp[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      kp[e] = kb + min(j0 + 8 * e + g, last) * p.k_token + c2 * 2;  // (past the last key: that key again, without weight)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[e][x] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      uint32_t q[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) q[x] = live[x & 1] ? load(qp[x & 1] + 32 * d + 16 * (x >> 1)) : 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mma16816<T>(s[e], q, load(kp[e] + 32 * d), load(kp[e] + 32 * d + 16));
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float& v = s[e >> 1][2 * x + (e & 1)];
+        v = sees(x, j0 + 8 * (e >> 1) + c2 + (e & 1)) ? v * p.sl2 : -INFINITY;
+        top = fmaxf(top, v);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mn = fmaxf(m[x], top - kWeightBits<T>), keep = m[x] == -INFINITY ? 0.f : ex2_approx(m[x] - mn);
+      m[x] = mn;
+      l[x] *= keep;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][2 * x] *= keep;
+        o[n][2 * x + 1] *= keep;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float& v = s[e >> 1][2 * x + (e & 1)];
+        v = v == -INFINITY ? 0.f : ex2_approx(v - mn);
+        l[x] += v;
+      }
+    }
+    const uint32_t a[4] = {from_f32x2<T>(s[0][0], s[0][1]), from_f32x2<T>(s[0][2], s[0][3]), from_f32x2<T>(s[1][0], s[1][1]),
+                           from_f32x2<T>(s[1][2], s[1][3])};
+    uint32_t some = 0;  // eights of dims with a V that is not finite
+    const uint16_t* vp[4];  // this thread's keys c2, c2 + 1 of both eights, dim g of every 8
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      vp[x] = reinterpret_cast<const uint16_t*>(vb + min(j0 + 8 * (x >> 1) + c2 + (x & 1), last) * p.v_token) + g;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      uint32_t v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        v[x] = vp[x][8 * n];
+        if (odd(v[x])) {
+          some |= 1u << n;
+          v[x] = 0u;
+        }
+      }
+      mma16816<T>(o[n], a, v[0] | v[1] << 16, v[2] | v[3] << 16);
+    }
+    some = __reduce_or_sync(0xffffffffu, some);
+    if (some) {
+      const int keys = min(16, last + 1 - j0);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        if (!(some >> n & 1u)) continue;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t v = k < keys ? load(vb + (j0 + k) * p.v_token + 16 * n + c2 * 2) : 0u;
+          const float2 f = to_f32x2<T>(v);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float even = k & 8 ? s[1][2 * x] : s[0][2 * x], uneven = k & 8 ? s[1][2 * x + 1] : s[0][2 * x + 1];
+            const float weight = __shfl_sync(0xffffffffu, k & 1 ? uneven : even, (lane & ~3) + ((k & 7) >> 1));
+            if (odd(v) && sees(x, j0 + k)) o[n][2 * x] += weight * f.x;
+            if (odd(v >> 16) && sees(x, j0 + k)) o[n][2 * x + 1] += weight * f.y;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    if (!live[x]) continue;
+    const float inv = 1.f / l[x];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(op[x] + 16 * n);
+      const uint32_t was = *at, now = l[x] == 0.f ? 0u : from_f32x2<T>(o[n][2 * x] * inv, o[n][2 * x + 1] * inv);
+      *at = (odd(was) ? now & 0xffffu : was & 0xffffu) | (odd(was >> 16) ? now & 0xffff0000u : was & 0xffff0000u);
+    }
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_constant__ WindowParams p) {
   using namespace win;
@@ -424,6 +533,7 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
   }
   __syncthreads();
   const int items = plan.sorted ? plan.above[0] * p.kv_heads : plan.cum[p.batch];
+  if (threadIdx.x == 0) reinterpret_cast<int2*>(base + S::kAgainOff)[8] = make_int2(plan.sorted, plan.gran);
   // The list of the CTA's items: the first kHeld looked up by all warps at once, later ones by warp 3, half a list at a
   // time.  (Looked up by each warp as it came to them, the code in every role cost 4%: instruction fetch.)
   WinItem* held = reinterpret_cast<WinItem*>(base + S::kHeldOff);
@@ -608,6 +718,8 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * t + lanes, to = tmem + kColO + 128 * t + lanes;
     const int tok = row / p.group, hg = row - tok * p.group;
+    int2* const again = reinterpret_cast<int2*>(base + S::kAgainOff) + warp - 4;
+    if (lane == 0) *again = make_int2(-1, -1);
     bool ok = true;
     int ns = 0, no = 0;  // S blocks and items seen
     for (int it = 0; ok && win_index(it) < items; ++it) {
@@ -730,7 +842,6 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       }
       if (!ok) break;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool bad = !(l <= 3.0e38f);
       unsigned long long zero = 0ull;  // 0 times every sum: NaN if one is not finite
       if (w.nb) {
         ok = __all_sync(0xffffffffu, mbar_wait(&ofull[t], no & 1, c, kSiteTmemFull));
@@ -781,18 +892,35 @@ __global__ void __launch_bounds__(win::kThreads, 1) window_kernel(const __grid_c
       }
       float z0, z1;
       f2_split(zero, z0, z1);
-      bad |= !(z0 + z1 == 0.f);
+      if (__any_sync(0xffffffffu, live && l == l && !(z0 + z1 == 0.f))) {
+        if (lane == 0) {
+          if (again->x < 0) again->x = it;
+          again->y = it;
+        }
+      }
       if (live && p.lse)
         p.lse[static_cast<long long>(w.s.q0 + i) * p.heads + w.hk * p.group + hg] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
       tc_fence_before();
-      // rows with a non-finite result, once more from what they see (after the stores above, of other lanes)
       __syncwarp();
-      for (uint32_t again = __ballot_sync(0xffffffffu, bad && live); again; again &= again - 1) {
-        const int x = __ffs(again) - 1;
-        window_row<T, D>(p, __shfl_sync(0xffffffffu, w.s.q0 + i, x), w.hk * p.group + __shfl_sync(0xffffffffu, hg, x),
-                         __shfl_sync(0xffffffffu, pos, x), w.s.k0, lane);
+    }
+    __syncwarp();
+    const int2 range = *again;
+    if (ok && range.x >= 0) {  // (the rows were stored by other lanes: the barriers above)
+      // (the plan from shared memory: registers would hold it all along)
+      WinPlan late;
+      const int2 numbers = reinterpret_cast<const int2*>(base + S::kAgainOff)[8];
+      late.sorted = numbers.x != 0;
+      late.gran = numbers.y;
+      late.cum = reinterpret_cast<int*>(base + S::kCumOff);
+      late.above = reinterpret_cast<int*>(base + S::kPlanOff);
+      late.off = late.above + kLevels + 1;
+      late.pairs = late.off + kSorted;
+      for (int it = range.x; it <= range.y; ++it) {
+        const WinItem w = win_item(p, late, win_index(it), lane);
+        if (w.nb == 0 || (t && !w.two)) continue;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) window_again<T, D>(p, w, t, (warp & 3) * 32 + 16 * h, lane);
       }
-      __syncwarp();
     }
   }
   tc_fence_before();

@@ -494,6 +494,8 @@ int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, cons
  *   out[i][h] = softmax_j(scale * q[i][h] . k[j][h / G]) . v[j][h / G],  lse as tl_paged_attention.
  * A query with nothing visible (p < 0), or only scores of -inf, has out = 0 and lse = -inf.  A key that is not visible to a
  * query has no effect on it, whatever it holds (infinities and NaN too).
+ * Infinities and NaN in v cost time: results that they make non-finite are computed twice, the second time more
+ * slowly (about 20 times a whole call's time if every query sees one).  In k they cost none.
  * q, out: dtype [total_q x heads x d]; k, v: dtype [total_k x kv_heads x d], strides as given (out
  * must not overlap the inputs).  lse: fp32 [total_q x heads] or NULL.  cu_q, cu_k: int32 [batch + 1], not
  * decreasing, cu_q[0] >= 0, cu_q[batch] <= total_q, cu_k likewise (rows outside every sequence are

@@ -98,3 +98,77 @@ def test_paged_attention_keeps_small_fp16_weights(tl, ctx, dtype, cache, d):
     shape = (batch, kv, d)
     close(f64(out), np.broadcast_to(want, shape), np.broadcast_to(tol, shape), "out")
     close(f64(e), np.broadcast_to(lse, shape[:2]), np.broadcast_to(ltol, shape[:2]), "lse")
+
+
+# ------------------------------------------------------------------------------------------------ non-finite values
+def check_rows(q, k, v, rows, out, e, window=0, sinks=0):
+    """Some queries of one prompt against the oracle."""
+    dtype = "bf16" if q.dtype == torch.bfloat16 else "fp16"
+    g, n, scale = q.shape[1] // k.shape[1], q.shape[0], q.shape[2] ** -0.5
+    qs, ks, vs = f64(q), f64(k), f64(v)
+    for i in rows:
+        seen = serving.visible(i, n, window, sinks)
+        for h in range(q.shape[1]):
+            with np.errstate(invalid="ignore"):
+                want, lse, tol, ltol = serving.attend(qs[i, h], ks[seen, h // g], vs[seen, h // g], scale,
+                                                      serving.HALF_STEP[dtype], dtype == "fp16")
+            tol = np.where(np.isfinite(want), tol, 0.0)
+            close(f64(out[i, h]), want, tol, f"out {i} {h}")
+            close(f64(e[i, h]), lse, ltol, f"lse {i} {h}")
+
+
+@pytest.mark.parametrize("heads,kv", [(4, 1), (3, 1), (2, 2)])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16")])
+def test_window_attention_non_finite_values_of_a_long_prompt(tl, ctx, heads, kv, d, dtype):
+    """Values that are not finite reach the queries that see them, in their dim, as the sum has them: NaN, an infinity,
+    or NaN where two infinities meet.  Every other result keeps its bits."""
+    n = 2600
+    q, k, v = (t.clone() for t in packed([n], [n], heads, kv, d, dtype, seed=heads))
+    cu = [0, n]
+    for window, sinks in ((0, 0), (500, 3), (130, 140)):
+        clean, _ = run_window(tl, ctx, q, k, v, cu, cu, window=window, sinks=sinks)
+        w = v.clone()
+        w[2, 0, 7], w[1300, 0, 9], w[2000, 0, 9], w[1301, 0, 10] = math.nan, math.inf, -math.inf, -math.inf
+        w[2590, 0, 11] = math.nan
+        out, e = run_window(tl, ctx, q, k, w, cu, cu, window=window, sinks=sinks)
+        assert ctx.check() == tl.TL_OK
+        rows = [0, 1, 2, 3, 63, 64, 130, 499, 502, 503, 1269, 1299, 1300, 1301, 1330, 1429, 1430, 1431, 1799, 1800, 1801, 1999,
+                2000, 2130, 2499, 2560, 2589, 2590, 2599]
+        check_rows(q, k, w, rows, out, e, window, sinks)
+        fine = torch.ones(d, dtype=torch.bool)
+        fine[[7, 9, 10, 11]] = False
+        assert torch.equal(out[:, :, fine], clean[:, :, fine])
+
+
+def test_window_attention_an_early_nan_costs_no_wait(tl):
+    """A NaN that nearly every query of a prompt sees is an answer, not a reason for a wait to run out (4 ms here)."""
+    n = 8192
+    q, k, v = (t.clone() for t in packed([n], [n], 8, 2, 128, "bf16", seed=12))
+    out, clean = torch.empty_like(q), torch.empty_like(q)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    with tl.Context(0, timeout_ns=1_000_000) as c:
+        tl.tl_window_attention(c, q, k, v, cu, cu, clean)
+        assert c.check() == tl.TL_OK
+        v[3, 0, 0] = math.nan
+        tl.tl_window_attention(c, q, k, v, cu, cu, out)
+        assert c.check() == tl.TL_OK
+        assert torch.isnan(out[3:, :4, 0]).all()
+        assert torch.equal(out[:3], clean[:3]) and torch.equal(out[:, :, 1:], clean[:, :, 1:]) and torch.equal(out[:, 4:], clean[:, 4:])
+        k[5, 1, 0] = math.nan                                # and one in a key: the whole row is NaN
+        tl.tl_window_attention(c, q, k, v, cu, cu, out)
+        assert c.check() == tl.TL_OK
+        assert torch.isnan(out[5:, 4:]).all() and torch.equal(out[:5, 4:], clean[:5, 4:])
+
+
+def test_window_attention_values_near_the_end_of_the_range(tl, ctx):
+    """A stale maximum leaves weights of up to 2^8: values whose sums pass the fp32 range that way, and back in it by
+    the division, are still found."""
+    n = 300
+    q, k, v = (t.clone() for t in packed([n], [n], 2, 1, 64, "bf16", seed=14))
+    q[:] = 0
+    k[:] = 0
+    q[:, :, 0], k[200, 0, 0] = 8.0, 5.0                     # its weight is 2^7.2 beside the others' 1
+    v[200, 0, 3] = 3.0e38
+    out, e = run_window(tl, ctx, q, k, v, [0, n], [0, n])
+    assert torch.isfinite(out).all()
+    check_rows(q, k, v, [0, 199, 200, 201, 299], out, e)
