@@ -690,8 +690,10 @@ __device__ __forceinline__ void moet_multiply(const MoeTokParams& p, MoeTables& 
             const int f = this_col * ln.kCols + wq * 32 + m * 16 + g + 8 * (j >> 1);
             if (f < N) {
               const float a = acc[m][b][j], v = a / (1.f + expf(-a)) * acc[2 + m][b][j];
-              const __nv_bfloat16 h0 = __float2bfloat16_rn(v);
-              const float r1 = v - __bfloat162float(h0);
+              // (a value that rounds to infinity is cut off to bf16's largest instead; an infinity has no remainder)
+              __nv_bfloat16 h0 = __float2bfloat16_rn(v);
+              if (__hisinf(h0)) h0 = __float2bfloat16_rz(v);
+              const float f0 = __bfloat162float(h0), r1 = v == f0 ? 0.f : v - f0;
               const __nv_bfloat16 h1 = __float2bfloat16_rn(r1);
               const size_t at = static_cast<size_t>(row0 + r) * p.F + f;
               p.h[at] = h0;

@@ -172,3 +172,24 @@ def test_window_attention_values_near_the_end_of_the_range(tl, ctx):
     out, e = run_window(tl, ctx, q, k, v, [0, n], [0, n])
     assert torch.isfinite(out).all()
     check_rows(q, k, v, [0, 199, 200, 201, 299], out, e)
+
+
+# ------------------------------------------------------------------------------------------------ MoE
+@pytest.mark.parametrize("T", [1, 9])
+def test_moe_tokens_large_hidden_values(tl, ctx, T):
+    """h at the end of the range: an infinity stays one (not NaN), and a value that bf16 would round to one is carried
+    in full."""
+    H, E, F = 64, 2, 64
+    x, lg = torch.zeros((T, H)), torch.zeros((T, E))
+    x[:, 0], lg[:, 1] = 2.0 ** 62, -40.0
+    for gate, up, inf in ((2.0, 8.0, True),                         # 2^63 times 2^65
+                          (2 * 129 / 128, 4 * 254 / 128, False)):   # (2 - 2^-13) 2^127, over bf16's largest
+        w = [torch.zeros((E, H, F)), torch.zeros((E, H, F)), torch.full((E, F, H), 2.0 ** -20)]
+        w[0][:, 0, 5], w[1][:, 0, 5] = gate, up
+        case = [t.cuda() for t in (x.bfloat16(), lg, *(m.bfloat16() for m in w))]
+        out, ex, g = run_moe(tl, ctx, *case, 1)
+        assert ctx.check() == tl.TL_OK
+        if inf:
+            assert (out == math.inf).all()
+        else:
+            check_moe(*case, 1, out, ex, g)
