@@ -319,6 +319,7 @@ __device__ __forceinline__ bool wait_item(const unsigned* ctr, unsigned want, co
       }
     }
   }
+  __syncwarp();  // orders the other lanes' reads of h after lane 0's acquire; the shuffle orders no memory
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
