@@ -305,8 +305,10 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
   // 7.6, 11.4, 9.8 and 15.5.
   const uint32_t mean = (total + p.batch * subs - 1) / (p.batch * subs);
   const uint32_t per = max(max((total + gridDim.x - 1) / gridDim.x, (mean + 31) / 32), min((mean + 15) / 16, 2u << p.lw));
-  const uint32_t first = per * blockIdx.x;  // at most total + grid^2
-  if (first >= total) return;
+  // (where an item's parts are limited, `per` is up to grid / 32 even shares: 20 times the line does not fit 32 bits)
+  const unsigned long long line = static_cast<unsigned long long>(per) * blockIdx.x;
+  if (line >= total) return;
+  const uint32_t first = static_cast<uint32_t>(line);
   const int nsteps = static_cast<int>(per < total - first ? per : total - first);
 
   PagedAt at;
