@@ -469,7 +469,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
         raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
     pages, page, heads, d = shape
     a, b, c, one = strides
-    if v_cache.stride() != strides or one != 1:
+    if one != 1 or v_cache.stride() != strides and any(  # (of a dimension of one entry nothing uses the stride)
+            n > 1 and s != t for n, s, t in zip(shape, strides, v_cache.stride())):
         raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(),
                        0 if k_scale is None else _vec(k_scale, heads, "f32", "k_scale"),

@@ -193,3 +193,22 @@ def test_moe_tokens_large_hidden_values(tl, ctx, T):
             assert (out == math.inf).all()
         else:
             check_moe(*case, 1, out, ex, g)
+
+
+# ------------------------------------------------------------------------------------------------ layouts and plans
+def test_strides_of_dimensions_of_one_entry_do_not_matter(tl, ctx):
+    """One kv head, head-major keys and token-major values: the same addresses, other strides on paper."""
+    q, pools, table, lengths = paged_case([40, 3], 4, 1, 64, 16, "bf16", "bf16", False, seed=2, spoil=False)
+    major = torch.empty((pools[0].shape[0], 1, 16, 64), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    major.copy_(pools[0])
+    assert major.stride() != pools[1].stride()
+    want, _ = run_paged(tl, ctx, q, pools, table, lengths)
+    out, e = run_paged(tl, ctx, q, (major, pools[1]), table, lengths)
+    assert torch.equal(out, want)
+    row = draws(1, 1, 1, 64).bfloat16().cuda()
+    tl.tl_kv_append(ctx, row, row, major, pools[1], torch.tensor([5], dtype=torch.int32, device="cuda"))
+    assert torch.equal(major[0, 5], row[0]) and torch.equal(pools[1][0, 5], row[0])
+    with pytest.raises(ValueError, match="strides"):
+        two = torch.zeros((3, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+        tl.tl_kv_append(ctx, row.expand(1, 2, 64), row.expand(1, 2, 64), two, two.transpose(1, 2).contiguous().transpose(1, 2),
+                        torch.tensor([5], dtype=torch.int32, device="cuda"))
