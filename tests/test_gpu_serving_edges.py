@@ -212,3 +212,50 @@ def test_strides_of_dimensions_of_one_entry_do_not_matter(tl, ctx):
         two = torch.zeros((3, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
         tl.tl_kv_append(ctx, row.expand(1, 2, 64), row.expand(1, 2, 64), two, two.transpose(1, 2).contiguous().transpose(1, 2),
                         torch.tensor([5], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 2)])
+def test_paged_attention_of_many_sequences(tl, ctx, window, sinks):
+    """More sequences than threads of a CTA, empty ones at both ends and in runs: each thread plans several."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 90, 700)
+    lens[:9], lens[128:140], lens[-20:] = 0, 0, 0
+    lens[300] = 1500
+    q, pools, table, lengths = paged_case(lens.tolist(), 4, 2, 64, 16, "bf16", "bf16", False, seed=700, window=window, sinks=sinks)
+    out, e = run_paged(tl, ctx, q, pools, table, lengths, window=window, sinks=sinks)
+    assert ctx.check() == tl.TL_OK
+    check_paged(q, pools, table, lengths, out, e, window, sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_window_attention_of_continued_prompts_ordered_by_length(tl, ctx, window, sinks):
+    """More items than CTAs, of sequences that stand at different places of their keys."""
+    lens_q, lens_k = [300, 257, 20], [310, 700, 400]
+    q, k, v = packed(lens_q, lens_k, 48, 48, 64, "bf16", seed=21)
+    out, e = run_window(tl, ctx, q, k, v, cum(lens_q), cum(lens_k), window=window, sinks=sinks)
+    assert ctx.check() == tl.TL_OK
+    check_window(q, k, v, cum(lens_q), cum(lens_k), out, e, window, sinks)
+
+
+def test_window_attention_head_major_inputs_and_a_strided_output(tl, ctx):
+    lens = [130, 77]
+    n, heads, kv, d = sum(lens), 6, 2, 64
+    q, k, v = (draws(31 + i, h, n, d).bfloat16().cuda().transpose(0, 1) for i, h in enumerate((heads, kv, kv)))
+    room = torch.full((n, heads + 3, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor(cum(lens), dtype=torch.int32, device="cuda")
+    e = torch.empty((n, heads), device="cuda")
+    for out in (room[:, 2:2 + heads], torch.full((heads, n, d), 7.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)):
+        tl.tl_window_attention(ctx, q, k, v, cu, cu, out, lse=e, window=50, sinks=1)
+        assert ctx.check() == tl.TL_OK
+        check_window(q, k, v, cum(lens), cum(lens), out, e, 50, 1)
+    assert (room[:, :2] == 7).all() and (room[:, -1] == 7).all()
+
+
+def test_paged_attention_into_a_strided_output(tl, ctx):
+    q, pools, table, lengths = paged_case([3001, 0, 40], 8, 2, 128, 16, "bf16", "bf16", False, seed=6)
+    room = torch.full((3, 11, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[:, 1:9]
+    tl.tl_paged_attention(ctx, q, *pools, table, lengths, out, ws(tl.tl_paged_attention_workspace_bytes(3, 8, 2, 128)))
+    assert ctx.check() == tl.TL_OK
+    check_paged(q, pools, table, lengths, out, None)
+    assert (room[:, 0] == 7).all() and (room[:, 9:] == 7).all()
