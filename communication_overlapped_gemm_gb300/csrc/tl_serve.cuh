@@ -92,7 +92,7 @@ inline bool smem_ready(std::atomic<unsigned long long>& ready, int device, const
 // of a cut piece is that of the CTA it starts in.
 constexpr int kCutCounters = 1024;         // by CTA: the largest grid
 constexpr int kItemCounters = 1024;        // MoE: by item, at most 128 tokens x topk 8
-constexpr int kTokenCounters = 128 * 256;  // MoE: by token and block of 128 of at most 32768 columns
+constexpr int kTokenCounters = 128 * 256;  // MoE: by token and block of 256 of at most 32768 columns (twice what that takes)
 constexpr size_t kCounterBytes = (kCutCounters + kItemCounters + kTokenCounters) * 4;
 static_assert(kCounterBytes == TL_SERVE_COUNTER_BYTES, "header");
 

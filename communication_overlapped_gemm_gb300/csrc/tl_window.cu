@@ -126,7 +126,9 @@ __device__ __forceinline__ WinSeq win_seq(const WindowParams& p, int b, bool rep
 
 // The order of the items.  Of 2 to 32 sequences with several items a CTA, those whose tiles stand further into their keys come first,
 // in 256 levels of `gran` positions, so that a round of CTAs has items of about the same length; otherwise
-// sequence by sequence, the last tiles first.
+// sequence by sequence, the last tiles first.  (Sequence by sequence and so, 32 heads on 8, d 128, causal: 2 of up to 8k
+// tokens 571 and 536 us, 8 of up to 4k 503 and 454, 32 of up to 4k 1295 and 1242; short ones lose, 32 of up to 600 101
+// and 107.  A lane has a sequence, hence 32; a batch of 33 of up to 4k takes what it takes by sequence, 786.)
 struct WinPlan {
   bool sorted;
   int* cum;    // [batch + 1]: items before each sequence (if not sorted)

@@ -476,6 +476,10 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
  * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
  * batch == 0 or heads == 0 is a no-op.
+ * Precision: scores, weights and all sums are fp32; a weight is rounded to 16 bits (dtype; fp16 if the cache is e4m3)
+ * where it meets V: off by half a step of that type, or in fp16 by 2^-32 of the largest weight if that is more
+ * (tl_window_attention: the same).  The division by the weights' sum comes last, and a weight may be 2^8 until then:
+ * sums of bf16 rows within 2^-8 / n of fp32's largest value can overflow.
  * The result does not depend on what else runs, and is bit-identical run to run on one device.
  */
 size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d);
@@ -517,8 +521,8 @@ int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long long q_token
  * few tokens of a decoding step, where reading the chosen experts' weights is all that takes time:
  *   y_(t,j) = (SiLU(x_t . Wg_e) * (x_t . Wu_e)) . Wd_e,   out_t = sum_j gate_(t,j) * y_(t,j)
  * Unlike there, h keeps fp32 precision between the two products, the sums over j are taken in fp32
- * in the order j = 0, 1, ... and each distinct expert's weights are read from HBM once (an expert with more
- * than 16 of the tokens, more than 8 if T <= 8, reads them again, mostly from L2); results are bit-identical
+ * in the order j = 0, 1, ... and each distinct expert's weights are read once for every 16 of its tokens (again
+ * from L2 where the experts are small, from HBM where one alone is larger than L2); results are bit-identical
  * run to run.
  * x: bf16 [T x H]; logits: fp32 [T x E]; w_gate, w_up: bf16 [E x H x F]; w_down: bf16 [E x F x H];
  * out: fp32 [T x H].  experts_out (int32 [T x topk]) and gates_out (fp32 [T x topk]) are optional: the
