@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
 //
 // e4m3 rows are widened to fp16 (exact) in registers; q is brought to fp16 by a power of two per row
 // that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products
-// run in fp16.  Weights are rounded to the products' 16-bit type (half a step; fp16 ones are held times 2^7,
-// kWeightBits, m being 7 less) to meet V there; l sums them unrounded in fp32.
+// run in fp16.  Weights meet V in the products' 16-bit type, fp16 ones held times 2^7 (kWeightBits, m being 7 less): over
+// a 16-bit cache as a sum of two terms, off by half a step of half a step, so that a bf16 output is off by its own
+// rounding (relative 1.6e-3; with one term 2.2e-3, and 0.6% less time: the tensor pipe waits for HBM), over an
+// e4m3 cache, whose rows have 4 bits, as one fp16 term.  l sums them unrounded in fp32.
 namespace paged {
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys;
 template <bool Fp8, int D, int NB>
@@ -567,7 +569,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
             }
           }
       }
-      uint32_t pf[NB][2];  // the weights as the next product's B: keys by pairs in a column of queries
+      // the weights as the next product's B: keys by pairs in a column of queries; for a 16-bit cache as a sum of two terms
+      constexpr int kTerms = Fp8 ? 1 : 2;
+      uint32_t pf[NB][kTerms][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float w[4];
@@ -576,8 +580,15 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
           w[j] = ex2_approx(x[b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
           l[b][j & 1] += w[j];
         }
-        pf[b][0] = transpose8x8(from_f32x2<M>(w[0], w[1]));
-        pf[b][1] = transpose8x8(from_f32x2<M>(w[2], w[3]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t top = from_f32x2<M>(w[2 * e], w[2 * e + 1]);
+          pf[b][0][e] = transpose8x8(top);
+          if constexpr (!Fp8) {
+            const float2 f = to_f32x2<M>(top);
+            pf[b][1][e] = transpose8x8(from_f32x2<M>(w[2 * e] - f.x, w[2 * e + 1] - f.y));
+          }
+        }
       }
       if constexpr (!Fp8) {
         const int key = (lane & 7) + ((lane >> 4) << 3);
@@ -586,7 +597,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
           uint32_t a[4];
           ldsm4t(a, sv + key * S::kRowBytes + (((2 * d + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
 #pragma unroll
-          for (int b = 0; b < NB; ++b) mma16816<M>(o[d][b], a, pf[b][0], pf[b][1]);
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = kTerms - 1; e >= 0; --e) mma16816<M>(o[d][b], a, pf[b][e][0], pf[b][e][1]);
         }
       } else {
         // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8), transposed bytewise: rows
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
             widen_e4m3(__byte_perm(w[0][i], w[1][i], z ? 0x7362 : 0x5140), a[0], a[1]);
             widen_e4m3(__byte_perm(w[2][i], w[3][i], z ? 0x7362 : 0x5140), a[2], a[3]);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816<M>(o[2 * i + z][b], a, pf[b][0], pf[b][1]);
+            for (int b = 0; b < NB; ++b) mma16816<M>(o[2 * i + z][b], a, pf[b][0][0], pf[b][0][1]);
           }
       }
     }

@@ -476,10 +476,10 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
  * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
  * batch == 0 or heads == 0 is a no-op.
- * Precision: scores, weights and all sums are fp32; a weight is rounded to 16 bits (dtype; fp16 if the cache is e4m3)
- * where it meets V: off by half a step of that type, or in fp16 by 2^-32 of the largest weight if that is more
- * (tl_window_attention: the same).  The division by the weights' sum comes last, and a weight may be 2^8 until then:
- * sums of bf16 rows within 2^-8 / n of fp32's largest value can overflow.
+ * Precision: scores, weights and all sums are fp32.  Where a weight meets V it is a sum of two terms of dtype, off by
+ * half a step squared; with an e4m3 cache one fp16 term, and in tl_window_attention one term of dtype, off by half
+ * a step.  fp16 terms are also off by up to 2^-32 of the largest weight.  The division by the weights' sum comes
+ * last, and a weight may be 2^8 until then: sums of bf16 rows within 2^-8 / n of fp32's largest value can overflow.
  * The result does not depend on what else runs, and is bit-identical run to run on one device.
  */
 size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d);

@@ -259,3 +259,19 @@ def test_paged_attention_into_a_strided_output(tl, ctx):
     assert ctx.check() == tl.TL_OK
     check_paged(q, pools, table, lengths, out, None)
     assert (room[:, 0] == 7).all() and (room[:, 9:] == 7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(8, 2), (12, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_paged_attention_is_off_by_its_output_rounding_alone(tl, ctx, dtype, heads, kv, d):
+    """Over a 16-bit cache a weight meets V as two 16-bit terms, off by half a step of half a step: u^2 (and what fp16 cuts
+    off), so that u is left for the output."""
+    q, pools, table, lengths = paged_case([700, 40, 5000], heads, kv, d, 16, dtype, dtype, False, seed=heads + d, spoil=False)
+    out, e = run_paged(tl, ctx, q, pools, table, lengths)
+    assert ctx.check() == tl.TL_OK
+    u = serving.HALF_STEP[dtype]
+    args = (f64(q), f64(pools[0]), f64(pools[1]), table.cpu().numpy(), lengths.tolist(), d ** -0.5)
+    want, _, tol, _ = serving.paged_attention(*args, u=0.0, fp16_weights=dtype == "fp16")
+    per_unit = serving.paged_attention(*args, u=1.0, fp16_weights=dtype == "fp16")[2] - tol   # sum p |v| + |out|
+    close(f64(out), want, tol + u * u * (per_unit - np.abs(want)) + u * np.abs(want), "out")
