@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
 // a tcgen05 instruction, and CUDA cores alone would need G fused multiply-adds per element, 27 T/s
 // at G = 8 and full HBM rate of the 39 T/s that the SMs have.
 // Measured (32 heads on 8, d 128): 32 bf16 sequences of up to 8k 88 us, 6.19 TB/s, 0.91 of the copy rate; 64 heads
-// over 128 e4m3 sequences of up to 16k 352 us, 0.91; one sequence of 4k 8.8 us against 2.5 for its bytes: length, table
+// over 128 e4m3 sequences of up to 16k 352 us, 0.91; one sequence of 4k 9.0 us against 2.5 for its bytes: length, table
 // entry, row, part, counter and the parts again are waited for in turn.
 //
 // Work: an item is (sequence, kv head, block of 8 or 16 query heads), a tile 64 of its visible keys.
