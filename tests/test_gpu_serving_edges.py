@@ -275,3 +275,23 @@ def test_paged_attention_is_off_by_its_output_rounding_alone(tl, ctx, dtype, hea
     want, _, tol, _ = serving.paged_attention(*args, u=0.0, fp16_weights=dtype == "fp16")
     per_unit = serving.paged_attention(*args, u=1.0, fp16_weights=dtype == "fp16")[2] - tol   # sum p |v| + |out|
     close(f64(out), want, tol + u * u * (per_unit - np.abs(want)) + u * np.abs(want), "out")
+
+
+@pytest.mark.parametrize("group", [1, 4])
+def test_window_attention_spoilt_values_that_a_row_walks_by(tl, ctx, group):
+    """A value that shares a block with the sinks, and one before rows that see nothing: weight 0 for these rows."""
+    n = 700
+    q, k, v = (t.clone() for t in packed([n], [n], group, 1, 64, "bf16", seed=group))
+    v[20, 0, 5], v[3, 0, 6] = math.nan, math.inf
+    for window, sinks in ((100, 3), (100, 33), (300, 200)):
+        out, e = run_window(tl, ctx, q, k, v, [0, n], [0, n], window=window, sinks=sinks)
+        assert ctx.check() == tl.TL_OK
+        check_rows(q, k, v, [0, 2, 3, 19, 20, 99, 102, 103, 119, 120, 150, 320, 500, 699], out, e, window, sinks)
+    # queries of a sequence whose keys begin after them: 0, whatever V holds
+    lens_q, lens_k = [200, 9], [100, 4]
+    q, k, v = (t.clone() for t in packed(lens_q, lens_k, group, 1, 64, "bf16", seed=group + 7))
+    v[2, 0, 1], v[101, 0, 2] = math.nan, -math.inf
+    out, e = run_window(tl, ctx, q, k, v, cum(lens_q), cum(lens_k))
+    assert ctx.check() == tl.TL_OK
+    assert (out[:100] == 0).all() and (e[:100] == -math.inf).all() and (out[200:205] == 0).all()
+    check_window(q, k, v, cum(lens_q), cum(lens_k), out, e)
