@@ -7,9 +7,9 @@ and streams.  There is no fallback: if the library is missing or the device is
 not sm_103, the calls raise.
 
 Entry points (same names as the C ABI): ``tl_ag_gemm``, ``tl_gemm_rs``,
-``tl_mlp2``, ``tl_moe_combine``, the serving operators ``tl_kv_append``,
-``tl_paged_attention``, ``tl_window_attention`` and ``tl_moe_tokens``, their
-``*_workspace_bytes`` sizes, plus
+``tl_mlp2``, ``tl_moe_combine``, the serving operators ``tl_cache_plan``, ``tl_norm_rope``,
+``tl_kv_append``, ``tl_kv_gather``, ``tl_paged_attention``, ``tl_window_attention``, ``tl_moe_tokens``
+and ``tl_token_logprobs``, their ``*_workspace_bytes`` sizes, plus
 ``Context`` (tl_ctx_create / tl_ctx_check / tl_ctx_destroy / tl_ctx_set_trace),
 the host-side tile maps ``tl_ag_tile_order`` / ``tl_rs_tile_order`` and
 ``tl_trace_bytes`` (the trace buffer is read by ``.trace``).
@@ -24,14 +24,15 @@ from . import _build
 
 __all__ = [
     "TL_OK", "TL_ERR_INVALID", "TL_ERR_UNSUPPORTED", "TL_ERR_CUDA", "TL_ERR_TIMEOUT", "TL_ERR_WORKSPACE",
-    "TL_ERR_INDEX", "TL_BF16", "TL_FP16", "TL_E4M3", "TLError", "PagedCache", "Config", "Context", "lib", "library_path", "build",
+    "TL_ERR_INDEX", "TL_BF16", "TL_FP16", "TL_E4M3", "TL_FP32", "TL_E2M1", "TLError", "PagedCache", "Config", "Context", "lib", "library_path", "build",
     "tl_ag_gemm", "tl_ag_gemm_ll_capable", "tl_allgather", "tl_gemm_rs", "tl_reduce_scatter", "tl_mlp2",
     "tl_moe_combine",
     "tl_ag_gemm_workspace_bytes", "tl_gemm_rs_workspace_bytes", "tl_gemm_rs_ring_workspace_bytes",
     "tl_mlp2_workspace_bytes", "tl_rs_ring_tile_order", "tl_moe_tile_order", "tl_moe_combine_order",
     "tl_moe_workspace_bytes", "tl_ag_tile_order", "tl_rs_tile_order", "tl_trace_bytes", "tl_ag_attention",
     "tl_ag_attention_workspace_bytes", "tl_kv_append", "tl_paged_attention", "tl_paged_attention_workspace_bytes",
-    "tl_window_attention", "tl_moe_tokens", "tl_moe_tokens_workspace_bytes", "EXPORTED_SYMBOLS",
+    "tl_window_attention", "tl_moe_tokens", "tl_moe_tokens_workspace_bytes", "tl_kv_gather", "tl_cache_plan", "tl_norm_rope",
+    "tl_token_logprobs", "tl_token_logprobs_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 TL_OK = 0
@@ -45,6 +46,8 @@ TL_ERR_INDEX = -6
 TL_BF16 = 0
 TL_FP16 = 1
 TL_E4M3 = 2
+TL_FP32 = 3
+TL_E2M1 = 4
 
 library_path = _build.LIB
 build = _build.build
@@ -89,6 +92,11 @@ class PagedCache(ctypes.Structure):
         ("page_size", _i),
         ("kv_heads", _i),
         ("d", _i),
+        ("k_blocks", _vp),
+        ("v_blocks", _vp),
+        ("block_page_stride", ctypes.c_longlong),
+        ("block_row_stride", ctypes.c_longlong),
+        ("block_head_stride", ctypes.c_longlong),
     ]
 
 
@@ -125,6 +133,12 @@ _SIGS = {
     "tl_ag_attention": (_i, [_vp, _i, _i, _vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), _vp, _vp, _c_size, _i, _i,
                              _i, _vp]),
     "tl_kv_append": (_i, [_vp, _vp, _i, _vp, _vp, _ll, _ll, _ll, _ll, _vp, _i, _vp]),
+    "tl_kv_gather": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _ll, _ll, _ll, _ll, _vp]),
+    "tl_cache_plan": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "tl_norm_rope": (_i, [_vp, _i, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _vp, _i, _f, _vp, _vp, _i, _i, _vp, _ll, _ll, _vp, _ll,
+                          _ll, _i, _i, _i, _i, _vp]),
+    "tl_token_logprobs_workspace_bytes": (_c_size, [_i, _i, _i]),
+    "tl_token_logprobs": (_i, [_vp, _i, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _i, _i, _vp, _c_size, _vp]),
     "tl_paged_attention_workspace_bytes": (_c_size, [_i, _i, _i, _i]),
     "tl_paged_attention": (_i, [_vp, _vp, _i, _vp, _ll, _ll, _vp, _i, _vp, _vp, _ll, _ll, _vp, _i, _i, _f, _i, _i, _vp,
                                 _c_size, _vp]),
@@ -209,11 +223,16 @@ def _stream(stream, device: int | None = None) -> int:
 _dtypes: dict = {}
 
 
-def _need(t, dtype_name: str, what: str):
+def _dtype_of(dtype_name: str):
     if not _dtypes:
         import torch
-        _dtypes.update({"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8})
-    dt = _dtypes[dtype_name]
+        _dtypes.update({"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
+                        "e4m3": torch.float8_e4m3fn})
+    return _dtypes[dtype_name]
+
+
+def _need(t, dtype_name: str, what: str):
+    dt = _dtype_of(dtype_name)
     if t is None:
         raise ValueError(f"{what} is required")
     if not t.is_cuda or t.dtype != dt or not t.is_contiguous():
@@ -455,15 +474,20 @@ def _vec(t, n: int, dtype_name: str, what: str) -> int:
     return t.data_ptr()
 
 
-_pack_cache = struct.Struct("=4Q3q5i4x").pack  # PagedCache, at half its cost
-assert struct.calcsize("=4Q3q5i4x") == ctypes.sizeof(PagedCache)
+_pack_cache = struct.Struct("=4Q3q5i4x").pack  # PagedCache, at half its cost: what every cache has,
+_pack_blocks = struct.Struct("=2Q3q").pack     # and a 4-bit one's block scales
+assert struct.calcsize("=4Q3q5i4x2Q3q") == ctypes.sizeof(PagedCache)
+_NO_BLOCKS = _pack_blocks(0, 0, 0, 0, 0)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
+def _cache(k_cache, v_cache, k_scale, v_scale, k_blocks=None, v_blocks=None):
     """A tl_paged_cache (as bytes) and its kv heads and d."""
     shape, strides = k_cache.shape, k_cache.stride()
-    code = _codes.get(k_cache.dtype)
-    if code is None or not k_cache.is_cuda:
+    code, tail = _codes.get(k_cache.dtype), _NO_BLOCKS
+    if k_blocks is not None or v_blocks is not None:
+        tail = _blocks(k_cache, k_blocks, v_blocks)
+        code = TL_E2M1
+    elif code is None or not k_cache.is_cuda:
         code = _code(k_cache, "k_cache")
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_cuda:
         raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
@@ -472,17 +496,37 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
     if one != 1 or v_cache.stride() != strides and any(  # (of a dimension of one entry nothing uses the stride)
             n > 1 and s != t for n, s, t in zip(shape, strides, v_cache.stride())):
         raise ValueError("k_cache and v_cache must have the same strides, the last one 1")
+    if code == TL_E2M1:
+        d *= 2
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(),
                        0 if k_scale is None else _vec(k_scale, heads, "f32", "k_scale"),
                        0 if v_scale is None else _vec(v_scale, heads, "f32", "v_scale"), a if pages > 1 else 0,
-                       b if page > 1 else 0, c if heads > 1 else 0, code, pages, page, heads, d), heads, d
+                       b if page > 1 else 0, c if heads > 1 else 0, code, pages, page, heads, d) + tail, heads, d
 
 
-def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None) -> None:
+def _blocks(k_cache, k_blocks, v_blocks):
+    """The end of a 4-bit cache's tl_paged_cache: uint8 codes [pages, page_size, kv_heads, d / 2], e4m3 scales [.., d / 16]."""
+    if k_blocks is None or v_blocks is None or k_cache.dtype is not _dtype_of("u8") or not k_cache.is_cuda:
+        raise ValueError("a 4-bit cache is CUDA uint8 codes with k_blocks and v_blocks")
+    shape, strides = k_blocks.shape, k_blocks.stride()
+    for t in (k_blocks, v_blocks):
+        if t.dtype is not _dtype_of("e4m3") or not t.is_cuda or k_cache.dim() != 4 or t.shape != (*k_cache.shape[:3], k_cache.shape[3] // 8):
+            raise ValueError("k_blocks and v_blocks must be CUDA float8_e4m3fn [pages, page_size, kv_heads, d / 16]")
+    pages, page, heads, n = shape
+    a, b, c, one = strides
+    if (one != 1 and n > 1) or any(m > 1 and s != t for m, s, t in zip(shape, strides, v_blocks.stride())):
+        raise ValueError("k_blocks and v_blocks must have the same strides, the last one 1")
+    return _pack_blocks(k_blocks.data_ptr(), v_blocks.data_ptr(), a if pages > 1 else 0, b if page > 1 else 0,
+                        c if heads > 1 else 0)
+
+
+def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None, k_blocks=None,
+                 v_blocks=None) -> None:
     """Write the rows k, v (bf16 or fp16 [tokens, kv_heads, d]) into a paged cache ([pages, page_size,
     kv_heads, d] views of any page, row and head strides; the type of k, or float8_e4m3fn holding
-    k / k_scale[h]) at slots (int32 [tokens]: page * page_size + row; negative: skipped)."""
-    cache, heads, d = _cache(k_cache, v_cache, k_scale, v_scale)
+    k / k_scale[h], or 4 bits: uint8 codes [.., d / 2] with e4m3 scales k_blocks, v_blocks [.., d / 16] of 16 values each)
+    at slots (int32 [tokens]: page * page_size + row; negative: skipped)."""
+    cache, heads, d = _cache(k_cache, v_cache, k_scale, v_scale, k_blocks, v_blocks)
     code, shape = _code(k, "k"), k.shape
     if len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or not v.is_cuda or shape[1] != heads or \
             shape[2] != d:
@@ -497,17 +541,130 @@ def tl_kv_append(ctx: Context, k, v, k_cache, v_cache, slots, k_scale=None, v_sc
         _check(rc, "tl_kv_append")
 
 
+def tl_kv_gather(ctx: Context, k_cache, v_cache, slots, k, v, k_scale=None, v_scale=None, stream=None, k_blocks=None,
+                 v_blocks=None) -> None:
+    """tl_kv_append's way back: the cache's rows at slots (int32 [tokens]; negative: the row is left as it is)
+    into k, v (bf16 or fp16 [tokens, kv_heads, d]), as the values that they stand for."""
+    cache, heads, d = _cache(k_cache, v_cache, k_scale, v_scale, k_blocks, v_blocks)
+    code, shape = _code(k, "k"), k.shape
+    if len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or not v.is_cuda or shape[1] != heads or \
+            shape[2] != d:
+        raise ValueError("inconsistent shapes")
+    n = shape[0]
+    sp = _vec(slots, n, "i32", "slots")
+    ka, kb = _rows(k, "k")
+    va, vb = _rows(v, "v")
+    rc = lib().tl_kv_gather(ctx.handle, cache, code, sp, n, k.data_ptr(), v.data_ptr(), ka, kb, va, vb,
+                            _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_kv_gather")
+
+
+def tl_cache_plan(ctx: Context, lengths, page_table, page_size: int, free_pages, taken, taken_out, new_lengths, cu_q, slots,
+                  positions=None, counts=None, cu_k=None, kv_slots=None, stream=None) -> None:
+    """Where a step's new tokens go in a paged cache, all int32 on the GPU.  Sequence b holds lengths[b] rows and gets
+    counts[b] (None: one each) more; pages that it still needs are free_pages[taken[0] ..], in the order of the
+    sequences, and are entered into page_table [batch, max_pages].  Written: cu_q [batch + 1], slots and
+    positions of the packed tokens (any number of entries; -1 and 0 past the last token), new_lengths (may be
+    lengths), taken_out [1] (may be taken), and where given cu_k [batch + 1] and kv_slots, the slots of all rows."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    batch, pages = page_table.shape
+    n, m = slots.numel(), 0 if kv_slots is None else kv_slots.numel()
+    rc = lib().tl_cache_plan(ctx.handle, _vec(lengths, batch, "i32", "lengths"), _vec(counts, batch, "i32", "counts"), batch,
+                             page_size, _vec(page_table, batch * pages, "i32", "page_table"), pages,
+                             _vec(free_pages, free_pages.numel(), "i32", "free_pages"), free_pages.numel(),
+                             _vec(taken, 1, "i32", "taken"), _vec(taken_out, 1, "i32", "taken_out"),
+                             _vec(new_lengths, batch, "i32", "new_lengths"), _vec(cu_q, batch + 1, "i32", "cu_q"),
+                             _vec(cu_k, batch + 1, "i32", "cu_k"), _vec(slots, n, "i32", "slots"),
+                             _vec(positions, n, "i32", "positions"), n, _vec(kv_slots, m, "i32", "kv_slots"), m,
+                             _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_cache_plan")
+
+
+def tl_norm_rope(ctx: Context, q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None) -> None:
+    """Each head's row of q [tokens, heads, d] and k [tokens, kv_heads, d] (bf16 or fp16, any strides) through an RMS norm
+    (with a weight [d], of their type or fp32; None: none) and the rotation by positions (int32 [tokens]) of its first
+    2 len(inv_freq) values (fp32; None: none), into q_out, k_out (which may be q, k).  Pairs are (p, p + rotary / 2),
+    or (2p, 2p + 1) if interleaved."""
+    code, dtype, shape, kshape = _code(q, "q"), q.dtype, q.shape, k.shape
+    if len(shape) != 3 or len(kshape) != 3 or q_out.shape != shape or k_out.shape != kshape or kshape[0] != shape[0] or \
+            kshape[2] != shape[2]:
+        raise ValueError("inconsistent shapes")
+    for t, what in ((k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+        if t.dtype is not dtype or not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor of q's type (got {t.dtype}, {t.device})")
+    tokens, heads, d = shape
+    wcode, wp = code, [0, 0]
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is not None:
+            if w.dtype is not dtype:
+                _need(w, "f32", "a norm's weight of another type than q")
+                wcode = TL_FP32
+            if w.numel() != d or not w.is_cuda or not w.is_contiguous():
+                raise ValueError(f"a norm's weight must be a contiguous CUDA tensor of {d} entries (got {tuple(w.shape)})")
+            wp[i] = w.data_ptr()
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise ValueError("q_weight and k_weight must be of one type")
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    qa, qb = _rows(q, "q")
+    ka, kb = _rows(k, "k")
+    oa, ob = _rows(q_out, "q_out")
+    pa, pb = _rows(k_out, "k_out")
+    rc = lib().tl_norm_rope(ctx.handle, code, q.data_ptr(), qa, qb, k.data_ptr(), ka, kb, wp[0], wp[1], wcode, eps,
+                            _vec(positions, tokens, "i32", "positions"), _vec(inv_freq, pairs, "f32", "inv_freq"), 2 * pairs,
+                            1 if interleaved else 0, q_out.data_ptr(), oa, ob, k_out.data_ptr(), pa, pb, tokens, heads,
+                            kshape[1], d, _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_norm_rope")
+
+
+def tl_token_logprobs_workspace_bytes(rows, vocab, top) -> int:
+    return lib().tl_token_logprobs_workspace_bytes(rows, vocab, top)
+
+
+def tl_token_logprobs(ctx: Context, logits, targets, logprob, workspace, entropy=None, lse=None, top_logprobs=None,
+                      top_ids=None, scale: float = 1.0, stream=None) -> None:
+    """With p = softmax(scale * logits) of each row (bf16, fp16 or fp32 [rows, vocab], any row stride): logprob = ln p
+    of the row's target (int32 [rows]; negative: the row is skipped), entropy and lse (fp32 [rows]), and the most
+    likely tokens' ln p and indices, best first (top_logprobs fp32, top_ids int32 [rows, top], top <= 32).  targets
+    and logprob may be None."""
+    code = TL_FP32 if logits.dtype is _dtype_of("f32") and logits.is_cuda else _code(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits must be contiguous in its last dimension")
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    if (top_ids is None) != (top_logprobs is None) or top_ids is not None and (
+            top_ids.shape != (rows, top) or top_logprobs.shape != (rows, top)):
+        raise ValueError("top_logprobs and top_ids must both be [rows, top]")
+    _need(workspace, "u8", "workspace")
+    rc = lib().tl_token_logprobs(ctx.handle, code, logits.data_ptr(), stride if rows > 1 else 0,
+                                 _vec(targets, rows, "i32", "targets"), _vec(logprob, rows, "f32", "logprob"),
+                                 _vec(entropy, rows, "f32", "entropy"), _vec(lse, rows, "f32", "lse"),
+                                 _vec(top_logprobs, rows * top, "f32", "top_logprobs"),
+                                 _vec(top_ids, rows * top, "i32", "top_ids"), top, scale, rows, vocab,
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream, ctx.device))
+    if rc:
+        _check(rc, "tl_token_logprobs")
+
+
 def tl_paged_attention_workspace_bytes(batch, heads, kv_heads, d) -> int:
     return lib().tl_paged_attention_workspace_bytes(batch, heads, kv_heads, d)
 
 
 def tl_paged_attention(ctx: Context, q, k_cache, v_cache, page_table, lengths, out, workspace, lse=None, scale=None,
-                       window: int = 0, sinks: int = 0, k_scale=None, v_scale=None, stream=None) -> None:
+                       window: int = 0, sinks: int = 0, k_scale=None, v_scale=None, stream=None, k_blocks=None,
+                       v_blocks=None) -> None:
     """out[b, h] = softmax(scale q[b, h] K^T) V over the visible rows of sequence b in a paged cache: the
     first lengths[b] rows, with a window only the last `window` and the first `sinks` of them.
     q, out: bf16 or fp16 [batch, heads, d]; caches as tl_kv_append; page_table int32 [batch, max_pages];
     lengths int32 [batch] (the new token's row counted); lse fp32 [batch, heads]; scale: 1/sqrt(d)."""
-    cache, _, d = _cache(k_cache, v_cache, k_scale, v_scale)
+    cache, _, d = _cache(k_cache, v_cache, k_scale, v_scale, k_blocks, v_blocks)
     code, shape, tshape = _code(q, "q"), q.shape, page_table.shape
     if len(shape) != 3 or out.shape != shape or out.dtype is not q.dtype or not out.is_cuda or shape[2] != d or \
             len(tshape) != 2 or tshape[0] != shape[0]:

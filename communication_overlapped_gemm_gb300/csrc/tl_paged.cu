@@ -13,14 +13,11 @@ struct CacheArgs {
   const float* k_scale;
   const float* v_scale;
   long long page_stride, row_stride, head_stride;  // bytes
+  uint8_t* k_blocks;                               // 4 bits: e4m3 scales of 16 values each
+  uint8_t* v_blocks;
+  long long page_blocks, row_blocks, head_blocks;  // bytes
   int num_pages, page_size, kv_heads;
 };
-
-// n / d for n < 2^31 as (umulhi(n, mul) + n) >> shift, exact.
-struct FastDiv {
-  uint32_t mul, shift;
-};
-__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
 // ---------------------------------------------------------------------------- append
 // Each thread copies 16 bytes of a K and of a V row (8 bytes written for e4m3): a row a thread, all threads of an
@@ -111,6 +108,183 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
   }
 }
 
+// ---------------------------------------------------------------------------- 4 bits
+// A block of 16 values x of a row, s its head's scale, is held as e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+// a sign; the lower half of a byte first) and one e4m3 scale b:
+//   b = e4m3(max |x| / (6 s)),  code = e2m1(x / (b s)),  value = code b s,
+// each quotient and product rounded to fp32, each conversion to nearest even and saturating.  code b has 6 bits: fp16
+// and fp32 hold it exactly.  A block whose b is 0 is all 0; a NaN makes its block's b NaN, so all 16 are NaN.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t to_e2m1(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+// Eight codes as four pairs of fp16, exactly.
+__device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(v));
+}
+// Two e4m3 values as a pair of fp16, exactly.
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t v) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+struct Block4 {
+  uint2 codes;
+  uint8_t scale;
+};
+template <class T>
+__device__ __forceinline__ Block4 quantise16(uint4 lo, uint4 hi, float s) {
+  const uint32_t in[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  float x[16], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = to_f32x2<T>(in[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+    top = fmax_nan(top, fmax_nan(fabsf(f.x), fabsf(f.y)));
+  }
+  Block4 q;
+  q.scale = __nv_cvt_float_to_fp8(__fdiv_rn(top, 6.f * s), __NV_SATFINITE, __NV_E4M3);
+  const float t = __half2float(__half(__nv_cvt_fp8_to_halfraw(q.scale, __NV_E4M3))) * s;
+  if (t == 0.f) {
+    q.codes = make_uint2(0u, 0u);
+    return q;
+  }
+  // the IEEE quotients, as for e4m3 above
+  const float y = __frcp_rn(t);
+  const bool plain = fabsf(t) >= 0x1p-60f && fabsf(t) <= 0x1p60f && top <= 0x1p60f;
+  float lo8[8], hi8[8];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float d = x[i] * y;
+    d = fmaf(fmaf(d, -t, x[i]), y, d);
+    d = fmaf(fmaf(d, -t, x[i]), y, d);
+    d = copysignf(d, x[i]);
+    if (!plain) d = __fdiv_rn(x[i], t);
+    (i < 8 ? lo8 : hi8)[i & 7] = d;
+  }
+  q.codes = make_uint2(to_e2m1(lo8), to_e2m1(hi8));
+  return q;
+}
+
+// Each thread takes a block of a K and of a V row.
+template <class T, int D>
+__global__ void __launch_bounds__(256) append4_kernel(const AppendParams p) {
+  constexpr int kVec = D / 16;
+  const int vec = threadIdx.x % kVec;
+  const uint32_t r = blockIdx.x * (256 / kVec) + threadIdx.x / kVec;
+  if (r >= p.rows) return;
+  const uint32_t t = divide(r, p.by_heads), h = r - t * p.c.kv_heads;
+  const int slot = __ldg(p.slots + t);
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_token + h * p.k_head) + 2 * vec;
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head) + 2 * vec;
+  const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+  if (slot < 0) return;
+  const uint32_t page = divide(static_cast<uint32_t>(slot), p.by_page);
+  if (page >= static_cast<uint32_t>(p.c.num_pages)) {
+    if (h == 0 && vec == 0) report_index(p.status, t);
+    return;
+  }
+  const int row = slot - static_cast<int>(page) * p.c.page_size;
+  const long long at = page * p.c.page_stride + row * p.c.row_stride + h * p.c.head_stride;
+  const long long bt = page * p.c.page_blocks + row * p.c.row_blocks + h * p.c.head_blocks + vec;
+  const Block4 k = quantise16<T>(k0, k1, p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
+  const Block4 v = quantise16<T>(v0, v1, p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f);
+  reinterpret_cast<uint2*>(p.c.k + at)[vec] = k.codes;
+  reinterpret_cast<uint2*>(p.c.v + at)[vec] = v.codes;
+  p.c.k_blocks[bt] = k.scale;
+  p.c.v_blocks[bt] = v.scale;
+}
+
+// ---------------------------------------------------------------------------- gather
+// The rows of a cache back as packed rows of T, the values that they stand for in fp32, rounded once.  A thread has
+// 16 bytes of a K and of a V row (8 of e4m3 codes; 4 bits: a block of 16 values).
+struct GatherParams {
+  CacheArgs c;
+  DevStatus* status;
+  uint8_t* k;
+  uint8_t* v;
+  long long k_token, k_head, v_token, v_head;  // bytes
+  const int* slots;
+  FastDiv by_heads, by_page;
+  uint32_t rows;  // tokens * kv_heads
+};
+template <class T>
+__device__ __forceinline__ uint4 widen8(uint2 u, float s) {  // eight e4m3 values
+  const uint32_t in[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = to_f32x2<__half>(widen_e4m3x2(in[i]));
+    out[i] = from_f32x2<T>(f.x * s, f.y * s);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+template <class T>
+__device__ __forceinline__ uint4 widen4(uint32_t codes, uint32_t b2, float s) {  // eight codes
+  uint32_t r[4];
+  widen_e2m1(codes, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = to_f32x2<__half>(hmul2(r[i], b2));
+    r[i] = from_f32x2<T>(f.x * s, f.y * s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <class T, int Bits, int D>
+__global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
+  constexpr int kVec = Bits == 4 ? D / 16 : D / 8;
+  const int vec = threadIdx.x % kVec;
+  const uint32_t r = blockIdx.x * (256 / kVec) + threadIdx.x / kVec;
+  if (r >= p.rows) return;
+  const uint32_t t = divide(r, p.by_heads), h = r - t * p.c.kv_heads;
+  const int slot = __ldg(p.slots + t);
+  if (slot < 0) return;
+  const uint32_t page = divide(static_cast<uint32_t>(slot), p.by_page);
+  if (page >= static_cast<uint32_t>(p.c.num_pages)) {
+    if (h == 0 && vec == 0) report_index(p.status, t);
+    return;
+  }
+  const int row = slot - static_cast<int>(page) * p.c.page_size;
+  const long long at = page * p.c.page_stride + row * p.c.row_stride + h * p.c.head_stride;
+  uint4* k = reinterpret_cast<uint4*>(p.k + t * p.k_token + h * p.k_head);
+  uint4* v = reinterpret_cast<uint4*>(p.v + t * p.v_token + h * p.v_head);
+  if constexpr (Bits == 16) {
+    k[vec] = __ldg(reinterpret_cast<const uint4*>(p.c.k + at) + vec);
+    v[vec] = __ldg(reinterpret_cast<const uint4*>(p.c.v + at) + vec);
+  } else {
+    const float sk = p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f, sv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+    const uint2 kc = __ldg(reinterpret_cast<const uint2*>(p.c.k + at) + vec);
+    const uint2 vc = __ldg(reinterpret_cast<const uint2*>(p.c.v + at) + vec);
+    if constexpr (Bits == 8) {
+      k[vec] = widen8<T>(kc, sk);
+      v[vec] = widen8<T>(vc, sv);
+    } else {
+      const long long bt = page * p.c.page_blocks + row * p.c.row_blocks + h * p.c.head_blocks + vec;
+      const uint32_t kb = widen_e4m3x2(__ldg(p.c.k_blocks + bt) * 0x101u), vb = widen_e4m3x2(__ldg(p.c.v_blocks + bt) * 0x101u);
+      k[2 * vec] = widen4<T>(kc.x, kb, sk);
+      k[2 * vec + 1] = widen4<T>(kc.y, kb, sk);
+      v[2 * vec] = widen4<T>(vc.x, vb, sv);
+      v[2 * vec + 1] = widen4<T>(vc.y, vb, sv);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------- attention of one token
 // For each sequence and kv head, G = heads / kv_heads query rows meet the same K and V rows:
 //   s = sc K q^T,  p = 2^(s - m),  O^T = V^T p,  l = sum p,  out = O / l
@@ -147,19 +321,21 @@ __global__ void __launch_bounds__(256, 8) append_kernel(const AppendParams p) {
 // e4m3 cache, whose rows have 4 bits, as one fp16 term.  l sums them unrounded in fp32.
 namespace paged {
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys;
-template <bool Fp8, int D, int NB>
+template <int Bits, int D, int NB>
 struct Shape {
   static constexpr int kRows = 8 * NB;                   // query heads of an item
-  static constexpr int kRowBytes = D * (Fp8 ? 1 : 2);
+  static constexpr int kRowBytes = D * Bits / 8;
   static constexpr int kHalf = kKeys * kRowBytes;        // one warp's K (or V) rows of a stage
+  static constexpr int kScaleBytes = Bits == 4 ? D / 16 : 0;          // of a row's blocks
+  static constexpr int kStage = 2 * (kHalf + kKeys * kScaleBytes);    // K, V, K's and V's block scales
   // CTAs per SM, and the stages that fit: 64 KB of ring at two CTAs, 48 KB at three.  A step of
   // 8-bit or short rows brings few bytes for its instructions and wants the warps; the registers
   // allow three CTAs there.
-  static constexpr int kCtas = D == 64 || (Fp8 && NB == 1) ? 3 : 2;
-  static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * 2 * kHalf);
+  static constexpr int kCtas = D == 64 || (Bits < 16 && NB == 1) ? 3 : 2;
+  static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
-  static constexpr int kMergeOff = kStages * kWarps * 2 * kHalf;
+  static constexpr int kMergeOff = kStages * kWarps * kStage;
   static constexpr int kMlOff = kMergeOff + kWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kMlOff + kWarps * kRows * 2 * 4;
   static constexpr int kPartRows = NB == 1 ? 32 : 16;    // query heads of an item's kv heads, at most
@@ -234,6 +410,25 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
+template <int N>  // 4 or 8 bytes, or zeros
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 // Four e4m3 values as two pairs of fp16, exactly.
 __device__ __forceinline__ void widen_e4m3(uint32_t v, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
@@ -256,11 +451,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return d;
 }
 
-template <class T, bool Fp8, int D, int NB>
-__global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kCtas)) paged_kernel(const PagedParams p) {
+template <class T, int Bits, int D, int NB>
+__global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::kCtas)) paged_kernel(const PagedParams p) {
   using namespace paged;
-  using S = Shape<Fp8, D, NB>;
-  using M = typename std::conditional<Fp8, __half, T>::type;  // the products' type
+  using S = Shape<Bits, D, NB>;
+  constexpr bool kNarrow = Bits < 16;                           // 8 or 4 bits, widened to fp16
+  using M = typename std::conditional<kNarrow, __half, T>::type;  // the products' type
   constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_sum[kThreads], s_warp[kWarps];
@@ -358,13 +554,14 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     int page;        // as the table has it
     bool wanted;
     long long rest;  // from the page's start to the row's
+    long long scales;  // 4 bits: to its block scales
     int b;
   };
   auto look_up = [&](const PagedAt& a, bool more) {
     Place w;
     w.page = 0;
     w.wanted = false;
-    w.rest = 0;
+    w.rest = w.scales = 0;
     w.b = a.b;
     const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & 15);
     if (more && i < a.vis.count) {
@@ -374,12 +571,20 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       w.wanted = true;
       w.rest = (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
                (((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw) * p.c.head_stride;
+      if constexpr (Bits == 4)
+        w.scales = (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_blocks +
+                   (((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw) * p.c.head_blocks;
     }
     return w;
   };
-  const uint32_t ring = smem_u32(smem) + warp * (2 * S::kHalf);
-  auto stage_addr = [&](int s) { return ring + s * (kWarps * 2 * S::kHalf); };
+  const uint32_t ring = smem_u32(smem) + warp * S::kStage;
+  auto stage_addr = [&](int s) { return ring + s * (kWarps * S::kStage); };
   uint32_t masks[kStages];  // one per stage, the same in all lanes
+  // 4 bits: where chunk c of V row `key` lies
+  auto chunk4 = [](int key, int c) -> uint32_t {
+    if constexpr (D == 128) return (key >> 1) * 128 + ((((key & 1) * 4 + c) ^ (((key >> 1) & 3) << 1)) << 4);
+    else return (key >> 2) * 128 + ((((key & 3) * 2 + c) ^ (((key >> 2) & 1) << 1)) << 4);
+  };
   auto issue = [&](int s, uint32_t& mask, const Place& w) {
     const bool row_ok = w.wanted && w.page >= 0 && w.page < p.c.num_pages;
     if (w.wanted && !row_ok) report_index(p.status, static_cast<unsigned long long>(w.b));
@@ -394,8 +599,11 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         const int key = j * kPer + lane / kChunks;
         const long long off = __shfl_sync(0xffffffffu, row_off, key) + c * 16;
         const uint32_t bytes = (mask >> key) & 1u ? 16u : 0u;  // 0: filled with zeros, nothing is read
-        uint32_t ck, cv;  // 16-byte chunks are permuted within a row so that no read below conflicts
-        if constexpr (!Fp8) {
+        uint32_t ck, cv;  // 16-byte chunks are permuted within a row (4 bits: within 128 bytes) so that no read below conflicts
+        if constexpr (Bits == 4) {
+          ck = key * S::kRowBytes + (c << 4);
+          cv = chunk4(key, c);
+        } else if constexpr (!kNarrow) {
           ck = cv = key * S::kRowBytes + ((c ^ (key & 7)) << 4);
         } else if constexpr (D == 128) {
           ck = key * 128 + ((c ^ ((key & 1) << 2)) << 4);
@@ -406,6 +614,10 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         }
         cp_async16(sk + ck, p.c.k + off, bytes);
         cp_async16(sv + cv, p.c.v + off, bytes);
+      }
+      if constexpr (Bits == 4) {  // lanes 0..15 the K rows' scales, the others V's
+        const uint8_t* src = (lane < 16 ? p.c.k_blocks : p.c.v_blocks) + (row_ok ? w.page * p.c.page_blocks + w.scales : 0);
+        cp_async_small<S::kScaleBytes>(sk + 2 * S::kHalf + lane * S::kScaleBytes, src, row_ok ? S::kScaleBytes : 0);
       }
       ++step_loaded;
     }
@@ -438,19 +650,19 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     const int r0 = NB == 1 ? 0 : at.sub % p.blocks * kRows, h0 = hk * p.group + r0;
     const int rows = p.group - r0 < kRows ? p.group - r0 : kRows;
     // q as the products' B: column g of block b (zero past the group)
-    const float sl2 = Fp8 && p.c.k_scale ? p.sl2 * __ldg(p.c.k_scale + hk) : p.sl2;
+    const float sl2 = kNarrow && p.c.k_scale ? p.sl2 * __ldg(p.c.k_scale + hk) : p.sl2;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const bool there = g + 8 * b < rows;
       const uint8_t* qp = p.q + at.b * p.q_seq + (h0 + g + 8 * b) * p.q_head;
-      if constexpr (Fp8) {
+      if constexpr (kNarrow) {
         float top = 0.f;
         float2 x[kSteps * 2];
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(qp + (64 * h + 16 * t) * 2) + w) : make_uint4(0, 0, 0, 0);
+            const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(qp + (Bits == 4 ? D / 4 * t + 16 * h : 64 * h + 16 * t) * 2) + w) : make_uint4(0, 0, 0, 0);
             x[h * 8 + w * 4] = to_f32x2<T>(v.x);
             x[h * 8 + w * 4 + 1] = to_f32x2<T>(v.y);
             x[h * 8 + w * 4 + 2] = to_f32x2<T>(v.z);
@@ -512,7 +724,41 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[b][j] = 0.f;
-      if constexpr (!Fp8) {
+      if constexpr (Bits == 4) {
+        // a quarter of a row per thread: k index 2t, 2t + 1, 8 + 2t, 9 + 2t of step s is head dim
+        // D / 4 t + 4 s + 0..3, for q above likewise, so that a thread's dims of four steps are one block
+        const uint32_t ss = sk + 2 * S::kHalf;
+        uint32_t lo[D / 32], hi[D / 32], slo, shi;  // codes of rows g and g + 8; a pair of scales, or one twice
+        if constexpr (D == 128) {
+          const uint4 u = lds128(sk + g * 64 + t * 16), w = lds128(sk + (g + 8) * 64 + t * 16);
+          lo[0] = u.x, lo[1] = u.y, lo[2] = u.z, lo[3] = u.w;
+          hi[0] = w.x, hi[1] = w.y, hi[2] = w.z, hi[3] = w.w;
+          slo = widen_e4m3x2(lds_u16(ss + g * 8 + t * 2));
+          shi = widen_e4m3x2(lds_u16(ss + (g + 8) * 8 + t * 2));
+        } else {
+          const uint2 u = lds64(sk + g * 32 + t * 8), w = lds64(sk + (g + 8) * 32 + t * 8);
+          lo[0] = u.x, lo[1] = u.y;
+          hi[0] = w.x, hi[1] = w.y;
+          slo = widen_e4m3x2(lds_u8(ss + g * 4 + t));
+          shi = widen_e4m3x2(lds_u8(ss + (g + 8) * 4 + t));
+        }
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const uint32_t bl = __byte_perm(slo, slo, h ? 0x3232 : 0x1010), bh = __byte_perm(shi, shi, h ? 0x3232 : 0x1010);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t x0[4], x1[4];
+            widen_e2m1(lo[2 * h + w], x0);
+            widen_e2m1(hi[2 * h + w], x1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a[4] = {hmul2(x0[2 * k], bl), hmul2(x1[2 * k], bh), hmul2(x0[2 * k + 1], bl), hmul2(x1[2 * k + 1], bh)};
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816<M>(x[b], a, qf[4 * h + 2 * w + k][b][0], qf[4 * h + 2 * w + k][b][1]);
+            }
+          }
+        }
+      } else if constexpr (!kNarrow) {
         const int key = lane & 15;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
@@ -570,7 +816,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
           }
       }
       // the weights as the next product's B: keys by pairs in a column of queries; for a 16-bit cache as a sum of two terms
-      constexpr int kTerms = Fp8 ? 1 : 2;
+      constexpr int kTerms = kNarrow ? 1 : 2;
       uint32_t pf[NB][kTerms][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -584,13 +830,47 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
         for (int e = 0; e < 2; ++e) {
           const uint32_t top = from_f32x2<M>(w[2 * e], w[2 * e + 1]);
           pf[b][0][e] = transpose8x8(top);
-          if constexpr (!Fp8) {
+          if constexpr (!kNarrow) {
             const float2 f = to_f32x2<M>(top);
             pf[b][1][e] = transpose8x8(from_f32x2<M>(w[2 * e] - f.x, w[2 * e + 1] - f.y));
           }
         }
       }
-      if constexpr (!Fp8) {
+      if constexpr (Bits == 4) {
+        // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8), which lie in one block; pairs of rows
+        // interleaved by halves of bytes: rows g and g + 8 of product n are head dims g D/8 + 2n and + 2n + 1
+        constexpr int kW = D / 64;  // words
+        const uint32_t ss = sk + 2 * S::kHalf + kKeys * S::kScaleBytes + (D == 128 ? g : g >> 1);
+        uint32_t w[4][kW], sb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+          sb[k] = lds_u8(ss + key * S::kScaleBytes);
+          if constexpr (D == 128) {
+            const uint2 v = lds64(sv + chunk4(key, g >> 1) + (g & 1) * 8);
+            w[k][0] = v.x;
+            w[k][1] = v.y;
+          } else {
+            w[k][0] = lds32(sv + chunk4(key, g >> 2) + (g & 3) * 4);
+          }
+        }
+        const uint32_t s01 = widen_e4m3x2(sb[0] | (sb[1] << 8)), s23 = widen_e4m3x2(sb[2] | (sb[3] << 8));
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          uint32_t e01[4], o01[4], e23[4], o23[4];
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
+          widen_e2m1((w[0][i] & kLow) | ((w[1][i] << 4) & ~kLow), e01);
+          widen_e2m1(((w[0][i] >> 4) & kLow) | (w[1][i] & ~kLow), o01);
+          widen_e2m1((w[2][i] & kLow) | ((w[3][i] << 4) & ~kLow), e23);
+          widen_e2m1(((w[2][i] >> 4) & kLow) | (w[3][i] & ~kLow), o23);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23), hmul2(o23[j], s23)};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<M>(o[4 * i + j][b], a, pf[b][0][0], pf[b][0][1]);
+          }
+        }
+      } else if constexpr (!kNarrow) {
         const int key = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
@@ -650,7 +930,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
           if (g == 0) ml[warp * kRows + row] = make_float2(m[b][j], l[b][j]);
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
-            if constexpr (!Fp8) {
+            if constexpr (!kNarrow) {
               dst[16 * n + g] = o[n][b][j];
               dst[16 * n + g + 8] = o[n][b][j + 2];
             } else {
@@ -666,7 +946,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
     auto head_of = [&](int r) { return NB == 1 ? (r >= rows) + (r >= 2 * rows) + (r >= 3 * rows) : 0; };  // of the item's
     auto write_out = [&](int r, int d, float4 v, float mm, float ll) {
       const int head = head_of(r), kv = hk0 + head, h = kv * p.group + r0 + r - head * rows;
-      const float vs = Fp8 && p.c.v_scale ? __ldg(p.c.v_scale + kv) : 1.f, inv = ll == 0.f ? 0.f : vs / ll;
+      const float vs = kNarrow && p.c.v_scale ? __ldg(p.c.v_scale + kv) : 1.f, inv = ll == 0.f ? 0.f : vs / ll;
       *reinterpret_cast<uint2*>(p.out + at.b * p.out_seq + h * p.out_head + d * 2) =
           make_uint2(from_f32x2<T>(v.x * inv, v.y * inv), from_f32x2<T>(v.z * inv, v.w * inv));
       if (p.lse && d == 0)
@@ -788,19 +1068,27 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Fp8, D, NB>::kC
 
 // ---------------------------------------------------------------------------- host side
 static bool cache_ok(const tl_paged_cache* c, int dtype) {
-  if (!c || (dtype != TL_BF16 && dtype != TL_FP16) || (c->dtype != dtype && c->dtype != TL_E4M3)) return false;
-  const int es = c->dtype == TL_E4M3 ? 1 : 2;
+  if (!c || (dtype != TL_BF16 && dtype != TL_FP16) || (c->dtype != dtype && c->dtype != TL_E4M3 && c->dtype != TL_E2M1)) return false;
+  const bool narrow = c->dtype == TL_E4M3 || c->dtype == TL_E2M1;
+  const int es = narrow ? 1 : 2;
   if (c->num_pages < 0 || c->page_size < 1 || c->kv_heads < 0 || (c->d != 64 && c->d != 128)) return false;
   if (static_cast<long long>(c->num_pages) * c->page_size >= (1LL << 31)) return false;
   if (!esize_ok(c->page_stride, es) || !esize_ok(c->row_stride, es) || !esize_ok(c->head_stride, es)) return false;
-  if (c->dtype != TL_E4M3 && (c->k_scale || c->v_scale)) return false;
+  if (!narrow && (c->k_scale || c->v_scale)) return false;
   if (c->num_pages > 0 && c->kv_heads > 0 && (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))) return false;
+  if (c->dtype == TL_E2M1) {
+    const int row = c->d / 16;  // bytes of a row's block scales
+    for (long long s : {c->block_page_stride, c->block_row_stride, c->block_head_stride})
+      if (s < 0 || s % row != 0) return false;
+    if (c->num_pages > 0 && c->kv_heads > 0 && (!c->k_blocks || !c->v_blocks || !aligned16(c->k_blocks) || !aligned16(c->v_blocks)))
+      return false;
+  }
   return true;
 }
 
 static CacheArgs cache_args(const tl_paged_cache* c) {
-  const int es = c->dtype == TL_E4M3 ? 1 : 2;
-  CacheArgs a;
+  const int es = c->dtype == TL_E4M3 || c->dtype == TL_E2M1 ? 1 : 2;
+  CacheArgs a = {};
   a.k = static_cast<uint8_t*>(c->k);
   a.v = static_cast<uint8_t*>(c->v);
   a.k_scale = c->k_scale;
@@ -811,30 +1099,26 @@ static CacheArgs cache_args(const tl_paged_cache* c) {
   a.num_pages = c->num_pages;
   a.page_size = c->page_size;
   a.kv_heads = c->kv_heads;
+  if (c->dtype == TL_E2M1) {
+    a.k_blocks = static_cast<uint8_t*>(c->k_blocks);
+    a.v_blocks = static_cast<uint8_t*>(c->v_blocks);
+    a.page_blocks = c->block_page_stride;
+    a.row_blocks = c->block_row_stride;
+    a.head_blocks = c->block_head_stride;
+  }
   return a;
 }
 
-static FastDiv fast_div(int d) {
-  FastDiv f;
-  f.shift = 0;
-  while ((1ull << f.shift) < static_cast<unsigned long long>(d)) ++f.shift;
-  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
-  return f;
-}
-
-static int launched() {
-  if (cudaGetLastError() != cudaSuccess) return TL_ERR_CUDA;
-  return TL_OK;
-}
-
-// f(T{}, Fp8, D) for the call's types, as compile-time values.
+// f(T{}, bits, D) for the call's types, as compile-time values.
 template <class F>
 static int dispatch(int dtype, int cache_dtype, int d, F&& f) {
-  const bool fp8 = cache_dtype == TL_E4M3;
-  auto with_d = [&](auto t, auto fp8c) {
-    return d == 64 ? f(t, fp8c, std::integral_constant<int, 64>{}) : f(t, fp8c, std::integral_constant<int, 128>{});
+  auto with_d = [&](auto t, auto bits) {
+    return d == 64 ? f(t, bits, std::integral_constant<int, 64>{}) : f(t, bits, std::integral_constant<int, 128>{});
   };
-  auto with_t = [&](auto t) { return fp8 ? with_d(t, std::true_type{}) : with_d(t, std::false_type{}); };
+  auto with_t = [&](auto t) {
+    if (cache_dtype == TL_E2M1) return with_d(t, std::integral_constant<int, 4>{});
+    return cache_dtype == TL_E4M3 ? with_d(t, std::integral_constant<int, 8>{}) : with_d(t, std::integral_constant<int, 16>{});
+  };
   return dtype == TL_BF16 ? with_t(__nv_bfloat16{}) : with_t(__half{});
 }
 
@@ -866,11 +1150,44 @@ extern "C" int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype,
   p.rows = static_cast<uint32_t>(tokens) * cache->kv_heads;
   p.by_heads = fast_div(cache->kv_heads);
   p.by_page = fast_div(cache->page_size);
-  const long long per_cta = 256 / (cache->d / 8);
-  const long long ctas = (p.rows + per_cta - 1) / per_cta;
-  return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
-    append_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value>
-        <<<static_cast<unsigned>(ctas), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const long long per_cta = 256 / (cache->d / (cache->dtype == TL_E2M1 ? 16 : 8));
+  const unsigned ctas = static_cast<unsigned>((p.rows + per_cta - 1) / per_cta);
+  return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto bits, auto d) {
+    constexpr int kBits = decltype(bits)::value, kD = decltype(d)::value;
+    if constexpr (kBits == 4) append4_kernel<decltype(t), kD><<<ctas, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    else append_kernel<decltype(t), kBits == 8, kD><<<ctas, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launched();
+  });
+}
+
+extern "C" int tl_kv_gather(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const int* slots, int tokens, void* k,
+                            void* v, long long k_token_stride, long long k_head_stride, long long v_token_stride,
+                            long long v_head_stride, tl_stream_t stream) {
+  if (!ctx || !cache_ok(cache, dtype) || tokens < 0) return TL_ERR_INVALID;
+  if (!esize_ok(k_token_stride, 2) || !esize_ok(k_head_stride, 2) || !esize_ok(v_token_stride, 2) ||
+      !esize_ok(v_head_stride, 2))
+    return TL_ERR_INVALID;
+  if (tokens == 0 || cache->kv_heads == 0) return TL_OK;
+  if (static_cast<long long>(tokens) * cache->kv_heads >= (1LL << 30)) return TL_ERR_INVALID;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return TL_ERR_INVALID;
+  if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
+  GatherParams p;
+  p.c = cache_args(cache);
+  p.status = ctx->status;
+  p.k = static_cast<uint8_t*>(k);
+  p.v = static_cast<uint8_t*>(v);
+  p.k_token = 2 * k_token_stride;
+  p.k_head = 2 * k_head_stride;
+  p.v_token = 2 * v_token_stride;
+  p.v_head = 2 * v_head_stride;
+  p.slots = slots;
+  p.rows = static_cast<uint32_t>(tokens) * cache->kv_heads;
+  p.by_heads = fast_div(cache->kv_heads);
+  p.by_page = fast_div(cache->page_size);
+  const long long per_cta = 256 / (cache->d / (cache->dtype == TL_E2M1 ? 16 : 8));
+  const unsigned ctas = static_cast<unsigned>((p.rows + per_cta - 1) / per_cta);
+  return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto bits, auto d) {
+    gather_kernel<decltype(t), decltype(bits)::value, decltype(d)::value><<<ctas, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return launched();
   });
 }
@@ -933,16 +1250,16 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
   // kv heads read together: side by side, as many as make 256 bytes of a token
-  const int es = cache->dtype == TL_E4M3 ? 1 : 2;
+  const int bits = cache->dtype == TL_E2M1 ? 4 : cache->dtype == TL_E4M3 ? 8 : 16, row_bytes = cache->d * bits / 8;
   p.lw = 0;
-  if (p.group <= 8 && cache->head_stride == cache->d)
-    while (p.lw < 2 && ((cache->d * es) << p.lw) < 256 && cache->kv_heads % (2 << p.lw) == 0) ++p.lw;
+  if (p.group <= 8 && p.c.head_stride == row_bytes)
+    while (p.lw < 2 && (row_bytes << p.lw) < 256 && cache->kv_heads % (2 << p.lw) == 0) ++p.lw;
   const long long most = batch * static_cast<long long>(cache->kv_heads >> p.lw) * p.blocks * (cap / (paged::kTile >> p.lw) + 1);
   if (most >= (1LL << 31)) return TL_ERR_INVALID;
-  return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto fp8, auto d) {
+  return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto bits, auto d) {
     auto launch = [&](auto nb) {
-      using S = paged::Shape<decltype(fp8)::value, decltype(d)::value, decltype(nb)::value>;
-      auto kern = paged_kernel<decltype(t), decltype(fp8)::value, decltype(d)::value, decltype(nb)::value>;
+      using S = paged::Shape<decltype(bits)::value, decltype(d)::value, decltype(nb)::value>;
+      auto kern = paged_kernel<decltype(t), decltype(bits)::value, decltype(d)::value, decltype(nb)::value>;
       static std::atomic<unsigned long long> ready{0};  // devices on which the kernel may use its shared memory
       if (!smem_ready(ready, ctx->device, reinterpret_cast<const void*>(kern), S::kSmem)) return static_cast<int>(TL_ERR_CUDA);
       long long grid = static_cast<long long>(S::kCtas) * ctx->ctas;

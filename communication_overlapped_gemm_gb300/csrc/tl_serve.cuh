@@ -96,6 +96,25 @@ constexpr int kTokenCounters = 128 * 256;  // MoE: by token and block of 256 of 
 constexpr size_t kCounterBytes = (kCutCounters + kItemCounters + kTokenCounters) * 4;
 static_assert(kCounterBytes == TL_SERVE_COUNTER_BYTES, "header");
 
+// n / d for n < 2^31 as (umulhi(n, mul) + n) >> shift, exact.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
+inline FastDiv fast_div(int d) {
+  FastDiv f;
+  f.shift = 0;
+  while ((1ull << f.shift) < static_cast<unsigned long long>(d)) ++f.shift;
+  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+
+inline int launched() {
+  if (cudaGetLastError() != cudaSuccess) return TL_ERR_CUDA;
+  return TL_OK;
+}
+
 inline bool esize_ok(long long stride, int esize) { return stride >= 0 && (stride * esize) % 16 == 0; }
 
 inline bool heads_ok(int heads, int kv_heads, int d) {

@@ -1,0 +1,495 @@
+// What a serving step needs before its attention: the plan of its tokens in a paged cache, and the norms and the
+// rotation of its queries and keys.
+#include "tl_serve.cuh"
+
+namespace tl {
+
+// ---------------------------------------------------------------------------- plan
+// Sequence b holds n_b rows and gets c_b more: it needs ceil((n_b + c_b) / page) pages and has ceil(n_b / page), so
+// its new pages are free_pages[taken + sum of the needs before it ..].  Every CTA takes both prefix sums over
+// the batch for itself (4096 sequences at most), so one launch does without a hand-over between CTAs; then each
+// packed token finds its sequence by bisection of the bounds in shared memory, and the token that opens a page
+// writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
+// a write.  Lengths (and `taken`) that are brought up to date in place may only be written once every CTA has read
+// them: then the grid is one cluster, and a cluster barrier lies between.
+struct PlanParams {
+  DevStatus* status;
+  const int* lengths;
+  const int* counts;  // null: 1 each
+  int* table;
+  const int* free_pages;
+  const int* taken;
+  int* taken_out;
+  int* new_lengths;
+  int* cu_q;
+  int* cu_k;       // may be null
+  int* slots;
+  int* positions;  // may be null
+  int* kv_slots;   // may be null
+  int batch, max_pages, num_free, page_size, tokens, kv_tokens;
+  FastDiv by_page;
+};
+
+namespace plan {
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxBatch = 4096, kChunk = kMaxBatch / kThreads;
+constexpr uint32_t kMost = 0x7fffffffu;
+// Sums stop at 2^31 - 1 (in any order): whatever lies there is past every buffer.
+__device__ __forceinline__ uint32_t sat(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+// The sum over all threads before this one, and the sum over all.
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* warps, uint32_t& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t s = v;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, s, x);
+    if (lane >= x) s = sat(s, o);
+  }
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  const uint32_t mine = lane < kWarps ? warps[lane] : 0u;
+  uint32_t t = mine;
+#pragma unroll
+  for (int x = 1; x < kWarps; x <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, t, x);
+    if (lane >= x) t = sat(t, o);
+  }
+  all = __shfl_sync(0xffffffffu, t, kWarps - 1);
+  const uint32_t before = __shfl_sync(0xffffffffu, t, warp ? warp - 1 : 0);
+  const uint32_t up = __shfl_up_sync(0xffffffffu, s, 1);
+  return sat(warp ? before : 0u, lane ? up : 0u);
+}
+// The last b with bounds[b] <= i, for bounds[0] = 0 (so it holds i if any does).
+__device__ __forceinline__ int find(const int* bounds, int n, int i) {
+  int lo = 0, hi = n;  // bounds[lo] <= i < bounds[hi] (or past the end)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (bounds[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+}  // namespace plan
+
+template <bool InPlace>
+__global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p) {
+  using namespace plan;
+  extern __shared__ int smem[];
+  __shared__ uint32_t s_warps[4][kWarps];
+  int* const s_q = smem;                       // [batch + 1] first new token of a sequence
+  int* const s_k = s_q + p.batch + 1;          // [batch + 1] its first row among all
+  int* const s_len = s_k + p.batch + 1;        // [batch] rows held; ~rows if it gets none of its new ones
+  int* const s_first = s_len + p.batch;        // [batch] place of its first new page in the free list
+  const int chunk = (p.batch + kThreads - 1) / kThreads, b0 = static_cast<int>(threadIdx.x) * chunk;
+  const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
+  const bool report = blockIdx.x == 0;
+
+  const int taken = *p.taken;
+  const bool taken_ok = taken >= 0 && taken <= p.num_free;
+  const uint32_t left = taken_ok ? static_cast<uint32_t>(p.num_free - taken) : 0u;
+  int raw[kChunk], len[kChunk], cnt[kChunk];
+  uint32_t need[kChunk], sum_q = 0, sum_p = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    const int b = b0 + i;
+    raw[i] = len[i] = cnt[i] = 0;
+    need[i] = 0;
+    if (i >= chunk || b >= p.batch) continue;
+    raw[i] = len[i] = p.lengths[b];
+    cnt[i] = p.counts ? p.counts[b] : 1;
+    if (len[i] < 0 || cnt[i] < 0 || static_cast<long long>(len[i]) + cnt[i] > cap) {
+      if (report) report_index(p.status, static_cast<unsigned long long>(b));
+      if (len[i] < 0 || len[i] > cap) len[i] = 0;
+      cnt[i] = 0;
+    }
+    need[i] = divide(len[i] + cnt[i] + p.page_size - 1, p.by_page) - divide(len[i] + p.page_size - 1, p.by_page);
+    sum_q = sat(sum_q, cnt[i]);
+    sum_p = sat(sum_p, need[i]);
+  }
+  uint32_t all_q, all_p, all_k;
+  uint32_t at_q = scan(sum_q, s_warps[0], all_q), at_p = scan(sum_p, s_warps[1], all_p);
+  // A sequence gets its tokens if they and its pages are there: those that do not fit are the last ones.
+  uint32_t sum_k = 0, used = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    const int b = b0 + i;
+    if (i >= chunk || b >= p.batch) continue;
+    s_q[b] = static_cast<int>(at_q);
+    s_first[b] = static_cast<int>(taken + at_p);
+    at_q = sat(at_q, cnt[i]);
+    at_p = sat(at_p, need[i]);
+    const bool fits = at_q <= static_cast<uint32_t>(p.tokens) && (need[i] == 0 || at_p <= left);
+    if (!fits && cnt[i] > 0) {
+      if (report) report_index(p.status, static_cast<unsigned long long>(b));
+      cnt[i] = -1;
+    } else if (need[i] > 0) {
+      used = at_p;
+    }
+    s_len[b] = cnt[i] < 0 ? ~len[i] : len[i];
+    sum_k = sat(sum_k, len[i] + max(cnt[i], 0));
+  }
+  uint32_t at_k = scan(sum_k, s_warps[2], all_k);
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    const int b = b0 + i;
+    if (i >= chunk || b >= p.batch) continue;
+    s_k[b] = static_cast<int>(at_k);
+    at_k = sat(at_k, len[i] + max(cnt[i], 0));
+  }
+  if (threadIdx.x == 0) {
+    s_q[p.batch] = static_cast<int>(all_q);
+    s_k[p.batch] = static_cast<int>(all_k);
+  }
+  // the most pages that a sequence which gets its tokens ends at
+  {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, used);
+    if ((threadIdx.x & 31) == 0) s_warps[3][threadIdx.x >> 5] = top;
+  }
+  if constexpr (InPlace) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const int b = b0 + i;
+      if (i >= chunk || b >= p.batch) continue;
+      p.new_lengths[b] = cnt[i] > 0 ? len[i] + cnt[i] : raw[i];
+      p.cu_q[b] = s_q[b];
+      if (p.cu_k) p.cu_k[b] = s_k[b];
+    }
+    if (threadIdx.x == 0) {
+      uint32_t top = 0;
+      for (int w = 0; w < kWarps; ++w) top = max(top, s_warps[3][w]);
+      p.cu_q[p.batch] = s_q[p.batch];
+      if (p.cu_k) p.cu_k[p.batch] = s_k[p.batch];
+      *p.taken_out = taken + static_cast<int>(top);
+      if (!taken_ok || (p.kv_slots && s_k[p.batch] > p.kv_tokens)) report_index(p.status, static_cast<unsigned long long>(p.batch));
+    }
+  }
+
+  // The slot of row `pos` of sequence b: its page is in the table, or a new one.  -1 where there is none.
+  auto slot_of = [&](int b, int pos, int held, int& page_at, int& page) {
+    page_at = static_cast<int>(divide(static_cast<uint32_t>(pos), p.by_page));
+    const int has = static_cast<int>(divide(static_cast<uint32_t>(held + p.page_size - 1), p.by_page));
+    page = page_at < has ? p.table[static_cast<long long>(b) * p.max_pages + page_at] : __ldg(p.free_pages + s_first[b] + page_at - has);
+    const long long slot = static_cast<long long>(page) * p.page_size + (pos - page_at * p.page_size);
+    if (page < 0 || slot > static_cast<long long>(kMost)) {
+      report_index(p.status, static_cast<unsigned long long>(b));
+      return -1;
+    }
+    return static_cast<int>(slot);
+  };
+  const int step = static_cast<int>(gridDim.x) * kThreads, start = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+  const int total_q = s_q[p.batch], total_k = s_k[p.batch];
+  for (long long i = start; i < p.tokens; i += step) {
+    const int t = static_cast<int>(i);
+    int slot = -1, pos = 0;
+    if (t < total_q) {
+      const int b = find(s_q, p.batch, t), held = s_len[b];
+      pos = (held < 0 ? ~held : held) + t - s_q[b];
+      if (held >= 0) {
+        int page_at, page;
+        slot = slot_of(b, pos, held, page_at, page);
+        // its first row opens a page
+        if (pos == page_at * p.page_size) p.table[static_cast<long long>(b) * p.max_pages + page_at] = page;
+      }
+    }
+    p.slots[t] = slot;
+    if (p.positions) p.positions[t] = pos;
+  }
+  if (p.kv_slots)
+    for (long long i = start; i < p.kv_tokens; i += step) {
+      const int t = static_cast<int>(i);
+      int slot = -1;
+      if (t < total_k) {
+        const int b = find(s_k, p.batch, t), held = s_len[b];
+        int page_at, page;
+        slot = slot_of(b, t - s_k[b], held < 0 ? ~held : held, page_at, page);
+      }
+      p.kv_slots[t] = slot;
+    }
+}
+
+// ---------------------------------------------------------------------------- norms and rotation
+// A row x of d values (one head of one token) becomes
+//   y = x / sqrt(mean x^2 + eps) * w,   (y_i, y_j) -> (y_i cos a - y_j sin a, y_i sin a + y_j cos a)
+// for its r / 2 pairs, with the angle a = position * inv_freq of the pair.
+// HBM bounds it: each value is read and written once for some 6 operations.  D / 16 threads hold a row, 16 values
+// each: two vectors of 8 whose places are those of eight pairs, so that neither the rotation nor the store needs another
+// thread, and the mean takes 3 (d 64: 2) exchanges.  A thread has the same pairs in all rows of a token, which
+// share their angles.
+//
+// Angles: a position may be far and a frequency any number, and fp32 would leave a turn of 2^20 with 4 bits
+// behind the point.  So a frequency is held in turns as a 64-bit fraction, F = inv_freq / (2 pi) 2^64, whose product with
+// the position modulo 2^64 is the angle's fraction of a turn, off by at most position 2^-63 turns and exact in all the
+// turns before it.  sin and cos of the rest, within [-pi, pi], are off by 2^-21 at most (__sincosf), far below
+// half a step of the 16-bit result.
+struct RopeParams {
+  const uint8_t* x[2];  // q, k
+  uint8_t* y[2];
+  const void* weight[2];  // [D] of T or fp32; null: no norm
+  long long x_token[2], x_head[2], y_token[2], y_head[2];  // bytes
+  int heads[2];
+  const int* positions;
+  const float* inv_freq;  // [rotary / 2]
+  int tokens, rotary, weight_f32;
+  float eps;
+};
+
+namespace rope {
+constexpr int kThreads = 128;
+// inv_freq / (2 pi) in units of 2^-64 turns, modulo one turn.
+__device__ __forceinline__ unsigned long long turns(float f) {
+  constexpr unsigned long long kInv2Pi = 2935890503282001226ull;  // 2^64 / (2 pi), rounded
+  const uint32_t bits = __float_as_uint(f), e = (bits >> 23) & 0xffu;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int s = 150 - static_cast<int>(e ? e : 1);  // f = m 2^-s
+  unsigned long long v;
+  if (s > 64) v = s < 128 ? hi >> (s - 64) : 0;
+  else if (s == 64) v = hi;
+  else if (s > 0) v = (lo >> s) | (hi << (64 - s));
+  else v = -s < 64 ? lo << -s : 0;
+  return bits >> 31 ? 0 - v : v;
+}
+__device__ __forceinline__ float2 unit(unsigned long long turn, int position) {
+  const long long a = static_cast<long long>(turn * static_cast<unsigned long long>(static_cast<long long>(position)));
+  float2 cs;
+  __sincosf(static_cast<float>(static_cast<int>(a >> 32)) * 1.4629180792671596e-9f, &cs.y, &cs.x);  // 2 pi 2^-32
+  return cs;
+}
+}  // namespace rope
+
+template <class T, int D, bool Interleaved>
+__global__ void __launch_bounds__(rope::kThreads) rope_kernel(const RopeParams p) {
+  using namespace rope;
+  constexpr int kPer = D / 16, kRows = kThreads / kPer;  // threads of a row, rows at a time
+  __shared__ __align__(16) float s_weight[2][D];
+  const int j = threadIdx.x % kPer;
+  // the vectors (of 8 values) of this thread: a pair's two places lie in them both, or side by side
+  const int half = Interleaved ? p.rotary / 8 : p.rotary / 16;  // threads (of vectors: of pairs of them) that rotate
+  int va, vb;
+  bool turn_a, turn_b;
+  if constexpr (Interleaved) {
+    va = 2 * j;
+    vb = 2 * j + 1;
+    turn_a = va < half;
+    turn_b = vb < half;
+  } else {
+    turn_a = turn_b = j < half;
+    va = j < half ? j : 2 * j;
+    vb = j < half ? j + half : 2 * j + 1;
+  }
+  if (p.weight[0] || p.weight[1]) {
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+      const void* w = p.weight[i / D];
+      if (w) s_weight[i / D][i % D] = p.weight_f32 ? static_cast<const float*>(w)[i % D]
+                                                   : static_cast<float>(static_cast<const T*>(w)[i % D]);
+    }
+    __syncthreads();
+  }
+  unsigned long long f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // the frequency of pair i: place 8 va + i with its partner, or of places 2i, 2i + 1 of both vectors
+    if constexpr (Interleaved) f[i] = (i < 4 ? turn_a : turn_b) ? turns(__ldg(p.inv_freq + 8 * j + i)) : 0ull;
+    else f[i] = turn_a ? turns(__ldg(p.inv_freq + 8 * j + i)) : 0ull;
+  }
+  const int rows = p.heads[0] + p.heads[1];
+  const int lane_group = (threadIdx.x % 32) / kPer * kPer;
+  const uint32_t group_mask = ((1u << kPer) - 1u) << lane_group;
+  for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    float2 cs[8];
+    const int pos = p.rotary ? __ldg(p.positions + t) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = unit(f[i], pos);
+    for (int r = blockIdx.y * kRows + threadIdx.x / kPer; r < rows; r += gridDim.y * kRows) {
+      const int w = r >= p.heads[0], h = w ? r - p.heads[0] : r;
+      const uint4* src = reinterpret_cast<const uint4*>(p.x[w] + t * p.x_token[w] + h * p.x_head[w]);
+      const uint4 a4 = src[va], b4 = src[vb];
+      const uint32_t au[4] = {a4.x, a4.y, a4.z, a4.w}, bu[4] = {b4.x, b4.y, b4.z, b4.w};
+      float a[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = to_f32x2<T>(au[i]), y = to_f32x2<T>(bu[i]);
+        a[2 * i] = x.x;
+        a[2 * i + 1] = x.y;
+        b[2 * i] = y.x;
+        b[2 * i + 1] = y.y;
+      }
+      if (p.weight[w]) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+        for (int x = 1; x < kPer; x <<= 1) ss += __shfl_xor_sync(group_mask, ss, x);
+        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+        const float4* wa = reinterpret_cast<const float4*>(s_weight[w] + 8 * va);
+        const float4* wb = reinterpret_cast<const float4*>(s_weight[w] + 8 * vb);
+        const float4 w0 = wa[0], w1 = wa[1], w2 = wb[0], w3 = wb[1];
+        const float u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const float v[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = a[i] * inv * u[i];
+          b[i] = b[i] * inv * v[i];
+        }
+      }
+      if constexpr (Interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (turn_a) {
+            const float x = a[2 * i], y = a[2 * i + 1];
+            a[2 * i] = x * cs[i].x - y * cs[i].y;
+            a[2 * i + 1] = x * cs[i].y + y * cs[i].x;
+          }
+          if (turn_b) {
+            const float x = b[2 * i], y = b[2 * i + 1];
+            b[2 * i] = x * cs[4 + i].x - y * cs[4 + i].y;
+            b[2 * i + 1] = x * cs[4 + i].y + y * cs[4 + i].x;
+          }
+        }
+      } else if (turn_a) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = a[i], y = b[i];
+          a[i] = x * cs[i].x - y * cs[i].y;
+          b[i] = x * cs[i].y + y * cs[i].x;
+        }
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.y[w] + t * p.y_token[w] + h * p.y_head[w]);
+      dst[va] = make_uint4(from_f32x2<T>(a[0], a[1]), from_f32x2<T>(a[2], a[3]), from_f32x2<T>(a[4], a[5]), from_f32x2<T>(a[6], a[7]));
+      dst[vb] = make_uint4(from_f32x2<T>(b[0], b[1]), from_f32x2<T>(b[2], b[3]), from_f32x2<T>(b[4], b[5]), from_f32x2<T>(b[6], b[7]));
+    }
+  }
+}
+
+template <class T, int D>
+static void rope_launch(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_t stream) {
+  if (interleaved) rope_kernel<T, D, true><<<grid, rope::kThreads, 0, stream>>>(p);
+  else rope_kernel<T, D, false><<<grid, rope::kThreads, 0, stream>>>(p);
+}
+
+}  // namespace tl
+
+using namespace tl;
+
+extern "C" int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts, int batch, int page_size, int* page_table,
+                             int max_pages, const int* free_pages, int num_free, const int* taken, int* taken_out,
+                             int* new_lengths, int* cu_q, int* cu_k, int* slots, int* positions, int tokens, int* kv_slots,
+                             int kv_tokens, tl_stream_t stream) {
+  if (!ctx || batch < 0 || batch > plan::kMaxBatch || page_size < 1 || max_pages < 0 || num_free < 0 || tokens < 0 ||
+      kv_tokens < 0)
+    return TL_ERR_INVALID;
+  if (static_cast<long long>(max_pages) * page_size >= (1LL << 31) - page_size) return TL_ERR_INVALID;
+  if (!taken || !taken_out || !cu_q || (batch > 0 && (!lengths || !new_lengths)) || (tokens > 0 && !slots) ||
+      (batch > 0 && max_pages > 0 && !page_table) || (num_free > 0 && !free_pages) || (kv_tokens > 0 && !kv_slots))
+    return TL_ERR_INVALID;
+  if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
+  PlanParams p;
+  p.status = ctx->status;
+  p.lengths = lengths;
+  p.counts = counts;
+  p.table = page_table;
+  p.free_pages = free_pages;
+  p.taken = taken;
+  p.taken_out = taken_out;
+  p.new_lengths = new_lengths;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.slots = slots;
+  p.positions = positions;
+  p.kv_slots = kv_slots;
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.num_free = num_free;
+  p.page_size = page_size;
+  p.tokens = tokens;
+  p.kv_tokens = kv_tokens;
+  p.by_page = fast_div(page_size);
+  const int smem = (4 * batch + 2) * 4;
+  const long long items = static_cast<long long>(tokens) + kv_tokens;
+  long long ctas = (items + 2 * plan::kThreads - 1) / (2 * plan::kThreads);
+  const bool in_place = lengths == new_lengths || taken == taken_out;
+  const long long most = in_place ? 8 : ctx->sms;
+  if (ctas > most) ctas = most;
+  if (ctas < 1) ctas = 1;
+  const void* kern = in_place ? reinterpret_cast<const void*>(plan_kernel<true>) : reinterpret_cast<const void*>(plan_kernel<false>);
+  static std::atomic<unsigned long long> ready[2];
+  if (!smem_ready(ready[in_place], ctx->device, kern, (4 * plan::kMaxBatch + 2) * 4)) return TL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(plan::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = in_place ? 1 : 0;
+  const cudaError_t e = in_place ? cudaLaunchKernelEx(&cfg, plan_kernel<true>, p) : cudaLaunchKernelEx(&cfg, plan_kernel<false>, p);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return TL_ERR_CUDA;
+  }
+  return TL_OK;
+}
+
+extern "C" int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride,
+                            const void* k, long long k_token_stride, long long k_head_stride, const void* q_weight,
+                            const void* k_weight, int weight_dtype, float eps, const int* positions, const float* inv_freq,
+                            int rotary, int interleaved, void* q_out, long long q_out_token_stride,
+                            long long q_out_head_stride, void* k_out, long long k_out_token_stride,
+                            long long k_out_head_stride, int tokens, int heads, int kv_heads, int d, tl_stream_t stream) {
+  if (!ctx || (dtype != TL_BF16 && dtype != TL_FP16) || (weight_dtype != dtype && weight_dtype != TL_FP32) || tokens < 0 ||
+      heads < 0 || kv_heads < 0 || (d != 64 && d != 128) || rotary < 0 || rotary > d || rotary % 16 != 0 ||
+      (interleaved != 0 && interleaved != 1) || !(eps >= 0.f) || eps > 3.0e38f)
+    return TL_ERR_INVALID;
+  const long long strides[8] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride, q_out_token_stride,
+                                q_out_head_stride, k_out_token_stride, k_out_head_stride};
+  for (long long s : strides)
+    if (!esize_ok(s, 2)) return TL_ERR_INVALID;
+  if (tokens == 0 || heads + static_cast<long long>(kv_heads) == 0) return TL_OK;
+  if (heads + static_cast<long long>(kv_heads) > 65536) return TL_ERR_INVALID;
+  if ((heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) ||
+      (kv_heads > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out))) || (rotary > 0 && (!positions || !inv_freq)))
+    return TL_ERR_INVALID;
+  if (cudaSetDevice(ctx->device) != cudaSuccess) return TL_ERR_CUDA;
+  RopeParams p;
+  p.x[0] = static_cast<const uint8_t*>(q);
+  p.x[1] = static_cast<const uint8_t*>(k);
+  p.y[0] = static_cast<uint8_t*>(q_out);
+  p.y[1] = static_cast<uint8_t*>(k_out);
+  p.weight[0] = heads > 0 ? q_weight : nullptr;
+  p.weight[1] = kv_heads > 0 ? k_weight : nullptr;
+  for (int w = 0; w < 2; ++w) {
+    p.x_token[w] = 2 * strides[2 * w];
+    p.x_head[w] = 2 * strides[2 * w + 1];
+    p.y_token[w] = 2 * strides[4 + 2 * w];
+    p.y_head[w] = 2 * strides[5 + 2 * w];
+  }
+  p.heads[0] = heads;
+  p.heads[1] = kv_heads;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.tokens = tokens;
+  p.rotary = rotary;
+  p.weight_f32 = weight_dtype == TL_FP32;
+  p.eps = eps;
+  const int rows_at_once = rope::kThreads / (d / 16);
+  const int parts = (heads + kv_heads + rows_at_once - 1) / rows_at_once;
+  // A CTA takes all rows of a token, so that its angles are worked out once, unless there are fewer tokens than places.
+  const long long places = 8LL * ctx->sms;
+  dim3 grid(static_cast<unsigned>(tokens < places ? tokens : places), 1, 1);
+  if (tokens < places) grid.y = static_cast<unsigned>(tokens * static_cast<long long>(parts) <= places ? parts : 1);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == TL_BF16) {
+    if (d == 64) rope_launch<__nv_bfloat16, 64>(p, interleaved, grid, s);
+    else rope_launch<__nv_bfloat16, 128>(p, interleaved, grid, s);
+  } else {
+    if (d == 64) rope_launch<__half, 64>(p, interleaved, grid, s);
+    else rope_launch<__half, 128>(p, interleaved, grid, s);
+  }
+  return launched();
+}

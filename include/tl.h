@@ -3,7 +3,8 @@
  *
  * The library computes, on ONE GPU, the four overlapped operators of the pages it is
  * built from, with the W tensor-parallel ranks emulated as W separate HBM buffers (and, further down,
- * the operators of a decoder's serving step: cache append, paged and window attention, MoE for few tokens):
+ * the operators of a decoder's serving step: its plan, norms and rotation, cache append and gather, paged and
+ * window attention, MoE for few tokens, log probabilities):
  *
  *   tl_ag_gemm      AllGather + GEMM:        C = [A_0; A_1; ...; A_{W-1}] . B
  *   tl_gemm_rs      GEMM + ReduceScatter:    out_o = rows_o( sum_p A_p . B_p )
@@ -403,59 +404,136 @@ int tl_ag_gemm_static_scratch(tl_ctx* ctx, int W, int rank, const void* const* a
                               int m_per_rank, int n, int k, tl_stream_t stream);
 
 /* ---------------------------------------------------------------- serving: types and the paged cache
- * The operators of a decoder's serving step: the cache append, the attention of one new token
- * over the cache, the causal attention of prompts, and the MoE layer for a few tokens.  The
- * pages have no counterpart of these four entry points.  They are the single-GPU steps that
+ * The operators of a decoder's serving step: the plan of its tokens in the cache, the norms and the rotation of
+ * queries and keys, the cache append and gather, the attention of one new token over the cache, the causal
+ * attention of prompts, the MoE layer for a few tokens, and the log probabilities of the chosen ones.  The
+ * pages have no counterpart of these entry points.  They are the single-GPU steps that
  * run between the overlapped operators when a model answers, on the same buffers and streams.
  *
  * Types: bf16 or fp16 activations; a cache holds the activations' type, or e4m3 (8-bit float, 4
  * exponent and 3 mantissa bits, no infinity) with one fp32 scale per kv head: the value that a
- * stored byte b stands for is scale * b.
+ * stored byte b stands for is scale * b; or 4 bits (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign, two values a
+ * byte, the lower half first) with an e4m3 scale for every block of 16 values of a row beside the head's: the value
+ * that a code c stands for is c * block scale * scale.
  * Rows: the innermost dimension (d) is contiguous; every other stride is the caller's, in
- * elements, a multiple of 16 bytes.  So a view of a fused projection's output, or a cache that is
+ * elements (of a 4-bit cache in bytes), a multiple of 16 bytes.  So a view of a fused projection's output, or a cache that is
  * token-major [pages][page_size][kv_heads][d] or head-major [pages][kv_heads][page_size][d], is
  * passed as it is.
- * Indices read on the device (slots, page numbers, lengths) are checked there: an entry out of
+ * Indices read on the device (slots, page numbers, lengths, tokens) are checked there: an entry out of
  * range is left out, nothing outside the buffers is read or written, and tl_ctx_check returns
- * TL_ERR_INDEX.  All four can be captured into a graph and replayed.
+ * TL_ERR_INDEX.  All of them can be captured into a graph and replayed.
  * Workspaces: the first TL_SERVE_COUNTER_BYTES hold counters that each call leaves at zero again.  So one
- * workspace, zero-filled once, serves calls of tl_paged_attention and tl_moe_tokens of any shapes, in
+ * workspace, zero-filled once, serves calls of tl_paged_attention, tl_moe_tokens and tl_token_logprobs of any shapes, in
  * order; after another operator used it, those bytes have to be zero-filled again.
  */
 #define TL_SERVE_COUNTER_BYTES 139264
 #define TL_BF16 0
 #define TL_FP16 1
 #define TL_E4M3 2
+#define TL_FP32 3
+#define TL_E2M1 4
 
 typedef struct tl_paged_cache {
   void* k;                /* the K rows of all pages                                            */
   void* v;                /* the V rows; the same strides as k                                  */
-  const float* k_scale;   /* e4m3: fp32 [kv_heads] (NULL: all 1); otherwise NULL                 */
+  const float* k_scale;   /* e4m3, e2m1: fp32 [kv_heads] (NULL: all 1); otherwise NULL           */
   const float* v_scale;
-  long long page_stride;  /* elements from a page to the next                                   */
+  long long page_stride;  /* elements (e2m1: bytes) from a page to the next                     */
   long long row_stride;   /* elements from a row (token) of a page to the next                  */
   long long head_stride;  /* elements from a kv head to the next                                */
-  int dtype;              /* TL_BF16, TL_FP16 or TL_E4M3                                         */
+  int dtype;              /* TL_BF16, TL_FP16, TL_E4M3 or TL_E2M1                                */
   int num_pages;
   int page_size;          /* rows in a page, any number >= 1                                    */
   int kv_heads;
   int d;                  /* head dim: 64 or 128                                                */
+  /* only read where dtype is TL_E2M1: the e4m3 block scales, d / 16 bytes a row, with strides of their own
+     (bytes, multiples of d / 16); both 16-byte aligned */
+  void* k_blocks;
+  void* v_blocks;
+  long long block_page_stride;
+  long long block_row_stride;
+  long long block_head_stride;
 } tl_paged_cache;
+
+/* ---------------------------------------------------------------- plan of a step's tokens in the cache
+ * Sequence b holds lengths[b] rows and gets counts[b] new ones (counts NULL: one each).  Its rows lie in pages
+ * page_table[b][0 ..]; pages that it still needs are taken from free_pages, from entry *taken on, in the order of
+ * the sequences.  The call writes
+ *   page_table[b][i]  the new pages' entries (the others are left as they are),
+ *   cu_q              int32 [batch + 1]: bounds of the packed new tokens (the first at 0),
+ *   slots, positions  int32 [tokens]: of each packed new token its slot, page * page_size + row, as tl_kv_append takes it,
+ *                     and its position in its sequence; from cu_q[batch] on (padding) -1 and 0,
+ *   new_lengths       int32 [batch]: lengths with the new rows, as tl_paged_attention takes them,
+ *   *taken_out        the entries of free_pages taken so far,
+ *   cu_k              int32 [batch + 1] (may be NULL): bounds of the packed rows, old and new,
+ *   kv_slots          int32 [kv_tokens] (may be NULL): the slot of every row, as tl_kv_gather takes it; -1 from cu_k[batch] on.
+ * new_lengths may be lengths, and taken_out may be taken: a captured step then goes on by itself with each replay.
+ * The other outputs must not overlap the inputs (page_table is both).
+ * Reported (tl_ctx_check: TL_ERR_INDEX), with nothing written outside the buffers: a negative length or count, or more
+ * rows than max_pages * page_size (the sequence counts as one without new tokens, of no rows if its length is
+ * wrong); tokens beyond `tokens`, or pages beyond num_free (the sequence gets none of its new rows: its tokens have slot
+ * -1, its length stays); rows beyond kv_tokens (their slots are left out); a page that is negative (slot -1); a
+ * *taken outside 0..num_free (nothing can be taken).
+ * Shapes: batch <= 4096; page_size >= 1; (max_pages + 1) * page_size < 2^31.  No workspace.
+ */
+int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts, int batch, int page_size, int* page_table,
+                  int max_pages, const int* free_pages, int num_free, const int* taken, int* taken_out, int* new_lengths,
+                  int* cu_q, int* cu_k, int* slots, int* positions, int tokens, int* kv_slots, int kv_tokens,
+                  tl_stream_t stream);
+
+/* ---------------------------------------------------------------- norms and rotation of queries and keys
+ * Each row x of d values (one head of one token) of q and of k becomes, in one pass,
+ *   y = x / sqrt(mean(x^2) + eps) * weight                              (no weight: y = x)
+ *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_i sin a + y_j cos a),        a = positions[token] * inv_freq[p]
+ * for the pairs p = 0 .. rotary / 2 - 1 of its first `rotary` values: (i, j) = (p, p + rotary / 2), or with
+ * interleaved = 1 (2p, 2p + 1).  The other values are not turned.
+ * q, k and the outputs: dtype (TL_BF16 or TL_FP16) [tokens x heads (kv_heads) x d], strides as given; an output may be
+ * its input (the same pointer and strides), and must not overlap it otherwise.  q_weight, k_weight: [d] of
+ * weight_dtype (dtype or TL_FP32), or NULL: no norm.  positions: int32 [tokens], any value; inv_freq: fp32
+ * [rotary / 2], finite (both may be NULL if rotary is 0).
+ * Precision: all sums and products are fp32, rounded once; a row whose squares pass fp32's range becomes 0.  Angles are held
+ * as fractions of a turn in 64 bits, so that far positions lose nothing (off by 2^-31 turns where |inv_freq| <= 1);
+ * sines and cosines are off by 2^-21 at most.
+ * Shapes: d 64 or 128; rotary a multiple of 16, at most d; eps >= 0; heads + kv_heads <= 65536.  tokens == 0 or no
+ * heads is a no-op.  No workspace.
+ */
+int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride, const void* k,
+                 long long k_token_stride, long long k_head_stride, const void* q_weight, const void* k_weight,
+                 int weight_dtype, float eps, const int* positions, const float* inv_freq, int rotary, int interleaved,
+                 void* q_out, long long q_out_token_stride, long long q_out_head_stride, void* k_out,
+                 long long k_out_token_stride, long long k_out_head_stride, int tokens, int heads, int kv_heads, int d,
+                 tl_stream_t stream);
 
 /* ---------------------------------------------------------------- append to a paged cache
  *   K[slot / page_size][slot % page_size][h] = k[t][h], V likewise, for slot = slots[t]
  *
  * k, v: dtype (TL_BF16 or TL_FP16) [tokens x kv_heads x d] with the strides given.  slots: int32
  * [tokens]; a negative slot skips its token (padding); one >= num_pages * page_size is left out
- * and reported.  Two tokens with the same slot: either may end up there, row by row.
+ * and reported.  Two tokens with the same slot: either may end up there, row by row (in a 4-bit cache block by block, and
+ * a block's codes may be one's and its scale the other's).
  * A cache of the activations' type takes the rows as they are.  An e4m3 cache takes
  * k / k_scale[h], computed in fp32, rounded to nearest even and saturated at +-448 (infinities
- * too; NaN stays NaN).
+ * too; NaN stays NaN).  A 4-bit cache takes, for each block of 16 values x and s = k_scale[h] (finite, > 0), the scale
+ * b = e4m3(max |x| / (6 s)) and the codes e2m1(x / (b s)), each product and quotient in fp32, each conversion to nearest even and
+ * saturating (infinities too); a block with b = 0 is all 0, a NaN makes its whole block NaN.
  * Shapes: d 64 or 128; num_pages * page_size < 2^31; tokens * kv_heads < 2^30.  tokens == 0 or kv_heads == 0 is a no-op.
  */
 int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void* k, const void* v,
                  long long k_token_stride, long long k_head_stride, long long v_token_stride,
                  long long v_head_stride, const int* slots, int tokens, tl_stream_t stream);
+
+/* ---------------------------------------------------------------- rows of a paged cache, packed
+ *   k[t][h] = K[slot / page_size][slot % page_size][h], v likewise, for slot = slots[t]
+ *
+ * The way back: the rows that a later turn's queries need beside the new ones (tl_window_attention takes packed rows; the
+ * slots are tl_cache_plan's kv_slots).  k, v: dtype [tokens x kv_heads x d], strides as given; the values that the cache's
+ * rows stand for, computed in fp32 and rounded once (a cache of dtype: as they are).  A negative slot leaves its
+ * row of k and v as it is; one >= num_pages * page_size too, and is reported.
+ * Shapes as tl_kv_append.
+ */
+int tl_kv_gather(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const int* slots, int tokens, void* k, void* v,
+                 long long k_token_stride, long long k_head_stride, long long v_token_stride, long long v_head_stride,
+                 tl_stream_t stream);
 
 /* ---------------------------------------------------------------- attention of one new token
  * One query row per sequence over that sequence's rows of a paged cache.  n = lengths[b] counts
@@ -468,7 +546,7 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * A sequence with nothing visible (n == 0), or only scores of -inf, has out = 0 and lse = -inf.  Rows that are not visible
  * are not read: whatever they hold has no effect.
  * q, out: dtype (TL_BF16 or TL_FP16) [batch x heads x d] with the strides given (out must not
- * overlap q).  cache: dtype or TL_E4M3.  page_table: int32 [batch x max_pages], dense; only the entries
+ * overlap q).  cache: dtype, TL_E4M3 or TL_E2M1.  page_table: int32 [batch x max_pages], dense; only the entries
  * of visible rows are read.  lengths: int32 [batch]; a length over max_pages * page_size is cut to
  * that and reported, a page out of range is left out (its rows are not visible) and reported.
  * workspace: tl_paged_attention_workspace_bytes(): counters, and partial results of sequences split
@@ -477,7 +555,7 @@ int tl_kv_append(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const void
  * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
  * batch == 0 or heads == 0 is a no-op.
  * Precision: scores, weights and all sums are fp32.  Where a weight meets V it is a sum of two terms of dtype, off by
- * half a step squared; with an e4m3 cache one fp16 term, and in tl_window_attention one term of dtype, off by half
+ * half a step squared; with an e4m3 or 4-bit cache one fp16 term, and in tl_window_attention one term of dtype, off by half
  * a step.  fp16 terms are also off by up to 2^-32 of the largest weight.  The division by the weights' sum comes
  * last, and a weight may be 2^8 until then: sums of bf16 rows within 2^-8 / n of fp32's largest value can overflow.
  * The result does not depend on what else runs, and is bit-identical run to run on one device.
@@ -535,6 +613,26 @@ size_t tl_moe_tokens_workspace_bytes(int T, int H, int E, int F, int topk);
 int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, const void* w_gate, const void* w_up,
                   const void* w_down, float* out, int* experts_out, float* gates_out, void* workspace,
                   size_t workspace_bytes, int T, int H, int E, int F, tl_stream_t stream);
+
+/* ---------------------------------------------------------------- log probabilities of chosen tokens
+ * For each row x of logits, with p = softmax(scale * x):
+ *   logprob[r] = ln p[targets[r]],  entropy[r] = - sum_i p_i ln p_i,  lse[r] = ln sum_i exp(scale * x_i),
+ *   top_logprobs[r][0 .. top), top_ids[r][0 .. top): the most likely tokens' ln p and indices, best first
+ * (equal logits: the lower index first; NaN counts as the lowest).
+ * logits: dtype (TL_BF16, TL_FP16 or TL_FP32) [rows x vocab], a row row_stride elements after the one before (any
+ * number).  targets: int32 [rows]; a negative target skips its row (padding): its outputs are left as they are; one
+ * >= vocab too, and is reported.  targets may be NULL if logprob is: no row is skipped then.  logprob, entropy, lse: fp32
+ * [rows], any may be NULL.  top_logprobs: fp32, top_ids: int32 [rows x top].
+ * A logit of -inf (a masked token) has probability 0.  Where all of a row are -inf, its entropy is 0 and its
+ * lse and all its log probabilities are -inf.  A NaN or +inf among a row's logits makes all its fp32 outputs NaN (ids not).
+ * Precision: maxima, sums and logarithms are fp32.  Results are bit-identical run to run on one device.
+ * workspace: tl_token_logprobs_workspace_bytes(): counters, and parts of rows split over several CTAs.
+ * Shapes: 1 <= vocab <= 2^30; 0 <= top <= 32, top <= vocab; rows <= 2^24; scale finite and > 0.  rows == 0 is a no-op.
+ */
+size_t tl_token_logprobs_workspace_bytes(int rows, int vocab, int top);
+int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, long long row_stride, const int* targets, float* logprob,
+                      float* entropy, float* lse, float* top_logprobs, int* top_ids, int top, float scale, int rows,
+                      int vocab, void* workspace, size_t workspace_bytes, tl_stream_t stream);
 
 /* ---------------------------------------------------------------- host-side tile maps (no GPU)
  * The static tile-centric mappings the kernels use ([TL] §4.1), evaluated on the host by the
