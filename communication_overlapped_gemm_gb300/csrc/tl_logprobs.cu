@@ -1,5 +1,6 @@
 // Log probabilities of chosen tokens, with the entropy of the distribution and its most likely tokens.
 #include "tl_serve.cuh"
+#include "tl_softmax.cuh"
 
 namespace tl {
 
@@ -7,15 +8,18 @@ namespace tl {
 //   z = l (x - m),  S = sum 2^z,  T = sum z 2^z,
 //   lse = c m + ln S,   logprob = c (x_t - m) - ln S,   entropy = ln S - ln 2 T / S.
 // (x - m comes first: l x of a mask's lowest value would be -inf, and a row of nothing else has no maximum then.)
-// Every logit is read once for some ten instructions, so HBM bounds it.  A CTA takes a chunk of a row at a time
-// into registers, 32 values a thread, each thread with its own m, S and T; few rows are cut into parts, which the CTA
-// that finishes a row's last part joins.
+// Every logit is read once for some five instructions, so HBM bounds it.  A CTA streams a row, or a part of one
+// where there are few rows; thread i has the vectors i, i + 256, .. with its own m, S and T.  The parts of a row are
+// joined by the CTA that finishes the last one, in their order.
 //
-// The most likely k <= 32 tokens: an order of 64-bit keys, the value's bits above the complement of its index, has
-// no ties (equal values: the lower index is the larger key).  In a chunk the k-th largest of the 256
-// threads' maxima is a bound that at least k keys reach, and only the k threads with such a maximum can hold one: at
-// most 32 k candidates, whatever the logits are (ties, masked stretches, sorted rows).  A warp sorts 32 keys by
-// exchanges between lanes, and two sorted lists merge into their best 32 in 6 steps.
+// The most likely k <= 32 tokens need nothing in that loop but the maximum that a thread has anyway.  The k-th
+// largest of the 256 threads' maxima is a bound that at least k logits reach, and only the threads (k of them, if no two
+// are equal) whose maximum reaches it can hold one: their vectors are read a second time, from L2, and the logits that
+// reach the bound, k and a few, are sorted.  An order of 64-bit keys, the value's bits above the complement of its index,
+// has no ties (of equal logits the lower index is the larger key).  Logits that are alike in great number
+// (masks, rows of one value) would make too many candidates: then only those above the bound are taken, from a higher bound if these
+// too are many, and the first ones equal to it are looked up from the row's start.
+// A warp sorts 32 keys by exchanges between lanes, and merges two sorted lists into their best 32 in 6 steps.
 struct ScoreParams {
   DevStatus* status;
   const uint8_t* x;
@@ -28,33 +32,38 @@ struct ScoreParams {
   int* top_id;
   float* part;        // [row][split][kPart]
   unsigned* counter;  // [row]
-  int rows, vocab, top, splits, chunks;  // chunks of a row
+  int rows, vocab, top, splits;
   float scale;
 };
 
 namespace score {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kTop = 32;
+constexpr int kCandidates = 512;
 constexpr int kPart = 4 + 2 * kTop;  // floats of a part: m, S, T, then its best keys
 constexpr int kMaxSplitRows = 1024;  // (a counter for each row that is split)
 using Key = unsigned long long;
 
-__device__ __forceinline__ Key key_of(float x, int i) {
-  const uint32_t b = __float_as_uint(x + 0.f);  // (a zero has one sign)
-  const uint32_t o = x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return (static_cast<Key>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
+// Larger values, larger numbers; NaN the lowest; a zero has one sign.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float value_of(Key k) {
-  const uint32_t o = static_cast<uint32_t>(k >> 32);
+__device__ __forceinline__ float value_of(uint32_t o) {
   return o == 0u ? __uint_as_float(0x7fffffffu) : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ Key key_of(float x, int i) {
+  return (static_cast<Key>(order_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
 }
 __device__ __forceinline__ int index_of(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
 
-__device__ __forceinline__ Key exchange(Key k, int j, bool larger) {
-  const Key o = __shfl_xor_sync(0xffffffffu, k, j);
+template <class K>
+__device__ __forceinline__ K exchange(K k, int j, bool larger) {
+  const K o = __shfl_xor_sync(0xffffffffu, k, j);
   return (k > o) == larger ? k : o;
 }
 // The largest first, a key a lane.
-__device__ __forceinline__ Key sort32(Key k) {
+template <class K>
+__device__ __forceinline__ K sort32(K k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 2; n <= 32; n <<= 1)
@@ -63,13 +72,30 @@ __device__ __forceinline__ Key sort32(Key k) {
   return k;
 }
 // The best 32 of two sorted lists, sorted.
-__device__ __forceinline__ Key merge32(Key a, Key b) {
+template <class K>
+__device__ __forceinline__ K merge32(K a, K b) {
   const int lane = threadIdx.x & 31;
-  const Key o = __shfl_xor_sync(0xffffffffu, b, 31);
-  Key k = a > o ? a : o;
+  const K o = __shfl_xor_sync(0xffffffffu, b, 31);
+  K k = a > o ? a : o;
 #pragma unroll
   for (int j = 16; j > 0; j >>= 1) k = exchange(k, j, (lane & j) == 0);
   return k;
+}
+// The best 32 of a sorted list from each warp, in lists[0] (and the first warp's lanes).
+template <class K>
+__device__ __forceinline__ K merge_warps(K list, K (*lists)[kTop]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  lists[warp][lane] = list;
+  __syncthreads();
+#pragma unroll
+  for (int n = kWarps / 2; n > 0; n >>= 1) {
+    if (warp < n) {
+      list = merge32(list, lists[warp + n][lane]);
+      lists[warp][lane] = list;
+    }
+    __syncthreads();
+  }
+  return list;
 }
 
 struct Sums {
@@ -82,47 +108,79 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float l2) {
   const float fa = ex2_approx(da), fb = ex2_approx(db);
   Sums c;
   c.m = m;
-  c.s = a.s * fa + b.s * fb;
+  c.s = __fadd_rn(__fmul_rn(a.s, fa), __fmul_rn(b.s, fb));  // (either way round the same)
   // (a part so far below the other that nothing is left of it)
-  c.t = (fa == 0.f ? 0.f : fa * (a.t + da * a.s)) + (fb == 0.f ? 0.f : fb * (b.t + db * b.s));
+  c.t = __fadd_rn(fa == 0.f ? 0.f : fa * (a.t + da * a.s), fb == 0.f ? 0.f : fb * (b.t + db * b.s));
   return c;
 }
-}  // namespace score
+// The same in all lanes, whatever their order in a pair.
+__device__ __forceinline__ Sums join_warp(Sums a, float l2) {
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) {
+    Sums o;
+    o.m = __shfl_xor_sync(0xffffffffu, a.m, j);
+    o.s = __shfl_xor_sync(0xffffffffu, a.s, j);
+    o.t = __shfl_xor_sync(0xffffffffu, a.t, j);
+    a = join(a, o, l2);
+  }
+  return a;
+}
 
+// A 16-byte vector of logits.
 template <class T>
 struct Logits {
   static constexpr int kVec = 8;
-  __device__ static void unpack(uint4 v, float* x) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = to_f32x2<T>(u[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+  static constexpr uint32_t kNone = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;  // -inf
+  __device__ static float2 pair(const uint4& v, int i) {
+    return to_f32x2<T>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
   }
-  __device__ static float one(const uint8_t* p) { return static_cast<float>(*reinterpret_cast<const T*>(p)); }
 };
 template <>
 struct Logits<float> {
   static constexpr int kVec = 4;
-  __device__ static void unpack(uint4 v, float* x) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+  static constexpr uint32_t kNone = 0xff800000u;
+  __device__ static float2 pair(const uint4& v, int i) {
+    return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y)) : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ static float one(const uint8_t* p) { return *reinterpret_cast<const float*>(p); }
 };
 
+// A row, or a part of it: its logits have the places [off, end), counted from the 16-byte boundary at or before the row.
+template <class T>
+struct Row {
+  static constexpr int kVec = Logits<T>::kVec;
+  const uint8_t* base;
+  int off, end;
+  __device__ float one(int place) const {
+    return static_cast<float>(*reinterpret_cast<const T*>(base + static_cast<long long>(place) * static_cast<int>(sizeof(T))));
+  }
+  // The vector at `place` (a multiple of kVec); -inf where the row is not.
+  __device__ uint4 load(long long place) const {
+    const uint8_t* at = base + place * static_cast<int>(sizeof(T));
+    if (place >= off && place + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(at));
+    uint32_t u[4] = {Logits<T>::kNone, Logits<T>::kNone, Logits<T>::kNone, Logits<T>::kNone};
+    if (place < end) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (place + i >= off && place + i < end) {
+          if constexpr (sizeof(T) == 4) u[i] = *reinterpret_cast<const uint32_t*>(at + 4 * i);
+          else u[i / 2] = __byte_perm(u[i / 2], *reinterpret_cast<const uint16_t*>(at + 2 * i), i & 1 ? 0x5410 : 0x3254);
+        }
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+}  // namespace score
+
 template <class T, int NV>
-__global__ void __launch_bounds__(score::kThreads) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScoreParams p) {
   using namespace score;
-  constexpr int kVec = Logits<T>::kVec, kVals = NV * kVec, kChunk = kThreads * kVals;
+  constexpr int kVec = Logits<T>::kVec;
   __shared__ Key s_list[kWarps][kTop];
-  __shared__ Key s_cand[kTop * kVals];
+  __shared__ uint32_t s_order[kWarps][kTop];
+  __shared__ Key s_cand[kCandidates];
+  __shared__ uint8_t s_flag[kThreads];
   __shared__ Sums s_sums[kWarps];
-  __shared__ int s_count;
+  __shared__ int s_count, s_flags;
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
@@ -136,116 +194,135 @@ __global__ void __launch_bounds__(score::kThreads) score_kernel(const ScoreParam
     }
   }
   const uint8_t* x0 = p.x + row * p.stride;
-  // places are counted from the 16-byte boundary at or before the row
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15u) / static_cast<int>(sizeof(T));
-  const int end = off + p.vocab;
-  const uint8_t* base = x0 - off * static_cast<int>(sizeof(T));
+  Row<T> r;
+  r.off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15u) / static_cast<int>(sizeof(T));
+  r.end = r.off + p.vocab;
+  r.base = x0 - r.off * static_cast<int>(sizeof(T));
+  const int off = r.off;
   const float l2 = p.scale * kLog2E;
-  const int c0 = static_cast<int>(static_cast<long long>(p.chunks) * split / p.splits);
-  const int c1 = static_cast<int>(static_cast<long long>(p.chunks) * (split + 1) / p.splits);
+  // this CTA's vectors
+  const long long all = (static_cast<long long>(r.end) + kVec - 1) / kVec;
+  const int v0 = static_cast<int>(all * split / p.splits), v1 = static_cast<int>(all * (split + 1) / p.splits);
+  if (v1 * static_cast<long long>(kVec) < r.end) r.end = v1 * kVec;
+  const long long first = static_cast<long long>(v0) * kVec;
+  const int count = (v1 - v0 + kThreads - 1) / kThreads;  // vectors of a thread, at most
+  if (first > r.off) r.off = static_cast<int>(first);
 
   Sums sums = {-INFINITY, 0.f, 0.f};
-  Key best = 0;  // warp 0: the best keys so far, sorted
-  Key bound = 0; // the k-th of them
-  for (int c = c0; c < c1; ++c) {
-    const long long first = static_cast<long long>(c) * kChunk;
-    if (first >= end) break;
-    float x[kVals];
-    int at[NV];  // the place of a vector's first value
+  {
+    const long long mine = first + static_cast<int>(threadIdx.x) * kVec;
+    uint4 next[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const long long place = first + (v * kThreads + static_cast<int>(threadIdx.x)) * kVec;
-      at[v] = place < end ? static_cast<int>(place) : end;
-      if (at[v] >= off && at[v] + kVec <= end) {
-        Logits<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(at[v]) * static_cast<int>(sizeof(T)))), x + v * kVec);
-      } else {
+    for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(v) * (kThreads * kVec));
+    for (int i = 0; i < count; i += NV) {
+      uint4 x[NV];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const int e = at[v] + i;
-          x[v * kVec + i] = e >= off && e < end ? Logits<T>::one(base + static_cast<long long>(e) * static_cast<int>(sizeof(T))) : -INFINITY;
-        }
+      for (int v = 0; v < NV; ++v) x[v] = next[v];
+      if (i + NV < count) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(i + NV + v) * (kThreads * kVec));
       }
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) m = fmaxf(m, x[i]);
-    sums = join(sums, Sums{m, 0.f, 0.f}, l2);
-    const float top = sums.m == -INFINITY ? 0.f : sums.m;
-#pragma unroll
-    for (int i = 0; i < kVals; ++i) {
-      const float z = (x[i] - top) * l2, w = ex2_approx(z);
-      sums.s += w;
-      sums.t = fmaf(w, fmaxf(z, -200.f), sums.t);
-    }
-    if (p.top == 0) continue;
-    // ---------------------------------------------------------------- the best of this chunk
-    Key mine = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int e = at[v] + i;
-        if (e >= off && e < end) {
-          const Key k = key_of(x[v * kVec + i], e - off);
-          if (k > mine) mine = k;
-        }
-      }
-    if (!__syncthreads_or(mine > bound)) continue;
-    if (threadIdx.x == 0) s_count = 0;
-    Key list = sort32(mine);
-    s_list[warp][lane] = list;
-    __syncthreads();
-#pragma unroll
-    for (int n = kWarps / 2; n > 0; n >>= 1) {
-      if (warp < n) {
-        list = merge32(list, s_list[warp + n][lane]);
-        s_list[warp][lane] = list;
-      }
-      __syncthreads();
-    }
-    const Key low = s_list[0][p.top - 1], least = low > bound ? low : bound;
-    if (mine >= least && mine > 0) {
+      float m = sums.m;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const int e = at[v] + i;
-          if (e >= off && e < end) {
-            const Key k = key_of(x[v * kVec + i], e - off);
-            if (k >= least) s_cand[atomicAdd(&s_count, 1)] = k;
+        for (int e = 0; e < kVec / 2; ++e) {
+          const float2 f = Logits<T>::pair(x[v], e);
+          m = fmax3(m, f.x, f.y);
+        }
+      if (m > sums.m) sums = join(sums, Sums{m, 0.f, 0.f}, l2);
+      const float top = m == -INFINITY ? 0.f : m;
+      const unsigned long long lm = f2(-top, -top), ll = f2(l2, l2);
+      unsigned long long ss = f2(0.f, 0.f), tt = ss;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {
+          const float2 f = Logits<T>::pair(x[v], e);
+          float z0, z1;
+          f2_split(fmul2(fadd2(f2(f.x, f.y), lm), ll), z0, z1);
+          const unsigned long long w = f2(ex2_approx(z0), ex2_approx(z1));
+          ss = fadd2(ss, w);
+          tt = ffma2(w, f2(fmaxf(z0, -200.f), fmaxf(z1, -200.f)), tt);  // (of a masked logit 0 times -inf)
+        }
+      float a, b;
+      f2_split(ss, a, b);
+      sums.s += a + b;
+      f2_split(tt, a, b);
+      sums.t += a + b;
+    }
+  }
+
+  // ---------------------------------------------------------------- the best of the CTA's part
+  Key best = 0;  // the first warp's
+  if (p.top) {
+    if (threadIdx.x == 0) s_count = s_flags = 0;
+    merge_warps(sort32(order_of(sums.m)), s_order);
+    float bound = value_of(s_order[0][p.top - 1]);
+    bool equal = true;
+    int n;
+    for (;;) {
+      if (equal ? sums.m >= bound : sums.m > bound) s_flag[atomicAdd(&s_flags, 1)] = static_cast<uint8_t>(threadIdx.x);
+      __syncthreads();
+      const int flags = s_flags, items = flags * count;
+      for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int nth = i / flags;
+        const long long place = first + (static_cast<long long>(nth) * kThreads + s_flag[i - nth * flags]) * kVec;
+        const uint4 x = r.load(place);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const float2 f = Logits<T>::pair(x, e / 2);
+          const float y = e & 1 ? f.y : f.x;
+          const long long at = place + e;
+          if ((equal ? y >= bound : y > bound) && at >= r.off && at < r.end) {
+            const int k = atomicAdd(&s_count, 1);
+            if (k < kCandidates) s_cand[k] = key_of(y, static_cast<int>(at) - off);
           }
         }
+      }
+      __syncthreads();
+      n = s_count;
+      const int held = n < kCandidates ? n : kCandidates;
+      if (warp == 0) {
+        best = 0;
+        for (int i = 0; i < held; i += 32) best = merge32(best, sort32(i + lane < held ? s_cand[i + lane] : Key{0}));
+        s_list[0][lane] = best;
+      }
+      if (n <= kCandidates) break;
+      __syncthreads();
+      if (threadIdx.x == 0) s_count = s_flags = 0;
+      __syncthreads();
+      if (!equal) bound = value_of(static_cast<uint32_t>(s_list[0][p.top - 1] >> 32));
+      equal = false;
     }
-    __syncthreads();
-    if (warp == 0) {
-      const int n = s_count;
-      for (int i = 0; i < n; i += 32) best = merge32(best, sort32(i + lane < n ? s_cand[i + lane] : 0));
-      s_list[0][lane] = best;
+    if (warp == 0 && n < p.top) {
+      // fewer than k above the bound: the first ones equal to it, then NaN (and where both are too few, the part is)
+      for (int pass = equal ? 1 : 0; pass < 2 && n < p.top; ++pass)
+        for (int i = r.off; i < r.end && n < p.top; i += 32) {
+          const bool there = i + lane < r.end;
+          const float y = there ? r.one(i + lane) : 0.f;
+          const bool hit = there && (pass ? y != y : y == bound);
+          const unsigned hits = __ballot_sync(0xffffffffu, hit);
+          const int nth = n + __popc(hits & ((1u << lane) - 1u));
+          if (hit && nth < p.top) s_cand[nth] = key_of(y, i + lane - off);
+          __syncwarp();
+          const int now = min(p.top, n + __popc(hits));
+          if (lane >= n && lane < now) best = s_cand[lane];
+          __syncwarp();
+          n = now;
+        }
     }
-    __syncthreads();
-    bound = s_list[0][p.top - 1];
-    __syncthreads();
   }
 
   // ---------------------------------------------------------------- the CTA's part of the row
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) {
-    Sums o;
-    o.m = __shfl_xor_sync(0xffffffffu, sums.m, j);
-    o.s = __shfl_xor_sync(0xffffffffu, sums.s, j);
-    o.t = __shfl_xor_sync(0xffffffffu, sums.t, j);
-    sums = join(sums, o, l2);
-  }
+  sums = join_warp(sums, l2);
   if (lane == 0) s_sums[warp] = sums;
   __syncthreads();
-  if (warp != 0 && p.splits == 1) return;
-  if (warp == 0) {
-    sums = s_sums[0];
-    for (int w = 1; w < kWarps; ++w) sums = join(sums, s_sums[w], l2);
-  }
+  if (warp == 0) sums = join_warp(lane < kWarps ? s_sums[lane] : Sums{-INFINITY, 0.f, 0.f}, l2);
   if (p.splits > 1) {
-    float* part = p.part + (static_cast<size_t>(row) * p.splits + split) * kPart;
+    const float* parts = p.part + static_cast<size_t>(row) * p.splits * kPart;
     if (warp == 0) {
+      float* part = p.part + (static_cast<size_t>(row) * p.splits + split) * kPart;
       if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(sums.m, sums.s, sums.t, 0.f);
       if (p.top) reinterpret_cast<Key*>(part + 4)[lane] = best;
       __threadfence();
@@ -259,40 +336,44 @@ __global__ void __launch_bounds__(score::kThreads) score_kernel(const ScoreParam
     }
     __syncthreads();
     if (!s_last) return;
-    // the row's parts, in their order
-    if (warp != 0) return;
-    sums = {-INFINITY, 0.f, 0.f};
-    best = 0;
-    for (int s = 0; s < p.splits; ++s) {
-      const float* src = p.part + (static_cast<size_t>(row) * p.splits + s) * kPart;
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-      sums = join(sums, Sums{o.x, o.y, o.z}, l2);
-      if (p.top) best = merge32(best, __ldcg(reinterpret_cast<const Key*>(src + 4) + lane));
+    if (p.top) {
+      best = 0;
+      for (int s = warp; s < p.splits; s += kWarps)
+        best = merge32(best, __ldcg(reinterpret_cast<const Key*>(parts + static_cast<size_t>(s) * kPart + 4) + lane));
+      best = merge_warps(best, s_list);
+    }
+    if (warp == 0) {
+      sums = {-INFINITY, 0.f, 0.f};
+      for (int s = lane; s < p.splits; s += 32) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(parts + static_cast<size_t>(s) * kPart));
+        sums = join(sums, Sums{o.x, o.y, o.z}, l2);
+      }
+      sums = join_warp(sums, l2);
     }
   }
+  if (warp != 0) return;
   const bool none = sums.m == -INFINITY && sums.s == 0.f;  // every logit is -inf
   const float ln = logf(sums.s);
   if (lane == 0) {
-    if (p.logprob)
-      p.logprob[row] = none ? -INFINITY : (Logits<T>::one(x0 + target * static_cast<long long>(sizeof(T))) - sums.m) * p.scale - ln;
+    if (p.logprob) p.logprob[row] = none ? -INFINITY : (r.one(off + target) - sums.m) * p.scale - ln;
     if (p.entropy) p.entropy[row] = none ? 0.f : ln - kLn2 * (sums.t / sums.s);
     if (p.lse) p.lse[row] = none ? -INFINITY : fmaf(sums.m, p.scale, ln);
   }
   if (lane < p.top) {
     const long long at = static_cast<long long>(row) * p.top + lane;
     p.top_id[at] = index_of(best);
-    p.top_logprob[at] = none ? -INFINITY : (value_of(best) - sums.m) * p.scale - ln;
+    p.top_logprob[at] = none ? -INFINITY : (value_of(static_cast<uint32_t>(best >> 32)) - sums.m) * p.scale - ln;
   }
 }
 
-// The parts that a row is cut into: as many as fill the SMs, no finer than a chunk.
-static int score_splits(int rows, int chunks, int sms) {
+// The parts that a row is cut into: as many as fill the SMs, none of less than a vector or two a thread.
+constexpr int kScoreParts = 640;  // of all rows together, beside one a row
+static int score_splits(int rows, int vocab, int sms) {
   if (rows <= 0 || rows > score::kMaxSplitRows) return 1;
-  int s = (2 * sms + rows - 1) / rows;
-  return s < chunks ? s : chunks;
+  int places = 4 * sms < kScoreParts ? 4 * sms : kScoreParts;
+  const int s = (places + rows - 1) / rows, most = vocab / (score::kThreads * 8);
+  return s < most ? s : most < 1 ? 1 : most;
 }
-constexpr int kScoreVals = 32;  // values of a thread
-static int score_chunks(int vocab) { return (vocab + 7 + score::kThreads * kScoreVals - 1) / (score::kThreads * kScoreVals); }
 
 }  // namespace tl
 
@@ -300,10 +381,7 @@ using namespace tl;
 
 extern "C" size_t tl_token_logprobs_workspace_bytes(int rows, int vocab, int top) {
   if (rows < 0 || vocab < 1 || top < 0 || top > score::kTop || top > vocab) return 0;
-  const size_t split_rows = rows < score::kMaxSplitRows ? rows : score::kMaxSplitRows;
-  // (at most 2 splits for each of at most 320 SMs beside one a row)
-  const size_t chunks = score_chunks(vocab);
-  const size_t parts = split_rows + 640 < split_rows * chunks ? split_rows + 640 : split_rows * chunks;
+  const size_t parts = rows > score::kMaxSplitRows ? 0 : static_cast<size_t>(rows) + kScoreParts;
   return kCounterBytes + parts * score::kPart * 4;
 }
 
@@ -337,12 +415,11 @@ extern "C" int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, lon
   p.vocab = vocab;
   p.top = top;
   p.scale = scale;
-  p.chunks = score_chunks(vocab);
-  p.splits = score_splits(rows, p.chunks, ctx->sms < 320 ? ctx->sms : 320);
+  p.splits = score_splits(rows, vocab, ctx->sms);
   const unsigned grid = static_cast<unsigned>(rows) * p.splits;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == TL_FP32) score_kernel<float, 8><<<grid, score::kThreads, 0, s>>>(p);
-  else if (dtype == TL_BF16) score_kernel<__nv_bfloat16, 4><<<grid, score::kThreads, 0, s>>>(p);
-  else score_kernel<__half, 4><<<grid, score::kThreads, 0, s>>>(p);
+  if (dtype == TL_FP32) score_kernel<float, 4><<<grid, score::kThreads, 0, s>>>(p);
+  else if (dtype == TL_BF16) score_kernel<__nv_bfloat16, 3><<<grid, score::kThreads, 0, s>>>(p);
+  else score_kernel<__half, 3><<<grid, score::kThreads, 0, s>>>(p);
   return launched();
 }
