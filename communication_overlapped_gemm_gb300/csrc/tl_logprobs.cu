@@ -13,13 +13,12 @@ namespace tl {
 // joined by the CTA that finishes the last one, in their order.
 //
 // The most likely k <= 32 tokens need nothing in that loop but the maximum that a thread has anyway.  The k-th
-// largest of the 256 threads' maxima is a bound that at least k logits reach, and only the threads (k of them, if no two
-// are equal) whose maximum reaches it can hold one: their vectors are read a second time, from L2, and the logits that
-// reach the bound, k and a few, are sorted.  An order of 64-bit keys, the value's bits above the complement of its index,
-// has no ties (of equal logits the lower index is the larger key).  Logits that are alike in great number
-// (masks, rows of one value) would make too many candidates: then only those above the bound are taken, from a higher bound if these
-// too are many, and the first ones equal to it are looked up from the row's start.
-// A warp sorts 32 keys by exchanges between lanes, and merges two sorted lists into their best 32 in 6 steps.
+// largest of 32 maxima, of 8 threads each, is a bound that at least k logits reach (and few more than k, in no
+// order), and only threads whose maximum reaches it can hold one: their vectors are read a second time, from L2, and of
+// the logits that reach the bound each counts how many are larger: its place.  An order of 64-bit keys, the value's bits above
+// the complement of its index, has no ties (of equal logits the lower index is the larger key).  Logits that are alike in
+// great number (masks, rows of one value) would make too many candidates: then only those above the bound are taken, from a
+// higher bound if these too are many, and the first ones equal to it are looked up from the row's start.
 struct ScoreParams {
   DevStatus* status;
   const uint8_t* x;
@@ -38,9 +37,10 @@ struct ScoreParams {
 
 namespace score {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kTop = 32;
-constexpr int kCandidates = 512;
+constexpr int kAgain = 2;  // vectors that a thread reads again at once
+constexpr int kCandidates = 1024;    // (a join has at most k k / j + k of them, see below)
 constexpr int kPart = 4 + 2 * kTop;  // floats of a part: m, S, T, then its best keys
-constexpr int kMaxSplitRows = 1024;  // (a counter for each row that is split)
+constexpr int kMaxSplitRows = 2400;  // (a counter for each row that is split)
 using Key = unsigned long long;
 
 // Larger values, larger numbers; NaN the lowest; a zero has one sign.
@@ -56,46 +56,27 @@ __device__ __forceinline__ Key key_of(float x, int i) {
 }
 __device__ __forceinline__ int index_of(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
 
-template <class K>
-__device__ __forceinline__ K exchange(K k, int j, bool larger) {
-  const K o = __shfl_xor_sync(0xffffffffu, k, j);
-  return (k > o) == larger ? k : o;
-}
-// The largest first, a key a lane.
-template <class K>
-__device__ __forceinline__ K sort32(K k) {
+// The k-th largest of the lanes' numbers.
+__device__ __forceinline__ uint32_t kth_of_warp(uint32_t v, int k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 2; n <= 32; n <<= 1)
 #pragma unroll
-    for (int j = n / 2; j > 0; j >>= 1) k = exchange(k, j, ((lane & j) == 0) == ((lane & n) == 0));
-  return k;
-}
-// The best 32 of two sorted lists, sorted.
-template <class K>
-__device__ __forceinline__ K merge32(K a, K b) {
-  const int lane = threadIdx.x & 31;
-  const K o = __shfl_xor_sync(0xffffffffu, b, 31);
-  K k = a > o ? a : o;
-#pragma unroll
-  for (int j = 16; j > 0; j >>= 1) k = exchange(k, j, (lane & j) == 0);
-  return k;
-}
-// The best 32 of a sorted list from each warp, in lists[0] (and the first warp's lanes).
-template <class K>
-__device__ __forceinline__ K merge_warps(K list, K (*lists)[kTop]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  lists[warp][lane] = list;
-  __syncthreads();
-#pragma unroll
-  for (int n = kWarps / 2; n > 0; n >>= 1) {
-    if (warp < n) {
-      list = merge32(list, lists[warp + n][lane]);
-      lists[warp][lane] = list;
+    for (int j = n / 2; j > 0; j >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+      v = ((lane & j) == 0) == ((lane & n) == 0) ? max(v, o) : min(v, o);
     }
-    __syncthreads();
+  return __shfl_sync(0xffffffffu, v, k - 1);
+}
+// Puts the k largest of n keys (none twice) in their order; the CTA's barrier before and after it.
+__device__ __forceinline__ void place_best(const Key* keys, int n, Key* best, int k) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Key mine = keys[i];
+    int larger = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) larger += keys[j] > mine;
+    if (larger < k) best[larger] = mine;
   }
-  return list;
 }
 
 struct Sums {
@@ -175,24 +156,15 @@ template <class T, int NV>
 __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScoreParams p) {
   using namespace score;
   constexpr int kVec = Logits<T>::kVec;
-  __shared__ Key s_list[kWarps][kTop];
-  __shared__ uint32_t s_order[kWarps][kTop];
-  __shared__ Key s_cand[kCandidates];
+  __shared__ uint32_t s_order[32];
+  __shared__ Key s_cand[kCandidates], s_best[kTop];
   __shared__ uint8_t s_flag[kThreads];
   __shared__ Sums s_sums[kWarps];
   __shared__ int s_count, s_flags;
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits;
-  int target = 0;
-  if (p.targets) {
-    target = __ldg(p.targets + row);
-    if (target < 0) return;
-    if (target >= p.vocab) {
-      if (split == 0 && threadIdx.x == 0) report_index(p.status, static_cast<unsigned long long>(row));
-      return;
-    }
-  }
+  const int target = p.targets ? __ldg(p.targets + row) : 0;
   const uint8_t* x0 = p.x + row * p.stride;
   Row<T> r;
   r.off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15u) / static_cast<int>(sizeof(T));
@@ -214,6 +186,11 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
     uint4 next[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(v) * (kThreads * kVec));
+    if (target < 0) return;
+    if (target >= p.vocab) {
+      if (split == 0 && threadIdx.x == 0) report_index(p.status, static_cast<unsigned long long>(row));
+      return;
+    }
     for (int i = 0; i < count; i += NV) {
       uint4 x[NV];
 #pragma unroll
@@ -254,46 +231,61 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
   }
 
   // ---------------------------------------------------------------- the best of the CTA's part
-  Key best = 0;  // the first warp's
   if (p.top) {
     if (threadIdx.x == 0) s_count = s_flags = 0;
-    merge_warps(sort32(order_of(sums.m)), s_order);
-    float bound = value_of(s_order[0][p.top - 1]);
+    if (threadIdx.x < kTop) s_best[threadIdx.x] = 0;
+    uint32_t o = order_of(sums.m);
+#pragma unroll
+    for (int j = 1; j < 8; j <<= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, j));
+    if (lane % 8 == 0) s_order[threadIdx.x / 8] = o;
+    __syncthreads();
+    float bound = value_of(kth_of_warp(s_order[lane], p.top));
     bool equal = true;
     int n;
     for (;;) {
       if (equal ? sums.m >= bound : sums.m > bound) s_flag[atomicAdd(&s_flags, 1)] = static_cast<uint8_t>(threadIdx.x);
       __syncthreads();
       const int flags = s_flags, items = flags * count;
-      for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int nth = i / flags;
-        const long long place = first + (static_cast<long long>(nth) * kThreads + s_flag[i - nth * flags]) * kVec;
-        const uint4 x = r.load(place);
+      for (int i0 = threadIdx.x; i0 < items; i0 += kAgain * kThreads) {
+        uint4 x[kAgain];
+        long long place[kAgain];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float2 f = Logits<T>::pair(x, e / 2);
-          const float y = e & 1 ? f.y : f.x;
-          const long long at = place + e;
-          if ((equal ? y >= bound : y > bound) && at >= r.off && at < r.end) {
-            const int k = atomicAdd(&s_count, 1);
-            if (k < kCandidates) s_cand[k] = key_of(y, static_cast<int>(at) - off);
+        for (int u = 0; u < kAgain; ++u) {
+          const int i = i0 + u * kThreads, nth = i / flags;
+          place[u] = i < items ? first + (static_cast<long long>(nth) * kThreads + s_flag[i - nth * flags]) * kVec : r.end;
+          x[u] = r.load(place[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAgain; ++u) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kVec / 2; ++e) {
+            const float2 f = Logits<T>::pair(x[u], e);
+            top = fmax3(top, f.x, f.y);
           }
+          if (equal ? top >= bound : top > bound)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+              const float2 f = Logits<T>::pair(x[u], e / 2);
+              const float y = e & 1 ? f.y : f.x;
+              const long long at = place[u] + e;
+              if ((equal ? y >= bound : y > bound) && at >= r.off && at < r.end) {
+                const int k = atomicAdd(&s_count, 1);
+                if (k < kCandidates) s_cand[k] = key_of(y, static_cast<int>(at) - off);
+              }
+            }
         }
       }
       __syncthreads();
       n = s_count;
-      const int held = n < kCandidates ? n : kCandidates;
-      if (warp == 0) {
-        best = 0;
-        for (int i = 0; i < held; i += 32) best = merge32(best, sort32(i + lane < held ? s_cand[i + lane] : Key{0}));
-        s_list[0][lane] = best;
-      }
-      if (n <= kCandidates) break;
+      place_best(s_cand, n < kCandidates ? n : kCandidates, s_best, p.top);
       __syncthreads();
+      if (n <= kCandidates) break;
+      if (!equal) bound = value_of(static_cast<uint32_t>(s_best[p.top - 1] >> 32));
+      equal = false;
       if (threadIdx.x == 0) s_count = s_flags = 0;
       __syncthreads();
-      if (!equal) bound = value_of(static_cast<uint32_t>(s_list[0][p.top - 1] >> 32));
-      equal = false;
+      if (threadIdx.x < kTop) s_best[threadIdx.x] = 0;
     }
     if (warp == 0 && n < p.top) {
       // fewer than k above the bound: the first ones equal to it, then NaN (and where both are too few, the part is)
@@ -304,13 +296,10 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
           const bool hit = there && (pass ? y != y : y == bound);
           const unsigned hits = __ballot_sync(0xffffffffu, hit);
           const int nth = n + __popc(hits & ((1u << lane) - 1u));
-          if (hit && nth < p.top) s_cand[nth] = key_of(y, i + lane - off);
-          __syncwarp();
-          const int now = min(p.top, n + __popc(hits));
-          if (lane >= n && lane < now) best = s_cand[lane];
-          __syncwarp();
-          n = now;
+          if (hit && nth < p.top) s_best[nth] = key_of(y, i + lane - off);
+          n += __popc(hits);
         }
+      __syncwarp();
     }
   }
 
@@ -324,7 +313,7 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
     if (warp == 0) {
       float* part = p.part + (static_cast<size_t>(row) * p.splits + split) * kPart;
       if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(sums.m, sums.s, sums.t, 0.f);
-      if (p.top) reinterpret_cast<Key*>(part + 4)[lane] = best;
+      if (p.top) reinterpret_cast<Key*>(part + 4)[lane] = s_best[lane];
       __threadfence();
       __syncwarp();
       if (lane == 0) {
@@ -337,10 +326,39 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
     __syncthreads();
     if (!s_last) return;
     if (p.top) {
-      best = 0;
-      for (int s = warp; s < p.splits; s += kWarps)
-        best = merge32(best, __ldcg(reinterpret_cast<const Key*>(parts + static_cast<size_t>(s) * kPart + 4) + lane));
-      best = merge_warps(best, s_list);
+      // With j = k / splits (rounded up), k / j of the parts' j-th keys reach the (k / j)-th largest of these: so do k keys.
+      const Key* keys = reinterpret_cast<const Key*>(parts + 4);
+      constexpr int kStride = kPart / 2;
+      const int nth = (p.top + p.splits - 1) / p.splits, need = (p.top + nth - 1) / nth;
+      if (threadIdx.x == 0) s_count = 0;
+      for (int s = threadIdx.x; s < p.splits; s += kThreads) s_cand[s] = __ldcg(keys + static_cast<size_t>(s) * kStride + nth - 1);
+      __syncthreads();
+      for (int s = threadIdx.x; s < p.splits; s += kThreads) {
+        // (equal ones are zeros, from parts of fewer keys)
+        const Key mine = s_cand[s];
+        int larger = 0, same = 0;
+#pragma unroll 8
+        for (int i = 0; i < p.splits; ++i) {
+          larger += s_cand[i] > mine;
+          same += s_cand[i] == mine && i < s;
+        }
+        if (larger + same == need - 1) s_best[0] = mine;
+      }
+      __syncthreads();
+      const Key bound = s_best[0] > 0 ? s_best[0] : 1;
+      __syncthreads();
+      if (threadIdx.x < kTop) s_best[threadIdx.x] = 0;
+      for (int i = threadIdx.x; i < p.splits * kTop; i += kThreads) {
+        if (i % kTop >= p.top) continue;
+        const Key k = __ldcg(keys + static_cast<size_t>(i / kTop) * kStride + i % kTop);
+        if (k >= bound) {
+          const int c = atomicAdd(&s_count, 1);
+          if (c < kCandidates) s_cand[c] = k;
+        }
+      }
+      __syncthreads();
+      place_best(s_cand, min(s_count, kCandidates), s_best, p.top);
+      __syncthreads();
     }
     if (warp == 0) {
       sums = {-INFINITY, 0.f, 0.f};
@@ -361,6 +379,7 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
   }
   if (lane < p.top) {
     const long long at = static_cast<long long>(row) * p.top + lane;
+    const Key best = s_best[lane];
     p.top_id[at] = index_of(best);
     p.top_logprob[at] = none ? -INFINITY : (value_of(static_cast<uint32_t>(best >> 32)) - sums.m) * p.scale - ln;
   }
@@ -370,8 +389,8 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
 constexpr int kScoreParts = 640;  // of all rows together, beside one a row
 static int score_splits(int rows, int vocab, int sms) {
   if (rows <= 0 || rows > score::kMaxSplitRows) return 1;
-  int places = 4 * sms < kScoreParts ? 4 * sms : kScoreParts;
-  const int s = (places + rows - 1) / rows, most = vocab / (score::kThreads * 8);
+  int places = 3 * sms < kScoreParts ? 3 * sms : kScoreParts;
+  const int s = (places + rows - 1) / rows, most = vocab / (score::kThreads * 16);
   return s < most ? s : most < 1 ? 1 : most;
 }
 
