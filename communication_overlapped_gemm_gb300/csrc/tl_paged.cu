@@ -320,9 +320,13 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // rounding (relative 1.6e-3; with one term 2.2e-3, and 0.6% less time: the tensor pipe waits for HBM), over an
 // e4m3 cache, whose rows have 4 bits, as one fp16 term.  l sums them unrounded in fp32.
 namespace paged {
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kTile = kWarps * kKeys;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int tile_bits(int bits) { return bits == 4 ? 7 : 6; }  // log2 of a tile's keys
 template <int Bits, int D, int NB>
 struct Shape {
+  static constexpr int kTileBits = tile_bits(Bits), kTile = 1 << kTileBits;
+  static constexpr int kKeys = kTile / kWarps;           // of a warp in a tile
+
   static constexpr int kRows = 8 * NB;                   // query heads of an item
   static constexpr int kRowBytes = D * Bits / 8;
   static constexpr int kHalf = kKeys * kRowBytes;        // one warp's K (or V) rows of a stage
@@ -332,7 +336,7 @@ struct Shape {
   // 8-bit or short rows brings few bytes for its instructions and wants the warps; the registers
   // allow three CTAs there.
   static constexpr int kCtas = D == 64 || (Bits < 16 && NB == 1) ? 3 : 2;
-  static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * kStage);
+  static constexpr int kFit = (kCtas == 3 ? Bits == 4 ? 57344 : 49152 : 65536) / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
   static constexpr int kMergeOff = kStages * kWarps * kStage;
@@ -393,7 +397,8 @@ __device__ __forceinline__ int paged_length(const PagedParams& p, int b, bool re
   }
   return n;
 }
-__device__ __forceinline__ int paged_tiles(int count, int lw) { return (count + (paged::kTile >> lw) - 1) >> (6 - lw); }
+// The tiles of `count` keys, for `shift` the log2 of a tile's keys of a kv head.
+__device__ __forceinline__ int paged_tiles(int count, int shift) { return (count + (1 << shift) - 1) >> shift; }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -457,13 +462,14 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   using S = Shape<Bits, D, NB>;
   constexpr bool kNarrow = Bits < 16;                           // 8 or 4 bits, widened to fp16
   using M = typename std::conditional<kNarrow, __half, T>::type;  // the products' type
-  constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows;
+  constexpr int kSteps = D / 16, kStages = S::kStages, kRows = S::kRows, kKeys = S::kKeys, kTile = S::kTile;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_sum[kThreads], s_warp[kWarps];
   __shared__ unsigned s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int subs = (p.c.kv_heads >> p.lw) * p.blocks;
-  // this warp's kv head of an item's, and its 16 keys of a tile's
+  const int shift = S::kTileBits - p.lw;
+  // this warp's kv head of an item's, and its 16 (32) keys of a tile's
   const int hw = warp & ((1 << p.lw) - 1), kb = warp >> p.lw;
 
   // ---------------------------------------------------------------- plan
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       const int b = static_cast<int>(threadIdx.x) * chunk + i;
       if (b >= p.batch) break;
       const int count = visible_rows(paged_length(p, b, blockIdx.x == 0), p.window, p.sinks).count;
-      sum += paged_tiles(count, p.lw);
+      sum += paged_tiles(count, shift);
       if (count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
         for (int h = 0; h < p.heads; ++h) {
           uint4* o = reinterpret_cast<uint4*>(p.out + b * p.out_seq + h * p.out_head);
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     at.b = (32 * w + i) * chunk;
     for (;;) {
       at.vis = visible_rows(paged_length(p, at.b, false), p.window, p.sinks);
-      at.tiles = paged_tiles(at.vis.count, p.lw);
+      at.tiles = paged_tiles(at.vis.count, shift);
       const uint32_t here = static_cast<uint32_t>(at.tiles) * subs;
       if (first < pos + here) break;
       pos += here;
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     a.sub = 0;
     while (++a.b < p.batch) {
       a.vis = visible_rows(paged_length(p, a.b, false), p.window, p.sinks);
-      a.tiles = paged_tiles(a.vis.count, p.lw);
+      a.tiles = paged_tiles(a.vis.count, shift);
       if (a.tiles > 0) return;
     }
   };
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     w.wanted = false;
     w.rest = w.scales = 0;
     w.b = a.b;
-    const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & 15);
+    const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & (kKeys - 1));
     if (more && i < a.vis.count) {
       const int row = i < a.vis.head ? i : i + a.vis.skip;
       const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
@@ -579,6 +585,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   };
   const uint32_t ring = smem_u32(smem) + warp * S::kStage;
   auto stage_addr = [&](int s) { return ring + s * (kWarps * S::kStage); };
+  constexpr uint32_t kAllKeys = 0xffffffffu >> (32 - kKeys);
   uint32_t masks[kStages];  // one per stage, the same in all lanes
   // 4 bits: where chunk c of V row `key` lies
   auto chunk4 = [](int key, int c) -> uint32_t {
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     const bool row_ok = w.wanted && w.page >= 0 && w.page < p.c.num_pages;
     if (w.wanted && !row_ok) report_index(p.status, static_cast<unsigned long long>(w.b));
     const long long row_off = row_ok ? w.page * p.c.page_stride + w.rest : 0;
-    mask = __ballot_sync(0xffffffffu, row_ok) & 0xffffu;
+    mask = __ballot_sync(0xffffffffu, row_ok) & kAllKeys;
     if (step_loaded < nsteps) {
       constexpr int kChunks = S::kRowBytes / 16, kPer = 32 / kChunks;  // rows a warp-wide copy covers
       const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
@@ -615,9 +622,11 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         cp_async16(sk + ck, p.c.k + off, bytes);
         cp_async16(sv + cv, p.c.v + off, bytes);
       }
-      if constexpr (Bits == 4) {  // lanes 0..15 the K rows' scales, the others V's
-        const uint8_t* src = (lane < 16 ? p.c.k_blocks : p.c.v_blocks) + (row_ok ? w.page * p.c.page_blocks + w.scales : 0);
-        cp_async_small<S::kScaleBytes>(sk + 2 * S::kHalf + lane * S::kScaleBytes, src, row_ok ? S::kScaleBytes : 0);
+      if constexpr (Bits == 4) {  // a lane its key's block scales
+        const long long scales = row_ok ? w.page * p.c.page_blocks + w.scales : 0;
+        const uint32_t dst = sk + 2 * S::kHalf + lane * S::kScaleBytes, bytes = row_ok ? S::kScaleBytes : 0;
+        cp_async_small<S::kScaleBytes>(dst, p.c.k_blocks + scales, bytes);
+        cp_async_small<S::kScaleBytes>(dst + kKeys * S::kScaleBytes, p.c.v_blocks + scales, bytes);
       }
       ++step_loaded;
     }
@@ -719,42 +728,47 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
-      float x[NB][4];  // scores of keys g (0, 1) and g + 8 (2, 3) at columns 2t, 2t + 1
+      constexpr int kU = kKeys / 16;  // groups of 16 keys
+      float x[kU * NB][4];  // scores of keys g (0, 1) and g + 8 (2, 3) of each group at columns 2t, 2t + 1
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < kU * NB; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[b][j] = 0.f;
       if constexpr (Bits == 4) {
         // a quarter of a row per thread: k index 2t, 2t + 1, 8 + 2t, 9 + 2t of step s is head dim
         // D / 4 t + 4 s + 0..3, for q above likewise, so that a thread's dims of four steps are one block
-        const uint32_t ss = sk + 2 * S::kHalf;
-        uint32_t lo[D / 32], hi[D / 32], slo, shi;  // codes of rows g and g + 8; a pair of scales, or one twice
-        if constexpr (D == 128) {
-          const uint4 u = lds128(sk + g * 64 + t * 16), w = lds128(sk + (g + 8) * 64 + t * 16);
-          lo[0] = u.x, lo[1] = u.y, lo[2] = u.z, lo[3] = u.w;
-          hi[0] = w.x, hi[1] = w.y, hi[2] = w.z, hi[3] = w.w;
-          slo = widen_e4m3x2(lds_u16(ss + g * 8 + t * 2));
-          shi = widen_e4m3x2(lds_u16(ss + (g + 8) * 8 + t * 2));
-        } else {
-          const uint2 u = lds64(sk + g * 32 + t * 8), w = lds64(sk + (g + 8) * 32 + t * 8);
-          lo[0] = u.x, lo[1] = u.y;
-          hi[0] = w.x, hi[1] = w.y;
-          slo = widen_e4m3x2(lds_u8(ss + g * 4 + t));
-          shi = widen_e4m3x2(lds_u8(ss + (g + 8) * 4 + t));
-        }
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint32_t bl = __byte_perm(slo, slo, h ? 0x3232 : 0x1010), bh = __byte_perm(shi, shi, h ? 0x3232 : 0x1010);
+        for (int u = 0; u < kU; ++u) {
+          const uint32_t sc0 = sk + 2 * S::kHalf + u * 16 * S::kScaleBytes, su = sk + u * 16 * S::kRowBytes;
+          uint32_t lo[D / 32], hi[D / 32], slo, shi;  // codes of rows g and g + 8; a pair of scales, or one twice
+          if constexpr (D == 128) {
+            const uint4 y = lds128(su + g * 64 + t * 16), z = lds128(su + (g + 8) * 64 + t * 16);
+            lo[0] = y.x, lo[1] = y.y, lo[2] = y.z, lo[3] = y.w;
+            hi[0] = z.x, hi[1] = z.y, hi[2] = z.z, hi[3] = z.w;
+            slo = widen_e4m3x2(lds_u16(sc0 + g * 8 + t * 2));
+            shi = widen_e4m3x2(lds_u16(sc0 + (g + 8) * 8 + t * 2));
+          } else {
+            const uint2 y = lds64(su + g * 32 + t * 8), z = lds64(su + (g + 8) * 32 + t * 8);
+            lo[0] = y.x, lo[1] = y.y;
+            hi[0] = z.x, hi[1] = z.y;
+            slo = widen_e4m3x2(lds_u8(sc0 + g * 4 + t));
+            shi = widen_e4m3x2(lds_u8(sc0 + (g + 8) * 4 + t));
+          }
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint32_t x0[4], x1[4];
-            widen_e2m1(lo[2 * h + w], x0);
-            widen_e2m1(hi[2 * h + w], x1);
+          for (int h = 0; h < D / 64; ++h) {
+            const uint32_t bl = __byte_perm(slo, slo, h ? 0x3232 : 0x1010), bh = __byte_perm(shi, shi, h ? 0x3232 : 0x1010);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t a[4] = {hmul2(x0[2 * k], bl), hmul2(x1[2 * k], bh), hmul2(x0[2 * k + 1], bl), hmul2(x1[2 * k + 1], bh)};
+            for (int w = 0; w < 2; ++w) {
+              uint32_t x0[4], x1[4];
+              widen_e2m1(lo[2 * h + w], x0);
+              widen_e2m1(hi[2 * h + w], x1);
 #pragma unroll
-              for (int b = 0; b < NB; ++b) mma16816<M>(x[b], a, qf[4 * h + 2 * w + k][b][0], qf[4 * h + 2 * w + k][b][1]);
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a[4] = {hmul2(x0[2 * k], bl), hmul2(x1[2 * k], bh), hmul2(x0[2 * k + 1], bl), hmul2(x1[2 * k + 1], bh)};
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  mma16816<M>(x[u * NB + b], a, qf[4 * h + 2 * w + k][b][0], qf[4 * h + 2 * w + k][b][1]);
+              }
             }
           }
         }
@@ -788,19 +802,24 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       }
       bool moved = false;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[b][j] *= sc[b][j & 1];
-          if (mask != 0xffffu && !((mask >> (g + 8 * (j >> 1))) & 1u)) x[b][j] = -INFINITY;
-          moved |= x[b][j] > m[b][j & 1] + (8.f + kWeightBits<M>);
-        }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& y = x[u * NB + b][j];
+            y *= sc[b][j & 1];
+            if (mask != kAllKeys && !((mask >> (16 * u + g + 8 * (j >> 1))) & 1u)) y = -INFINITY;
+            moved |= y > m[b][j & 1] + (8.f + kWeightBits<M>);
+          }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float top = fmaxf(x[b][j], x[b][j + 2]);
+#pragma unroll
+            for (int u = 1; u < kU; ++u) top = fmax3(top, x[u * NB + b][j], x[u * NB + b][j + 2]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -817,57 +836,62 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       }
       // the weights as the next product's B: keys by pairs in a column of queries; for a 16-bit cache as a sum of two terms
       constexpr int kTerms = kNarrow ? 1 : 2;
-      uint32_t pf[NB][kTerms][2];
+      uint32_t pf[kU * NB][kTerms][2];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float w[4];
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = ex2_approx(x[b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
-          l[b][j & 1] += w[j];
-        }
+        for (int b = 0; b < NB; ++b) {
+          float w[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t top = from_f32x2<M>(w[2 * e], w[2 * e + 1]);
-          pf[b][0][e] = transpose8x8(top);
-          if constexpr (!kNarrow) {
-            const float2 f = to_f32x2<M>(top);
-            pf[b][1][e] = transpose8x8(from_f32x2<M>(w[2 * e] - f.x, w[2 * e + 1] - f.y));
+          for (int j = 0; j < 4; ++j) {
+            w[j] = ex2_approx(x[u * NB + b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
+            l[b][j & 1] += w[j];
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t top = from_f32x2<M>(w[2 * e], w[2 * e + 1]);
+            pf[u * NB + b][0][e] = transpose8x8(top);
+            if constexpr (!kNarrow) {
+              const float2 f = to_f32x2<M>(top);
+              pf[u * NB + b][1][e] = transpose8x8(from_f32x2<M>(w[2 * e] - f.x, w[2 * e + 1] - f.y));
+            }
           }
         }
-      }
       if constexpr (Bits == 4) {
         // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8), which lie in one block; pairs of rows
         // interleaved by halves of bytes: rows g and g + 8 of product n are head dims g D/8 + 2n and + 2n + 1
         constexpr int kW = D / 64;  // words
         const uint32_t ss = sk + 2 * S::kHalf + kKeys * S::kScaleBytes + (D == 128 ? g : g >> 1);
-        uint32_t w[4][kW], sb[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 2 * t + (k & 1) + 8 * (k >> 1);
-          sb[k] = lds_u8(ss + key * S::kScaleBytes);
-          if constexpr (D == 128) {
-            const uint2 v = lds64(sv + chunk4(key, g >> 1) + (g & 1) * 8);
-            w[k][0] = v.x;
-            w[k][1] = v.y;
-          } else {
-            w[k][0] = lds32(sv + chunk4(key, g >> 2) + (g & 3) * 4);
+        for (int u = 0; u < kU; ++u) {
+          uint32_t w[4][kW], sb[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = 16 * u + 2 * t + (k & 1) + 8 * (k >> 1);
+            sb[k] = lds_u8(ss + key * S::kScaleBytes);
+            if constexpr (D == 128) {
+              const uint2 v = lds64(sv + chunk4(key, g >> 1) + (g & 1) * 8);
+              w[k][0] = v.x;
+              w[k][1] = v.y;
+            } else {
+              w[k][0] = lds32(sv + chunk4(key, g >> 2) + (g & 3) * 4);
+            }
           }
-        }
-        const uint32_t s01 = widen_e4m3x2(sb[0] | (sb[1] << 8)), s23 = widen_e4m3x2(sb[2] | (sb[3] << 8));
+          const uint32_t s01 = widen_e4m3x2(sb[0] | (sb[1] << 8)), s23 = widen_e4m3x2(sb[2] | (sb[3] << 8));
 #pragma unroll
-        for (int i = 0; i < kW; ++i) {
-          uint32_t e01[4], o01[4], e23[4], o23[4];
-          constexpr uint32_t kLow = 0x0f0f0f0fu;
-          widen_e2m1((w[0][i] & kLow) | ((w[1][i] << 4) & ~kLow), e01);
-          widen_e2m1(((w[0][i] >> 4) & kLow) | (w[1][i] & ~kLow), o01);
-          widen_e2m1((w[2][i] & kLow) | ((w[3][i] << 4) & ~kLow), e23);
-          widen_e2m1(((w[2][i] >> 4) & kLow) | (w[3][i] & ~kLow), o23);
+          for (int i = 0; i < kW; ++i) {
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            widen_e2m1((w[0][i] & kLow) | ((w[1][i] << 4) & ~kLow), e01);
+            widen_e2m1(((w[0][i] >> 4) & kLow) | (w[1][i] & ~kLow), o01);
+            widen_e2m1((w[2][i] & kLow) | ((w[3][i] << 4) & ~kLow), e23);
+            widen_e2m1(((w[2][i] >> 4) & kLow) | (w[3][i] & ~kLow), o23);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23), hmul2(o23[j], s23)};
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23), hmul2(o23[j], s23)};
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816<M>(o[4 * i + j][b], a, pf[b][0][0], pf[b][0][1]);
+              for (int b = 0; b < NB; ++b) mma16816<M>(o[4 * i + j][b], a, pf[u * NB + b][0][0], pf[u * NB + b][0][1]);
+            }
           }
         }
       } else if constexpr (!kNarrow) {
@@ -1254,7 +1278,8 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   p.lw = 0;
   if (p.group <= 8 && p.c.head_stride == row_bytes)
     while (p.lw < 2 && (row_bytes << p.lw) < 256 && cache->kv_heads % (2 << p.lw) == 0) ++p.lw;
-  const long long most = batch * static_cast<long long>(cache->kv_heads >> p.lw) * p.blocks * (cap / (paged::kTile >> p.lw) + 1);
+  const long long most = batch * static_cast<long long>(cache->kv_heads >> p.lw) * p.blocks *
+                         ((cap >> (paged::tile_bits(bits) - p.lw)) + 1);
   if (most >= (1LL << 31)) return TL_ERR_INVALID;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto bits, auto d) {
     auto launch = [&](auto nb) {
