@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_sum[kThreads], s_warp[kWarps];
   __shared__ unsigned s_last;
+  __shared__ uint32_t s_mask[kWarps][Bits == 4 ? kStages : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int subs = (p.c.kv_heads >> p.lw) * p.blocks;
   const int shift = S::kTileBits - p.lw;
@@ -592,15 +593,29 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     if constexpr (D == 128) return (key >> 1) * 128 + ((((key & 1) * 4 + c) ^ (((key >> 1) & 3) << 1)) << 4);
     else return (key >> 2) * 128 + ((((key & 3) * 2 + c) ^ (((key >> 2) & 1) << 1)) << 4);
   };
+  // and where this lane's chunk of the first rows that it copies goes (that of later rows as many rows on)
+  constexpr int kRowChunks = S::kRowBytes / 16;
+  const uint32_t first_k = Bits == 4 ? lane * 16 : 0, first_v = Bits == 4 ? chunk4(lane / kRowChunks, lane % kRowChunks) : 0;
   auto issue = [&](int s, uint32_t& mask, const Place& w) {
     const bool row_ok = w.wanted && w.page >= 0 && w.page < p.c.num_pages;
     if (w.wanted && !row_ok) report_index(p.status, static_cast<unsigned long long>(w.b));
     const long long row_off = row_ok ? w.page * p.c.page_stride + w.rest : 0;
     mask = __ballot_sync(0xffffffffu, row_ok) & kAllKeys;
+    if constexpr (Bits == 4) {
+      if (lane == 0) s_mask[warp][s] = mask;
+    }
     if (step_loaded < nsteps) {
       constexpr int kChunks = S::kRowBytes / 16, kPer = 32 / kChunks;  // rows a warp-wide copy covers
       const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
       const int c = lane % kChunks;
+      if (Bits == 4 && mask == kAllKeys) {  // nothing left out
+#pragma unroll
+        for (int j = 0; j < kKeys / kPer; ++j) {
+          const long long off = __shfl_sync(0xffffffffu, row_off, j * kPer + lane / kChunks) + c * 16;
+          cp_async16(sk + first_k + j * kPer * S::kRowBytes, p.c.k + off, 16u);
+          cp_async16(sv + first_v + j * kPer * S::kRowBytes, p.c.v + off, 16u);
+        }
+      } else
 #pragma unroll
       for (int j = 0; j < kKeys / kPer; ++j) {
         const int key = j * kPer + lane / kChunks;
@@ -608,8 +623,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         const uint32_t bytes = (mask >> key) & 1u ? 16u : 0u;  // 0: filled with zeros, nothing is read
         uint32_t ck, cv;  // 16-byte chunks are permuted within a row (4 bits: within 128 bytes) so that no read below conflicts
         if constexpr (Bits == 4) {
-          ck = key * S::kRowBytes + (c << 4);
-          cv = chunk4(key, c);
+          ck = first_k + j * kPer * S::kRowBytes;
+          cv = first_v + j * kPer * S::kRowBytes;
         } else if constexpr (!kNarrow) {
           ck = cv = key * S::kRowBytes + ((c ^ (key & 7)) << 4);
         } else if constexpr (D == 128) {
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     for (int s = 0; s < kStages - 1; ++s) issue(s, masks[s], places[s]);
   }
 
-  int step = 0;
+  int step = 0, slot = 0;  // (slot: step modulo kStages)
   while (step < nsteps) {
     // a segment: this CTA's tiles of one item
     const int seg_tile = at.tile;
@@ -715,18 +730,23 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     for (int i = 0; i < seg; ++i, ++step) {
       // the stage of step - 1 is free (every lane has read it): fill it with step + kStages - 1
       __syncwarp();
-      const int s = step % kStages, sn = (step + kStages - 1) % kStages;
+      const int s = Bits == 4 ? slot : step % kStages, sn = Bits == 4 ? (slot ? slot - 1 : kStages - 1) : (step + kStages - 1) % kStages;
       uint32_t mask = 0, fresh;
       issue(sn, fresh, next);
       if (step_loaded < nsteps) advance(load_at);
       next = look_up(load_at, step_loaded < nsteps);
+      if constexpr (Bits == 4) {
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+      } else {
 #pragma unroll
-      for (int x = 0; x < kStages; ++x) {
-        if (x == sn) masks[x] = fresh;
-        if (x == s) mask = masks[x];
+        for (int x = 0; x < kStages; ++x) {
+          if (x == sn) masks[x] = fresh;
+          if (x == s) mask = masks[x];
+        }
       }
       cp_async_wait<kStages - 1>();
       __syncwarp();
+      if constexpr (Bits == 4) mask = s_mask[warp][s];
       const uint32_t sk = stage_addr(s), sv = sk + S::kHalf;
       constexpr int kU = kKeys / 16;  // groups of 16 keys
       float x[kU * NB][4];  // scores of keys g (0, 1) and g + 8 (2, 3) of each group at columns 2t, 2t + 1
@@ -801,17 +821,40 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         }
       }
       bool moved = false;
+      if constexpr (Bits == 4) {  // (the fewest instructions: they are what bounds it)
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+        for (int u = 0; u < kU * NB; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[u][j] *= sc[u % NB][j & 1];
+        if (mask != kAllKeys) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((mask >> (16 * u + g + 8 * e)) & 1u)) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) x[u * NB + b][2 * e] = x[u * NB + b][2 * e + 1] = -INFINITY;
+              }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(x[b][j], x[b][j + 2]);
+#pragma unroll
+            for (int u = 1; u < kU; ++u) top = fmax3(top, x[u * NB + b][j], x[u * NB + b][j + 2]);
+            moved |= top > m[b][j] + (8.f + kWeightBits<M>);
+          }
+      } else {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float& y = x[u * NB + b][j];
-            y *= sc[b][j & 1];
-            if (mask != kAllKeys && !((mask >> (16 * u + g + 8 * (j >> 1))) & 1u)) y = -INFINITY;
-            moved |= y > m[b][j & 1] + (8.f + kWeightBits<M>);
+            x[b][j] *= sc[b][j & 1];
+            if (mask != kAllKeys && !((mask >> (g + 8 * (j >> 1))) & 1u)) x[b][j] = -INFINITY;
+            moved |= x[b][j] > m[b][j & 1] + (8.f + kWeightBits<M>);
           }
+      }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -861,20 +904,22 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         // rows 2t, 2t + 1, 8 + 2t, 9 + 2t at head dims [g D/8, (g + 1) D/8), which lie in one block; pairs of rows
         // interleaved by halves of bytes: rows g and g + 8 of product n are head dims g D/8 + 2n and + 2n + 1
         constexpr int kW = D / 64;  // words
-        const uint32_t ss = sk + 2 * S::kHalf + kKeys * S::kScaleBytes + (D == 128 ? g : g >> 1);
+        const uint32_t ss = sk + 2 * S::kHalf + kKeys * S::kScaleBytes + (D == 128 ? g : g >> 1) + 2 * t * S::kScaleBytes;
+        // (rows 8 and 16 further on lie 8 and 16 rows further on)
+        const uint32_t v_even = sv + (D == 128 ? chunk4(2 * t, g >> 1) + (g & 1) * 8 : chunk4(2 * t, g >> 2) + (g & 3) * 4);
+        const uint32_t v_odd = sv + (D == 128 ? chunk4(2 * t + 1, g >> 1) + (g & 1) * 8 : chunk4(2 * t + 1, g >> 2) + (g & 3) * 4);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           uint32_t w[4][kW], sb[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int key = 16 * u + 2 * t + (k & 1) + 8 * (k >> 1);
-            sb[k] = lds_u8(ss + key * S::kScaleBytes);
+            sb[k] = lds_u8(ss + (16 * u + (k & 1) + 8 * (k >> 1)) * S::kScaleBytes);
             if constexpr (D == 128) {
-              const uint2 v = lds64(sv + chunk4(key, g >> 1) + (g & 1) * 8);
+              const uint2 v = lds64((k & 1 ? v_odd : v_even) + (16 * u + 8 * (k >> 1)) * S::kRowBytes);
               w[k][0] = v.x;
               w[k][1] = v.y;
             } else {
-              w[k][0] = lds32(sv + chunk4(key, g >> 2) + (g & 3) * 4);
+              w[k][0] = lds32((k & 1 ? v_odd : v_even) + ((16 * u + 8 * (k >> 1)) * S::kRowBytes));
             }
           }
           const uint32_t s01 = widen_e4m3x2(sb[0] | (sb[1] << 8)), s23 = widen_e4m3x2(sb[2] | (sb[3] << 8));
