@@ -366,6 +366,8 @@ struct PagedParams {
   FastDiv by_page;
   float sl2;          // scale * log2(e)
   int window, sinks;
+  // 4 bits: the strides of rows and of their block scales in units of `unit` and `unit_b` bytes, in which 32 bits reach the whole cache
+  uint32_t page_u, row_u, head_u, page_ub, row_ub, head_ub, unit, unit_b;
 };
 
 // The visible rows of a sequence of n, counted from 0: the first `head` are rows [0, head), the
@@ -561,14 +563,15 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     int page;        // as the table has it
     bool wanted;
     long long rest;  // from the page's start to the row's
-    long long scales;  // 4 bits: to its block scales
+    uint32_t unit, unit_b;  // 4 bits: the same in units, and to its block scales
     int b;
   };
   auto look_up = [&](const PagedAt& a, bool more) {
     Place w;
     w.page = 0;
     w.wanted = false;
-    w.rest = w.scales = 0;
+    w.rest = 0;
+    w.unit = w.unit_b = 0u;
     w.b = a.b;
     const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & (kKeys - 1));
     if (more && i < a.vis.count) {
@@ -576,11 +579,13 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
       w.page = __ldg(p.table + static_cast<long long>(a.b) * p.max_pages + pg);
       w.wanted = true;
-      w.rest = (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_stride +
-               (((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw) * p.c.head_stride;
-      if constexpr (Bits == 4)
-        w.scales = (row - static_cast<int>(pg) * p.c.page_size) * p.c.row_blocks +
-                   (((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw) * p.c.head_blocks;
+      const int in_page = row - static_cast<int>(pg) * p.c.page_size, head = ((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw;
+      if constexpr (Bits == 4) {
+        w.unit = in_page * p.row_u + head * p.head_u;
+        w.unit_b = in_page * p.row_ub + head * p.head_ub;
+      } else {
+        w.rest = in_page * p.c.row_stride + head * p.c.head_stride;
+      }
     }
     return w;
   };
@@ -596,10 +601,13 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   // and where this lane's chunk of the first rows that it copies goes (that of later rows as many rows on)
   constexpr int kRowChunks = S::kRowBytes / 16;
   const uint32_t first_k = Bits == 4 ? lane * 16 : 0, first_v = Bits == 4 ? chunk4(lane / kRowChunks, lane % kRowChunks) : 0;
+  const uint8_t* const lane_k = p.c.k + lane % kRowChunks * 16;
+  const uint8_t* const lane_v = p.c.v + lane % kRowChunks * 16;
   auto issue = [&](int s, uint32_t& mask, const Place& w) {
     const bool row_ok = w.wanted && w.page >= 0 && w.page < p.c.num_pages;
     if (w.wanted && !row_ok) report_index(p.status, static_cast<unsigned long long>(w.b));
-    const long long row_off = row_ok ? w.page * p.c.page_stride + w.rest : 0;
+    const long long row_off = Bits == 4 || !row_ok ? 0 : w.page * p.c.page_stride + w.rest;
+    const uint32_t row_unit = Bits == 4 && row_ok ? w.page * p.page_u + w.unit : 0u;
     mask = __ballot_sync(0xffffffffu, row_ok) & kAllKeys;
     if constexpr (Bits == 4) {
       if (lane == 0) s_mask[warp][s] = mask;
@@ -611,15 +619,17 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       if (Bits == 4 && mask == kAllKeys) {  // nothing left out
 #pragma unroll
         for (int j = 0; j < kKeys / kPer; ++j) {
-          const long long off = __shfl_sync(0xffffffffu, row_off, j * kPer + lane / kChunks) + c * 16;
-          cp_async16(sk + first_k + j * kPer * S::kRowBytes, p.c.k + off, 16u);
-          cp_async16(sv + first_v + j * kPer * S::kRowBytes, p.c.v + off, 16u);
+          const uint32_t unit = __shfl_sync(0xffffffffu, row_unit, j * kPer + lane / kChunks);
+          cp_async16(sk + first_k + j * kPer * S::kRowBytes, lane_k + static_cast<unsigned long long>(unit) * p.unit, 16u);
+          cp_async16(sv + first_v + j * kPer * S::kRowBytes, lane_v + static_cast<unsigned long long>(unit) * p.unit, 16u);
         }
       } else
 #pragma unroll
       for (int j = 0; j < kKeys / kPer; ++j) {
         const int key = j * kPer + lane / kChunks;
-        const long long off = __shfl_sync(0xffffffffu, row_off, key) + c * 16;
+        long long off;
+        if constexpr (Bits == 4) off = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, row_unit, key)) * p.unit + c * 16;
+        else off = __shfl_sync(0xffffffffu, row_off, key) + c * 16;
         const uint32_t bytes = (mask >> key) & 1u ? 16u : 0u;  // 0: filled with zeros, nothing is read
         uint32_t ck, cv;  // 16-byte chunks are permuted within a row (4 bits: within 128 bytes) so that no read below conflicts
         if constexpr (Bits == 4) {
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         cp_async16(sv + cv, p.c.v + off, bytes);
       }
       if constexpr (Bits == 4) {  // a lane its key's block scales
-        const long long scales = row_ok ? w.page * p.c.page_blocks + w.scales : 0;
+        const unsigned long long scales = static_cast<unsigned long long>(row_ok ? w.page * p.page_ub + w.unit_b : 0u) * p.unit_b;
         const uint32_t dst = sk + 2 * S::kHalf + lane * S::kScaleBytes, bytes = row_ok ? S::kScaleBytes : 0;
         cp_async_small<S::kScaleBytes>(dst, p.c.k_blocks + scales, bytes);
         cp_async_small<S::kScaleBytes>(dst + kKeys * S::kScaleBytes, p.c.v_blocks + scales, bytes);
@@ -699,10 +709,15 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         // 2^-e and 2^e for top in [2^e, 2^(e+1)), e kept to where both are normal
         int e = static_cast<int>(__float_as_uint(top) >> 23);
         e = e < 2 ? 2 : e > 252 ? 252 : e;
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
         sc[b][0] = sl2 * __shfl_sync(0xffffffffu, up, 8 * t);      // column 2t lives in lanes g = 2t
         sc[b][1] = sl2 * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+        if constexpr (Bits == 4) {  // the factor's sign goes to q; a factor of 0 (or nearly) would make NaN of -inf
+          if (sl2 < 0.f) down = -down;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sc[b][j] = fabsf(sc[b][j]) < 1e-37f ? 1e-37f : fabsf(sc[b][j]);
+        }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           qf[i][b][0] = from_f32x2<__half>(x[2 * i].x * down, x[2 * i].y * down);
@@ -821,11 +836,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         }
       }
       bool moved = false;
-      if constexpr (Bits == 4) {  // (the fewest instructions: they are what bounds it)
-#pragma unroll
-        for (int u = 0; u < kU * NB; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[u][j] *= sc[u % NB][j & 1];
+      float top[NB][2];  // 4 bits: this thread's largest scores
+      if constexpr (Bits == 4) {  // (the fewest instructions: they are what bounds it; sc > 0, so maxima need no scaling)
         if (mask != kAllKeys) {
 #pragma unroll
           for (int u = 0; u < kU; ++u)
@@ -840,10 +852,11 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(x[b][j], x[b][j + 2]);
+            top[b][j] = fmaxf(x[b][j], x[b][j + 2]);
 #pragma unroll
-            for (int u = 1; u < kU; ++u) top = fmax3(top, x[u * NB + b][j], x[u * NB + b][j + 2]);
-            moved |= top > m[b][j] + (8.f + kWeightBits<M>);
+            for (int u = 1; u < kU; ++u) top[b][j] = fmax3(top[b][j], x[u * NB + b][j], x[u * NB + b][j + 2]);
+            top[b][j] *= sc[b][j];
+            moved |= top[b][j] > m[b][j] + (8.f + kWeightBits<M>);
           }
       } else {
 #pragma unroll
@@ -860,13 +873,11 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(x[b][j], x[b][j + 2]);
-#pragma unroll
-            for (int u = 1; u < kU; ++u) top = fmax3(top, x[u * NB + b][j], x[u * NB + b][j + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float mn = fmaxf(m[b][j], top - kWeightBits<M>);
+            float most = Bits == 4 ? top[b][j] : fmaxf(x[b][j], x[b][j + 2]);
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+            const float mn = fmaxf(m[b][j], most - kWeightBits<M>);
             const float keep = mn == -INFINITY ? 0.f : ex2_approx(m[b][j] - mn);
             m[b][j] = mn;
             l[b][j] *= keep;
@@ -885,10 +896,23 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float w[4];
+          if constexpr (Bits == 4) {
+            const unsigned long long base = f2(m[b][0] == -INFINITY ? 0.f : -m[b][0], m[b][1] == -INFINITY ? 0.f : -m[b][1]);
+            const unsigned long long by = f2(sc[b][0], sc[b][1]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] = ex2_approx(x[u * NB + b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
-            l[b][j & 1] += w[j];
+            for (int e = 0; e < 2; ++e) {
+              float y0, y1;
+              f2_split(ffma2(f2(x[u * NB + b][2 * e], x[u * NB + b][2 * e + 1]), by, base), y0, y1);
+              w[2 * e] = ex2_approx(y0);
+              w[2 * e + 1] = ex2_approx(y1);
+              f2_split(fadd2(f2(l[b][0], l[b][1]), f2(w[2 * e], w[2 * e + 1])), l[b][0], l[b][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = ex2_approx(x[u * NB + b][j] - (m[b][j & 1] == -INFINITY ? 0.f : m[b][j & 1]));
+              l[b][j & 1] += w[j];
+            }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -922,7 +946,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
               w[k][0] = lds32((k & 1 ? v_odd : v_even) + ((16 * u + 8 * (k >> 1)) * S::kRowBytes));
             }
           }
-          const uint32_t s01 = widen_e4m3x2(sb[0] | (sb[1] << 8)), s23 = widen_e4m3x2(sb[2] | (sb[3] << 8));
+          const uint32_t s01 = widen_e4m3x2(__byte_perm(sb[0], sb[1], 0x5540)), s23 = widen_e4m3x2(__byte_perm(sb[2], sb[3], 0x5540));
 #pragma unroll
           for (int i = 0; i < kW; ++i) {
             uint32_t e01[4], o01[4], e23[4], o23[4];
@@ -1267,6 +1291,21 @@ static int paged_blocks(int heads, int kv_heads) {
   return (heads / kv_heads + paged_rows(heads, kv_heads) - 1) / paged_rows(heads, kv_heads);
 }
 
+// Strides (bytes) in units of the largest power of two that divides them; false if 32 bits of these do not reach every row.
+static bool units(long long page, long long row, long long head, const tl_paged_cache* c, uint32_t& page_u, uint32_t& row_u,
+                  uint32_t& head_u, uint32_t& unit) {
+  const unsigned long long all = static_cast<unsigned long long>(page | row | head);
+  unit = all == 0 ? 1u : static_cast<uint32_t>(all & -all & 0x7fffffffull);
+  if (unit == 0) unit = 1u << 30;
+  const __int128 last = (static_cast<__int128>(page) * (c->num_pages - 1) + static_cast<__int128>(row) * (c->page_size - 1) +
+                         static_cast<__int128>(head) * (c->kv_heads - 1)) / unit;
+  if (last >= (static_cast<__int128>(1) << 32)) return false;
+  page_u = static_cast<uint32_t>(page / unit);
+  row_u = static_cast<uint32_t>(row / unit);
+  head_u = static_cast<uint32_t>(head / unit);
+  return true;
+}
+
 extern "C" size_t tl_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int d) {
   if (batch < 0 || batch > 4096 || !heads_ok(heads, kv_heads, d)) return 0;
   const int rows = paged_rows(heads, kv_heads) == 8 ? 32 : 16;  // Shape::kPartRows
@@ -1319,6 +1358,10 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   long long cap = static_cast<long long>(max_pages) * cache->page_size;
   if (window > 0 && cap > static_cast<long long>(window) + sinks) cap = static_cast<long long>(window) + sinks;
   // kv heads read together: side by side, as many as make 256 bytes of a token
+  if (cache->dtype == TL_E2M1 &&
+      (!units(p.c.page_stride, p.c.row_stride, p.c.head_stride, cache, p.page_u, p.row_u, p.head_u, p.unit) ||
+       !units(p.c.page_blocks, p.c.row_blocks, p.c.head_blocks, cache, p.page_ub, p.row_ub, p.head_ub, p.unit_b)))
+    return TL_ERR_INVALID;
   const int bits = cache->dtype == TL_E2M1 ? 4 : cache->dtype == TL_E4M3 ? 8 : 16, row_bytes = cache->d * bits / 8;
   p.lw = 0;
   if (p.group <= 8 && p.c.head_stride == row_bytes)

@@ -553,6 +553,8 @@ int tl_kv_gather(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const int*
  * over several CTAs.
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
  * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
+ * A 4-bit cache's codes reach over less than 2^32 units of the largest power of two that divides their strides (rows side by
+ * side, d 64: 128 GB), its block scales likewise.
  * batch == 0 or heads == 0 is a no-op.
  * Precision: scores, weights and all sums are fp32.  Where a weight meets V it is a sum of two terms of dtype, off by
  * half a step squared; with an e4m3 or 4-bit cache one fp16 term, and in tl_window_attention one term of dtype, off by half
