@@ -483,12 +483,12 @@ _NO_BLOCKS = _pack_blocks(0, 0, 0, 0, 0)
 def _cache(k_cache, v_cache, k_scale, v_scale, k_blocks=None, v_blocks=None):
     """A tl_paged_cache (as bytes) and its kv heads and d."""
     shape, strides = k_cache.shape, k_cache.stride()
-    code, tail = _codes.get(k_cache.dtype), _NO_BLOCKS
-    if k_blocks is not None or v_blocks is not None:
-        tail = _blocks(k_cache, k_blocks, v_blocks)
-        code = TL_E2M1
-    elif code is None or not k_cache.is_cuda:
-        code = _code(k_cache, "k_cache")
+    if k_blocks is None and v_blocks is None:
+        code, tail = _codes.get(k_cache.dtype), _NO_BLOCKS
+        if code is None or not k_cache.is_cuda:
+            code = _code(k_cache, "k_cache")
+    else:
+        code, tail = TL_E2M1, _blocks(k_cache, shape, k_blocks, v_blocks)
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or not v_cache.is_cuda:
         raise ValueError("k_cache and v_cache must be alike: [pages, page_size, kv_heads, d]")
     pages, page, heads, d = shape
@@ -504,18 +504,19 @@ def _cache(k_cache, v_cache, k_scale, v_scale, k_blocks=None, v_blocks=None):
                        b if page > 1 else 0, c if heads > 1 else 0, code, pages, page, heads, d) + tail, heads, d
 
 
-def _blocks(k_cache, k_blocks, v_blocks):
+def _blocks(k_cache, codes, k_blocks, v_blocks):
     """The end of a 4-bit cache's tl_paged_cache: uint8 codes [pages, page_size, kv_heads, d / 2], e4m3 scales [.., d / 16]."""
     if k_blocks is None or v_blocks is None or k_cache.dtype is not _dtype_of("u8") or not k_cache.is_cuda:
         raise ValueError("a 4-bit cache is CUDA uint8 codes with k_blocks and v_blocks")
-    shape, strides = k_blocks.shape, k_blocks.stride()
-    for t in (k_blocks, v_blocks):
-        if t.dtype is not _dtype_of("e4m3") or not t.is_cuda or k_cache.dim() != 4 or t.shape != (*k_cache.shape[:3], k_cache.shape[3] // 8):
-            raise ValueError("k_blocks and v_blocks must be CUDA float8_e4m3fn [pages, page_size, kv_heads, d / 16]")
-    pages, page, heads, n = shape
-    a, b, c, one = strides
-    if (one != 1 and n > 1) or any(m > 1 and s != t for m, s, t in zip(shape, strides, v_blocks.stride())):
+    e4m3, shape, strides = _dtypes["e4m3"], k_blocks.shape, k_blocks.stride()
+    if k_blocks.dtype is not e4m3 or v_blocks.dtype is not e4m3 or not k_blocks.is_cuda or not v_blocks.is_cuda or \
+            len(shape) != 4 or len(codes) != 4 or v_blocks.shape != shape or codes[:3] != shape[:3] or codes[3] != 8 * shape[3]:
+        raise ValueError("k_blocks and v_blocks must be CUDA float8_e4m3fn [pages, page_size, kv_heads, d / 16]")
+    if strides[3] != 1 or v_blocks.stride() != strides and any(
+            n > 1 and s != t for n, s, t in zip(shape, strides, v_blocks.stride())):
         raise ValueError("k_blocks and v_blocks must have the same strides, the last one 1")
+    pages, page, heads, _ = shape
+    a, b, c, _ = strides
     return _pack_blocks(k_blocks.data_ptr(), v_blocks.data_ptr(), a if pages > 1 else 0, b if page > 1 else 0,
                         c if heads > 1 else 0)
 
