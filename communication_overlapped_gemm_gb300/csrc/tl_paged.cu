@@ -481,22 +481,19 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   __shared__ unsigned s_last;
   __shared__ uint32_t s_mask[kWarps][Bits == 4 ? kStages : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int subs = (p.c.kv_heads >> p.lw) * p.blocks;
-  const int shift = S::kTileBits - p.lw;
-  // this warp's kv head of an item's, and its 16 (32) keys of a tile's
-  const int hw = warp & ((1 << p.lw) - 1), kb = warp >> p.lw;
-
+  int lw = Bits == 4 ? 0 : p.lw;  // (log2 of an item's kv heads; over 4 bits by the number of tiles, below)
+  int subs = (p.c.kv_heads >> lw) * p.blocks, shift = S::kTileBits - lw;
   // ---------------------------------------------------------------- plan
   // Thread i sums the tiles of sequences [i chunk, (i + 1) chunk); s_sum holds the sums inside a warp.
   const int chunk = (p.batch + kThreads - 1) / kThreads;
-  {
+  auto tile_sums = [&](bool once) {
     uint32_t sum = 0;
     for (int i = 0; i < chunk; ++i) {
       const int b = static_cast<int>(threadIdx.x) * chunk + i;
       if (b >= p.batch) break;
-      const int count = visible_rows(paged_length(p, b, blockIdx.x == 0), p.window, p.sinks).count;
+      const int count = visible_rows(paged_length(p, b, once && blockIdx.x == 0), p.window, p.sinks).count;
       sum += paged_tiles(count, shift);
-      if (count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
+      if (once && count == 0 && b % gridDim.x == blockIdx.x) {  // nothing visible: no item
         for (int h = 0; h < p.heads; ++h) {
           uint4* o = reinterpret_cast<uint4*>(p.out + b * p.out_seq + h * p.out_head);
           for (int v = 0; v < D / 8; ++v) o[v] = make_uint4(0, 0, 0, 0);
@@ -512,17 +509,39 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     s_sum[threadIdx.x] = sum;
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-  }
+  };
+  tile_sums(true);
   uint32_t total = 0;  // below 2^31 (the host checks)
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += s_warp[w];
   total *= subs;
+  if constexpr (Bits == 4) {
+    // Rows are short, and kv heads that are read together join as one item of 32 rows, which costs more than scattered
+    // reads do where there is little to read: heads apart up to 10 tiles a CTA, two up to 30, then as many as make 256 bytes.
+    // One sequence of 8k rows of 8 heads of 128 12.7 us with heads apart, 19.8 by four; 16 of 8k 54, by two 42, by four 45; 64
+    // of 16k 461, 261, 231.
+    const uint32_t share = total / gridDim.x;
+    const int want = share < 10 ? 0 : share < 30 ? 1 : 2;
+    if (want > 0 && p.lw > 0) {
+      lw = min(want, p.lw);
+      subs = (p.c.kv_heads >> lw) * p.blocks;
+      shift = S::kTileBits - lw;
+      __syncthreads();
+      tile_sums(false);
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) total += s_warp[w];
+      total *= subs;
+    }
+  }
+  // this warp's kv head of an item's, and its 16 (32) keys of a tile's
+  const int hw = warp & ((1 << lw) - 1), kb = warp >> lw;
   // Tiles of a CTA: an even share, but, by the mean item, no more than 32 parts of an item, and no more than 16 if
   // that takes a CTA up to 2 tiles (4 or 8 of the shorter ones of `wh` heads): a join waits for 16 parts at a
   // time.  One sequence of 2k and 8k rows by the even share alone: bf16 8.3 and 11.3 us, e4m3 15.4 and 21.5; so
-  // 7.6, 11.4, 9.8 and 15.5.
+  // 7.6, 11.4, 9.8 and 15.5.  (Over 4 bits, with tiles of 128 keys, 16 up to 4 tiles: one of 8k rows 11.4 us, 12.2 up to 2.)
   const uint32_t mean = (total + p.batch * subs - 1) / (p.batch * subs);
-  const uint32_t per = max(max((total + gridDim.x - 1) / gridDim.x, (mean + 31) / 32), min((mean + 15) / 16, 2u << p.lw));
+  const uint32_t per = max(max((total + gridDim.x - 1) / gridDim.x, (mean + 31) / 32), min((mean + 15) / 16, (Bits == 4 ? 4u : 2u) << lw));
   // (where an item's parts are limited, `per` is up to grid / 32 even shares: 20 times the line does not fit 32 bits)
   const unsigned long long line = static_cast<unsigned long long>(per) * blockIdx.x;
   if (line >= total) return;
@@ -584,13 +603,13 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     w.rest = 0;
     w.unit = w.unit_b = 0u;
     w.b = a.b;
-    const int i = a.tile * (kTile >> p.lw) + kb * kKeys + (lane & (kKeys - 1));
+    const int i = a.tile * (kTile >> lw) + kb * kKeys + (lane & (kKeys - 1));
     if (more && i < a.vis.count) {
       const int row = i < a.vis.head ? i : i + a.vis.skip;
       const uint32_t pg = divide(static_cast<uint32_t>(row), p.by_page);
       w.page = __ldg(p.table + static_cast<long long>(a.b) * p.max_pages + pg);
       w.wanted = true;
-      const int in_page = row - static_cast<int>(pg) * p.c.page_size, head = ((NB == 1 ? a.sub : a.sub / p.blocks) << p.lw) + hw;
+      const int in_page = row - static_cast<int>(pg) * p.c.page_size, head = ((NB == 1 ? a.sub : a.sub / p.blocks) << lw) + hw;
       if constexpr (Bits == 4) {
         w.unit = in_page * p.row_u + head * p.head_u;
         w.unit_b = in_page * p.row_ub + head * p.head_ub;
@@ -691,7 +710,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
     // a segment: this CTA's tiles of one item
     const int seg_tile = at.tile;
     const int seg = nsteps - step < at.tiles - at.tile ? nsteps - step : at.tiles - at.tile;
-    const int hk0 = (NB == 1 ? at.sub : at.sub / p.blocks) << p.lw, hk = hk0 + hw;  // (NB 1: one block)
+    const int hk0 = (NB == 1 ? at.sub : at.sub / p.blocks) << lw, hk = hk0 + hw;  // (NB 1: one block)
     const int r0 = NB == 1 ? 0 : at.sub % p.blocks * kRows, h0 = hk * p.group + r0;
     const int rows = p.group - r0 < kRows ? p.group - r0 : kRows;
     // q as the products' B: column g of block b (zero past the group)
@@ -1045,7 +1064,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       }
     __syncthreads();
     const bool whole = seg == at.tiles;
-    const int all = rows << p.lw, vecs = all * (D / 4);  // the item's query heads; float4s of them
+    const int all = rows << lw, vecs = all * (D / 4);  // the item's query heads; float4s of them
     float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (seg_tile ? 0 : 1)) * S::kPart;
     auto head_of = [&](int r) { return NB == 1 ? (r >= rows) + (r >= 2 * rows) + (r >= 3 * rows) : 0; };  // of the item's
     auto write_out = [&](int r, int d, float4 v, float mm, float ll) {
@@ -1067,9 +1086,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
       const int head = head_of(r), row = r - head * rows;
       float mm = -INFINITY, ll = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = head; w < kWarps; w += 1 << p.lw) mm = fmaxf(mm, ml[w * kRows + row].x);
+      for (int w = head; w < kWarps; w += 1 << lw) mm = fmaxf(mm, ml[w * kRows + row].x);
       const float base = mm == -INFINITY ? 0.f : mm;
-      for (int w = head; w < kWarps; w += 1 << p.lw) {
+      for (int w = head; w < kWarps; w += 1 << lw) {
         const float2 z = ml[w * kRows + row];
         const float f = ex2_approx(z.x - base);
         ll += f * z.y;
@@ -1377,8 +1396,11 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
   p.lw = 0;
   if (p.group <= 8 && p.c.head_stride == row_bytes)
     while (p.lw < 2 && (row_bytes << p.lw) < 256 && cache->kv_heads % (2 << p.lw) == 0) ++p.lw;
-  const long long most = batch * static_cast<long long>(cache->kv_heads >> p.lw) * p.blocks *
-                         ((cap >> (paged::tile_bits(bits) - p.lw)) + 1);
+  long long most = 0;  // (over 4 bits the kernel reads 1 to 1 << p.lw heads together)
+  for (int w = bits == 4 ? 0 : p.lw; w <= p.lw; ++w) {
+    const long long tiles = batch * static_cast<long long>(cache->kv_heads >> w) * p.blocks * ((cap >> (paged::tile_bits(bits) - w)) + 1);
+    if (tiles > most) most = tiles;
+  }
   if (most >= (1LL << 31)) return TL_ERR_INVALID;
   return dispatch(dtype, cache->dtype, cache->d, [&](auto t, auto bits, auto d) {
     auto launch = [&](auto nb) {
