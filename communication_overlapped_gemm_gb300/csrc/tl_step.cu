@@ -37,28 +37,35 @@ constexpr int kMaxBatch = 4096, kChunk = kMaxBatch / kThreads;
 constexpr uint32_t kMost = 0x7fffffffu;
 // Sums stop at 2^31 - 1 (in any order): whatever lies there is past every buffer.
 __device__ __forceinline__ uint32_t sat(uint32_t a, uint32_t b) { return min(a + b, kMost); }
-// The sum over all threads before this one, and the sum over all.
-__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* warps, uint32_t& all) {
+// The sums over all threads before this one, and those over all, of N numbers.
+template <int N>
+__device__ __forceinline__ void scan(uint32_t (&v)[N], uint32_t (*warps)[kWarps], uint32_t (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t s = v;
+  uint32_t s[N];
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, s, x);
-    if (lane >= x) s = sat(s, o);
+  for (int n = 0; n < N; ++n) {
+    s[n] = v[n];
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, s[n], x);
+      if (lane >= x) s[n] = sat(s[n], o);
+    }
+    if (lane == 31) warps[n][warp] = s[n];
   }
-  if (lane == 31) warps[warp] = s;
   __syncthreads();
-  const uint32_t mine = lane < kWarps ? warps[lane] : 0u;
-  uint32_t t = mine;
 #pragma unroll
-  for (int x = 1; x < kWarps; x <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, t, x);
-    if (lane >= x) t = sat(t, o);
+  for (int n = 0; n < N; ++n) {
+    uint32_t t = lane < kWarps ? warps[n][lane] : 0u;
+#pragma unroll
+    for (int x = 1; x < kWarps; x <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, t, x);
+      if (lane >= x) t = sat(t, o);
+    }
+    all[n] = __shfl_sync(0xffffffffu, t, kWarps - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, t, warp ? warp - 1 : 0);
+    const uint32_t up = __shfl_up_sync(0xffffffffu, s[n], 1);
+    v[n] = sat(warp ? before : 0u, lane ? up : 0u);
   }
-  all = __shfl_sync(0xffffffffu, t, kWarps - 1);
-  const uint32_t before = __shfl_sync(0xffffffffu, t, warp ? warp - 1 : 0);
-  const uint32_t up = __shfl_up_sync(0xffffffffu, s, 1);
-  return sat(warp ? before : 0u, lane ? up : 0u);
 }
 // The last b with bounds[b] <= i, for bounds[0] = 0 (so it holds i if any does).
 __device__ __forceinline__ int find(const int* bounds, int n, int i) {
@@ -106,8 +113,9 @@ __global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p
     sum_q = sat(sum_q, cnt[i]);
     sum_p = sat(sum_p, need[i]);
   }
-  uint32_t all_q, all_p, all_k;
-  uint32_t at_q = scan(sum_q, s_warps[0], all_q), at_p = scan(sum_p, s_warps[1], all_p);
+  uint32_t at[2] = {sum_q, sum_p}, all[2];
+  scan(at, s_warps, all);
+  uint32_t &at_q = at[0], &at_p = at[1];
   // A sequence gets its tokens if they and its pages are there: those that do not fit are the last ones.
   uint32_t sum_k = 0, used = 0;
 #pragma unroll
@@ -128,17 +136,18 @@ __global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p
     s_len[b] = cnt[i] < 0 ? ~len[i] : len[i];
     sum_k = sat(sum_k, len[i] + max(cnt[i], 0));
   }
-  uint32_t at_k = scan(sum_k, s_warps[2], all_k);
+  if (threadIdx.x == 0) s_q[p.batch] = static_cast<int>(all[0]);
+  if (p.cu_k || p.kv_slots) {
+    uint32_t at_k[1] = {sum_k}, all_k[1];
+    scan(at_k, s_warps + 2, all_k);
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) {
-    const int b = b0 + i;
-    if (i >= chunk || b >= p.batch) continue;
-    s_k[b] = static_cast<int>(at_k);
-    at_k = sat(at_k, len[i] + max(cnt[i], 0));
-  }
-  if (threadIdx.x == 0) {
-    s_q[p.batch] = static_cast<int>(all_q);
-    s_k[p.batch] = static_cast<int>(all_k);
+    for (int i = 0; i < kChunk; ++i) {
+      const int b = b0 + i;
+      if (i >= chunk || b >= p.batch) continue;
+      s_k[b] = static_cast<int>(at_k[0]);
+      at_k[0] = sat(at_k[0], len[i] + max(cnt[i], 0));
+    }
+    if (threadIdx.x == 0) s_k[p.batch] = static_cast<int>(all_k[0]);
   }
   // the most pages that a sequence which gets its tokens ends at
   {
@@ -465,22 +474,27 @@ extern "C" int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts,
   if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
   const void* kern = in_place ? reinterpret_cast<const void*>(plan_kernel<true>) : reinterpret_cast<const void*>(plan_kernel<false>);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   static std::atomic<unsigned long long> ready[2];
-  if (!smem_ready(ready[in_place], ctx->device, kern, (4 * plan::kMaxBatch + 2) * 4)) return TL_ERR_CUDA;
+  if (smem > (48 << 10) - 1024 && !smem_ready(ready[in_place], ctx->device, kern, (4 * plan::kMaxBatch + 2) * 4)) return TL_ERR_CUDA;
+  if (!in_place || ctas == 1) {  // (nothing written that another CTA reads; or a CTA's own barrier is enough)
+    if (in_place) plan_kernel<true><<<1, plan::kThreads, smem, st>>>(p);
+    else plan_kernel<false><<<static_cast<unsigned>(ctas), plan::kThreads, smem, st>>>(p);
+    return launched();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(plan::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = in_place ? 1 : 0;
-  const cudaError_t e = in_place ? cudaLaunchKernelEx(&cfg, plan_kernel<true>, p) : cudaLaunchKernelEx(&cfg, plan_kernel<false>, p);
-  if (e != cudaSuccess) {
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, plan_kernel<true>, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return TL_ERR_CUDA;
   }
