@@ -510,7 +510,7 @@ def _blocks(k_cache, codes, k_blocks, v_blocks):
         raise ValueError("a 4-bit cache is CUDA uint8 codes with k_blocks and v_blocks")
     e4m3, shape, strides = _dtypes["e4m3"], k_blocks.shape, k_blocks.stride()
     if k_blocks.dtype is not e4m3 or v_blocks.dtype is not e4m3 or not k_blocks.is_cuda or not v_blocks.is_cuda or \
-            len(shape) != 4 or len(codes) != 4 or v_blocks.shape != shape or codes[:3] != shape[:3] or codes[3] != 8 * shape[3]:
+            len(codes) != 4 or v_blocks.shape != shape or shape != (*codes[:3], codes[3] >> 3) or codes[3] & 7:
         raise ValueError("k_blocks and v_blocks must be CUDA float8_e4m3fn [pages, page_size, kv_heads, d / 16]")
     if strides[3] != 1 or v_blocks.stride() != strides and any(
             n > 1 and s != t for n, s, t in zip(shape, strides, v_blocks.stride())):

@@ -1,11 +1,14 @@
 """A small decoder served with the library: prompts, then one token at a time.
 
-Each layer is attention and a mixture of experts, with random weights.  A prompt's tokens go through
-``tl_window_attention`` (every other layer with a sliding window and sinks), their K and V rows
-into pages by ``tl_kv_append``; then every step appends one row per sequence and attends to the
-pages with ``tl_paged_attention``.  The experts run in ``tl_moe_combine`` for a prompt of more than
-128 tokens and in ``tl_moe_tokens`` for the few tokens of a step.  The decoding step is captured
-into a CUDA graph once and replayed.  At the end the same tokens are run as prompts, and the logits of
+Each layer is attention and a mixture of experts, with random weights.  ``tl_cache_plan`` works out where new
+tokens go: pages from a list of free ones, slots, positions, bounds.  Queries and keys pass through
+``tl_norm_rope`` (a norm of each head and the rotation by position), K and V rows go into pages by
+``tl_kv_append``.  A prompt's tokens then attend with ``tl_window_attention`` (every other layer with a sliding window
+and sinks) to the rows read back by ``tl_kv_gather``, so that prompts and steps see the same 16-, 8- or 4-bit rows; a
+step's tokens attend to the pages with ``tl_paged_attention``.  The experts run in ``tl_moe_combine`` for a prompt of more than
+128 tokens and in ``tl_moe_tokens`` for the few tokens of a step, and ``tl_token_logprobs`` picks the next token with its log
+probability.  A decoding step, from its plan to its next token, is captured into a CUDA graph once and replayed: lengths,
+pages and tokens go on by themselves.  At the end the same tokens are run as prompts, and the logits of
 every sequence's last token are compared.
 
     python examples/decode.py --batch 4 --prompt 200 --steps 16
@@ -28,9 +31,9 @@ class Decoder:
     """Weights, the paged cache of every layer, and the two ways through: prompts and steps."""
 
     def __init__(self, ctx, layers=2, hidden=512, heads=8, kv_heads=2, d=64, experts=16, ffn=256, topk=2, vocab=1000,
-                 window=64, sinks=4, cache_dtype=BF, seed=0):
+                 window=64, sinks=4, cache="bf16", seed=0):
         self.ctx, self.hidden, self.heads, self.kv, self.d, self.topk = ctx, hidden, heads, kv_heads, d, topk
-        self.sinks, self.cache_dtype = sinks, cache_dtype
+        self.sinks, self.format = sinks, cache
         gen = torch.Generator(device="cuda").manual_seed(seed)
 
         def w(*shape):
@@ -40,23 +43,43 @@ class Decoder:
         self.head = w(hidden, vocab)
         self.layers = [dict(qkv=w(hidden, (heads + 2 * kv_heads) * d), o=w(heads * d, hidden), router=w(hidden, experts),
                             gate=w(experts, hidden, ffn), up=w(experts, hidden, ffn), down=w(experts, ffn, hidden),
+                            q_norm=1 + w(d, 1)[:, 0], k_norm=1 + w(d, 1)[:, 0],
                             window=window if i % 2 else 0) for i in range(layers)]
-        self.scale = None if cache_dtype == BF else torch.full((kv_heads,), 0.02, device="cuda")
+        self.freq = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().cuda()
+        # of an 8-bit cache 448 stands for 9, of a 4-bit one 6 times 448: values of rows whose mean square is 1 lie within
+        scale = {"bf16": None, "e4m3": 0.02, "e2m1": 0.02 / 6}[cache]
+        self.scale = None if scale is None else torch.full((kv_heads,), scale, device="cuda")
         few = tl.tl_moe_tokens_workspace_bytes(128, hidden, experts, ffn, topk)
         decode = tl.tl_paged_attention_workspace_bytes(256, heads, kv_heads, d)
-        self.work = torch.zeros(max(few, decode), dtype=torch.uint8, device="cuda")  # one for both, in turn
+        score = tl.tl_token_logprobs_workspace_bytes(256, vocab, 1)
+        self.work = torch.zeros(max(few, decode, score), dtype=torch.uint8, device="cuda")  # one for all, in turn
         self.shape = (experts, ffn)
 
     def open(self, batch, longest, page=16):
-        """Pages for `batch` sequences of up to `longest` tokens, in any order."""
+        """Pages for `batch` sequences of up to `longest` tokens, all free, in any order."""
         self.page, per = page, -(-longest // page)
-        shape = (batch * per, page, self.kv, self.d)
-        self.cache = [[torch.zeros(shape, dtype=BF, device="cuda").to(self.cache_dtype) for _ in "kv"] for _ in self.layers]
-        self.table = torch.randperm(batch * per, device="cuda").to(torch.int32).view(batch, per)
+        pages, row = batch * per, (page, self.kv, self.d)
+        if self.format == "e2m1":
+            row = (page, self.kv, self.d // 2)
+            blocks = [torch.zeros((pages, page, self.kv, self.d // 16), device="cuda").to(torch.float8_e4m3fn) for _ in range(2 * len(self.layers))]
+        kind = {"bf16": BF, "e4m3": torch.float8_e4m3fn, "e2m1": torch.uint8}[self.format]
+        self.cache = [[torch.zeros((pages, *row), device="cuda").to(kind) for _ in "kv"] for _ in self.layers]
+        self.kinds = [dict(k_scale=self.scale, v_scale=self.scale) for _ in self.layers]
+        if self.format == "e2m1":
+            for i, k in enumerate(self.kinds):
+                k.update(k_blocks=blocks[2 * i], v_blocks=blocks[2 * i + 1])
+        ints = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.table, self.lengths, self.taken = ints(batch, per) - 1, ints(batch), ints(1)
+        self.free = torch.randperm(pages, device="cuda").to(torch.int32)
 
-    def slots(self, seq, pos):
-        page = torch.div(pos, self.page, rounding_mode="floor")
-        return (self.table[seq, page] * self.page + pos % self.page).to(torch.int32)
+    def plan(self, tokens, counts=None, rows=0):
+        """Where `tokens` new rows go, and the slots of all `rows`; lengths, table and pages taken are brought up to date."""
+        batch = self.lengths.numel()
+        slots, positions, all_slots = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (tokens, tokens, rows))
+        cu_q, cu_k = (torch.empty(batch + 1, dtype=torch.int32, device="cuda") for _ in "qk")
+        tl.tl_cache_plan(self.ctx, self.lengths, self.table, self.page, self.free, self.taken, self.taken, self.lengths, cu_q, slots,
+                         positions, counts=counts, cu_k=cu_k, kv_slots=all_slots if rows else None)
+        return slots, positions, cu_q, cu_k, all_slots
 
     def norm(self, x):
         f = x.float()
@@ -73,33 +96,46 @@ class Decoder:
             tl.tl_moe_combine(*args, torch.zeros(n, dtype=torch.uint8, device="cuda"))
         return (x.float() + out).to(BF)
 
-    def qkv(self, layer, x):
+    def qkv(self, layer, x, positions):
         rows = (self.norm(x) @ layer["qkv"]).view(-1, self.heads + 2 * self.kv, self.d)
-        return rows[:, :self.heads], rows[:, self.heads:self.heads + self.kv], rows[:, self.heads + self.kv:]
+        q, k, v = rows[:, :self.heads], rows[:, self.heads:self.heads + self.kv], rows[:, self.heads + self.kv:]
+        tl.tl_norm_rope(self.ctx, q, k, positions, self.freq, q, k, q_weight=layer["q_norm"], k_weight=layer["k_norm"])
+        return q, k, v
 
-    def prompt(self, tokens, cu, slots=None):
-        """Packed prompts; their rows go into the cache at `slots`.  Logits of each sequence's last token."""
+    def prompt(self, tokens, counts, rows):
+        """Packed prompts of `counts` tokens each, after the rows that are there; `rows`: those of all sequences then.
+        Logits of each sequence's last token."""
+        slots, positions, cu_q, cu_k, all_slots = self.plan(tokens.numel(), counts, rows)
         x = self.embed[tokens]
-        for layer, cache in zip(self.layers, self.cache):
-            q, k, v = self.qkv(layer, x)
-            if slots is not None:
-                tl.tl_kv_append(self.ctx, k, v, *cache, slots, k_scale=self.scale, v_scale=self.scale)
+        for layer, cache, kind in zip(self.layers, self.cache, self.kinds):
+            q, k, v = self.qkv(layer, x, positions)
+            tl.tl_kv_append(self.ctx, k, v, *cache, slots, **kind)
+            keys, values = (torch.empty((rows, self.kv, self.d), dtype=BF, device="cuda") for _ in "kv")
+            tl.tl_kv_gather(self.ctx, *cache, all_slots, keys, values, **kind)
             a = torch.empty((x.shape[0], self.heads, self.d), dtype=BF, device="cuda")
-            tl.tl_window_attention(self.ctx, q, k, v, cu, cu, a, window=layer["window"], sinks=self.sinks)
+            tl.tl_window_attention(self.ctx, q, keys, values, cu_q, cu_k, a, window=layer["window"], sinks=self.sinks)
             x = self.experts(layer, (x.float() + (a.flatten(1) @ layer["o"]).float()).to(BF))
-        return self.norm(x[cu[1:].long() - 1]) @ self.head
+        return self.norm(x[cu_q[1:].long() - 1]) @ self.head
 
-    def step(self, tokens, slots, lengths):
-        """One new token of each sequence; `lengths` count it."""
+    def step(self, tokens):
+        """One new token of each sequence: its logits."""
+        slots, positions, *_ = self.plan(tokens.numel())
         x = self.embed[tokens]
-        for layer, cache in zip(self.layers, self.cache):
-            q, k, v = self.qkv(layer, x)
-            tl.tl_kv_append(self.ctx, k, v, *cache, slots, k_scale=self.scale, v_scale=self.scale)
+        for layer, cache, kind in zip(self.layers, self.cache, self.kinds):
+            q, k, v = self.qkv(layer, x, positions)
+            tl.tl_kv_append(self.ctx, k, v, *cache, slots, **kind)
             a = torch.empty((x.shape[0], self.heads, self.d), dtype=BF, device="cuda")
-            tl.tl_paged_attention(self.ctx, q, *cache, self.table, lengths, a, self.work, window=layer["window"],
-                                  sinks=self.sinks, k_scale=self.scale, v_scale=self.scale)
+            tl.tl_paged_attention(self.ctx, q, *cache, self.table, self.lengths, a, self.work, window=layer["window"],
+                                  sinks=self.sinks, **kind)
             x = self.experts(layer, (x.float() + (a.flatten(1) @ layer["o"]).float()).to(BF))
         return self.norm(x) @ self.head
+
+    def choose(self, logits):
+        """The most likely token of each row, and its log probability."""
+        n = logits.shape[0]
+        ids, best = torch.empty((n, 1), dtype=torch.int32, device="cuda"), torch.empty((n, 1), device="cuda")
+        tl.tl_token_logprobs(self.ctx, logits, None, None, self.work, top_logprobs=best, top_ids=ids)
+        return ids[:, 0].long(), best[:, 0]
 
 
 def main(argv=None):
@@ -108,45 +144,52 @@ def main(argv=None):
     ap.add_argument("--prompt", type=int, default=200, help="longest prompt")
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--e2m1", action="store_true", help="a 4-bit cache")
     a = ap.parse_args(argv)
     with tl.Context(0) as ctx:
-        m = Decoder(ctx, cache_dtype=torch.float8_e4m3fn if a.e4m3 else BF)
+        m = Decoder(ctx, cache="e2m1" if a.e2m1 else "e4m3" if a.e4m3 else "bf16")
         lens = torch.tensor([max(1, a.prompt - 37 * b) for b in range(a.batch)])
-        m.open(a.batch, a.prompt + a.steps + 1)
         text = [torch.randint(0, 1000, (int(n),), device="cuda") for n in lens]
 
-        def packed(seqs):
-            cu = torch.zeros(len(seqs) + 1, dtype=torch.int32)
-            cu[1:] = torch.tensor([t.numel() for t in seqs]).cumsum(0)
-            return torch.cat(seqs), cu.cuda()
+        def prompts(seqs):
+            counts = torch.tensor([t.numel() for t in seqs], dtype=torch.int32)
+            return m.prompt(torch.cat(seqs), counts.cuda(), int(counts.sum()))
 
-        tokens, cu = packed(text)
-        seq = torch.repeat_interleave(torch.arange(a.batch), lens).cuda()
-        logits = m.prompt(tokens, cu, m.slots(seq, torch.cat([torch.arange(int(n)) for n in lens]).cuda()))
+        m.open(a.batch, a.prompt + a.steps + 2)
+        new, _ = m.choose(prompts(text))
 
-        # the step, captured once
-        new, lengths = logits.argmax(-1), (lens + 1).to(torch.int32).cuda()
-        slots = m.slots(torch.arange(a.batch, device="cuda"), lengths.long() - 1)
-        m.step(new, slots, lengths)  # warm up
+        # the step, captured once: it takes its tokens from `new` and leaves the next ones there
+        state = [t.clone() for t in (m.table, m.lengths, m.taken, new)]
+        scores = torch.zeros(a.batch, device="cuda")
+
+        def step():
+            logits = m.step(new)
+            following, score = m.choose(logits)
+            new.copy_(following)
+            scores.add_(score)
+            return logits
+
+        step()  # warm up, and back
+        for t, was in zip((m.table, m.lengths, m.taken, new), state):
+            t.copy_(was)
+        scores.zero_()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            out = m.step(new, slots, lengths)
+            out = step()
+        fed = torch.empty((a.steps, a.batch), dtype=torch.int64, device="cuda")
         torch.cuda.synchronize()
         t0 = time.perf_counter()
         for i in range(a.steps):
-            if i:
-                new.copy_(out.argmax(-1))
-                lengths += 1
-                slots.copy_(m.slots(torch.arange(a.batch, device="cuda"), lengths.long() - 1))
-            text = [torch.cat([t, n[None]]) for t, n in zip(text, new)]
+            fed[i].copy_(new)
             graph.replay()
         torch.cuda.synchronize()
         took = (time.perf_counter() - t0) / max(1, a.steps)
         if ctx.check() != tl.TL_OK:
             raise RuntimeError("an index was out of range or a wait ran out")
-        again = m.prompt(*packed(text))
+        m.open(a.batch, a.prompt + a.steps + 2)
+        again = prompts([torch.cat([t, fed[:, b]]) for b, t in enumerate(text)])
         off = float((out.float() - again.float()).norm() / again.float().norm())
-        print(f"{a.steps} steps of {a.batch} sequences, {took * 1e6:.0f} us a step; "
+        print(f"{a.steps} steps of {a.batch} sequences, {took * 1e6:.0f} us a step, log probability {float(scores.mean()):.2f} a sequence; "
               f"last logits against the whole text as a prompt: {off:.4f}")
         return off
 
