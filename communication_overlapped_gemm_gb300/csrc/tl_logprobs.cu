@@ -412,7 +412,7 @@ extern "C" int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, lon
       top > score::kTop || top > vocab || row_stride < 0 || !(scale > 0.f) || scale > 3.0e38f)
     return TL_ERR_INVALID;
   if (rows == 0) return TL_OK;
-  if (rows > (1 << 24) || !logits || !aligned16(logits) || !workspace || !aligned16(workspace) || (logprob && !targets) ||
+  if (rows > (1 << 24) || !logits || reinterpret_cast<uintptr_t>(logits) % (dtype == TL_FP32 ? 4 : 2) != 0 || !workspace || !aligned16(workspace) || (logprob && !targets) ||
       (top > 0 && (!top_logprobs || !top_ids)))
     return TL_ERR_INVALID;
   if (workspace_bytes < tl_token_logprobs_workspace_bytes(rows, vocab, top)) return TL_ERR_WORKSPACE;

@@ -516,7 +516,7 @@ extern "C" int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_t
   for (long long s : strides)
     if (!esize_ok(s, 2)) return TL_ERR_INVALID;
   if (tokens == 0 || heads + static_cast<long long>(kv_heads) == 0) return TL_OK;
-  if (heads + static_cast<long long>(kv_heads) > 65536) return TL_ERR_INVALID;
+  if (heads + static_cast<long long>(kv_heads) > 65536 || tokens >= (1 << 30)) return TL_ERR_INVALID;
   if ((heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) ||
       (kv_heads > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out))) || (rotary > 0 && (!positions || !inv_freq)))
     return TL_ERR_INVALID;

@@ -494,7 +494,7 @@ int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts, int batch,
  * Precision: all sums and products are fp32, rounded once; a row whose squares pass fp32's range becomes 0.  Angles are held
  * as fractions of a turn in 64 bits, so that far positions lose nothing (off by 2^-31 turns where |inv_freq| <= 1);
  * sines and cosines are off by 2^-21 at most.
- * Shapes: d 64 or 128; rotary a multiple of 16, at most d; eps >= 0; heads + kv_heads <= 65536.  tokens == 0 or no
+ * Shapes: d 64 or 128; rotary a multiple of 16, at most d; eps >= 0; heads + kv_heads <= 65536; tokens < 2^30.  tokens == 0 or no
  * heads is a no-op.  No workspace.
  */
 int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride, const void* k,
@@ -621,8 +621,8 @@ int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, con
  *   logprob[r] = ln p[targets[r]],  entropy[r] = - sum_i p_i ln p_i,  lse[r] = ln sum_i exp(scale * x_i),
  *   top_logprobs[r][0 .. top), top_ids[r][0 .. top): the most likely tokens' ln p and indices, best first
  * (equal logits: the lower index first; NaN counts as the lowest).
- * logits: dtype (TL_BF16, TL_FP16 or TL_FP32) [rows x vocab], a row row_stride elements after the one before (any
- * number).  targets: int32 [rows]; a negative target skips its row (padding): its outputs are left as they are; one
+ * logits: dtype (TL_BF16, TL_FP16 or TL_FP32) [rows x vocab], starting at any element, a row row_stride elements after the
+ * one before (any number).  targets: int32 [rows]; a negative target skips its row (padding): its outputs are left as they are; one
  * >= vocab too, and is reported.  targets may be NULL if logprob is: no row is skipped then.  logprob, entropy, lse: fp32
  * [rows], any may be NULL.  top_logprobs: fp32, top_ids: int32 [rows x top].
  * A logit of -inf (a masked token) has probability 0.  Where all of a row are -inf, its entropy is 0 and its
