@@ -184,8 +184,19 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
   {
     const long long mine = first + static_cast<int>(threadIdx.x) * kVec;
     uint4 next[NV];
+    // The vectors of steps i to i + NV - 1; but at a row's ends all of the CTA's lie within it.
+    const int inner = r.end - static_cast<int>(first) >= kThreads * kVec ? (r.end - static_cast<int>(first)) / (kThreads * kVec) : 0;
+    auto fetch = [&](int i) {
+      if (i + NV <= inner && (i > 0 || first >= r.off)) {
+        const uint4* at = reinterpret_cast<const uint4*>(r.base + mine * static_cast<int>(sizeof(T))) + static_cast<long long>(i) * kThreads;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(v) * (kThreads * kVec));
+        for (int v = 0; v < NV; ++v) next[v] = __ldg(at + v * kThreads);
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(i + v) * (kThreads * kVec));
+      }
+    };
+    fetch(0);
     if (target < 0) return;
     if (target >= p.vocab) {
       if (split == 0 && threadIdx.x == 0) report_index(p.status, static_cast<unsigned long long>(row));
@@ -195,10 +206,7 @@ __global__ void __launch_bounds__(score::kThreads, 4) score_kernel(const ScorePa
       uint4 x[NV];
 #pragma unroll
       for (int v = 0; v < NV; ++v) x[v] = next[v];
-      if (i + NV < count) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) next[v] = r.load(mine + static_cast<long long>(i + NV + v) * (kThreads * kVec));
-      }
+      if (i + NV < count) fetch(i + NV);
       float m = sums.m;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
