@@ -445,8 +445,8 @@ extern "C" int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, lon
   p.splits = score_splits(rows, vocab, ctx->sms);
   const unsigned grid = static_cast<unsigned>(rows) * p.splits;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == TL_FP32) score_kernel<float, 4><<<grid, score::kThreads, 0, s>>>(p);
-  else if (dtype == TL_BF16) score_kernel<__nv_bfloat16, 3><<<grid, score::kThreads, 0, s>>>(p);
-  else score_kernel<__half, 3><<<grid, score::kThreads, 0, s>>>(p);
+  if (dtype == TL_FP32) score_kernel<float, 5><<<grid, score::kThreads, 0, s>>>(p);
+  else if (dtype == TL_BF16) score_kernel<__nv_bfloat16, 4><<<grid, score::kThreads, 0, s>>>(p);
+  else score_kernel<__half, 4><<<grid, score::kThreads, 0, s>>>(p);
   return launched();
 }
