@@ -225,10 +225,12 @@ __global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p
 // for its r / 2 pairs, with the angle a = position * inv_freq of the pair.
 // HBM bounds it: each value is read and written once for some 6 operations.  D / 16 threads hold a row, 16 values
 // each: two vectors of 8 whose places are those of eight pairs, so that neither the rotation nor the store needs another
-// thread, and the mean takes 3 (d 64: 2) exchanges.  A CTA takes all rows of a token; its threads work out the next token's
-// angles, one pair each, while they have the rows of this one, and each thread's next row is on its way.
-// 8192 tokens of 32 and 8 heads of 128: 31.3 us, 5.4 TB/s, 0.79 of the copy rate (without the norms 29.2; angles in every
-// thread for itself 36.7, with 24 warps an SM for their registers).  One step of 64: 3.0 us, the launch and two waits.
+// thread, and the mean takes 3 (d 64: 2) exchanges.  A CTA has some rows of a token, the same ones of each of its tokens; its
+// threads work out the next token's angles, one pair each, before they turn to their rows of this one, and each thread's
+// next row is on its way.
+// 8192 tokens of 32 and 8 heads of 128: 30.2 us, 5.6 TB/s, 0.82 of the copy rate (without the norms 29.3; 64 and 8 heads 51,
+// 0.87; angles in every thread for itself 36.7, with 24 warps an SM for their registers; frequencies in turns kept from token to
+// token 32.2).  One step of 64: 2.8 us, the launch and two waits.
 //
 // Angles: a position may be far and a frequency any number, and fp32 would leave a turn of 2^20 with 4 bits
 // behind the point.  So a frequency is held in turns as a 64-bit fraction, F = inv_freq / (2 pi) 2^64, whose product with
@@ -271,15 +273,15 @@ __device__ __forceinline__ float2 unit(unsigned long long turn, int position) {
 }
 }  // namespace rope
 
-// The rows of a CTA at a time: blockDim / (D / 16), which the host chooses so that they divide a token's rows well.
+// A CTA has the same blockDim / (D / 16) rows of each of its tokens, a thread the same part of one row: its places and weights
+// stay in registers.
 template <class T, int D, bool Interleaved>
 __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopeParams p) {
   using namespace rope;
   constexpr int kPer = D / 16;  // threads of a row
-  __shared__ __align__(16) float s_weight[2][D];
   // cosines and sines of a token's pairs, and of the next one's
   __shared__ __align__(16) float s_cos[2][D / 2], s_sin[2][D / 2];
-  const int j = threadIdx.x % kPer, rows_at_once = blockDim.x / kPer;
+  const int j = threadIdx.x % kPer;
   // The vectors (of 8 values) of this thread: a pair's two places lie in both, or side by side in one.  (Interleaved pairs
   // have vectors half a row apart too, so that neighbours read neighbouring ones.)
   const int half = p.rotary / 16;
@@ -296,20 +298,19 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
     va = j < half ? j : 2 * j;
     vb = j < half ? j + half : 2 * j + 1;
   }
-  const int rows = p.heads[0] + p.heads[1], first = blockIdx.y * rows_at_once + threadIdx.x / kPer, step = gridDim.y * rows_at_once;
+  const int r = blockIdx.y * (blockDim.x / kPer) + threadIdx.x / kPer;
+  const bool there = r < p.heads[0] + p.heads[1];
   const uint32_t group_mask = ((1u << kPer) - 1u) << (threadIdx.x % 32 / kPer * kPer);
-
-  // A thread's rows, token by token; the next one is on its way while one is worked on.
-  int t = blockIdx.x, r = first;
-  auto source = [&](int token, int row) {
-    const int w = row >= p.heads[0];
-    return reinterpret_cast<const uint4*>(p.x[w] + token * p.x_token[w] + (w ? row - p.heads[0] : row) * p.x_head[w]);
-  };
+  const int w = r >= p.heads[0], h = w ? r - p.heads[0] : r;
+  int t = blockIdx.x;
+  // the next token's row is on its way while this one's is worked on
+  const uint8_t* src = p.x[w] + t * p.x_token[w] + h * p.x_head[w];
+  uint8_t* dst = p.y[w] + t * p.y_token[w] + h * p.y_head[w];
+  const long long src_step = gridDim.x * p.x_token[w], dst_step = gridDim.x * p.y_token[w];
   uint4 next_a = make_uint4(0, 0, 0, 0), next_b = next_a;
-  if (r < rows) {
-    const uint4* src = source(t, r);
-    next_a = src[va];
-    next_b = src[vb];
+  if (there) {
+    next_a = reinterpret_cast<const uint4*>(src)[va];
+    next_b = reinterpret_cast<const uint4*>(src)[vb];
   }
   auto angles = [&](int token, int slot) {
     for (int i = threadIdx.x; i < p.rotary / 2; i += blockDim.x) {
@@ -319,26 +320,35 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
     }
   };
   angles(t, 0);
-  if (p.weight[0] || p.weight[1])
-    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
-      const void* w = p.weight[i / D];
-      if (w) s_weight[i / D][i % D] = p.weight_f32 ? static_cast<const float*>(w)[i % D]
-                                                   : static_cast<float>(static_cast<const T*>(w)[i % D]);
+  const bool norm = there && p.weight[w] != nullptr;
+  unsigned long long ua[4], ub[4];
+  if (norm) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ia = 8 * va + 2 * i, ib = 8 * vb + 2 * i;
+      if (p.weight_f32) {
+        const float* f = static_cast<const float*>(p.weight[w]);
+        ua[i] = f2(f[ia], f[ia + 1]);
+        ub[i] = f2(f[ib], f[ib + 1]);
+      } else {
+        const T* f = static_cast<const T*>(p.weight[w]);
+        ua[i] = f2(static_cast<float>(f[ia]), static_cast<float>(f[ia + 1]));
+        ub[i] = f2(static_cast<float>(f[ib]), static_cast<float>(f[ib + 1]));
+      }
     }
+  }
 
-  for (int slot = 0; t < p.tokens; t += gridDim.x, slot ^= 1) {
+  for (int slot = 0; t < p.tokens; t += gridDim.x, slot ^= 1, dst += dst_step) {
     __syncthreads();  // this token's angles are there, and the one before is done with its own
     const bool more = t + static_cast<int>(gridDim.x) < p.tokens;
     if (more) angles(t + static_cast<int>(gridDim.x), slot ^ 1);
-    for (r = first; r < rows; r += step) {
+    if (there) {
       const uint32_t au[4] = {next_a.x, next_a.y, next_a.z, next_a.w}, bu[4] = {next_b.x, next_b.y, next_b.z, next_b.w};
-      const bool same = r + step < rows;
-      if (same || more) {
-        const uint4* src = source(same ? t : t + static_cast<int>(gridDim.x), same ? r + step : first);
-        next_a = src[va];
-        next_b = src[vb];
+      if (more) {
+        src += src_step;
+        next_a = reinterpret_cast<const uint4*>(src)[va];
+        next_b = reinterpret_cast<const uint4*>(src)[vb];
       }
-      const int w = r >= p.heads[0], h = w ? r - p.heads[0] : r;
       unsigned long long a[4], b[4];  // two values each
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
         a[i] = f2(x.x, x.y);
         b[i] = f2(y.x, y.y);
       }
-      if (p.weight[w]) {
+      if (norm) {
         unsigned long long s0 = fmul2(a[0], a[0]), s1 = fmul2(b[0], b[0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) {
@@ -360,15 +370,10 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
         for (int k = 1; k < kPer; k <<= 1) ss += __shfl_xor_sync(group_mask, ss, k);
         const float inv = rsqrtf(ss * (1.f / D) + p.eps);
         const unsigned long long both = f2(inv, inv);
-        const ulonglong2* wa = reinterpret_cast<const ulonglong2*>(s_weight[w] + 8 * va);
-        const ulonglong2* wb = reinterpret_cast<const ulonglong2*>(s_weight[w] + 8 * vb);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const ulonglong2 u = wa[i], v = wb[i];
-          a[2 * i] = fmul2(fmul2(a[2 * i], both), u.x);
-          a[2 * i + 1] = fmul2(fmul2(a[2 * i + 1], both), u.y);
-          b[2 * i] = fmul2(fmul2(b[2 * i], both), v.x);
-          b[2 * i + 1] = fmul2(fmul2(b[2 * i + 1], both), v.y);
+        for (int i = 0; i < 4; ++i) {
+          a[i] = fmul2(fmul2(a[i], both), ua[i]);
+          b[i] = fmul2(fmul2(b[i], both), ub[i]);
         }
       }
       auto table = [&](const float* values, int at, unsigned long long(&v)[2]) {  // four of a table's entries
@@ -378,12 +383,13 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
       };
       if constexpr (Interleaved) {
         auto rotate = [&](unsigned long long(&v)[4], int at) {
+          const float4 c4 = *reinterpret_cast<const float4*>(s_cos[slot] + at), n4 = *reinterpret_cast<const float4*>(s_sin[slot] + at);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, n[4] = {n4.x, n4.y, n4.z, n4.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float cos = s_cos[slot][at + i], sin = s_sin[slot][at + i];
             float x, y;
             f2_split(v[i], x, y);
-            v[i] = f2(x * cos - y * sin, x * sin + y * cos);
+            v[i] = f2(x * c[i] - y * n[i], x * n[i] + y * c[i]);
           }
         };
         if (turn) rotate(a, 4 * va);
@@ -404,7 +410,6 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
           }
         }
       }
-      uint4* dst = reinterpret_cast<uint4*>(p.y[w] + t * p.y_token[w] + h * p.y_head[w]);
       auto pack = [](const unsigned long long(&v)[4]) {
         uint32_t r[4];
 #pragma unroll
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
         }
         return make_uint4(r[0], r[1], r[2], r[3]);
       };
-      dst[va] = pack(a);
-      dst[vb] = pack(b);
+      reinterpret_cast<uint4*>(dst)[va] = pack(a);
+      reinterpret_cast<uint4*>(dst)[vb] = pack(b);
     }
   }
 }
@@ -427,7 +432,7 @@ static void rope_launch(const RopeParams& p, bool interleaved, dim3 grid, int th
   else rope_kernel<T, D, false><<<grid, threads, 0, stream>>>(p);
 }
 
-constexpr int kRopeWarps = 32;  // resident on an SM (at 64 registers)
+constexpr int kRopeWarps = 32, kRopeThreads = 256;  // warps resident on an SM (at 64 registers), threads of a CTA at most
 
 }  // namespace tl
 
@@ -542,15 +547,15 @@ extern "C" int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_t
   p.rotary = rotary;
   p.weight_f32 = weight_dtype == TL_FP32;
   p.eps = eps;
-  // A CTA takes all rows of a token, so that its angles are worked out once, in as few rounds as 256 threads allow; unless
-  // there are fewer tokens than places: then a token's rows are spread, some 64 threads each.
+  // CTAs of some 160 threads (64 where there are few tokens, so that their rows spread over the SMs), as many as are resident.
   const int per = d / 16, rows = heads + kv_heads;
   const bool spread = static_cast<long long>(tokens) * ((rows * per + 63) / 64) <= 8LL * ctx->sms;
-  const int most = spread ? 64 : rope::kMaxThreads;
+  const int most = spread ? 64 : kRopeThreads;
   const int rounds = (rows * per + most - 1) / most, at_once = (rows + rounds - 1) / rounds;
-  const int threads = (at_once * per + 31) / 32 * 32;
-  const long long places = static_cast<long long>(spread ? 8 : kRopeWarps / (threads / 32)) * ctx->sms;
-  const dim3 grid(static_cast<unsigned>(tokens < places ? tokens : places), spread ? rounds : 1, 1);
+  const int threads = (at_once * per + 31) / 32 * 32, parts = (rows + threads / per - 1) / (threads / per);
+  long long places = static_cast<long long>(kRopeWarps / (threads / 32)) * ctx->sms / parts;  // (one CTA too many waits for all others)
+  if (places < 1) places = 1;
+  const dim3 grid(static_cast<unsigned>(spread || tokens < places ? tokens : places), parts, 1);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TL_BF16) {
     if (d == 64) rope_launch<__nv_bfloat16, 64>(p, interleaved, grid, threads, s);
