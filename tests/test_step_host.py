@@ -85,7 +85,7 @@ def test_norm_rope_refusals(tl, ctx):
     assert call() == tl.TL_OK and call(tokens=3, heads=0, kv_heads=0) == tl.TL_OK
     for bad in (dict(ctx=None), dict(dtype=2), dict(dtype=3), dict(wdtype=1), dict(wdtype=2), dict(eps=-1.0), dict(eps=float("nan")),
                 dict(eps=float("inf")), dict(rotary=8), dict(rotary=80), dict(rotary=-16), dict(inter=2), dict(qt=257), dict(koh=4),
-                dict(kot=-64), dict(tokens=-1), dict(heads=-1), dict(d=96), dict(tokens=1, heads=65536)):
+                dict(kot=-64), dict(tokens=-1), dict(heads=-1), dict(d=96), dict(tokens=1, heads=65536), dict(tokens=1 << 30)):
         assert call(**bad) == tl.TL_ERR_INVALID, bad
     for bad in (dict(q=None), dict(q=264), dict(k=None), dict(qo=None), dict(ko=8), dict(pos=None), dict(freq=None)):
         assert call(tokens=1, **bad) == tl.TL_ERR_INVALID, bad
