@@ -252,3 +252,17 @@ def test_token_logprobs_rows_past_32_bits(tl, ctx):
     out, best, ids = run_score(tl, ctx, x, t, 4)
     assert ctx.check() == tl.TL_OK
     check_score(x, t, 4, out, best, ids)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab,kind", [(1, "plain"), (40, "ties"), (515, "masked"), (2999, "plain"), (8190, "same"), (8192, "lowest"), (1200, "tail")])
+def test_token_logprobs_many_short_rows(tl, ctx, vocab, kind, dtype):
+    """More rows than CTAs fit: rows that start anywhere, a target for every fifth."""
+    rows, top = 701, min(vocab, 32)
+    x = logits(rows, vocab + 3, dtype, vocab, kind).cuda()[:, 1:vocab + 1]
+    t = torch.full((rows,), -1, dtype=torch.int32)
+    t[::5] = torch.from_numpy(np.random.default_rng(1).integers(0, vocab, len(t[::5])).astype(np.int32))
+    t = t.cuda()
+    out, best, ids = run_score(tl, ctx, x, t, top)
+    assert ctx.check() == tl.TL_OK
+    check_score(x, t, top, out, best, ids)
