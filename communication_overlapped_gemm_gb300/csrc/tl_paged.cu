@@ -144,6 +144,13 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 // Half a block (16 bytes of a row), the other half in the neighbouring lane: eight codes, and the block's scale.
+// One of a pair of fp16, twice (the products read it as it lies).
+__device__ __forceinline__ uint32_t both_halves(uint32_t v, int h) {
+  uint32_t d;
+  if (h) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(v));
+  else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
 struct Half4 {
   uint32_t codes;
   uint8_t scale;
@@ -829,7 +836,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
           }
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
-            const uint32_t bl = __byte_perm(slo, slo, h ? 0x3232 : 0x1010), bh = __byte_perm(shi, shi, h ? 0x3232 : 0x1010);
+            const uint32_t bl = both_halves(slo, h), bh = both_halves(shi, h);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               uint32_t x0[4], x1[4];
