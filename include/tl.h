@@ -627,7 +627,8 @@ int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, con
  * [rows], any may be NULL.  top_logprobs: fp32, top_ids: int32 [rows x top].
  * A logit of -inf (a masked token) has probability 0.  Where all of a row are -inf, its entropy is 0 and its
  * lse and all its log probabilities are -inf.  A NaN or +inf among a row's logits makes all its fp32 outputs NaN (ids not).
- * Precision: maxima, sums and logarithms are fp32.  Results are bit-identical run to run on one device.
+ * Precision: maxima, sums and logarithms are fp32; a result below fp32's range (scale times a mask's lowest value) is -inf.
+ * Results are bit-identical run to run on one device.
  * workspace: tl_token_logprobs_workspace_bytes(): counters, and parts of rows split over several CTAs.
  * Shapes: 1 <= vocab <= 2^30; 0 <= top <= 32, top <= vocab; rows <= 2^24; scale finite and > 0.  rows == 0 is a no-op.
  */
