@@ -347,6 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
       const int nth = (p.top + p.splits - 1) / p.splits, need = (p.top + nth - 1) / nth;
       if (threadIdx.x == 0) s_count = 0;
       for (int s = threadIdx.x; s < p.splits; s += kThreads) s_cand[s] = __ldcg(keys + static_cast<size_t>(s) * kStride + nth - 1);
+      constexpr int kAhead = 4;  // keys of a thread that are on their way meanwhile
+      const int all_keys = p.splits * kTop;
+      Key held[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        held[u] = i < all_keys && i % kTop < p.top ? __ldcg(keys + static_cast<size_t>(i / kTop) * kStride + i % kTop) : 0;
+      }
       __syncthreads();
       for (int s = threadIdx.x; s < p.splits; s += kThreads) {
         // (equal ones are zeros, from parts of fewer keys)
@@ -363,14 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
       const Key bound = s_best[0] > 0 ? s_best[0] : 1;
       __syncthreads();
       if (threadIdx.x < kTop) s_best[threadIdx.x] = 0;
-      for (int i = threadIdx.x; i < p.splits * kTop; i += kThreads) {
-        if (i % kTop >= p.top) continue;
-        const Key k = __ldcg(keys + static_cast<size_t>(i / kTop) * kStride + i % kTop);
+      auto keep = [&](Key k) {
         if (k >= bound) {
           const int c = atomicAdd(&s_count, 1);
           if (c < kCandidates) s_cand[c] = k;
         }
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) keep(held[u]);
+      for (int i = threadIdx.x + kAhead * kThreads; i < all_keys; i += kThreads)
+        if (i % kTop < p.top) keep(__ldcg(keys + static_cast<size_t>(i / kTop) * kStride + i % kTop));
       __syncthreads();
       place_best(s_cand, min(s_count, kCandidates), s_best, p.top);
       __syncthreads();
