@@ -12,7 +12,7 @@ namespace tl {
 // where there are few rows; thread i has the vectors i, i + 256, .. with its own m, S and T.  The parts of a row are
 // joined by the CTA that finishes the last one, in their order.
 // Measured: 2048 rows of 50001 fp32 logits with the best token 75.6 us, 5.4 TB/s, 0.80 of the copy rate (without 68.4, 0.88; with
-// the best 20 93); 64 rows of 131072 bf16 with the best 5 12.9 us; one row of 131072 fp32 with the best 20 9.0 us, without 5.2:
+// the best 20 93); 64 rows of 131072 bf16 with the best 5 12.5 us; one row of 131072 fp32 with the best 20 8.7 us, without 5.1:
 // the launch, the logits, the bound, the second look, the part, and the join are waited for in turn.  (One line of all rows cut
 // evenly over CTAs that stay: 83 to 99 us and 12; rows beyond the last full round cut in two or three: 81 to 84.)
 //

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // shared by 32 lanes.  A code is widened to fp16 by a conversion of two and multiplied by its block's scale, both exact; a thread's
 // dims of a step lie in one block, for K a quarter of a row, for V D / 8 dims of four keys, whose halves of bytes are
 // interleaved first, so that keys lie in pairs.  These two instructions for two values bound it: 128 sequences of up to 16k, 64 heads on
-// 8, 241 us, 5.1 TB/s, 0.75 of the copy rate (without the conversions 210, without the products 220; without either 0.87, which
+// 8, 236 us, 5.2 TB/s, 0.77 of the copy rate (without the conversions 210, without the products 220; without either 0.87, which
 // is what the reads alone reach), the ALUs at 51% and the issue slots at 60%.  16 keys a warp: 336 us; four CTAs an SM of 128
 // registers and two stages: 253.
 //
