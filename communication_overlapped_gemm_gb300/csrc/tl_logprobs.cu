@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
   }
 }
 
-// The parts that a row is cut into: as many as fill the SMs, none of less than a vector or two a thread.
+// The parts that a row is cut into: three CTAs an SM of all rows (64 bf16 rows of 131072 without best tokens 9.5 us; two 10.1, four
+// 10.7; 300 fp32 rows with 5 33, 33 and 43), none of less than 4096 logits (one row with the best 20: 8.9 us; 2048 10.4, 8192 9.5).
 constexpr int kScoreParts = 640;  // of all rows together, beside one a row
 static int score_splits(int rows, int vocab, int sms) {
   if (rows <= 0 || rows > score::kMaxSplitRows) return 1;

@@ -12,9 +12,10 @@ namespace tl {
 // packed token finds its sequence by bisection of the bounds in shared memory, and the token that opens a page
 // writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
 // a write.  Lengths (and `taken`) that are brought up to date in place may only be written once every CTA has read
-// them: then the grid is one cluster, and a cluster barrier lies between.
+// them: a grid of up to 8 CTAs is one cluster then, with a barrier between; behind a larger one a second launch of one
+// CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows: 9.1 us, as one cluster 40; one of 3000 tokens, a cluster of 6: 4.4, not in place 4.1).
 // The launch and some four waits bound it: lengths, two rounds of sums, the table's entry, the stores.  A step of 64 sequences
-// 3.8 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 6.1 us.
+// 3.9 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 6.2 us.
 struct PlanParams {
   DevStatus* status;
   const int* lengths;
@@ -30,17 +31,18 @@ struct PlanParams {
   int* positions;  // may be null
   int* kv_slots;   // may be null
   int batch, max_pages, num_free, page_size, tokens, kv_tokens;
+  int parts;       // plan::kTokens, plan::kLengths
   FastDiv by_page;
 };
 
 namespace plan {
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxBatch = 4096, kChunk = kMaxBatch / kThreads;
+constexpr int kMaxBatch = 4096;
+constexpr int kTokens = 1, kLengths = 2;  // what a launch writes: bounds, slots, pages; lengths and pages taken
 constexpr uint32_t kMost = 0x7fffffffu;
 // Sums stop at 2^31 - 1 (in any order): whatever lies there is past every buffer.
 __device__ __forceinline__ uint32_t sat(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 // The sums over all threads before this one, and those over all, of N numbers.
-template <int N>
+template <int kWarps, int N>
 __device__ __forceinline__ void scan(uint32_t (&v)[N], uint32_t (*warps)[kWarps], uint32_t (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t s[N];
@@ -80,9 +82,10 @@ __device__ __forceinline__ int find(const int* bounds, int n, int i) {
 }
 }  // namespace plan
 
-template <bool InPlace>
-__global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p) {
+template <bool Cluster, int kThreads>
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   using namespace plan;
+  constexpr int kWarps = kThreads / 32, kChunk = kMaxBatch / kThreads;
   extern __shared__ int smem[];
   __shared__ uint32_t s_warps[4][kWarps];
   int* const s_q = smem;                       // [batch + 1] first new token of a sequence
@@ -156,27 +159,29 @@ __global__ void __launch_bounds__(plan::kThreads) plan_kernel(const PlanParams p
     const uint32_t top = __reduce_max_sync(0xffffffffu, used);
     if ((threadIdx.x & 31) == 0) s_warps[3][threadIdx.x >> 5] = top;
   }
-  if constexpr (InPlace) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if constexpr (Cluster) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   __syncthreads();
 
+  const bool tokens = p.parts & kTokens;
   if (blockIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
       const int b = b0 + i;
       if (i >= chunk || b >= p.batch) continue;
-      p.new_lengths[b] = cnt[i] > 0 ? len[i] + cnt[i] : raw[i];
-      p.cu_q[b] = s_q[b];
-      if (p.cu_k) p.cu_k[b] = s_k[b];
+      if (p.parts & kLengths) p.new_lengths[b] = cnt[i] > 0 ? len[i] + cnt[i] : raw[i];
+      if (tokens) p.cu_q[b] = s_q[b];
+      if (tokens && p.cu_k) p.cu_k[b] = s_k[b];
     }
     if (threadIdx.x == 0) {
       uint32_t top = 0;
       for (int w = 0; w < kWarps; ++w) top = max(top, s_warps[3][w]);
-      p.cu_q[p.batch] = s_q[p.batch];
-      if (p.cu_k) p.cu_k[p.batch] = s_k[p.batch];
-      *p.taken_out = taken + static_cast<int>(top);
+      if (p.parts & kLengths) *p.taken_out = taken + static_cast<int>(top);
+      if (tokens) p.cu_q[p.batch] = s_q[p.batch];
+      if (tokens && p.cu_k) p.cu_k[p.batch] = s_k[p.batch];
       if (!taken_ok || (p.kv_slots && s_k[p.batch] > p.kv_tokens)) report_index(p.status, static_cast<unsigned long long>(p.batch));
     }
   }
+  if (!tokens) return;
 
   // The slot of row `pos` of sequence b: its page is in the table, or a new one.  -1 where there is none.
   auto slot_of = [&](int b, int pos, int held, int& page_at, int& page) {
@@ -434,7 +439,7 @@ static void rope_launch(const RopeParams& p, bool interleaved, dim3 grid, int th
   else rope_kernel<T, D, false><<<grid, threads, 0, stream>>>(p);
 }
 
-constexpr int kRopeWarps = 32, kRopeThreads = 256;  // warps resident on an SM (at 64 registers), threads of a CTA at most
+constexpr int kRopeWarps = 32;  // resident on an SM (at 64 registers)
 
 }  // namespace tl
 
@@ -473,39 +478,47 @@ extern "C" int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts,
   p.tokens = tokens;
   p.kv_tokens = kv_tokens;
   p.by_page = fast_div(page_size);
-  const int smem = (4 * batch + 2) * 4;
+  // More than 512 sequences go to CTAs of 1024 threads (a step of 4000: 10.3 us, with 512 threads 13.5; one of 64: 4.1 and 3.85),
+  // two packed tokens a thread up to a CTA an SM (one: the same; eight: 37 prompts 8.5 us instead of 6.2).
+  const int threads = batch > 512 ? 1024 : 512, smem = (4 * batch + 2) * 4;
   const long long items = static_cast<long long>(tokens) + kv_tokens;
-  long long ctas = (items + 2 * plan::kThreads - 1) / (2 * plan::kThreads);
-  const bool in_place = lengths == new_lengths || taken == taken_out;
-  const long long most = in_place ? 8 : ctx->sms;
-  if (ctas > most) ctas = most;
+  long long ctas = (items + 2 * threads - 1) / (2 * threads);
+  if (ctas > ctx->sms) ctas = ctx->sms;
   if (ctas < 1) ctas = 1;
-  const void* kern = in_place ? reinterpret_cast<const void*>(plan_kernel<true>) : reinterpret_cast<const void*>(plan_kernel<false>);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  static std::atomic<unsigned long long> ready[2];
-  if (smem > (48 << 10) - 1024 && !smem_ready(ready[in_place], ctx->device, kern, (4 * plan::kMaxBatch + 2) * 4)) return TL_ERR_CUDA;
-  if (!in_place || ctas == 1) {  // (nothing written that another CTA reads; or a CTA's own barrier is enough)
-    if (in_place) plan_kernel<true><<<1, plan::kThreads, smem, st>>>(p);
-    else plan_kernel<false><<<static_cast<unsigned>(ctas), plan::kThreads, smem, st>>>(p);
-    return launched();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  cfg.blockDim = dim3(plan::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, plan_kernel<true>, p) != cudaSuccess) {
+  const bool in_place = lengths == new_lengths || taken == taken_out;
+  static std::atomic<unsigned long long> ready[4];
+  auto launch = [&](int parts, long long grid, bool cluster) {
+    p.parts = parts;
+    auto kern = threads == 512 ? (cluster ? plan_kernel<true, 512> : plan_kernel<false, 512>)
+                               : (cluster ? plan_kernel<true, 1024> : plan_kernel<false, 1024>);
+    if (smem > (48 << 10) - 1024 && !smem_ready(ready[2 * cluster + (threads == 512)], ctx->device, reinterpret_cast<const void*>(kern),
+                                                (4 * plan::kMaxBatch + 2) * 4))
+      return static_cast<int>(TL_ERR_CUDA);
+    if (!cluster) {
+      kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(p);
+      return launched();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(grid);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess) return static_cast<int>(TL_OK);
     (void)cudaGetLastError();
-    return TL_ERR_CUDA;
-  }
-  return TL_OK;
+    return static_cast<int>(TL_ERR_CUDA);
+  };
+  if (!in_place || ctas == 1) return launch(plan::kTokens | plan::kLengths, ctas, false);  // (or a CTA's own barrier is enough)
+  if (ctas <= 8) return launch(plan::kTokens | plan::kLengths, ctas, true);
+  const int rc = launch(plan::kTokens, ctas, false);
+  return rc == TL_OK ? launch(plan::kLengths, 1, false) : rc;
 }
 
 extern "C" int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_token_stride, long long q_head_stride,
@@ -549,15 +562,14 @@ extern "C" int tl_norm_rope(tl_ctx* ctx, int dtype, const void* q, long long q_t
   p.rotary = rotary;
   p.weight_f32 = weight_dtype == TL_FP32;
   p.eps = eps;
-  // CTAs of some 160 threads (64 where there are few tokens, so that their rows spread over the SMs), as many as are resident.
+  // A token's rows in as few CTAs as 256 threads allow, evenly (32 and 8 heads of 128: two of 160 threads, 30.2 us for 8192 tokens; of
+  // 128 threads at most 32.2), as many CTAs as are resident: one more would wait for all others (64 and 8 heads 51 us, then 80).
   const int per = d / 16, rows = heads + kv_heads;
-  const bool spread = static_cast<long long>(tokens) * ((rows * per + 63) / 64) <= 8LL * ctx->sms;
-  const int most = spread ? 64 : kRopeThreads;
-  const int rounds = (rows * per + most - 1) / most, at_once = (rows + rounds - 1) / rounds;
+  const int rounds = (rows * per + rope::kMaxThreads - 1) / rope::kMaxThreads, at_once = (rows + rounds - 1) / rounds;
   const int threads = (at_once * per + 31) / 32 * 32, parts = (rows + threads / per - 1) / (threads / per);
-  long long places = static_cast<long long>(kRopeWarps / (threads / 32)) * ctx->sms / parts;  // (one CTA too many waits for all others)
+  long long places = static_cast<long long>(kRopeWarps / (threads / 32)) * ctx->sms / parts;
   if (places < 1) places = 1;
-  const dim3 grid(static_cast<unsigned>(spread || tokens < places ? tokens : places), parts, 1);
+  const dim3 grid(static_cast<unsigned>(tokens < places ? tokens : places), parts, 1);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TL_BF16) {
     if (d == 64) rope_launch<__nv_bfloat16, 64>(p, interleaved, grid, threads, s);
