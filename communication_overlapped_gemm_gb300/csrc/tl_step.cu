@@ -9,13 +9,14 @@ namespace tl {
 // Sequence b holds n_b rows and gets c_b more: it needs ceil((n_b + c_b) / page) pages and has ceil(n_b / page), so
 // its new pages are free_pages[taken + sum of the needs before it ..].  Every CTA takes both prefix sums over
 // the batch for itself (4096 sequences at most), so one launch does without a hand-over between CTAs; then each
-// packed token finds its sequence by bisection of the bounds in shared memory, and the token that opens a page
-// writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
+// packed token finds its sequence by bisection of the bounds in shared memory (mostly it is that of the lane's token before),
+// and the token that opens a page writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
 // a write.  Lengths (and `taken`) that are brought up to date in place may only be written once every CTA has read
 // them: a grid of up to 8 CTAs is one cluster then, with a barrier between; behind a larger one a second launch of one
 // CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows: 9.1 us, as one cluster 40; one of 3000 tokens, a cluster of 6: 4.4, not in place 4.1).
 // The launch and some four waits bound it: lengths, two rounds of sums, the table's entry, the stores.  A step of 64 sequences
-// 3.9 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 6.2 us.
+// 4.0 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 5.8 us; the slots of 8.3 million rows of 1000
+// sequences 22.6 us (each by a bisection of its own 61; four of a lane's pages read at once 24.7, and pages of one row 37 instead of 44).
 struct PlanParams {
   DevStatus* status;
   const int* lengths;
@@ -71,9 +72,9 @@ __device__ __forceinline__ void scan(uint32_t (&v)[N], uint32_t (*warps)[kWarps]
     v[n] = sat(warp ? before : 0u, lane ? up : 0u);
   }
 }
-// The last b with bounds[b] <= i, for bounds[0] = 0 (so it holds i if any does).
-__device__ __forceinline__ int find(const int* bounds, int n, int i) {
-  int lo = 0, hi = n;  // bounds[lo] <= i < bounds[hi] (or past the end)
+// The last b of lo .. n - 1 with bounds[b] <= i, for bounds[lo] <= i (so it holds i if any does).
+__device__ __forceinline__ int find(const int* bounds, int lo, int n, int i) {
+  int hi = n;  // bounds[lo] <= i < bounds[hi] (or past the end)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (bounds[mid] <= i) lo = mid; else hi = mid;
@@ -183,47 +184,64 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   }
   if (!tokens) return;
 
-  // The slot of row `pos` of sequence b: its page is in the table, or a new one.  -1 where there is none.
-  auto slot_of = [&](int b, int pos, int held, int& page_at, int& page) {
+  // Each warp has a range of packed tokens, a lane every 32nd of it: the sequence of one is mostly that of the lane's next one.
+  const int lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * kWarps, warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  struct Sequence {
+    int b, begin, past;  // its packed tokens
+    int held, has;       // rows and pages held; held is ~rows if it gets none of its new ones
+    const int* table;
+    const int* fresh;    // new pages, of page `has` on
+  };
+  auto enter = [&](const int* bounds, Sequence& q, int t) {
+    q.b = find(bounds, q.b, p.batch, t);
+    q.begin = bounds[q.b];
+    q.past = bounds[q.b + 1];
+    q.held = s_len[q.b];
+    q.has = static_cast<int>(divide(static_cast<uint32_t>((q.held < 0 ? ~q.held : q.held) + p.page_size - 1), p.by_page));
+    q.table = p.table + static_cast<long long>(q.b) * p.max_pages;
+    q.fresh = p.free_pages + s_first[q.b] - q.has;
+  };
+  // The slot of row `pos`: its page is in the table, or a new one.  -1 where there is none.
+  auto slot_of = [&](const Sequence& q, int pos, int& page_at, int& page) {
     page_at = static_cast<int>(divide(static_cast<uint32_t>(pos), p.by_page));
-    const int has = static_cast<int>(divide(static_cast<uint32_t>(held + p.page_size - 1), p.by_page));
-    page = page_at < has ? p.table[static_cast<long long>(b) * p.max_pages + page_at] : __ldg(p.free_pages + s_first[b] + page_at - has);
+    page = page_at < q.has ? q.table[page_at] : __ldg(q.fresh + page_at);
     const long long slot = static_cast<long long>(page) * p.page_size + (pos - page_at * p.page_size);
     if (page < 0 || slot > static_cast<long long>(kMost)) {
-      report_index(p.status, static_cast<unsigned long long>(b));
+      report_index(p.status, static_cast<unsigned long long>(q.b));
       return -1;
     }
     return static_cast<int>(slot);
   };
-  const int step = static_cast<int>(gridDim.x) * kThreads, start = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
-  const int total_q = s_q[p.batch], total_k = s_k[p.batch];
-  for (long long i = start; i < p.tokens; i += step) {
-    const int t = static_cast<int>(i);
+  auto each = [&](int n, const int* bounds, auto&& token) {
+    const long long range = ((n + warps - 1) / warps + 31) / 32 * 32, begin = warp * range, end = begin + range < n ? begin + range : n;
+    const int total = bounds[p.batch];
+    Sequence q = {};
+    for (long long i = begin + lane; i < end; i += 32) {
+      const int t = static_cast<int>(i);
+      if (t < total && t >= q.past) enter(bounds, q, t);
+      token(t, t < total, q);
+    }
+  };
+  each(p.tokens, s_q, [&](int t, bool there, const Sequence& q) {
     int slot = -1, pos = 0;
-    if (t < total_q) {
-      const int b = find(s_q, p.batch, t), held = s_len[b];
-      pos = (held < 0 ? ~held : held) + t - s_q[b];
-      if (held >= 0) {
+    if (there) {
+      pos = (q.held < 0 ? ~q.held : q.held) + t - q.begin;
+      if (q.held >= 0) {
         int page_at, page;
-        slot = slot_of(b, pos, held, page_at, page);
+        slot = slot_of(q, pos, page_at, page);
         // its first row opens a page
-        if (pos == page_at * p.page_size) p.table[static_cast<long long>(b) * p.max_pages + page_at] = page;
+        if (pos == page_at * p.page_size) p.table[static_cast<long long>(q.b) * p.max_pages + page_at] = page;
       }
     }
     p.slots[t] = slot;
     if (p.positions) p.positions[t] = pos;
-  }
+  });
   if (p.kv_slots)
-    for (long long i = start; i < p.kv_tokens; i += step) {
-      const int t = static_cast<int>(i);
-      int slot = -1;
-      if (t < total_k) {
-        const int b = find(s_k, p.batch, t), held = s_len[b];
-        int page_at, page;
-        slot = slot_of(b, t - s_k[b], held < 0 ? ~held : held, page_at, page);
-      }
-      p.kv_slots[t] = slot;
-    }
+    each(p.kv_tokens, s_k, [&](int t, bool there, const Sequence& q) {
+      int page_at, page;
+      p.kv_slots[t] = there ? slot_of(q, t - q.begin, page_at, page) : -1;
+    });
 }
 
 // ---------------------------------------------------------------------------- norms and rotation
