@@ -13,9 +13,9 @@ namespace tl {
 // and the token that opens a page writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
 // a write.  Lengths (and `taken`) that are brought up to date in place may only be written once every CTA has read
 // them: a grid of up to 8 CTAs is one cluster then, with a barrier between; behind a larger one a second launch of one
-// CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows: 9.1 us, as one cluster 40; one of 3000 tokens, a cluster of 6: 4.4, not in place 4.1).
+// CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows: 7.5 us, as one cluster 40; one of 3000 tokens, a cluster of 6: 4.1, not in place 3.7).
 // The launch and some four waits bound it: lengths, two rounds of sums, the table's entry, the stores.  A step of 64 sequences
-// 4.0 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 5.8 us; the slots of 8.3 million rows of 1000
+// 3.5 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 5.4 us; the slots of 8.3 million rows of 1000
 // sequences 22.6 us (each by a bisection of its own 61; four of a lane's pages read at once 24.7, and pages of one row 37 instead of 44).
 struct PlanParams {
   DevStatus* status;
@@ -37,7 +37,7 @@ struct PlanParams {
 };
 
 namespace plan {
-constexpr int kMaxBatch = 4096;
+constexpr int kMaxBatch = 4096, kThreads = 1024, kFewThreads = 512;  // threads of a CTA, and for up to as many sequences
 constexpr int kTokens = 1, kLengths = 2;  // what a launch writes: bounds, slots, pages; lengths and pages taken
 constexpr uint32_t kMost = 0x7fffffffu;
 // Sums stop at 2^31 - 1 (in any order): whatever lies there is past every buffer.
@@ -86,7 +86,7 @@ __device__ __forceinline__ int find(const int* bounds, int lo, int n, int i) {
 template <bool Cluster, int kThreads>
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
   using namespace plan;
-  constexpr int kWarps = kThreads / 32, kChunk = kMaxBatch / kThreads;
+  constexpr int kWarps = kThreads / 32, kChunk = kThreads == kFewThreads ? 1 : kMaxBatch / kThreads;  // sequences of a thread, at most
   extern __shared__ int smem[];
   __shared__ uint32_t s_warps[4][kWarps];
   int* const s_q = smem;                       // [batch + 1] first new token of a sequence
@@ -496,21 +496,24 @@ extern "C" int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts,
   p.tokens = tokens;
   p.kv_tokens = kv_tokens;
   p.by_page = fast_div(page_size);
-  // More than 512 sequences go to CTAs of 1024 threads (a step of 4000: 10.3 us, with 512 threads 13.5; one of 64: 4.1 and 3.85),
-  // two packed tokens a thread up to a CTA an SM (one: the same; eight: 37 prompts 8.5 us instead of 6.2).
-  const int threads = batch > 512 ? 1024 : 512, smem = (4 * batch + 2) * 4;
+  // More than 512 sequences go to CTAs of 1024 threads (a step of 4000: 10.5 us, with 512 threads 13.5; one of 64: 4.1 and 3.5),
+  // two packed tokens a thread up to 1024 threads an SM (one: the same; eight: 37 prompts 8.5 us instead of 6.2; 500 sequences with the
+  // slots of 4.1 million rows 12.7 us, with 512 threads an SM 16.5, with 2048 14.8).
+  const int threads = batch > plan::kFewThreads ? plan::kThreads : plan::kFewThreads, smem = (4 * batch + 2) * 4;
   const long long items = static_cast<long long>(tokens) + kv_tokens;
   long long ctas = (items + 2 * threads - 1) / (2 * threads);
-  if (ctas > ctx->sms) ctas = ctx->sms;
+  const int most = (threads == plan::kFewThreads ? 2 : 1) * ctx->sms;
+  if (ctas > most) ctas = most;
   if (ctas < 1) ctas = 1;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool in_place = lengths == new_lengths || taken == taken_out;
   static std::atomic<unsigned long long> ready[4];
   auto launch = [&](int parts, long long grid, bool cluster) {
     p.parts = parts;
-    auto kern = threads == 512 ? (cluster ? plan_kernel<true, 512> : plan_kernel<false, 512>)
-                               : (cluster ? plan_kernel<true, 1024> : plan_kernel<false, 1024>);
-    if (smem > (48 << 10) - 1024 && !smem_ready(ready[2 * cluster + (threads == 512)], ctx->device, reinterpret_cast<const void*>(kern),
+    using namespace plan;
+    auto kern = threads == kFewThreads ? (cluster ? plan_kernel<true, kFewThreads> : plan_kernel<false, kFewThreads>)
+                                       : (cluster ? plan_kernel<true, plan::kThreads> : plan_kernel<false, plan::kThreads>);
+    if (smem > (48 << 10) - 1024 && !smem_ready(ready[2 * cluster + (threads == kFewThreads)], ctx->device, reinterpret_cast<const void*>(kern),
                                                 (4 * plan::kMaxBatch + 2) * 4))
       return static_cast<int>(TL_ERR_CUDA);
     if (!cluster) {
