@@ -334,17 +334,18 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 // 4-bit rows come with their block scales as copies of their own, 32 keys of a warp at a time, so that the work of finding a row is
 // shared by 32 lanes.  A code is widened to fp16 by a conversion of two and multiplied by its block's scale, both exact; a thread's
 // dims of a step lie in one block, for K a quarter of a row, for V D / 8 dims of four keys, whose halves of bytes are
-// interleaved first, so that keys lie in pairs.  These two instructions for two values bound it: 128 sequences of up to 16k, 64 heads on
-// 8, 236 us, 5.2 TB/s, 0.77 of the copy rate (without the conversions 210, without the products 220; without either 0.87, which
-// is what the reads alone reach), the ALUs at 51% and the issue slots at 60%.  16 keys a warp: 336 us; four CTAs an SM of 128
-// registers and two stages: 253.
+// interleaved first, so that keys lie in pairs.  These two instructions for two values and the weights' second terms bound it: 128
+// sequences of up to 16k, 64 heads on 8, 263 us, 4.6 TB/s, 0.68 of the copy rate (0.87 is what the reads alone reach).  With one
+// term of a weight 238, the ALUs at 51% and the issue slots at 60% (without the conversions 210, without the products 220; 16 keys a
+// warp 336; four CTAs an SM of 128 registers and two stages 253).
 //
 // e4m3 rows are widened to fp16 (exact) in registers; q is brought to fp16 by a power of two per row
 // that puts its largest element in [1, 2) (exact but for elements 2^-14 below it), so both products
 // run in fp16.  Weights meet V in the products' 16-bit type, fp16 ones held times 2^7 (kWeightBits, m being 7 less): over
-// a 16-bit cache as a sum of two terms, off by half a step of half a step, so that a bf16 output is off by its own
-// rounding (relative 1.6e-3; with one term 2.2e-3, and 0.6% less time: the tensor pipe waits for HBM), over an
-// e4m3 cache, whose rows have 4 bits, as one fp16 term.  l sums them unrounded in fp32.
+// a 16-bit or a 4-bit cache as a sum of two terms, off by half a step of half a step, so that an output is off by its own
+// rounding (bf16 over 16 bits 1.6e-3 relative, with one term 2.2e-3, and 0.6% less time: the tensor pipe waits for HBM; fp16 over
+// 4 bits 2.1e-4, with one 2.8e-4, and 4 to 10% less time), over an e4m3 cache, whose rows have 4 bits, as one fp16 term.  l sums them
+// unrounded in fp32.
 namespace paged {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int tile_bits(int bits) { return bits == 4 ? 7 : 6; }  // log2 of a tile's keys
@@ -364,7 +365,8 @@ struct Shape {
   static constexpr int kCtas = D == 64 || (Bits < 16 && NB == 1) ? 3 : 2;
   static constexpr int kFit = (kCtas == 3 ? Bits == 4 ? 57344 : 49152 : 65536) / (kWarps * kStage);
   // (4 bits: a stage of 32 keys is long, and short sequences wait for all of a ring's first stages: two instead of three stages of
-  // 18 KB 128 sequences of 500 rows 27.9 us instead of 30.2, one of 8k 11.5 instead of 12.0, 128 of up to 16k 237.6 instead of 235)
+  // 18 KB, with one term of a weight, 128 sequences of 500 rows 27.9 us instead of 30.2, one of 8k 11.5 instead of 12.0, 128 of up to 16k
+  // 237.6 instead of 235)
   static constexpr int kMost = Bits == 4 ? (D == 128 ? 2 : 3) : 6;
   static constexpr int kStages = kFit > kMost ? kMost : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
@@ -936,8 +938,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
             }
           }
       }
-      // the weights as the next product's B: keys by pairs in a column of queries; for a 16-bit cache as a sum of two terms
-      constexpr int kTerms = kNarrow ? 1 : 2;
+      // the weights as the next product's B: keys by pairs in a column of queries; but for an 8-bit cache as a sum of two terms
+      constexpr int kTerms = Bits == 8 ? 1 : 2;
       uint32_t pf[kU * NB][kTerms][2];
 #pragma unroll
       for (int u = 0; u < kU; ++u)
@@ -966,7 +968,7 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
           for (int e = 0; e < 2; ++e) {
             const uint32_t top = from_f32x2<M>(w[2 * e], w[2 * e + 1]);
             pf[u * NB + b][0][e] = transpose8x8(top);
-            if constexpr (!kNarrow) {
+            if constexpr (kTerms == 2) {
               const float2 f = to_f32x2<M>(top);
               pf[u * NB + b][1][e] = transpose8x8(from_f32x2<M>(w[2 * e] - f.x, w[2 * e + 1] - f.y));
             }
@@ -1007,7 +1009,9 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
             for (int j = 0; j < 4; ++j) {
               const uint32_t a[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23), hmul2(o23[j], s23)};
 #pragma unroll
-              for (int b = 0; b < NB; ++b) mma16816<M>(o[4 * i + j][b], a, pf[u * NB + b][0][0], pf[u * NB + b][0][1]);
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = kTerms - 1; e >= 0; --e) mma16816<M>(o[4 * i + j][b], a, pf[u * NB + b][e][0], pf[u * NB + b][e][1]);
             }
           }
         }
