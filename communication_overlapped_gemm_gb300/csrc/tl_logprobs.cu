@@ -435,7 +435,7 @@ extern "C" int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, lon
                                  float scale, int rows, int vocab, void* workspace, size_t workspace_bytes,
                                  tl_stream_t stream) {
   if (!ctx || (dtype != TL_BF16 && dtype != TL_FP16 && dtype != TL_FP32) || rows < 0 || vocab < 1 || vocab > (1 << 30) || top < 0 ||
-      top > score::kTop || top > vocab || row_stride < 0 || !(scale > 0.f) || scale > 3.0e38f)
+      top > score::kTop || top > vocab || row_stride < 0 || !scale_ok(scale))
     return TL_ERR_INVALID;
   if (rows == 0) return TL_OK;
   if (rows > (1 << 24) || !logits || reinterpret_cast<uintptr_t>(logits) % (dtype == TL_FP32 ? 4 : 2) != 0 || !workspace || !aligned16(workspace) || (logprob && !targets) ||

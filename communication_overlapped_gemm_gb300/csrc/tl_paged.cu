@@ -1370,7 +1370,7 @@ extern "C" int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int 
                                   float* lse, int batch, int heads, float scale, int window, int sinks, void* workspace,
                                   size_t workspace_bytes, tl_stream_t stream) {
   if (!ctx || !cache_ok(cache, dtype) || batch < 0 || batch > 4096 || !heads_ok(heads, cache->kv_heads, cache->d) ||
-      max_pages < 0 || window < 0 || sinks < 0 || !(scale > 0.f) || scale > 3.0e38f)
+      max_pages < 0 || window < 0 || sinks < 0 || !scale_ok(scale))
     return TL_ERR_INVALID;
   if (static_cast<long long>(max_pages) * cache->page_size >= (1LL << 31)) return TL_ERR_INVALID;
   if (!esize_ok(q_seq_stride, 2) || !esize_ok(q_head_stride, 2) || !esize_ok(out_seq_stride, 2) ||

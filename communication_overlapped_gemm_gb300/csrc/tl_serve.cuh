@@ -115,6 +115,9 @@ inline int launched() {
   return TL_OK;
 }
 
+// Softmax kernels work with scale * log2(e), which has to be finite too (0 times it is 0): scales up to 2.358e38.
+inline bool scale_ok(float scale) { return scale > 0.f && scale * kLog2E <= 3.402823466e38f; }
+
 inline bool esize_ok(long long stride, int esize) { return stride >= 0 && (stride * esize) % 16 == 0; }
 
 inline bool heads_ok(int heads, int kv_heads, int d) {

@@ -956,8 +956,8 @@ extern "C" int tl_window_attention(tl_ctx* ctx, int dtype, const void* q, long l
                                    int total_q, int total_k, int heads, int kv_heads, int d, float scale, int window,
                                    int sinks, tl_stream_t stream) {
   if (!ctx || (dtype != TL_BF16 && dtype != TL_FP16) || !heads_ok(heads, kv_heads, d) || heads / kv_heads > 128 ||
-      batch < 0 || batch > 1024 || total_q < 0 || total_k < 0 || window < 0 || sinks < 0 || !(scale > 0.f) ||
-      scale > 3.0e38f || static_cast<long long>(total_q) * heads >= (1LL << 31))
+      batch < 0 || batch > 1024 || total_q < 0 || total_k < 0 || window < 0 || sinks < 0 || !scale_ok(scale) ||
+      static_cast<long long>(total_q) * heads >= (1LL << 31))
     return TL_ERR_INVALID;
   for (long long s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
                       out_token_stride, out_head_stride})

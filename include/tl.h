@@ -552,7 +552,7 @@ int tl_kv_gather(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const int*
  * workspace: tl_paged_attention_workspace_bytes(): counters, and partial results of sequences split
  * over several CTAs.
  * Shapes: batch <= 4096; heads % kv_heads == 0; d 64 or 128; window, sinks >= 0; max_pages *
- * page_size < 2^31; scale finite and > 0; batch * heads * (visible rows at most / 64 + 1) < 2^31.
+ * page_size < 2^31; scale > 0 and at most 2.358e38 (times log2(e) finite); batch * heads * (visible rows at most / 64 + 1) < 2^31.
  * A 4-bit cache's codes reach over less than 2^32 units of the largest power of two that divides their strides (rows side by
  * side, d 64: 128 GB), its block scales likewise.
  * batch == 0 or heads == 0 is a no-op.
@@ -585,7 +585,7 @@ int tl_paged_attention(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, cons
  * decreasing, cu_q[0] >= 0, cu_q[batch] <= total_q, cu_k likewise (rows outside every sequence are
  * left alone); a bound out of order or range leaves that sequence out and is reported.
  * Shapes: batch <= 1024; heads % kv_heads == 0, heads / kv_heads <= 128; d 64 or 128; window, sinks >= 0;
- * scale finite and > 0; total_q * heads < 2^31.
+ * scale as tl_paged_attention; total_q * heads < 2^31.
  * strides of q, k and v > 0 where the dimension has more than one entry.
  * total_q == 0, heads == 0 or batch == 0 is a no-op.  No workspace.
  */
@@ -630,7 +630,7 @@ int tl_moe_tokens(tl_ctx* ctx, const void* x, const float* logits, int topk, con
  * Precision: maxima, sums and logarithms are fp32; a result below fp32's range (scale times a mask's lowest value) is -inf.
  * Results are bit-identical run to run on one device.
  * workspace: tl_token_logprobs_workspace_bytes(): counters, and parts of rows split over several CTAs.
- * Shapes: 1 <= vocab <= 2^30; 0 <= top <= 32, top <= vocab; rows <= 2^24; scale finite and > 0.  rows == 0 is a no-op.
+ * Shapes: 1 <= vocab <= 2^30; 0 <= top <= 32, top <= vocab; rows <= 2^24; scale as tl_paged_attention.  rows == 0 is a no-op.
  */
 size_t tl_token_logprobs_workspace_bytes(int rows, int vocab, int top);
 int tl_token_logprobs(tl_ctx* ctx, int dtype, const void* logits, long long row_stride, const int* targets, float* logprob,
