@@ -276,6 +276,8 @@ struct RopeParams {
 
 namespace rope {
 constexpr int kMaxThreads = 256;
+// Rows whose squares' sum is below kSmall, times kUp: from bf16's smallest value on the squares are normal numbers then.
+constexpr float kSmall = 0x1p-90f, kUp = 0x1p80f;
 // inv_freq / (2 pi) in units of 2^-64 turns, modulo one turn.
 __device__ __forceinline__ unsigned long long turns(float f) {
   constexpr unsigned long long kInv2Pi = 2935890503282001226ull;  // 2^64 / (2 pi), rounded
@@ -390,10 +392,30 @@ __global__ void __launch_bounds__(rope::kMaxThreads, 4) rope_kernel(const RopePa
         }
         float x, y;
         f2_split(fadd2(s0, s1), x, y);
-        float ss = x + y;
+        auto row_sum = [&](float v) {
 #pragma unroll
-        for (int k = 1; k < kPer; k <<= 1) ss += __shfl_xor_sync(group_mask, ss, k);
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+          for (int k = 1; k < kPer; k <<= 1) v += __shfl_xor_sync(group_mask, v, k);
+          return v;
+        };
+        const float ss = row_sum(x + y);
+        float inv = rsqrtf(ss * (1.f / D) + p.eps);
+        // Squares of small bf16 values leave fp32's range below, which shows where eps is next to nothing: such a row is brought up
+        // by a power of two first.  (The same in all threads of a row; 8192 tokens 30.6 us, without it 30.5.)
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          if (ss < kSmall && p.eps < kSmall) {
+            const unsigned long long up = f2(kUp, kUp);
+            s0 = s1 = f2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = fmul2(a[i], up);
+              b[i] = fmul2(b[i], up);
+              s0 = ffma2(a[i], a[i], s0);
+              s1 = ffma2(b[i], b[i], s1);
+            }
+            f2_split(fadd2(s0, s1), x, y);
+            inv = rsqrtf(row_sum(x + y) * (1.f / D) + p.eps * kUp * kUp);
+          }
+        }
         const unsigned long long both = f2(inv, inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -491,7 +491,8 @@ int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts, int batch,
  * its input (the same pointer and strides), and must not overlap it otherwise.  q_weight, k_weight: [d] of
  * weight_dtype (dtype or TL_FP32), or NULL: no norm.  positions: int32 [tokens], any value; inv_freq: fp32
  * [rotary / 2], finite (both may be NULL if rotary is 0).
- * Precision: all sums and products are fp32, rounded once; a row whose squares pass fp32's range becomes 0.  Angles are held
+ * Precision: all sums and products are fp32, rounded once; a row whose squares pass fp32's range becomes 0 (one
+ * whose squares lie below it is scaled first, so eps may be 0).  Angles are held
  * as fractions of a turn in 64 bits, so that far positions lose nothing (off by 2^-31 turns where |inv_freq| <= 1);
  * sines and cosines are off by 2^-21 at most.
  * Shapes: d 64 or 128; rotary a multiple of 16, at most d; eps >= 0; heads + kv_heads <= 65536; tokens < 2^30.  tokens == 0 or no
