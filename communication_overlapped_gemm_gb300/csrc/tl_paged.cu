@@ -363,7 +363,7 @@ struct Shape {
   // 8-bit or short rows brings few bytes for its instructions and wants the warps; the registers
   // allow three CTAs there.
   static constexpr int kCtas = D == 64 || (Bits < 16 && NB == 1) ? 3 : 2;
-  static constexpr int kFit = (kCtas == 3 ? Bits == 4 ? 57344 : 49152 : 65536) / (kWarps * kStage);
+  static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * kStage);
   // (4 bits: a stage of 32 keys is long, and short sequences wait for all of a ring's first stages: two instead of three stages of
   // 18 KB, with one term of a weight, 128 sequences of 500 rows 27.9 us instead of 30.2, one of 8k 11.5 instead of 12.0, 128 of up to 16k
   // 237.6 instead of 235)
