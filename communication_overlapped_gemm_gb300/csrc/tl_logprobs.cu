@@ -9,10 +9,11 @@ namespace tl {
 //   lse = c m + ln S,   logprob = c (x_t - m) - ln S,   entropy = ln S - ln 2 T / S.
 // (x - m comes first: l x of a mask's lowest value would be -inf, and a row of nothing else has no maximum then.)
 // Every logit is read once for some thirteen instructions, so HBM bounds it.  A CTA streams a row, or a part of one
-// where there are few rows; thread i has the vectors i, i + 256, .. with its own m, S and T.  The parts of a row are
+// where there are few rows; thread i has the vectors i, i + threads, .. with its own m, S and T.  The parts of a row are
 // joined by the CTA that finishes the last one, in their order.
-// Measured: 2048 rows of 50001 fp32 logits with the best token 75.6 us, 5.4 TB/s, 0.80 of the copy rate (without 68.4, 0.88; with
-// the best 20 93); 64 rows of 131072 bf16 with the best 5 12.5 us; one row of 131072 fp32 with the best 20 8.7 us, without 5.1:
+// Measured: 2048 rows of 50001 fp32 logits with the best token 73 to 76 us, 5.4 TB/s, 0.80 of the copy rate (without 68.3, 0.88; with
+// the best 20 94), of bf16 51 (46; 65), where instructions bound it; 64 rows of 131072 bf16 with the best 5 12.5 us (without 8.6 to
+// 9.5); one row of 131072 fp32 with the best 20 8.7 us, without 5.1:
 // the launch, the logits, the bound, the second look, the part, and the join are waited for in turn.  (One line of all rows cut
 // evenly over CTAs that stay: 83 to 99 us and 12; rows beyond the last full round cut in two or three: 81 to 84.)
 //
@@ -22,7 +23,9 @@ namespace tl {
 // the logits that reach the bound each counts how many are larger: its place.  An order of 64-bit keys, the value's bits above
 // the complement of its index, has no ties (of equal logits the lower index is the larger key).  Logits that are alike in
 // great number (masks, rows of one value) would make too many candidates: then only those above the bound are taken, from a
-// higher bound if these too are many, and the first ones equal to it are looked up from the row's start.
+// higher bound if these too are many, and the first ones equal to it are looked up from the row's start, 32 at a time by one
+// warp.  That is short where they begin early, as masks do.  Where they lie in the last 2000 of 131072 logits, with lower ones
+// before them, one row (cut into parts) takes 53 us, 600 uncut rows 2.3 ms.
 struct ScoreParams {
   DevStatus* status;
   const uint8_t* x;
@@ -41,13 +44,15 @@ struct ScoreParams {
 
 namespace score {
 constexpr int kTop = 32, kThreads = 256;
-// More short rows than there are places for CTAs of 256 threads go to CTAs of 64: 2048 rows of 300 logits 8.3 us (with 256 threads
-// 19.4), of 4000 11.8 (21.0), of 8000 19.0 (26.7); 100 rows of 8000 11.7 (6.0).
+// More short rows than there are places for CTAs of 256 threads go to CTAs of 64.  fp32 with the best token: 610 rows of 300 logits 4.6
+// us (with 256 threads 8.3), of 4000 6.3 (8.6), of 8000 7.8 (10.1); 2048 rows 7.7 (18.4), 11.1 (19.5), 17.2 (25.3); bf16 with the best
+// 5, 610 rows of 8000 8.1 (10.2); 100 rows of 8000 11.7 (6.0).
 constexpr int kFewThreads = 64, kShortRow = 8192;
 constexpr int kAgain = 2;  // vectors that a thread reads again at once
-constexpr int kCandidates = 1024;    // (a join has at most k k / j + k of them, see below)
+constexpr int kCandidates = 1024;    // (a join never has more, see below)
 constexpr int kPart = 4 + 2 * kTop;  // floats of a part: m, S, T, then its best keys
 constexpr int kMaxSplitRows = 2400;  // (a counter for each row that is split)
+constexpr int kScoreParts = 640;     // parts of all rows together, beside one a row
 using Key = unsigned long long;
 
 // Larger values, larger numbers; NaN the lowest; a zero has one sign.
@@ -341,7 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
     __syncthreads();
     if (!s_last) return;
     if (p.top) {
-      // With j = k / splits (rounded up), k / j of the parts' j-th keys reach the (k / j)-th largest of these: so do k keys.
+      // With j = k / splits and need = k / j (both rounded up), `need` of the parts' j-th keys reach the need-th largest of them: so do
+      // k keys.  No part has more than k, and of the other parts fewer than j each reach it: need k + (splits - need) (j - 1) at
+      // most, which is k k for j = 1 and less otherwise.
+      static_assert(kTop * kTop <= kCandidates && kScoreParts <= kCandidates, "a join's keys");
       const Key* keys = reinterpret_cast<const Key*>(parts + 4);
       constexpr int kStride = kPart / 2;
       const int nth = (p.top + p.splits - 1) / p.splits, need = (p.top + nth - 1) / nth;
@@ -412,10 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) score_kernel(const 
 
 // The parts that a row is cut into: three CTAs an SM of all rows (64 bf16 rows of 131072 without best tokens 9.5 us; two 10.1, four
 // 10.7; 300 fp32 rows with 5 33, 33 and 43), none of less than 4096 logits (one row with the best 20: 8.9 us; 2048 10.4, 8192 9.5).
-constexpr int kScoreParts = 640;  // of all rows together, beside one a row
 static int score_splits(int rows, int vocab, int sms) {
   if (rows <= 0 || rows > score::kMaxSplitRows) return 1;
-  int places = 3 * sms < kScoreParts ? 3 * sms : kScoreParts;
+  int places = 3 * sms < score::kScoreParts ? 3 * sms : score::kScoreParts;
   const int s = (places + rows - 1) / rows, most = vocab / (score::kThreads * 16);
   return s < most ? s : most < 1 ? 1 : most;
 }
@@ -426,7 +433,7 @@ using namespace tl;
 
 extern "C" size_t tl_token_logprobs_workspace_bytes(int rows, int vocab, int top) {
   if (rows < 0 || vocab < 1 || top < 0 || top > score::kTop || top > vocab) return 0;
-  const size_t parts = rows > score::kMaxSplitRows ? 0 : static_cast<size_t>(rows) + kScoreParts;
+  const size_t parts = rows > score::kMaxSplitRows ? 0 : static_cast<size_t>(rows) + score::kScoreParts;
   return kCounterBytes + parts * score::kPart * 4;
 }
 

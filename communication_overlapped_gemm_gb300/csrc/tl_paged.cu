@@ -143,7 +143,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Half a block (16 bytes of a row), the other half in the neighbouring lane: eight codes, and the block's scale.
 // One of a pair of fp16, twice (the products read it as it lies).
 __device__ __forceinline__ uint32_t both_halves(uint32_t v, int h) {
   uint32_t d;
@@ -151,6 +150,7 @@ __device__ __forceinline__ uint32_t both_halves(uint32_t v, int h) {
   else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(v));
   return d;
 }
+// Half a block (16 bytes of a row), the other half in the neighbouring lane: eight codes, and the block's scale.
 struct Half4 {
   uint32_t codes;
   uint8_t scale;
@@ -200,8 +200,8 @@ __device__ __forceinline__ Half4 quantise_half(uint4 v, float s) {
 }
 
 // As append_kernel: a thread has 16 bytes of a K and of a V row, and 4 of each's codes, all threads of an SM resident.  The
-// quantisation bounds it: 8192 tokens of 8 heads of 128 take 14.0 us, 3.1 TB/s, and 9.9 with codes that cost nothing
-// (44 registers a thread, five CTAs: 15.4).
+// quantisation bounds it: 8192 tokens of 8 heads of 128 take 13.6 to 14.5 us, 3.0 TB/s, and 9.9 with codes that cost nothing
+// (32 registers a thread, 24 bytes of them spilled; 44 registers, five CTAs: 15.4).
 template <class T, int D>
 __global__ void __launch_bounds__(256, 8) append4_kernel(const AppendParams p) {
   constexpr int kVec = D / 8;
@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(256, 8) append4_kernel(const AppendParams p) {
 // ---------------------------------------------------------------------------- gather
 // The rows of a cache back as packed rows of T, the values that they stand for in fp32, rounded once.  A thread has
 // eight values of a K and of a V row.
-// 8192 tokens of 8 heads of 128 out of 4 bits: 11.0 us, 3.9 TB/s; the ramp of a short launch, as the append's.
+// 8192 tokens of 8 heads of 128 out of 4 bits: 10.7 to 11.7 us, 3.9 TB/s, out of 8 11.3 to 12.0, out of 16 12.4 to 12.9, rows in L2 or
+// not; the ramp of a short launch, as the append's.
 struct GatherParams {
   CacheArgs c;
   DevStatus* status;
@@ -365,8 +366,7 @@ struct Shape {
   static constexpr int kCtas = D == 64 || (Bits < 16 && NB == 1) ? 3 : 2;
   static constexpr int kFit = (kCtas == 3 ? 49152 : 65536) / (kWarps * kStage);
   // (4 bits: a stage of 32 keys is long, and short sequences wait for all of a ring's first stages: two instead of three stages of
-  // 18 KB, with one term of a weight, 128 sequences of 500 rows 27.9 us instead of 30.2, one of 8k 11.5 instead of 12.0, 128 of up to 16k
-  // 237.6 instead of 235)
+  // 18 KB 128 sequences of 500 rows 33.8 us instead of 36.5, one of 8k 11.8 instead of 12.0, 128 of up to 16k 263.8 instead of 262.5)
   static constexpr int kMost = Bits == 4 ? (D == 128 ? 2 : 3) : 6;
   static constexpr int kStages = kFit > kMost ? kMost : kFit;
   static constexpr int kPitch = D + 4;                   // floats of a merged row
@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   if constexpr (Bits == 4) {
     // Rows are short, and kv heads that are read together join as one item of 32 rows, which costs more than scattered
     // reads do where there is little to read: heads apart up to 10 tiles a CTA, two up to 30, then as many as make 256 bytes.
-    // One sequence of 8k rows of 8 heads of 128 12.7 us with heads apart, 19.8 by four; 16 of 8k 54, by two 42, by four 45; 64
-    // of 16k 461, 261, 231.
+    // One sequence of 8k rows of 8 heads of 128 11.6 us with heads apart, 15.1 by two, 23.7 by four; 16 of 2k 19.0, 20.9, 23.5; 16 of
+    // 8k 51, 43.7, 46; 64 of 16k 460, 249, 247.
     const uint32_t share = total / gridDim.x;
     const int want = share < 10 ? 0 : share < 30 ? 1 : 2;
     if (want > 0 && p.lw > 0) {
@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(paged::kThreads, (paged::Shape<Bits, D, NB>::k
   // Tiles of a CTA: an even share, but, by the mean item, no more than 32 parts of an item, and no more than 16 if
   // that takes a CTA up to 2 tiles (4 or 8 of the shorter ones of `wh` heads): a join waits for 16 parts at a
   // time.  One sequence of 2k and 8k rows by the even share alone: bf16 8.3 and 11.3 us, e4m3 15.4 and 21.5; so
-  // 7.6, 11.4, 9.8 and 15.5.  (Over 4 bits, with tiles of 128 keys, 16 up to 4 tiles: one of 8k rows 11.4 us, 12.2 up to 2.)
+  // 7.6, 11.4, 9.8 and 15.5.  (Over 4 bits, with tiles of 128 keys, 16 up to 4 tiles: two of 8k rows
+  // 14.4 us, 15.5 up to 2, one of 12k 13.4 and 14.0, one of 6k 11.2 and 10.9.)
   const uint32_t mean = (total + p.batch * subs - 1) / (p.batch * subs);
   const uint32_t per = max(max((total + gridDim.x - 1) / gridDim.x, (mean + 31) / 32), min((mean + 15) / 16, (Bits == 4 ? 4u : 2u) << lw));
   // (where an item's parts are limited, `per` is up to grid / 32 even shares: 20 times the line does not fit 32 bits)

@@ -13,10 +13,12 @@ namespace tl {
 // and the token that opens a page writes the page's entry.  New pages are read from the free list and not from the table, so nothing waits for
 // a write.  Lengths (and `taken`) that are brought up to date in place may only be written once every CTA has read
 // them: a grid of up to 8 CTAs is one cluster then, with a barrier between; behind a larger one a second launch of one
-// CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows: 7.5 us, as one cluster 40; one of 3000 tokens, a cluster of 6: 4.1, not in place 3.7).
-// The launch and some four waits bound it: lengths, two rounds of sums, the table's entry, the stores.  A step of 64 sequences
-// 3.5 us; 37 sequences with 76000 new tokens and the slots of all 189000 rows 5.4 us; the slots of 8.3 million rows of 1000
-// sequences 22.6 us (each by a bisection of its own 61; four of a lane's pages read at once 24.7, and pages of one row 37 instead of 44).
+// CTA works them out again (37 sequences with 76000 new tokens and the slots of 189000 rows, in place: 7.5 us, as one cluster 40; one of
+// 3000 tokens, a cluster of 6: 4.0 to 4.1, not in place 3.7).
+// The launch and some four waits bound it: lengths, two rounds of sums, the table's entry, the stores.  Not in place: a step of 64
+// sequences 3.4 us (in place 2.9 to 3.4); 37 sequences with 76000 new tokens and the slots of all 189000 rows 5.4 us; the slots of 8.3
+// million rows of 1000 sequences 22.8 us (each by a bisection of its own 61; four of a lane's pages read at once 24.7, and pages of one
+// row 37 instead of 44).
 struct PlanParams {
   DevStatus* status;
   const int* lengths;
@@ -254,13 +256,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
 // threads work out the next token's angles, one pair each, before they turn to their rows of this one, and each thread's
 // next row is on its way.
 // 8192 tokens of 32 and 8 heads of 128: 30.2 us, 5.6 TB/s, 0.82 of the copy rate (without the norms 29.3; 64 and 8 heads 51,
-// 0.87; angles in every thread for itself 36.7, with 24 warps an SM for their registers; frequencies in turns kept from token to
+// 0.87; interleaved pairs, which pass through single fp32 arithmetic, 34.4, 0.72; angles in every thread for itself 36.7, with 24 warps an SM for their registers; frequencies in turns kept from token to
 // token 32.2).  One step of 64: 2.8 us, the launch and two waits.
 //
 // Angles: a position may be far and a frequency any number, and fp32 would leave a turn of 2^20 with 4 bits
 // behind the point.  So a frequency is held in turns as a 64-bit fraction, F = inv_freq / (2 pi) 2^64, whose product with
-// the position modulo 2^64 is the angle's fraction of a turn, off by at most position 2^-63 turns and exact in all the
-// turns before it.  sin and cos of the rest, within [-pi, pi], are off by 2^-21 at most (__sincosf), far below
+// the position modulo 2^64 is the angle's fraction of a turn, off by at most position (1 + |inv_freq| / 2) 2^-64 turns (F is cut to a
+// whole number, and 1 / (2 pi) is rounded to 64 bits) and exact in all the turns before it.  sin and cos of the rest, within [-pi, pi], are off by 2^-21 at most (__sincosf), far below
 // half a step of the 16-bit result.
 struct RopeParams {
   const uint8_t* x[2];  // q, k
@@ -518,9 +520,10 @@ extern "C" int tl_cache_plan(tl_ctx* ctx, const int* lengths, const int* counts,
   p.tokens = tokens;
   p.kv_tokens = kv_tokens;
   p.by_page = fast_div(page_size);
-  // More than 512 sequences go to CTAs of 1024 threads (a step of 4000: 10.5 us, with 512 threads 13.5; one of 64: 4.1 and 3.5),
-  // two packed tokens a thread up to 1024 threads an SM (one: the same; eight: 37 prompts 8.5 us instead of 6.2; 500 sequences with the
-  // slots of 4.1 million rows 12.7 us, with 512 threads an SM 16.5, with 2048 14.8).
+  // More than 512 sequences go to CTAs of 1024 threads (a step of 4000: 10.5 us, with 512 threads 13.5; one of 64: 4.4 and 3.4),
+  // two packed tokens a thread up to 1024 threads an SM (one: a step of 4000 9.3 us instead of 10.7, the others the same; eight: 13.2,
+  // and 37 prompts 6.2 us instead of 5.4; 500 sequences with the slots of 4.1 million rows 12.7 us, with 512 threads an SM 16.5, with
+  // 2048 14.8).
   const int threads = batch > plan::kFewThreads ? plan::kThreads : plan::kFewThreads, smem = (4 * batch + 2) * 4;
   const long long items = static_cast<long long>(tokens) + kv_tokens;
   long long ctas = (items + 2 * threads - 1) / (2 * threads);
