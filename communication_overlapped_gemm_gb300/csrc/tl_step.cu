@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
 // thread, and the mean takes 3 (d 64: 2) exchanges.  A CTA has some rows of a token, the same ones of each of its tokens; its
 // threads work out the next token's angles, one pair each, before they turn to their rows of this one, and each thread's
 // next row is on its way.
-// 8192 tokens of 32 and 8 heads of 128: 30.2 us, 5.6 TB/s, 0.82 of the copy rate (without the norms 29.3; 64 and 8 heads 51,
+// 8192 tokens of 32 and 8 heads of 128: 30.3 to 30.6 us, 5.5 TB/s, 0.81 of the copy rate (without the norms 29.3; 64 and 8 heads 51,
 // 0.87; interleaved pairs, which pass through single fp32 arithmetic, 34.4, 0.72; angles in every thread for itself 36.7, with 24 warps an SM for their registers; frequencies in turns kept from token to
 // token 32.2).  One step of 64: 2.8 us, the launch and two waits.
 //
