@@ -12,9 +12,8 @@ namespace tl {
 // where there are few rows; thread i has the vectors i, i + threads, .. with its own m, S and T.  The parts of a row are
 // joined by the CTA that finishes the last one, in their order.
 // Measured: 2048 rows of 50001 fp32 logits with the best token 73 to 76 us, 5.4 TB/s, 0.80 of the copy rate (without 68.3, 0.88; with
-// the best 20 94), of bf16 51 (46; 65), where instructions bound it; 64 rows of 131072 bf16 with the best 5 12.5 us (without 8.6 to
-// 9.5); one row of 131072 fp32 with the best 20 8.7 us, without 5.1:
-// the launch, the logits, the bound, the second look, the part, and the join are waited for in turn.  (One line of all rows cut
+// the best 20 94), of bf16 51 (46; 65), where instructions bound it (16 bytes of spills at 64 registers); 64 rows of 131072 bf16 with
+// the best 5 12.5 us (without 8.6 to 9.5); one row of 131072 fp32 with the best 20 8.7 us, without 5.1: the launch, the logits, the bound, the second look, the part, and the join are waited for in turn.  (One line of all rows cut
 // evenly over CTAs that stay: 83 to 99 us and 12; rows beyond the last full round cut in two or three: 81 to 84.)
 //
 // The most likely k <= 32 tokens need nothing in that loop but the maximum that a thread has anyway.  The k-th

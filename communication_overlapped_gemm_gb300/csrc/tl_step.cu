@@ -256,14 +256,15 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
 // threads work out the next token's angles, one pair each, before they turn to their rows of this one, and each thread's
 // next row is on its way.
 // 8192 tokens of 32 and 8 heads of 128: 30.3 to 30.6 us, 5.5 TB/s, 0.81 of the copy rate (without the norms 29.3; 64 and 8 heads 51,
-// 0.87; interleaved pairs, which pass through single fp32 arithmetic, 34.4, 0.72; angles in every thread for itself 36.7, with 24 warps an SM for their registers; frequencies in turns kept from token to
-// token 32.2).  One step of 64: 2.8 us, the launch and two waits.
+// 0.87; interleaved pairs, which pass through single fp32 arithmetic, 33.7 to 34.5, 0.72; angles in every thread for itself 36.7, with
+// 24 warps an SM for their registers; frequencies in turns kept from token to token 32.2).  One step of 64: 2.7 to 3.0 us, the launch
+// and two waits.
 //
 // Angles: a position may be far and a frequency any number, and fp32 would leave a turn of 2^20 with 4 bits
 // behind the point.  So a frequency is held in turns as a 64-bit fraction, F = inv_freq / (2 pi) 2^64, whose product with
 // the position modulo 2^64 is the angle's fraction of a turn, off by at most position (1 + |inv_freq| / 2) 2^-64 turns (F is cut to a
-// whole number, and 1 / (2 pi) is rounded to 64 bits) and exact in all the turns before it.  sin and cos of the rest, within [-pi, pi], are off by 2^-21 at most (__sincosf), far below
-// half a step of the 16-bit result.
+// whole number, and 1 / (2 pi) is rounded to 64 bits) and exact in all the turns before it.  sin and cos of the rest, within
+// [-pi, pi], are off by 2^-21 at most (__sincosf), far below half a step of the 16-bit result.
 struct RopeParams {
   const uint8_t* x[2];  // q, k
   uint8_t* y[2];

@@ -558,8 +558,8 @@ int tl_kv_gather(tl_ctx* ctx, const tl_paged_cache* cache, int dtype, const int*
  * side, d 64: 128 GB), its block scales likewise.
  * batch == 0 or heads == 0 is a no-op.
  * Precision: scores, weights and all sums are fp32.  Where a weight meets V it is a sum of two terms of dtype, off by
- * half a step squared (over a 4-bit cache of fp16); with an e4m3 cache one fp16 term, and in tl_window_attention one term of dtype, off by half
- * a step.  fp16 terms are also off by up to 2^-32 of the largest weight.  The division by the weights' sum comes
+ * half a step squared (over a 4-bit cache of fp16); with an e4m3 cache one fp16 term, and in tl_window_attention one
+ * term of dtype, off by half a step.  fp16 terms are also off by up to 2^-32 of the largest weight.  The division by the weights' sum comes
  * last, and a weight may be 2^8 until then: sums of bf16 rows within 2^-8 / n of fp32's largest value can overflow.
  * The result does not depend on what else runs, and is bit-identical run to run on one device.
  */
